@@ -27,9 +27,11 @@ FMT = {"q4_0": Q4_0, "q4_1": Q4_1, "q8_0": Q8_0, "q8_1": Q8_1, "q4_k": Q4_K, "q5
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED_FORMAT, ERR_SHAPE, ERR_ALIGNMENT, ERR_WORKSPACE, ERR_CUDA, \
     ERR_DEVICE_STATUS, ERR_TIMEOUT = range(9)
 DEV_BAD_EXPERT_ID, DEV_DUP_EXPERT_ID, DEV_WAIT_TIMEOUT = 0x1, 0x2, 0x4
+DEV_KV_LENGTH, DEV_KV_BLOCKS, DEV_KV_PAGES, DEV_KV_TOKENS, DEV_KV_PAGE = 0x08, 0x10, 0x20, 0x40, 0x80
+F32, F16, BF16 = 0, 1, 30      # value types of keys, values and queries (cq_dtype)
 
 # Every symbol include/cq.h declares, with (restype, argtypes).
-_P, _I64, _I, _SZ = C.c_void_p, C.c_int64, C.c_int, C.c_size_t
+_P, _I64, _I, _SZ, _F = C.c_void_p, C.c_int64, C.c_int, C.c_size_t, C.c_float
 SIGNATURES = {
     "cq_quantize_act": (_I, [_I, _I64, _I64, _P, _P, _P]),
     "cq_gemv": (_I, [_I, _I64, _I64, _I64, _P, _P, _P, _P]),
@@ -53,7 +55,21 @@ SIGNATURES = {
     "cq_repack_size": (_SZ, [_I, _I64, _I64]),
     "cq_repack": (_I, [_I, _I64, _I64, _P, _P, _P]),
     "cq_gemv_packed": (_I, [_I, _I64, _I64, _I64, _P, _P, _P, _P]),
+    "cq_kv_plan": (_I, [_I64, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P]),
+    "cq_kv_append": (_I, [_P, _I, _I64, _P, _I64, _P, _I64, _P, _P]),
+    "cq_kv_read": (_I, [_P, _I, _I64, _P, _P, _P, _P]),
+    "cq_attn_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "cq_attn_paged": (_I, [_P, _I, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _F, _I, _I64, _P, _I64, _P,
+                           _P, _SZ, _P]),
 }
+
+
+class cq_kv_cache(C.Structure):
+    """The C struct of an 8-bit paged key/value cache (include/cq.h)."""
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("num_pages", _I64), ("page_stride", _I64),
+                ("scale_stride", _I64), ("page_size", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("reserved", C.c_int32)]
+
 
 OPT_WEIGHTS_CONST = 1
 
@@ -135,6 +151,31 @@ def cq_repack(w_fmt, N, K, W, Wp, stream=0):
 
 def cq_gemv_packed(w_fmt, M, N, K, Wp, xq, y, stream=0):
     return lib().cq_gemv_packed(w_fmt, M, N, K, Wp, xq, y, stream)
+
+
+def cq_kv_plan(R, page_size, max_blocks, num_pages, past_len, new_len, free_pages, n_free, block_table, T, kv_len,
+               q_start, slots, positions, used, stream=0):
+    return lib().cq_kv_plan(R, page_size, max_blocks, num_pages, past_len, new_len, free_pages, n_free, block_table, T,
+                            kv_len, q_start, slots, positions, used, stream)
+
+
+def cq_kv_append(cache, dtype, T, k, k_stride, v, v_stride, slots, stream=0):
+    """cache: the address of a cq_kv_cache (ctypes.addressof), as in the calls below."""
+    return lib().cq_kv_append(cache, dtype, T, k, k_stride, v, v_stride, slots, stream)
+
+
+def cq_kv_read(cache, dtype, T, slots, k_out, v_out, stream=0):
+    return lib().cq_kv_read(cache, dtype, T, slots, k_out, v_out, stream)
+
+
+def cq_attn_workspace_size(q_heads, kv_heads, head_dim):
+    return lib().cq_attn_workspace_size(q_heads, kv_heads, head_dim)
+
+
+def cq_attn_paged(cache, dtype, R, T, q_heads, max_new, max_kv, q, q_stride, block_table, max_blocks, kv_len, q_start,
+                  scale, causal, window, out, out_stride, lse, ws, ws_bytes, stream=0):
+    return lib().cq_attn_paged(cache, dtype, R, T, q_heads, max_new, max_kv, q, q_stride, block_table, max_blocks,
+                               kv_len, q_start, scale, causal, window, out, out_stride, lse, ws, ws_bytes, stream)
 
 
 def cq_gemm_workspace_size(w_fmt, M, N, K):
@@ -316,3 +357,137 @@ def moe_t(W_gate, W_up, W_down, ids, route_w, xq, K: int, F: int, ws=None, out=N
                                       W_down.data_ptr(), ids.data_ptr(), route_w.data_ptr(), xq.data_ptr(),
                                       y.data_ptr(), ws.data_ptr(), ws.numel(), _stream_handle()))
     return y, ws
+
+
+# ------------------------------------------------- 8-bit paged key/value cache
+def _dtype(t) -> int:
+    torch = _torch()
+    d = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}.get(t.dtype if hasattr(t, "data_ptr") else t)
+    if d is None:
+        raise CqError("cq_dtype", ERR_UNSUPPORTED_FORMAT)
+    return d
+
+
+def _rows(fn, t, width):
+    """Pointer, row stride (elements) and rows of [T, width] or [T, heads, head_dim] with contiguous rows."""
+    if t.dim() == 3:
+        ok = t.shape[1] * t.shape[2] == width and t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == t.shape[2])
+    else:
+        ok = t.dim() == 2 and t.shape[1] == width and t.stride(1) == 1
+    if not ok:
+        raise CqError(fn, ERR_SHAPE)
+    T = t.shape[0]
+    return t.data_ptr(), t.stride(0) if T > 1 else width, T
+
+
+def _want(fn, t, dtype, *shape):
+    """t is a contiguous CUDA tensor of this type and shape (None: any length)."""
+    if t.dtype != dtype or t.dim() != len(shape) or not t.is_contiguous() or \
+            any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise CqError(fn, ERR_SHAPE)
+    return t.data_ptr()
+
+
+class KVCache:
+    """An 8-bit paged key/value cache over the caller's tensors: k, v int8 [pages, kv heads, page tokens, head size]
+    (pages may be strided: halves of one allocation), k_scale, v_scale fp32 [pages, kv heads]."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "num_pages", "kv_heads", "page_size", "head_dim", "_c", "addr")
+
+    def __init__(self, k, v, k_scale, v_scale):
+        torch = _torch()
+        if k.dim() != 4 or v.shape != k.shape or k.dtype != torch.int8 or v.dtype != torch.int8 or \
+                v.stride() != k.stride() or k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or \
+                k_scale.shape != k.shape[:2] or v_scale.shape != k.shape[:2] or k_scale.stride() != v_scale.stride():
+            raise CqError("cq_kv_cache", ERR_SHAPE)
+        n, h, p, d = k.shape
+        if k.stride()[1:] != (p * d, d, 1) or (h > 1 and k_scale.stride(1) != 1):
+            raise CqError("cq_kv_cache", ERR_SHAPE)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = n, h, p, d
+        one = n <= 1     # a single page's strides say nothing
+        self._c = cq_kv_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n,
+                              h * p * d if one else k.stride(0), h if one else k_scale.stride(0), p, h, d, 0)
+        self.addr = C.addressof(self._c)
+
+    @classmethod
+    def empty(cls, num_pages, kv_heads, page_size, head_dim, device="cuda"):
+        """A new cache; its pages hold nothing until they are written."""
+        torch = _torch()
+        kv = torch.zeros((2, num_pages, kv_heads, page_size, head_dim), dtype=torch.int8, device=device)
+        sc = torch.zeros((2, num_pages, kv_heads), dtype=torch.float32, device=device)
+        return cls(kv[0], kv[1], sc[0], sc[1])
+
+
+def kv_plan_t(past_len, new_len, block_table, free_pages, page_size: int, num_pages: int, tokens: int):
+    """cq_kv_plan: int32 past_len, new_len [R], block_table [R, max_blocks] (updated in place), free_pages [n]
+    -> kv_len int32 [R], q_start int32 [R + 1], slots int64 [tokens], positions int32 [tokens], used int32 [2]."""
+    torch = _torch()
+    fn, i32, R = "cq_kv_plan", torch.int32, past_len.shape[0]
+    dev = past_len.device
+    words = torch.empty(2 * R + 1 + tokens + 2, dtype=i32, device=dev)
+    kv_len, q_start, positions, used = words.split((R, R + 1, tokens, 2))
+    slots = torch.empty(tokens, dtype=torch.int64, device=dev)
+    base = words.data_ptr()
+    _check(fn, cq_kv_plan(R, page_size, block_table.shape[1], num_pages, _want(fn, past_len, i32, R),
+                          _want(fn, new_len, i32, R), _want(fn, free_pages, i32, None), free_pages.shape[0],
+                          _want(fn, block_table, i32, R, None), tokens, base, base + 4 * R, slots.data_ptr(),
+                          base + 4 * (2 * R + 1), base + 4 * (2 * R + 1 + tokens), _stream_handle()))
+    return kv_len, q_start, slots, positions, used
+
+
+def kv_append_t(cache: KVCache, k, v, slots):
+    """cq_kv_append: k, v [T, heads * size] or [T, heads, size] (fp32, fp16 or bf16, rows may be strided), slots int64 [T]."""
+    fn, width = "cq_kv_append", cache.kv_heads * cache.head_dim
+    kp, ks, T = _rows(fn, k, width)
+    vp, vs, Tv = _rows(fn, v, width)
+    if Tv != T or v.dtype != k.dtype:
+        raise CqError(fn, ERR_SHAPE)
+    _check(fn, cq_kv_append(cache.addr, _dtype(k), T, kp, ks, vp, vs, _want(fn, slots, _torch().int64, T),
+                            _stream_handle()))
+
+
+def kv_read_t(cache: KVCache, slots, dtype=None):
+    """cq_kv_read: slots int64 [T] -> keys and values [T, heads, size] of `dtype` (fp32 by default)."""
+    torch = _torch()
+    T = slots.shape[0]
+    k, v = torch.empty((2, T, cache.kv_heads, cache.head_dim), dtype=dtype or torch.float32, device=slots.device).unbind(0)
+    _check("cq_kv_read", cq_kv_read(cache.addr, _dtype(k), T, _want("cq_kv_read", slots, torch.int64, T), k.data_ptr(),
+                                    v.data_ptr(), _stream_handle()))
+    return k, v
+
+
+def attn_workspace_t(q_heads: int, kv_heads: int, head_dim: int, device="cuda"):
+    """A workspace for attn_paged_t, zeroed as its first use wants it."""
+    need = cq_attn_workspace_size(q_heads, kv_heads, head_dim)
+    if need == 0:
+        raise CqError("cq_attn_workspace_size", ERR_SHAPE)
+    return _torch().zeros(need, dtype=_torch().uint8, device=device)
+
+
+def attn_paged_t(q, cache: KVCache, block_table, kv_len, q_start, max_new: int, max_kv: int, *, scale=None,
+                 causal: bool = True, window: int = 0, ws=None, out=None, lse=True):
+    """cq_attn_paged: q [T, q heads, size] (fp32, fp16 or bf16; rows may be strided) over the cache
+    -> (out [T, q heads, size], lse fp32 [T, q heads] or None). block_table int32 [R, max_blocks], kv_len int32 [R],
+    q_start int32 [R + 1]; scale 1 / sqrt(size) by default; ws: attn_workspace_t's, made here when not given."""
+    torch = _torch()
+    fn, D, i32 = "cq_attn_paged", cache.head_dim, torch.int32
+    if q.dim() != 3 or q.shape[2] != D:
+        raise CqError(fn, ERR_SHAPE)
+    heads, R = q.shape[1], kv_len.shape[0]
+    qp, qs, T = _rows(fn, q, heads * D)
+    if ws is None:
+        ws = attn_workspace_t(heads, cache.kv_heads, D, q.device)
+    if out is None:
+        out = torch.empty((T, heads, D), dtype=q.dtype, device=q.device)
+    op, os_, To = _rows(fn, out, heads * D)
+    if To != T or out.dtype != q.dtype:
+        raise CqError(fn, ERR_SHAPE)
+    if lse is True:
+        lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
+    lp = _want(fn, lse, torch.float32, T, heads) if lse is not None and lse is not False else None
+    _check(fn, cq_attn_paged(cache.addr, _dtype(q), R, T, heads, max_new, max_kv, qp, qs,
+                             _want(fn, block_table, i32, R, None), block_table.shape[1], _want(fn, kv_len, i32, R),
+                             _want(fn, q_start, i32, R + 1), D ** -0.5 if scale is None else scale, int(causal), window,
+                             op, os_, lp, ws.data_ptr(), ws.numel(), _stream_handle()))
+    return out, (lse if lp is not None else None)

@@ -11,6 +11,7 @@
 
 #include "cq.h"
 #include "cq_internal.h"
+#include "kv.cuh"
 
 namespace {
 
@@ -276,7 +277,8 @@ cq_status cq_read_global_status(int32_t* out_code, int clear) {
         if (cudaMemcpyToSymbol(g_cq_status, &z, sizeof z) != cudaSuccess) return CQ_ERR_CUDA;
     }
     *out_code = v;
-    return v ? CQ_ERR_TIMEOUT : CQ_OK;
+    if (v & CQ_DEV_WAIT_TIMEOUT) return CQ_ERR_TIMEOUT;
+    return v ? CQ_ERR_DEVICE_STATUS : CQ_OK;
 }
 
 }  // extern "C"
@@ -412,6 +414,154 @@ cq_status cq_moe_read_status(const void* workspace, int32_t* out_code, void* str
     *out_code = v;
     if (v & CQ_DEV_WAIT_TIMEOUT) return CQ_ERR_TIMEOUT;
     return v ? CQ_ERR_DEVICE_STATUS : CQ_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+int dtype_bytes(int dt) { return dt == CQ_F32 ? 4 : dt == CQ_F16 || dt == CQ_BF16 ? 2 : 0; }
+int page_shift(int64_t page_size) {
+    return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : page_size == 128 ? 7 : -1;
+}
+constexpr int64_t INT_LIMIT = (int64_t(1) << 31) - 1;
+
+// The cache's description: sizes first (none of them is dereferenced), then its pointers.
+cq_status check_cache(const cq_kv_cache* c, cq::KvView* out) {
+    if (c == nullptr || c->num_pages < 0) return CQ_ERR_INVALID_ARG;
+    const int shift = page_shift(c->page_size);
+    if (shift < 0 || (c->head_dim != 64 && c->head_dim != 128) || c->kv_heads < 1 || c->kv_heads > 1024 ||
+        c->num_pages > INT_LIMIT || c->reserved != 0)
+        return CQ_ERR_SHAPE;
+    if (c->page_stride < int64_t(c->kv_heads) * c->page_size * c->head_dim || c->scale_stride < c->kv_heads)
+        return CQ_ERR_SHAPE;
+    if (c->k == nullptr || c->v == nullptr || c->k_scale == nullptr || c->v_scale == nullptr) return CQ_ERR_INVALID_ARG;
+    if (!aligned16(c->k) || !aligned16(c->v) || (c->page_stride & 15) != 0 || !aligned4(c->k_scale) ||
+        !aligned4(c->v_scale))
+        return CQ_ERR_ALIGNMENT;
+    *out = cq::KvView{static_cast<int8_t*>(c->k), static_cast<int8_t*>(c->v), c->k_scale, c->v_scale, c->num_pages,
+                      c->page_stride, c->scale_stride, c->page_size, shift, c->kv_heads, c->head_dim};
+    return CQ_OK;
+}
+
+// Rows of `width` values: stride (elements) and base fit 16-byte accesses.
+cq_status check_rows(const void* p, int64_t stride, int64_t width, int bytes) {
+    if (p == nullptr) return CQ_ERR_INVALID_ARG;
+    if (stride < width || stride > (int64_t(1) << 40)) return CQ_ERR_SHAPE;
+    return aligned16(p) && (stride * bytes & 15) == 0 ? CQ_OK : CQ_ERR_ALIGNMENT;
+}
+
+cq_status status_of(cudaError_t e) { return e == cudaSuccess ? CQ_OK : CQ_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" {
+
+cq_status cq_kv_plan(int64_t R, int64_t page_size, int64_t max_blocks, int64_t num_pages, const int32_t* past_len,
+                     const int32_t* new_len, const int32_t* free_pages, int64_t n_free, int32_t* block_table,
+                     int64_t T, int32_t* kv_len, int32_t* q_start, int64_t* slots, int32_t* positions, int32_t* used,
+                     void* stream) {
+    if (R < 0 || max_blocks < 0 || num_pages < 0 || n_free < 0 || T < 0) return CQ_ERR_INVALID_ARG;
+    const int shift = page_shift(page_size);
+    if (shift < 0 || R > 16384 || T > INT_LIMIT || n_free > INT_LIMIT || num_pages > INT_LIMIT ||
+        max_blocks > (INT_LIMIT >> shift))
+        return CQ_ERR_SHAPE;
+    if (q_start == nullptr || used == nullptr || (T > 0 && (slots == nullptr || positions == nullptr)) ||
+        (R > 0 && (past_len == nullptr || new_len == nullptr || kv_len == nullptr)) ||
+        (R > 0 && max_blocks > 0 && block_table == nullptr) || (n_free > 0 && free_pages == nullptr))
+        return CQ_ERR_INVALID_ARG;
+    const void* words[] = {past_len, new_len, free_pages, block_table, kv_len, q_start, positions, used};
+    for (const void* p : words)
+        if (!aligned4(p)) return CQ_ERR_ALIGNMENT;
+    if (!aligned_to(slots, 8)) return CQ_ERR_ALIGNMENT;
+    cq::DeviceInfo dev;
+    if (cq::device_info(&dev) != cudaSuccess) return CQ_ERR_CUDA;
+    return status_of(cq::launch_kv_plan(dev, static_cast<int>(R), shift, max_blocks, num_pages, past_len, new_len,
+                                        free_pages, static_cast<int>(n_free), block_table, static_cast<int>(T), kv_len,
+                                        q_start, slots, positions, used, static_cast<cudaStream_t>(stream)));
+}
+
+cq_status cq_kv_append(const cq_kv_cache* cache, cq_dtype dtype, int64_t T, const void* k, int64_t k_stride,
+                       const void* v, int64_t v_stride, const int64_t* slots, void* stream) {
+    const int bytes = dtype_bytes(dtype);
+    if (bytes == 0) return CQ_ERR_UNSUPPORTED_FORMAT;
+    if (T < 0) return CQ_ERR_INVALID_ARG;
+    cq::KvView c;
+    cq_status st = check_cache(cache, &c);
+    if (st != CQ_OK) return st;
+    if (T > INT_LIMIT) return CQ_ERR_SHAPE;
+    if (T == 0) return CQ_OK;
+    const int64_t width = int64_t(c.heads) * c.dim;
+    if ((st = check_rows(k, k_stride, width, bytes)) != CQ_OK) return st;
+    if ((st = check_rows(v, v_stride, width, bytes)) != CQ_OK) return st;
+    if (slots == nullptr) return CQ_ERR_INVALID_ARG;
+    if (!aligned_to(slots, 8)) return CQ_ERR_ALIGNMENT;
+    cq::DeviceInfo dev;
+    if (cq::device_info(&dev) != cudaSuccess) return CQ_ERR_CUDA;
+    return status_of(cq::launch_kv_append(dev, c, dtype, T, k, k_stride, v, v_stride, slots,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+cq_status cq_kv_read(const cq_kv_cache* cache, cq_dtype dtype, int64_t T, const int64_t* slots, void* k_out,
+                     void* v_out, void* stream) {
+    if (dtype_bytes(dtype) == 0) return CQ_ERR_UNSUPPORTED_FORMAT;
+    if (T < 0) return CQ_ERR_INVALID_ARG;
+    cq::KvView c;
+    const cq_status st = check_cache(cache, &c);
+    if (st != CQ_OK) return st;
+    if (T > INT_LIMIT) return CQ_ERR_SHAPE;
+    if (T == 0 || (k_out == nullptr && v_out == nullptr)) return CQ_OK;
+    if (slots == nullptr) return CQ_ERR_INVALID_ARG;
+    if (!aligned_to(slots, 8) || !aligned16(k_out) || !aligned16(v_out)) return CQ_ERR_ALIGNMENT;
+    cq::DeviceInfo dev;
+    if (cq::device_info(&dev) != cudaSuccess) return CQ_ERR_CUDA;
+    return status_of(cq::launch_kv_read(dev, c, dtype, T, slots, k_out, v_out, static_cast<cudaStream_t>(stream)));
+}
+
+size_t cq_attn_workspace_size(int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+    if (kv_heads < 1 || q_heads < 1 || q_heads > 1024 || q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128))
+        return 0;
+    return cq::attn_workspace_size(q_heads, kv_heads, head_dim);
+}
+
+cq_status cq_attn_paged(const cq_kv_cache* cache, cq_dtype dtype, int64_t R, int64_t T, int64_t q_heads,
+                        int64_t max_new, int64_t max_kv, const void* q, int64_t q_stride, const int32_t* block_table,
+                        int64_t max_blocks, const int32_t* kv_len, const int32_t* q_start, float scale, int causal,
+                        int64_t window, void* out, int64_t out_stride, float* lse, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    const int bytes = dtype_bytes(dtype);
+    if (bytes == 0) return CQ_ERR_UNSUPPORTED_FORMAT;
+    if (R < 0 || T < 0 || q_heads < 0 || max_new < 0 || max_kv < 0 || max_blocks < 0 || window < 0 ||
+        (causal != 0 && causal != 1))
+        return CQ_ERR_INVALID_ARG;
+    cq::KvView c;
+    cq_status st = check_cache(cache, &c);
+    if (st != CQ_OK) return st;
+    if (q_heads < 1 || q_heads > 1024 || q_heads % c.heads != 0 || R > 16384 || T > INT_LIMIT ||
+        max_blocks > (INT_LIMIT >> c.page_shift))
+        return CQ_ERR_SHAPE;
+    if (R == 0 || T == 0) return CQ_OK;
+    const int64_t width = q_heads * c.dim;
+    if ((st = check_rows(q, q_stride, width, bytes)) != CQ_OK) return st;
+    if ((st = check_rows(out, out_stride, width, bytes)) != CQ_OK) return st;
+    if (kv_len == nullptr || q_start == nullptr || (max_blocks > 0 && block_table == nullptr)) return CQ_ERR_INVALID_ARG;
+    const size_t need = cq::attn_workspace_size(q_heads, c.heads, c.dim);
+    if (workspace == nullptr || workspace_bytes < need) return CQ_ERR_WORKSPACE;
+    if (!aligned4(kv_len) || !aligned4(q_start) || !aligned4(block_table) || !aligned4(lse) || !aligned_to(workspace, 256))
+        return CQ_ERR_ALIGNMENT;
+    cq::DeviceInfo dev;
+    if (cq::device_info(&dev) != cudaSuccess) return CQ_ERR_CUDA;
+    cq::AttnArgs a{};
+    a.q = q; a.out = out; a.lse = lse;
+    a.table = block_table; a.kv_len = kv_len; a.q_start = q_start;
+    a.status = dev.status; a.ws = workspace;
+    a.q_stride = q_stride; a.out_stride = out_stride;
+    a.max_blocks = max_blocks; a.window = window;
+    a.max_new = max_new; a.max_kv = max_kv;
+    a.scale = scale;
+    a.R = static_cast<int>(R); a.T = static_cast<int>(T); a.heads = static_cast<int>(q_heads); a.causal = causal;
+    return status_of(cq::launch_attn(dev, c, dtype, a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
