@@ -360,32 +360,57 @@ def moe_t(W_gate, W_up, W_down, ids, route_w, xq, K: int, F: int, ws=None, out=N
 
 
 # ------------------------------------------------- 8-bit paged key/value cache
-def _dtype(t) -> int:
-    torch = _torch()
-    d = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}.get(t.dtype if hasattr(t, "data_ptr") else t)
-    if d is None:
-        raise CqError("cq_dtype", ERR_UNSUPPORTED_FORMAT)
-    return d
+# These calls are made once a layer and step, on small batches too, so the
+# helpers look at each tensor once and keep what does not change.
+_tables = {}
+
+
+def _torch_tables():
+    """torch, its integer types, the cq_dtype of each value type, the current device and the raw stream of a device."""
+    if not _tables:
+        torch = _torch()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda d: torch.cuda.current_stream(d).cuda_stream)
+        _tables["all"] = (torch, torch.int32, torch.int64,
+                          {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}, raw)
+    return _tables["all"]
+
+
+def _stream_of(t, raw):
+    """The current stream of the tensor's device; no stream for a host tensor, whose call is refused here."""
+    i = t.get_device()
+    if i < 0:
+        raise CqError("cq", ERR_INVALID_ARG)
+    return raw(i)
 
 
 def _rows(fn, t, width):
     """Pointer, row stride (elements) and rows of [T, width] or [T, heads, head_dim] with contiguous rows."""
-    if t.dim() == 3:
-        ok = t.shape[1] * t.shape[2] == width and t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == t.shape[2])
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        ok = shape[1] * shape[2] == width and stride[2] == 1 and (shape[1] == 1 or stride[1] == shape[2])
     else:
-        ok = t.dim() == 2 and t.shape[1] == width and t.stride(1) == 1
+        ok = len(shape) == 2 and shape[1] == width and stride[1] == 1
     if not ok:
         raise CqError(fn, ERR_SHAPE)
-    T = t.shape[0]
-    return t.data_ptr(), t.stride(0) if T > 1 else width, T
+    T = shape[0]
+    return t.data_ptr(), stride[0] if T > 1 else width, T
 
 
-def _want(fn, t, dtype, *shape):
-    """t is a contiguous CUDA tensor of this type and shape (None: any length)."""
-    if t.dtype != dtype or t.dim() != len(shape) or not t.is_contiguous() or \
-            any(n is not None and n != m for n, m in zip(shape, t.shape)):
+def _vec(fn, t, dtype, n):
+    """Pointer of a contiguous vector of this type and length."""
+    shape = t.shape
+    if t.dtype != dtype or len(shape) != 1 or shape[0] != n or not t.is_contiguous():
         raise CqError(fn, ERR_SHAPE)
     return t.data_ptr()
+
+
+def _table(fn, t, i32, R):
+    """Pointer and width of a contiguous int32 block table of R rows."""
+    shape = t.shape
+    if t.dtype != i32 or len(shape) != 2 or shape[0] != R or not t.is_contiguous():
+        raise CqError(fn, ERR_SHAPE)
+    return t.data_ptr(), shape[1]
 
 
 class KVCache:
@@ -422,38 +447,51 @@ class KVCache:
 def kv_plan_t(past_len, new_len, block_table, free_pages, page_size: int, num_pages: int, tokens: int):
     """cq_kv_plan: int32 past_len, new_len [R], block_table [R, max_blocks] (updated in place), free_pages [n]
     -> kv_len int32 [R], q_start int32 [R + 1], slots int64 [tokens], positions int32 [tokens], used int32 [2]."""
-    torch = _torch()
-    fn, i32, R = "cq_kv_plan", torch.int32, past_len.shape[0]
+    torch, i32, i64, _, raw = _torch_tables()
+    fn, R, n_free = "cq_kv_plan", past_len.shape[0], free_pages.shape[0]
+    tp, wide = _table(fn, block_table, i32, R)
+    past, new, free = _vec(fn, past_len, i32, R), _vec(fn, new_len, i32, R), _vec(fn, free_pages, i32, n_free)
+    stream = _stream_of(past_len, raw)
     dev = past_len.device
     words = torch.empty(2 * R + 1 + tokens + 2, dtype=i32, device=dev)
-    kv_len, q_start, positions, used = words.split((R, R + 1, tokens, 2))
-    slots = torch.empty(tokens, dtype=torch.int64, device=dev)
+    slots = torch.empty(tokens, dtype=i64, device=dev)
     base = words.data_ptr()
-    _check(fn, cq_kv_plan(R, page_size, block_table.shape[1], num_pages, _want(fn, past_len, i32, R),
-                          _want(fn, new_len, i32, R), _want(fn, free_pages, i32, None), free_pages.shape[0],
-                          _want(fn, block_table, i32, R, None), tokens, base, base + 4 * R, slots.data_ptr(),
-                          base + 4 * (2 * R + 1), base + 4 * (2 * R + 1 + tokens), _stream_handle()))
+    st = (_lib or lib()).cq_kv_plan(R, page_size, wide, num_pages, past, new, free, n_free, tp, tokens, base,
+                                    base + 4 * R, slots.data_ptr(), base + 4 * (2 * R + 1),
+                                    base + 4 * (2 * R + 1 + tokens), stream)
+    if st:
+        raise CqError(fn, st)
+    kv_len, q_start, positions, used = words.split((R, R + 1, tokens, 2))
     return kv_len, q_start, slots, positions, used
 
 
 def kv_append_t(cache: KVCache, k, v, slots):
     """cq_kv_append: k, v [T, heads * size] or [T, heads, size] (fp32, fp16 or bf16, rows may be strided), slots int64 [T]."""
-    fn, width = "cq_kv_append", cache.kv_heads * cache.head_dim
+    _, _, i64, dtypes, raw = _torch_tables()
+    fn, width, dt = "cq_kv_append", cache.kv_heads * cache.head_dim, k.dtype
     kp, ks, T = _rows(fn, k, width)
     vp, vs, Tv = _rows(fn, v, width)
-    if Tv != T or v.dtype != k.dtype:
+    if Tv != T or v.dtype != dt:
         raise CqError(fn, ERR_SHAPE)
-    _check(fn, cq_kv_append(cache.addr, _dtype(k), T, kp, ks, vp, vs, _want(fn, slots, _torch().int64, T),
-                            _stream_handle()))
+    st = (_lib or lib()).cq_kv_append(cache.addr, dtypes.get(dt, -1), T, kp, ks, vp, vs, _vec(fn, slots, i64, T),
+                                      _stream_of(slots, raw))
+    if st:
+        raise CqError(fn, st)
 
 
 def kv_read_t(cache: KVCache, slots, dtype=None):
     """cq_kv_read: slots int64 [T] -> keys and values [T, heads, size] of `dtype` (fp32 by default)."""
-    torch = _torch()
-    T = slots.shape[0]
-    k, v = torch.empty((2, T, cache.kv_heads, cache.head_dim), dtype=dtype or torch.float32, device=slots.device).unbind(0)
-    _check("cq_kv_read", cq_kv_read(cache.addr, _dtype(k), T, _want("cq_kv_read", slots, torch.int64, T), k.data_ptr(),
-                                    v.data_ptr(), _stream_handle()))
+    torch, _, i64, dtypes, raw = _torch_tables()
+    fn, T = "cq_kv_read", slots.shape[0]
+    sp, stream = _vec(fn, slots, i64, T), _stream_of(slots, raw)
+    dt = dtype or torch.float32
+    if dt not in dtypes:
+        raise CqError(fn, ERR_UNSUPPORTED_FORMAT)
+    shape, dev = (T, cache.kv_heads, cache.head_dim), slots.device
+    k, v = torch.empty(shape, dtype=dt, device=dev), torch.empty(shape, dtype=dt, device=dev)
+    st = (_lib or lib()).cq_kv_read(cache.addr, dtypes[dt], T, sp, k.data_ptr(), v.data_ptr(), stream)
+    if st:
+        raise CqError(fn, st)
     return k, v
 
 
@@ -469,25 +507,37 @@ def attn_paged_t(q, cache: KVCache, block_table, kv_len, q_start, max_new: int, 
                  causal: bool = True, window: int = 0, ws=None, out=None, lse=True):
     """cq_attn_paged: q [T, q heads, size] (fp32, fp16 or bf16; rows may be strided) over the cache
     -> (out [T, q heads, size], lse fp32 [T, q heads] or None). block_table int32 [R, max_blocks], kv_len int32 [R],
-    q_start int32 [R + 1]; scale 1 / sqrt(size) by default; ws: attn_workspace_t's, made here when not given."""
-    torch = _torch()
-    fn, D, i32 = "cq_attn_paged", cache.head_dim, torch.int32
-    if q.dim() != 3 or q.shape[2] != D:
+    q_start int32 [R + 1]; scale 1 / sqrt(size) by default; ws: attn_workspace_t's, made here when not given;
+    lse: a tensor, True for a new one, or None."""
+    torch, i32, _, dtypes, raw = _torch_tables()
+    fn, D, dt = "cq_attn_paged", cache.head_dim, q.dtype
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != D:
         raise CqError(fn, ERR_SHAPE)
-    heads, R = q.shape[1], kv_len.shape[0]
-    qp, qs, T = _rows(fn, q, heads * D)
+    T, heads = shape[0], shape[1]
+    R, width = kv_len.shape[0], heads * D
+    qp, qs, _ = _rows(fn, q, width)
+    tp, wide = _table(fn, block_table, i32, R)
+    kvp, sp = _vec(fn, kv_len, i32, R), _vec(fn, q_start, i32, R + 1)
+    stream, dev = _stream_of(q, raw), q.device
     if ws is None:
-        ws = attn_workspace_t(heads, cache.kv_heads, D, q.device)
+        ws = attn_workspace_t(heads, cache.kv_heads, D, dev)
     if out is None:
-        out = torch.empty((T, heads, D), dtype=q.dtype, device=q.device)
-    op, os_, To = _rows(fn, out, heads * D)
-    if To != T or out.dtype != q.dtype:
-        raise CqError(fn, ERR_SHAPE)
+        out = torch.empty(shape, dtype=dt, device=dev)
+        op, os_ = out.data_ptr(), width
+    else:
+        op, os_, To = _rows(fn, out, width)
+        if To != T or out.dtype != dt:
+            raise CqError(fn, ERR_SHAPE)
     if lse is True:
-        lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
-    lp = _want(fn, lse, torch.float32, T, heads) if lse is not None and lse is not False else None
-    _check(fn, cq_attn_paged(cache.addr, _dtype(q), R, T, heads, max_new, max_kv, qp, qs,
-                             _want(fn, block_table, i32, R, None), block_table.shape[1], _want(fn, kv_len, i32, R),
-                             _want(fn, q_start, i32, R + 1), D ** -0.5 if scale is None else scale, int(causal), window,
-                             op, os_, lp, ws.data_ptr(), ws.numel(), _stream_handle()))
-    return out, (lse if lp is not None else None)
+        lse = torch.empty((T, heads), dtype=torch.float32, device=dev)
+    elif lse is False:
+        lse = None
+    elif lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, heads) or not lse.is_contiguous()):
+        raise CqError(fn, ERR_SHAPE)
+    st = (_lib or lib()).cq_attn_paged(cache.addr, dtypes.get(dt, -1), R, T, heads, max_new, max_kv, qp, qs, tp, wide,
+                                       kvp, sp, D ** -0.5 if scale is None else scale, 1 if causal else 0, window, op,
+                                       os_, None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), stream)
+    if st:
+        raise CqError(fn, st)
+    return out, lse

@@ -1,0 +1,94 @@
+// Shared pieces of the attention kernels: lengths and visible ranges, query
+// scaling, streaming loads, output rows.
+#pragma once
+#include <cstdint>
+
+#include "cq_device.cuh"
+#include "cq_internal.h"
+#include "kv.cuh"
+
+namespace cq {
+
+// CTAs that share the partial results of a call: the workspace has two slots
+// and a counter for each.
+constexpr int ATTN_MAX_CTAS = 256;
+
+struct RowsPlan {
+    int* count;          // [ATTN_MAX_CTAS], zero between calls
+    float* part;         // [ATTN_MAX_CTAS][2][16][head_dim + 4]
+};
+
+// Requests that the row-tile kernel takes.
+__device__ __forceinline__ bool rows_take(const RowsPlan&, int n, int) { return n > 0; }
+
+// First token, new tokens (clipped to T) and length (clipped to the table) of request r.
+__device__ __forceinline__ void request_of(const KvView& c, const AttnArgs& a, int r, int& first, int& n, int& kv) {
+    const int s = a.q_start[r], e = a.q_start[r + 1];
+    first = min(max(s, 0), a.T);
+    n = max(min(e, a.T) - first, 0);
+    kv = static_cast<int>(min(static_cast<int64_t>(max(a.kv_len[r], 0)), a.max_blocks << c.page_shift));
+}
+
+// Keys [from, stop) that the request's token t of n sees; 0, 0 if none.
+__device__ __forceinline__ void row_range(const AttnArgs& a, int n, int kv, int t, int& from, int& stop) {
+    const int64_t pos = static_cast<int64_t>(kv) - n + t;
+    int64_t s = a.causal ? min(static_cast<int64_t>(kv), pos + 1) : kv;
+    int64_t f = a.window > 0 ? max(int64_t(0), pos - a.window + 1) : 0;
+    if (s <= f) s = f = 0;
+    from = static_cast<int>(f);
+    stop = static_cast<int>(s);
+}
+
+// From the bits of a row's largest |value|: the power of two that brings it to
+// [2^8, 2^9) and its inverse; NaN for a row that is not finite.
+__device__ __forceinline__ void row_scale(uint32_t top, float& mul, float& back) {
+    const int e = static_cast<int>(top >> 23);              // biased exponent, 0 for zero and subnormal
+    if (e == 255) { mul = back = __uint_as_float(0x7fffffffu); return; }
+    const int up = min(135 - max(e, 1), 126);               // 2^up; stays a normal number
+    mul = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+    back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 load2(const __half* p) { return __half22float2(*reinterpret_cast<const __half2*>(p)); }
+__device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// Cache rows are read once: past L1.
+__device__ __forceinline__ uint4 ldg_stream16(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ldg_stream8(const void* p) {
+    uint2 v;
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+
+// Four values of an output row from the sums: rho counts the rows (token,
+// head) of the request's kv head; acc, l in units of 2^(m - off).
+template <typename T, int D>
+__device__ __forceinline__ void write_row(const AttnArgs& a, int first, int h, int G, int rho, int col, float4 acc,
+                                          float m, float l, float off) {
+    const int64_t tok = first + rho / G;
+    const int head = h * G + rho % G;
+    const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);      // 0 only where nothing was seen
+    store4(static_cast<T*>(a.out) + tok * a.out_stride + head * D + col,
+           make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    if (col == 0 && a.lse != nullptr)
+        a.lse[tok * a.heads + head] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m - off + log2f(l));
+}
+
+cudaError_t launch_attn_rows(const DeviceInfo& dev, const KvView& c, int dtype, const AttnArgs& a, const RowsPlan& pl,
+                             cudaStream_t s);
+
+}  // namespace cq

@@ -1,0 +1,572 @@
+// Attention over the 8-bit paged cache for few query rows a (request, kv head):
+// decoding and verification (cq_attn_paged in include/cq.h).
+//
+// With x_j = log2(e) * scale * s_k * (q . k_j) + log2(s_v), the int8 values k_j, v_j
+// and their blocks' scales s_k, s_v:
+//   P_j = 2^(x_j - M + OFF),  out = (sum_j P_j v_j) / (sum_j P_j / s_v),
+//   lse = ln 2 * (M - OFF + log2(sum_j P_j / s_v)),
+// so both scales cost one fused multiply-add a score and the tensor cores see
+// the stored integers (exact in binary16). M is a running reference, raised
+// only when a score passes it by 8: P_j then stays below 2^15, and a value
+// that is small against the largest keeps its 11 bits down to 2^-21 of it.
+//
+// Both products are mma.sync m16n8k16: 16 query rows (token, head of the kv
+// head's group) against 8 keys, and against 8 head dimensions. The cache is
+// read once, straight from global memory into the B fragments' registers: a
+// key row's 16-byte piece holds four k-steps of its lane, a value row's piece
+// one dimension of each of 16 (8 for D = 64) column tiles, so no shared memory
+// or shuffle stands between the load and the product. fp32 queries and
+// probabilities enter as two binary16 parts (22 bits).
+//
+// Work: every (request, kv head, row tile) is a group of units of 64 keys; the
+// units of all groups, in order, are split evenly over the CTAs, whatever the
+// lengths. A CTA's warps take its piece's tiles in turn and merge in shared
+// memory; pieces of a group that several CTAs share go to the workspace, and the
+// CTA that arrives last at the group's counter joins them in order.
+#include <algorithm>
+#include <type_traits>
+
+#include "attn_common.cuh"
+#include "cq_device.cuh"
+#include "cq_internal.h"
+#include "kv.cuh"
+#include "tc.cuh"
+
+namespace cq {
+namespace {
+
+constexpr int NW = 8;                     // warps a CTA
+constexpr int THREADS = NW * 32;
+constexpr int UNIT = 64;                  // keys of a work unit
+constexpr int MIN_UNITS = 2;              // a CTA is worth at least so many
+constexpr float OFF = 7.0f, RAISE = 8.0f;
+// fp32: probabilities below this leave binary16's range before they have given
+// 22 bits. They enter as two bfloat16 parts instead, in the tiles that have any
+// (2^-20 of the largest: rare unless the softmax is very peaked).
+constexpr float SMALL = 1.0f / 8192.0f;
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma16816_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+// Two binary16 integers of at most 8 bits as bfloat16 (exact).
+__device__ __forceinline__ uint32_t half_to_bf16(uint32_t h) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+}
+
+// What the rows of one group see, and its units.
+struct Group {
+    int r, h, i;             // request, kv head, row tile
+    int first;               // first token of the request
+    int n, kv;               // its new tokens and its length
+    int u0;                  // first key of the group's units (a multiple of UNIT)
+    int units;
+};
+
+// Keys [from, stop) that some row of the request sees.
+__device__ __forceinline__ void request_range(const AttnArgs& a, int n, int kv, int& from, int& stop) {
+    from = 0;
+    stop = kv;
+    if (a.window > 0) {
+        const int64_t f = static_cast<int64_t>(kv) - n + 1 - a.window;
+        if (f > 0) from = static_cast<int>(min(f, static_cast<int64_t>(kv)));
+    }
+}
+
+__device__ __forceinline__ int request_units(const AttnArgs& a, int n, int kv) {
+    int from, stop;
+    request_range(a, n, kv, from, stop);
+    const int u = (stop + UNIT - 1) / UNIT - from / UNIT;
+    return max(u, 1);
+}
+
+// Register buffers of one tile: NSUB sub-blocks of 16 keys.
+template <int D> struct Tile {
+    static constexpr int NSUB = 128 / D;
+    uint4 k[NSUB][2][D / 64];     // [sub-block][8 keys][64 dimensions]
+    uint32_t v[NSUB][4][D / 32];  // [sub-block][its keys 2t, 2t+1, 2t+8, 2t+9][words]
+    float ks[NSUB], vs[NSUB];
+    int row0[NSUB];               // first key; < 0: nothing of the sub-block counts
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(THREADS, 1) attn_rows_kernel(const KvView c, const AttnArgs a, const RowsPlan pl) {
+    pdl_trigger();
+    pdl_wait();
+    constexpr bool F32 = std::is_same<T, float>::value;
+    constexpr bool SPLIT_P = !std::is_same<T, __nv_bfloat16>::value;
+    constexpr int NSUB = Tile<D>::NSUB, KST = D / 16, NT = D / 8;
+    constexpr int TK = 16 * NSUB;                     // keys of a tile
+    constexpr int ROWF = D + 4;                       // floats of a merge row
+    extern __shared__ __align__(16) uint8_t rows_smem[];
+    int64_t* cum = reinterpret_cast<int64_t*>(rows_smem);                     // [R + 1] first unit of each request
+    const int cum_bytes = ((a.R + 1) * 8 + 15) & ~15;
+    uint4* qf = reinterpret_cast<uint4*>(rows_smem + cum_bytes);              // [1 or 2][KST][32] A fragments
+    float* rowf = reinterpret_cast<float*>(qf + (F32 ? 2 : 1) * KST * 32);    // [16] factor of each row's scores
+    float* merge = rowf + 16;                                                 // [NW][16][ROWF]
+    float* ml = merge + NW * 16 * ROWF;                                       // [NW][16][2]
+    __shared__ int64_t wsum[NW];
+    __shared__ int last_flag;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
+    const int G = a.heads / c.heads;
+
+    // ---- every CTA counts all requests' units
+    int64_t carry = 0;
+    for (int r0 = 0; r0 < a.R; r0 += THREADS) {
+        const int r = r0 + tid;
+        int64_t x = 0;
+        if (r < a.R) {
+            int first, n, kv;
+            request_of(c, a, r, first, n, kv);
+            if (rows_take(pl, n, G)) x = static_cast<int64_t>(request_units(a, n, kv)) * c.heads * ((static_cast<int64_t>(n) * G + 15) / 16);
+        }
+        int64_t s = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += up;
+        }
+        if (lane == 31) wsum[warp] = s;
+        __syncthreads();
+        int64_t before = carry, all = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) before += wsum[w];
+            all += wsum[w];
+        }
+        if (r < a.R) cum[r] = before + s - x;
+        carry += all;
+        __syncthreads();
+    }
+    if (tid == 0) cum[a.R] = carry;
+    __syncthreads();
+    const int64_t U = carry;
+    if (U == 0) return;
+    const int64_t nact = min(static_cast<int64_t>(gridDim.x), (U + MIN_UNITS - 1) / MIN_UNITS);
+    const int64_t me = blockIdx.x;
+    if (me >= nact) return;
+    int64_t u = me * U / nact;
+    const int64_t u_end = (me + 1) * U / nact;
+    const float lscale = fabsf(a.scale) * 1.4426950408889634f;
+    bool first_piece = true;
+
+    while (u < u_end) {
+        // ---- the group that unit u belongs to
+        Group gr;
+        {
+            int lo = 0, hi = a.R;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (cum[mid] <= u) lo = mid; else hi = mid;
+            }
+            gr.r = lo;
+        }
+        request_of(c, a, gr.r, gr.first, gr.n, gr.kv);
+        int from, stop;
+        request_range(a, gr.n, gr.kv, from, stop);
+        gr.u0 = (from / UNIT) * UNIT;
+        gr.units = request_units(a, gr.n, gr.kv);
+        const int64_t in = u - cum[gr.r], gi = in / gr.units;
+        const int piece0 = static_cast<int>(in - gi * gr.units);
+        const int nrt = (gr.n * G + 15) / 16;
+        gr.h = static_cast<int>(gi / nrt);
+        gr.i = static_cast<int>(gi - static_cast<int64_t>(gr.h) * nrt);
+        const int64_t group_u = u - piece0;                       // the group's first unit
+        const int piece1 = static_cast<int>(min(static_cast<int64_t>(gr.units), u_end - group_u));
+        const int rows = min(16, gr.n * G - 16 * gr.i);           // of this tile
+        // what this lane's two rows see, and what the tile's rows see together
+        int rfrom[2], rstop[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int rho = 16 * gr.i + g + 8 * e;
+            row_range(a, gr.n, gr.kv, rho / G, rfrom[e], rstop[e]);
+            if (g + 8 * e >= rows) rfrom[e] = rstop[e] = 0;
+        }
+        int tfrom, tstop, x0, x1;
+        row_range(a, gr.n, gr.kv, (16 * gr.i) / G, tfrom, x0);
+        row_range(a, gr.n, gr.kv, (16 * gr.i + rows - 1) / G, x1, tstop);
+        // keys that every row sees: from the last row's first to the first row's last
+        const int all_from = x1, all_stop = x0;
+
+        // ---- query fragments: k-step (j, s) of lane (g, t) holds dimensions 64j + 16t + 4s + 0..3
+        __syncthreads();                                          // the previous piece's readers are done
+        for (int row = warp; row < 16; row += NW) {
+            constexpr int PER = D / 32;                           // consecutive dimensions of a lane
+            float q[PER];
+            const int rho = 16 * gr.i + row;
+            const int64_t tok = gr.first + rho / G;
+            const int head = gr.h * G + rho % G;
+            const bool on = row < rows;
+#pragma unroll
+            for (int i = 0; i < PER; i += 2) {
+                float2 v = make_float2(0.0f, 0.0f);
+                if (on) v = load2(static_cast<const T*>(a.q) + tok * a.q_stride + head * D + lane * PER + i);
+                q[i] = v.x;
+                q[i + 1] = v.y;
+            }
+            // A power of two brings the row's largest value to [2^8, 2^9): exact, and
+            // nothing that matters is below binary16's range. NaN for a row that is not finite.
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) top = max(top, __float_as_uint(fabsf(q[i])));
+            top = __reduce_max_sync(0xffffffffu, top);
+            float mul, back;
+            row_scale(top, mul, back);
+            if (a.scale < 0.0f) mul = -mul;
+            if (lane == 0) rowf[row] = back * lscale;
+#pragma unroll
+            for (int i = 0; i < PER; i += 2) {
+                const int d = lane * PER + i;
+                const int j = d >> 6, t = (d >> 4) & 3, s = (d >> 2) & 3, half = (d >> 1) & 1;
+                const float v0 = q[i] * mul, v1 = q[i + 1] * mul;
+                const __half2 hi = __floats2half2_rn(v0, v1);
+                uint32_t* dst = reinterpret_cast<uint32_t*>(qf + (4 * j + s) * 32 + 4 * (row & 7) + t) + (row >> 3) + 2 * half;
+                *dst = *reinterpret_cast<const uint32_t*>(&hi);
+                if constexpr (F32) {
+                    const float2 back2 = __half22float2(hi);
+                    const __half2 lo = __floats2half2_rn(v0 - back2.x, v1 - back2.y);
+                    dst[KST * 32 * 4] = *reinterpret_cast<const uint32_t*>(&lo);
+                }
+            }
+        }
+        __syncthreads();
+        uint32_t qh[KST][4];
+#pragma unroll
+        for (int s = 0; s < KST; ++s) {
+            const uint4 x = qf[s * 32 + lane];
+            qh[s][0] = x.x; qh[s][1] = x.y; qh[s][2] = x.z; qh[s][3] = x.w;
+        }
+        const float rf[2] = {rowf[g], rowf[g + 8]};
+
+        // ---- the piece's tiles, one warp after another
+        float o[NT][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+        float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        const int k_begin = max(gr.u0 + piece0 * UNIT, (tfrom / TK) * TK);
+        const int k_end = min(gr.u0 + piece1 * UNIT, tstop);
+        const int ntile = k_end > k_begin ? (k_end - k_begin + TK - 1) / TK : 0;
+        const int mine = ntile > warp ? (ntile - warp + NW - 1) / NW : 0;       // tiles warp, warp + NW, ...
+        const int32_t* table = a.table + static_cast<int64_t>(gr.r) * a.max_blocks;
+        const int64_t head_off = static_cast<int64_t>(gr.h) * c.page_size * D;
+
+        // Lane b of a batch holds the page and scales of sub-block b of the warp's next 32.
+        int b_page = -1;
+        float b_ks = 0.0f, b_vs = 0.0f;
+        auto fetch_batch = [&](int t0) {
+            const int tl = t0 + lane / NSUB;                                    // the warp's tile
+            const int j0 = k_begin + (warp + tl * NW) * TK + (lane % NSUB) * 16;
+            b_page = -1;
+            b_ks = b_vs = 0.0f;
+            if (tl < mine && j0 < k_end) {
+                const int page = table[j0 >> c.page_shift];
+                if (page >= 0 && page < c.num_pages) {
+                    b_page = page;
+                    b_ks = c.k_scale[page * c.scale_stride + gr.h];
+                    b_vs = c.v_scale[page * c.scale_stride + gr.h];
+                } else {
+                    atomicOr(a.status, CQ_DEV_KV_PAGE);
+                }
+            }
+        };
+        auto load_tile = [&](Tile<D>& b, int t) {
+            const int at = (t % (32 / NSUB)) * NSUB;
+#pragma unroll
+            for (int s = 0; s < NSUB; ++s) {
+                const int page = __shfl_sync(0xffffffffu, b_page, at + s);
+                b.ks[s] = __shfl_sync(0xffffffffu, b_ks, at + s);
+                b.vs[s] = __shfl_sync(0xffffffffu, b_vs, at + s);
+                const int j0 = k_begin + (warp + t * NW) * TK + s * 16;
+                b.row0[s] = page >= 0 ? j0 : -1;
+                if (page >= 0) {
+                    const int64_t base = page * c.page_stride + head_off + static_cast<int64_t>(j0 & (c.page_size - 1)) * D;
+                    const int8_t* kp = c.k + base + g * D + 16 * tq;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < D / 64; ++j) b.k[s][i][j] = ldg_stream16(kp + 8 * i * D + 64 * j);
+                    const int8_t* vp = c.v + base + 2 * tq * D + g * (D / 8);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int8_t* p = vp + ((i & 1) + 8 * (i >> 1)) * D;
+                        if constexpr (D == 128) {
+                            const uint4 x = ldg_stream16(p);
+                            b.v[s][i][0] = x.x; b.v[s][i][1] = x.y; b.v[s][i][2] = x.z; b.v[s][i][3] = x.w;
+                        } else {
+                            const uint2 x = ldg_stream8(p);
+                            b.v[s][i][0] = x.x; b.v[s][i][1] = x.y;
+                        }
+                    }
+                }
+            }
+        };
+        auto use_tile = [&](const Tile<D>& b) {
+#pragma unroll
+            for (int s = 0; s < NSUB; ++s) {
+                if (b.row0[s] < 0) continue;                                   // warp-uniform
+                const int j0 = b.row0[s];
+                float sc[2][4] = {};
+#pragma unroll
+                for (int ks = 0; ks < KST; ++ks) {
+                    uint32_t ql[4];
+                    if constexpr (F32) {
+                        const uint4 x = qf[(KST + ks) * 32 + lane];
+                        ql[0] = x.x; ql[1] = x.y; ql[2] = x.z; ql[3] = x.w;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4& kk = b.k[s][i][ks >> 2];
+                        const uint32_t w = (ks & 3) == 0 ? kk.x : (ks & 3) == 1 ? kk.y : (ks & 3) == 2 ? kk.z : kk.w;
+                        uint32_t b0, b1;
+                        tc::s8x4_half(w, b0, b1);
+                        mma16816(sc[i], qh[ks], b0, b1);
+                        if constexpr (F32) mma16816(sc[i], ql, b0, b1);
+                    }
+                }
+                // x_j, hidden keys at -inf
+                const bool whole = j0 >= all_from && j0 + 16 <= all_stop;
+                const float lv = b.vs[s] == 0.0f ? 0.0f : log2f(b.vs[s]), rv = b.vs[s] == 0.0f ? 1.0f : __frcp_rn(b.vs[s]);
+                const float f0 = b.ks[s] * rf[0], f1 = b.ks[s] * rf[1];
+                float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x = fmaf(sc[i][e], e < 2 ? f0 : f1, lv);
+                        if (!whole) {
+                            const int j = j0 + 8 * i + 2 * tq + (e & 1);
+                            if (j < rfrom[e >> 1] || j >= rstop[e >> 1]) x = -INFINITY;
+                        }
+                        sc[i][e] = x;
+                        top[e >> 1] = fmaxf(top[e >> 1], x);
+                    }
+                if (__any_sync(0xffffffffu, top[0] > M[0] + RAISE || top[1] > M[1] + RAISE)) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float m = top[e];
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                        const float old = M[e];
+                        if (m > old + RAISE) {                                  // the row's own, the same in its four lanes
+                            M[e] = m;
+                            const float f = exp2_approx(old - m);               // 0 from -inf
+                            l[e] *= f;
+#pragma unroll
+                            for (int i = 0; i < NT; ++i) { o[i][2 * e] *= f; o[i][2 * e + 1] *= f; }
+                        }
+                    }
+                }
+                const float base0 = M[0] == -INFINITY ? 0.0f : M[0] - OFF, base1 = M[1] == -INFINITY ? 0.0f : M[1] - OFF;
+                uint32_t ph[4], plo[4], ps[4], pt[4];
+                bool small = false;
+                float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float base = e ? base1 : base0;
+                        float p0 = exp2_approx(sc[i][2 * e] - base), p1 = exp2_approx(sc[i][2 * e + 1] - base);
+                        sum[e] += p0 + p1;                  // unrounded: lse is held to fp32
+                        if constexpr (F32) {
+                            sc[i][2 * e] = p0 < SMALL ? p0 : 0.0f;
+                            sc[i][2 * e + 1] = p1 < SMALL ? p1 : 0.0f;
+                            small |= sc[i][2 * e] > 0.0f || sc[i][2 * e + 1] > 0.0f;
+                            p0 -= sc[i][2 * e];
+                            p1 -= sc[i][2 * e + 1];
+                        }
+                        const __half2 hi = __floats2half2_rn(p0, p1);
+                        ph[2 * i + e] = *reinterpret_cast<const uint32_t*>(&hi);
+                        if constexpr (SPLIT_P) {
+                            const float2 hf = __half22float2(hi);
+                            const __half2 lo = __floats2half2_rn(p0 - hf.x, p1 - hf.y);
+                            plo[2 * i + e] = *reinterpret_cast<const uint32_t*>(&lo);
+                        }
+                    }
+                if constexpr (F32) {
+                    small = __any_sync(0xffffffffu, small);
+                    if (small) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float p0 = sc[i][2 * e], p1 = sc[i][2 * e + 1];
+                                const uint32_t hi = bf16_pair(p0, p1);
+                                ps[2 * i + e] = hi;
+                                pt[2 * i + e] = bf16_pair(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
+                            }
+                    }
+                }
+                // a row that sees nothing here must not meet a scale that is not finite
+                l[0] += sum[0] != 0.0f ? sum[0] * rv : 0.0f;
+                l[1] += sum[1] != 0.0f ? sum[1] * rv : 0.0f;
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) {
+                    // four dimensions of keys (2t, 2t+1) and (2t+8, 2t+9), as pairs of keys
+                    uint32_t b0[4], b1[4];
+                    tc::s8x4_half(__byte_perm(b.v[s][0][w], b.v[s][1][w], 0x5140), b0[0], b0[1]);
+                    tc::s8x4_half(__byte_perm(b.v[s][0][w], b.v[s][1][w], 0x7362), b0[2], b0[3]);
+                    tc::s8x4_half(__byte_perm(b.v[s][2][w], b.v[s][3][w], 0x5140), b1[0], b1[1]);
+                    tc::s8x4_half(__byte_perm(b.v[s][2][w], b.v[s][3][w], 0x7362), b1[2], b1[3]);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        mma16816(o[4 * w + x], ph, b0[x], b1[x]);
+                        if constexpr (SPLIT_P) mma16816(o[4 * w + x], plo, b0[x], b1[x]);
+                        if constexpr (F32) {
+                            if (small) {
+                                const uint32_t c0 = half_to_bf16(b0[x]), c1 = half_to_bf16(b1[x]);
+                                mma16816_bf16(o[4 * w + x], ps, c0, c1);
+                                mma16816_bf16(o[4 * w + x], pt, c0, c1);
+                            }
+                        }
+                    }
+                }
+            }
+        };
+        {
+            constexpr int BT = 32 / NSUB;                                       // tiles of a batch
+            Tile<D> buf[2];
+            if (mine > 0) {
+                fetch_batch(0);
+                load_tile(buf[0], 0);
+            }
+            for (int t = 0; t < mine; t += 2) {
+                if (t + 1 < mine) load_tile(buf[1], t + 1);                     // t + 1 is odd: same batch as t
+                use_tile(buf[0]);
+                if (t + 2 < mine) {
+                    if ((t + 2) % BT == 0) fetch_batch(t + 2);
+                    load_tile(buf[0], t + 2);
+                }
+                if (t + 1 < mine) use_tile(buf[1]);
+            }
+        }
+
+        // ---- the warps' parts of the piece
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+            const int row = g + 8 * e;
+            if (row < rows) {
+                if (tq == 0) { ml[(warp * 16 + row) * 2] = M[e]; ml[(warp * 16 + row) * 2 + 1] = l[e]; }
+                // this lane's columns: dimensions of group 2t (c0) and 2t + 1 (c1), D / 8 each, NT of them
+                float* dst = merge + (warp * 16 + row) * ROWF + 2 * tq * (D / 8);
+#pragma unroll
+                for (int i = 0; i < NT; i += 4) {
+                    *reinterpret_cast<float4*>(dst + i) = make_float4(o[i][2 * e], o[i + 1][2 * e], o[i + 2][2 * e], o[i + 3][2 * e]);
+                    *reinterpret_cast<float4*>(dst + D / 8 + i) =
+                        make_float4(o[i][2 * e + 1], o[i + 1][2 * e + 1], o[i + 2][2 * e + 1], o[i + 3][2 * e + 1]);
+                }
+            }
+        }
+        __syncthreads();
+        const int used = min(NW, max(ntile, 1));                               // warps that had a tile (warp 0 always counts)
+        const bool whole = piece0 == 0 && piece1 == gr.units;
+        float* part = pl.part + (me * 2 + (first_piece ? 0 : 1)) * (16 * ROWF);
+        first_piece = false;
+        for (int x = tid; x < rows * (D / 4); x += THREADS) {
+            const int row = x / (D / 4), col = (x % (D / 4)) * 4;
+            float m = -INFINITY;
+            for (int w = 0; w < used; ++w) m = fmaxf(m, ml[(w * 16 + row) * 2]);
+            const float base = m == -INFINITY ? 0.0f : m;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float lt = 0.0f;
+            for (int w = 0; w < used; ++w) {
+                const float f = exp2_approx(ml[(w * 16 + row) * 2] - base);
+                const float4 v = *reinterpret_cast<const float4*>(merge + (w * 16 + row) * ROWF + col);
+                lt = fmaf(ml[(w * 16 + row) * 2 + 1], f, lt);
+                acc.x = fmaf(v.x, f, acc.x);
+                acc.y = fmaf(v.y, f, acc.y);
+                acc.z = fmaf(v.z, f, acc.z);
+                acc.w = fmaf(v.w, f, acc.w);
+            }
+            if (whole) {
+                write_row<T, D>(a, gr.first, gr.h, G, 16 * gr.i + row, col, acc, m, lt, OFF);
+            } else {
+                *reinterpret_cast<float4*>(part + row * ROWF + col) = acc;
+                if (col == 0) { part[row * ROWF + D] = m; part[row * ROWF + D + 1] = lt; }
+            }
+        }
+        if (!whole) {
+            // ---- the group's pieces lie with CTAs c0..c1; the last of them to arrive joins them
+            const int64_t c0 = ((group_u + 1) * nact - 1) / U, c1 = ((group_u + gr.units) * nact - 1) / U;
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const int before = atomicAdd(pl.count + c0, 1);
+                last_flag = before == static_cast<int>(c1 - c0);
+                if (last_flag) pl.count[c0] = 0;                               // as the next call wants it
+            }
+            __syncthreads();
+            if (last_flag) {
+                __threadfence();
+                for (int x = tid; x < rows * (D / 4); x += THREADS) {
+                    const int row = x / (D / 4), col = (x % (D / 4)) * 4;
+                    float m = -INFINITY;
+                    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    float lt = 0.0f;
+                    for (int64_t cc = c0; cc <= c1; ++cc) {
+                        // a CTA's second slot holds its last piece unless that is its first too
+                        const int64_t cta_u = cc * U / nact;
+                        const float* src = pl.part + (cc * 2 + (cta_u < group_u ? 1 : 0)) * (16 * ROWF) + row * ROWF;
+                        const float mc = __ldcg(src + D), lc = __ldcg(src + D + 1);
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(src + col));
+                        const float m2 = fmaxf(m, mc), base = m2 == -INFINITY ? 0.0f : m2;
+                        const float f = exp2_approx(m - base), fc = exp2_approx(mc - base);
+                        lt = lt * f + lc * fc;
+                        acc.x = acc.x * f + v.x * fc;
+                        acc.y = acc.y * f + v.y * fc;
+                        acc.z = acc.z * f + v.z * fc;
+                        acc.w = acc.w * f + v.w * fc;
+                        m = m2;
+                    }
+                    write_row<T, D>(a, gr.first, gr.h, G, 16 * gr.i + row, col, acc, m, lt, OFF);
+                }
+            }
+        }
+        u = group_u + piece1;
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_rows_t(const DeviceInfo& dev, const KvView& c, const AttnArgs& a, const RowsPlan& pl, cudaStream_t s) {
+    constexpr bool F32 = std::is_same<T, float>::value;
+    const int smem = (((a.R + 1) * 8 + 15) & ~15) + (F32 ? 2 : 1) * (D / 16) * 32 * 16 + 16 * 4 + NW * 16 * (D + 4) * 4 +
+                     NW * 16 * 2 * 4;
+    if (smem > dev.smem_optin) return cudaErrorInvalidConfiguration;
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_rows_kernel<T, D>), smem);
+    if (e != cudaSuccess) return e;
+    const int ctas = std::min(dev.sm_count, ATTN_MAX_CTAS);
+    return launch_kernel(attn_rows_kernel<T, D>, dim3(static_cast<unsigned>(ctas)), dim3(THREADS), static_cast<size_t>(smem), s, c, a, pl);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_rows(const DeviceInfo& dev, const KvView& c, int dtype, const AttnArgs& a, const RowsPlan& pl,
+                             cudaStream_t s) {
+    const bool d64 = c.dim == 64;
+    switch (dtype) {
+    case CQ_F32: return d64 ? launch_rows_t<float, 64>(dev, c, a, pl, s) : launch_rows_t<float, 128>(dev, c, a, pl, s);
+    case CQ_F16: return d64 ? launch_rows_t<__half, 64>(dev, c, a, pl, s) : launch_rows_t<__half, 128>(dev, c, a, pl, s);
+    case CQ_BF16:
+        return d64 ? launch_rows_t<__nv_bfloat16, 64>(dev, c, a, pl, s) : launch_rows_t<__nv_bfloat16, 128>(dev, c, a, pl, s);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace cq
