@@ -35,10 +35,13 @@
 namespace cq {
 namespace {
 
-constexpr int NW = 8;                     // warps a CTA
+constexpr int NW = 4;                     // warps a CTA
+constexpr int CTAS = 3;                   // CTAs an SM: one's merge hides behind the others' loads
 constexpr int THREADS = NW * 32;
 constexpr int UNIT = 64;                  // keys of a work unit
 constexpr int MIN_UNITS = 2;              // a CTA is worth at least so many
+constexpr int AHEAD = 4;                  // tiles that a warp has on their way into L2
+constexpr int KNOWN = THREADS;            // requests whose lengths stay in shared memory
 constexpr float OFF = 7.0f, RAISE = 8.0f;
 // fp32: probabilities below this leave binary16's range before they have given
 // 22 bits. They enter as two bfloat16 parts instead, in the tiles that have any
@@ -96,22 +99,13 @@ __device__ __forceinline__ int request_units(const AttnArgs& a, int n, int kv) {
     return max(u, 1);
 }
 
-// Register buffers of one tile: NSUB sub-blocks of 16 keys.
-template <int D> struct Tile {
-    static constexpr int NSUB = 128 / D;
-    uint4 k[NSUB][2][D / 64];     // [sub-block][8 keys][64 dimensions]
-    uint32_t v[NSUB][4][D / 32];  // [sub-block][its keys 2t, 2t+1, 2t+8, 2t+9][words]
-    float ks[NSUB], vs[NSUB];
-    int row0[NSUB];               // first key; < 0: nothing of the sub-block counts
-};
-
 template <typename T, int D>
-__global__ void __launch_bounds__(THREADS, 1) attn_rows_kernel(const KvView c, const AttnArgs a, const RowsPlan pl) {
+__global__ void __launch_bounds__(THREADS, CTAS) attn_rows_kernel(const KvView c, const AttnArgs a, const RowsPlan pl) {
     pdl_trigger();
     pdl_wait();
     constexpr bool F32 = std::is_same<T, float>::value;
     constexpr bool SPLIT_P = !std::is_same<T, __nv_bfloat16>::value;
-    constexpr int NSUB = Tile<D>::NSUB, KST = D / 16, NT = D / 8;
+    constexpr int NSUB = 128 / D, KST = D / 16, NT = D / 8;     // a tile: NSUB blocks of 16 keys, 2 KB of keys
     constexpr int TK = 16 * NSUB;                     // keys of a tile
     constexpr int ROWF = D + 4;                       // floats of a merge row
     extern __shared__ __align__(16) uint8_t rows_smem[];
@@ -123,6 +117,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_rows_kernel(const KvView c, c
     float* ml = merge + NW * 16 * ROWF;                                       // [NW][16][2]
     __shared__ int64_t wsum[NW];
     __shared__ int last_flag;
+    __shared__ int known[KNOWN][3];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
     const int G = a.heads / c.heads;
 
@@ -134,6 +129,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_rows_kernel(const KvView c, c
         if (r < a.R) {
             int first, n, kv;
             request_of(c, a, r, first, n, kv);
+            if (r < KNOWN) { known[r][0] = first; known[r][1] = n; known[r][2] = kv; }
             if (rows_take(pl, n, G)) x = static_cast<int64_t>(request_units(a, n, kv)) * c.heads * ((static_cast<int64_t>(n) * G + 15) / 16);
         }
         int64_t s = x;
@@ -177,7 +173,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_rows_kernel(const KvView c, c
             }
             gr.r = lo;
         }
-        request_of(c, a, gr.r, gr.first, gr.n, gr.kv);
+        if (gr.r < KNOWN) { gr.first = known[gr.r][0]; gr.n = known[gr.r][1]; gr.kv = known[gr.r][2]; }
+        else request_of(c, a, gr.r, gr.first, gr.n, gr.kv);
         int from, stop;
         request_range(a, gr.n, gr.kv, from, stop);
         gr.u0 = (from / UNIT) * UNIT;
@@ -246,12 +243,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_rows_kernel(const KvView c, c
             }
         }
         __syncthreads();
-        uint32_t qh[KST][4];
-#pragma unroll
-        for (int s = 0; s < KST; ++s) {
-            const uint4 x = qf[s * 32 + lane];
-            qh[s][0] = x.x; qh[s][1] = x.y; qh[s][2] = x.z; qh[s][3] = x.w;
-        }
         const float rf[2] = {rowf[g], rowf[g + 8]};
 
         // ---- the piece's tiles, one warp after another
@@ -267,93 +258,146 @@ __global__ void __launch_bounds__(THREADS, 1) attn_rows_kernel(const KvView c, c
         const int64_t head_off = static_cast<int64_t>(gr.h) * c.page_size * D;
 
         // Lane b of a batch holds the page and scales of sub-block b of the warp's next 32.
-        int b_page = -1;
-        float b_ks = 0.0f, b_vs = 0.0f;
+        constexpr int BT = 32 / NSUB;                                           // tiles of a batch
+        // Lane b's page and scales of the batch after it (n_) are on their way meanwhile.
+        int n_page = -1;
+        float n_ks = 0.0f, n_vs = 0.0f;
+        int64_t b_at = -1;                                                      // offset of the sub-block's keys (and values)
+        float b_ks = 0.0f, b_lv = 0.0f, b_rv = 0.0f;
+        auto place = [&](int tl) { return k_begin + (warp + tl * NW) * TK + (lane % NSUB) * 16; };
         auto fetch_batch = [&](int t0) {
-            const int tl = t0 + lane / NSUB;                                    // the warp's tile
-            const int j0 = k_begin + (warp + tl * NW) * TK + (lane % NSUB) * 16;
-            b_page = -1;
-            b_ks = b_vs = 0.0f;
+            const int tl = t0 + lane / NSUB, j0 = place(tl);                    // the warp's tile, its first key
+            n_page = -1;
             if (tl < mine && j0 < k_end) {
                 const int page = table[j0 >> c.page_shift];
                 if (page >= 0 && page < c.num_pages) {
-                    b_page = page;
-                    b_ks = c.k_scale[page * c.scale_stride + gr.h];
-                    b_vs = c.v_scale[page * c.scale_stride + gr.h];
+                    n_page = page;
+                    n_ks = c.k_scale[page * c.scale_stride + gr.h];
+                    n_vs = c.v_scale[page * c.scale_stride + gr.h];
                 } else {
                     atomicOr(a.status, CQ_DEV_KV_PAGE);
                 }
             }
         };
-        auto load_tile = [&](Tile<D>& b, int t) {
-            const int at = (t % (32 / NSUB)) * NSUB;
+        auto offset_of = [&](int page, int j0) {
+            return page * c.page_stride + head_off + static_cast<int64_t>(j0 & (c.page_size - 1)) * D;
+        };
+        auto next_batch = [&](int t0) {
+            b_at = n_page >= 0 ? offset_of(n_page, place(t0 + lane / NSUB)) : -1;
+            b_ks = n_ks;
+            b_lv = n_vs == 0.0f ? 0.0f : log2f(n_vs);
+            b_rv = n_vs == 0.0f ? 1.0f : __frcp_rn(n_vs);
+        };
+        // Tile t begins its way into L2: the lanes that hold it in its batch.
+        auto prefetch = [&](int t, bool next) {
+            if (lane / NSUB != t % BT) return;
+            const int64_t at = !next ? b_at : n_page >= 0 ? offset_of(n_page, place(t)) : -1;
+            if (at >= 0) { bulk_prefetch_l2(c.k + at, 16 * D); bulk_prefetch_l2(c.v + at, 16 * D); }
+        };
+        uint4 kr[NSUB][2][D / 64];          // [sub-block][8 keys][64 dimensions]
+        uint32_t vr[NSUB][4][D / 32];       // [sub-block][its keys 2t, 2t+1, 2t+8, 2t+9][words]
+        auto load_k = [&](int t) {
+            const int at = (t % BT) * NSUB;
 #pragma unroll
             for (int s = 0; s < NSUB; ++s) {
-                const int page = __shfl_sync(0xffffffffu, b_page, at + s);
-                b.ks[s] = __shfl_sync(0xffffffffu, b_ks, at + s);
-                b.vs[s] = __shfl_sync(0xffffffffu, b_vs, at + s);
-                const int j0 = k_begin + (warp + t * NW) * TK + s * 16;
-                b.row0[s] = page >= 0 ? j0 : -1;
-                if (page >= 0) {
-                    const int64_t base = page * c.page_stride + head_off + static_cast<int64_t>(j0 & (c.page_size - 1)) * D;
-                    const int8_t* kp = c.k + base + g * D + 16 * tq;
+                const int64_t off = __shfl_sync(0xffffffffu, b_at, at + s);
+                if (off < 0) continue;
+                const int8_t* p = c.k + off + g * D + 16 * tq;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int j = 0; j < D / 64; ++j) b.k[s][i][j] = ldg_stream16(kp + 8 * i * D + 64 * j);
-                    const int8_t* vp = c.v + base + 2 * tq * D + g * (D / 8);
+                    for (int j = 0; j < D / 64; ++j) kr[s][i][j] = ldg_stream16(p + 8 * i * D + 64 * j);
+            }
+        };
+        auto load_v = [&](int t) {
+            const int at = (t % BT) * NSUB;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int8_t* p = vp + ((i & 1) + 8 * (i >> 1)) * D;
-                        if constexpr (D == 128) {
-                            const uint4 x = ldg_stream16(p);
-                            b.v[s][i][0] = x.x; b.v[s][i][1] = x.y; b.v[s][i][2] = x.z; b.v[s][i][3] = x.w;
-                        } else {
-                            const uint2 x = ldg_stream8(p);
-                            b.v[s][i][0] = x.x; b.v[s][i][1] = x.y;
-                        }
+            for (int s = 0; s < NSUB; ++s) {
+                const int64_t off = __shfl_sync(0xffffffffu, b_at, at + s);
+                if (off < 0) continue;
+                const int8_t* p = c.v + off + 2 * tq * D + g * (D / 8);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int8_t* q = p + ((i & 1) + 8 * (i >> 1)) * D;
+                    if constexpr (D == 128) {
+                        const uint4 x = ldg_stream16(q);
+                        vr[s][i][0] = x.x; vr[s][i][1] = x.y; vr[s][i][2] = x.z; vr[s][i][3] = x.w;
+                    } else {
+                        const uint2 x = ldg_stream8(q);
+                        vr[s][i][0] = x.x; vr[s][i][1] = x.y;
                     }
                 }
             }
         };
-        auto use_tile = [&](const Tile<D>& b) {
+        if (mine > 0) {
+            fetch_batch(0);
+            next_batch(0);
+            load_k(0);
+            load_v(0);
+            for (int t = 1; t < AHEAD; ++t) prefetch(t, false);
+        }
+        for (int t = 0; t < mine; ++t) {
+            // what belongs to this tile, before the batch moves on
+            bool on[NSUB];
+            float ks_[NSUB], lv_[NSUB], rv_[NSUB];
 #pragma unroll
             for (int s = 0; s < NSUB; ++s) {
-                if (b.row0[s] < 0) continue;                                   // warp-uniform
-                const int j0 = b.row0[s];
-                float sc[2][4] = {};
+                const int at = (t % BT) * NSUB + s;
+                on[s] = __shfl_sync(0xffffffffu, b_at, at) >= 0;
+                ks_[s] = __shfl_sync(0xffffffffu, b_ks, at);
+                lv_[s] = __shfl_sync(0xffffffffu, b_lv, at);
+                rv_[s] = __shfl_sync(0xffffffffu, b_rv, at);
+            }
+            if (t % BT == BT / 2) fetch_batch(t - BT / 2 + BT);
+            prefetch(t + AHEAD, t % BT + AHEAD >= BT);
+            float sc[NSUB][2][4] = {};
 #pragma unroll
-                for (int ks = 0; ks < KST; ++ks) {
-                    uint32_t ql[4];
-                    if constexpr (F32) {
-                        const uint4 x = qf[(KST + ks) * 32 + lane];
-                        ql[0] = x.x; ql[1] = x.y; ql[2] = x.z; ql[3] = x.w;
-                    }
+            for (int ks = 0; ks < KST; ++ks) {
+                uint32_t qh[4], ql[4];
+                {
+                    const uint4 x = qf[ks * 32 + lane];
+                    qh[0] = x.x; qh[1] = x.y; qh[2] = x.z; qh[3] = x.w;
+                }
+                if constexpr (F32) {
+                    const uint4 x = qf[(KST + ks) * 32 + lane];
+                    ql[0] = x.x; ql[1] = x.y; ql[2] = x.z; ql[3] = x.w;
+                }
+#pragma unroll
+                for (int s = 0; s < NSUB; ++s)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint4& kk = b.k[s][i][ks >> 2];
+                        const uint4& kk = kr[s][i][ks >> 2];
                         const uint32_t w = (ks & 3) == 0 ? kk.x : (ks & 3) == 1 ? kk.y : (ks & 3) == 2 ? kk.z : kk.w;
                         uint32_t b0, b1;
                         tc::s8x4_half(w, b0, b1);
-                        mma16816(sc[i], qh[ks], b0, b1);
-                        if constexpr (F32) mma16816(sc[i], ql, b0, b1);
+                        mma16816(sc[s][i], qh, b0, b1);
+                        if constexpr (F32) mma16816(sc[s][i], ql, b0, b1);
                     }
-                }
+            }
+            // the next tile's keys come in behind the softmax and the second product, its values behind the next scores
+            const bool more = t + 1 < mine;
+            if (more) {
+                if ((t + 1) % BT == 0) next_batch(t + 1);
+                load_k(t + 1);
+            }
+            #pragma unroll
+            for (int s = 0; s < NSUB; ++s) {
+                if (!on[s]) continue;                                           // warp-uniform
+                const int j0 = k_begin + (warp + t * NW) * TK + s * 16;
                 // x_j, hidden keys at -inf
                 const bool whole = j0 >= all_from && j0 + 16 <= all_stop;
-                const float lv = b.vs[s] == 0.0f ? 0.0f : log2f(b.vs[s]), rv = b.vs[s] == 0.0f ? 1.0f : __frcp_rn(b.vs[s]);
-                const float f0 = b.ks[s] * rf[0], f1 = b.ks[s] * rf[1];
+                const float f0 = ks_[s] * rf[0], f1 = ks_[s] * rf[1];
                 float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float x = fmaf(sc[i][e], e < 2 ? f0 : f1, lv);
+                        float x = fmaf(sc[s][i][e], e < 2 ? f0 : f1, lv_[s]);
                         if (!whole) {
                             const int j = j0 + 8 * i + 2 * tq + (e & 1);
                             if (j < rfrom[e >> 1] || j >= rstop[e >> 1]) x = -INFINITY;
                         }
-                        sc[i][e] = x;
+                        sc[s][i][e] = x;
                         top[e >> 1] = fmaxf(top[e >> 1], x);
                     }
                 if (__any_sync(0xffffffffu, top[0] > M[0] + RAISE || top[1] > M[1] + RAISE)) {
@@ -381,14 +425,16 @@ __global__ void __launch_bounds__(THREADS, 1) attn_rows_kernel(const KvView c, c
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float base = e ? base1 : base0;
-                        float p0 = exp2_approx(sc[i][2 * e] - base), p1 = exp2_approx(sc[i][2 * e + 1] - base);
+                        float p0 = exp2_approx(sc[s][i][2 * e] - base), p1 = exp2_approx(sc[s][i][2 * e + 1] - base);
                         sum[e] += p0 + p1;                  // unrounded: lse is held to fp32
                         if constexpr (F32) {
-                            sc[i][2 * e] = p0 < SMALL ? p0 : 0.0f;
-                            sc[i][2 * e + 1] = p1 < SMALL ? p1 : 0.0f;
-                            small |= sc[i][2 * e] > 0.0f || sc[i][2 * e + 1] > 0.0f;
-                            p0 -= sc[i][2 * e];
-                            p1 -= sc[i][2 * e + 1];
+                            const float s0 = p0 < SMALL ? p0 : 0.0f, s1 = p1 < SMALL ? p1 : 0.0f;
+                            small |= s0 > 0.0f || s1 > 0.0f;
+                            p0 -= s0;
+                            p1 -= s1;
+                            const uint32_t hi = bf16_pair(s0, s1);
+                            ps[2 * i + e] = hi;
+                            pt[2 * i + e] = bf16_pair(s0 - __uint_as_float(hi << 16), s1 - __uint_as_float(hi & 0xffff0000u));
                         }
                         const __half2 hi = __floats2half2_rn(p0, p1);
                         ph[2 * i + e] = *reinterpret_cast<const uint32_t*>(&hi);
@@ -398,31 +444,19 @@ __global__ void __launch_bounds__(THREADS, 1) attn_rows_kernel(const KvView c, c
                             plo[2 * i + e] = *reinterpret_cast<const uint32_t*>(&lo);
                         }
                     }
-                if constexpr (F32) {
-                    small = __any_sync(0xffffffffu, small);
-                    if (small) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float p0 = sc[i][2 * e], p1 = sc[i][2 * e + 1];
-                                const uint32_t hi = bf16_pair(p0, p1);
-                                ps[2 * i + e] = hi;
-                                pt[2 * i + e] = bf16_pair(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
-                            }
-                    }
-                }
+                if constexpr (F32) small = __any_sync(0xffffffffu, small);
                 // a row that sees nothing here must not meet a scale that is not finite
-                l[0] += sum[0] != 0.0f ? sum[0] * rv : 0.0f;
-                l[1] += sum[1] != 0.0f ? sum[1] * rv : 0.0f;
+                l[0] += sum[0] != 0.0f ? sum[0] * rv_[s] : 0.0f;
+                l[1] += sum[1] != 0.0f ? sum[1] * rv_[s] : 0.0f;
+                // The second product follows at once: a later sub-block may raise M.
 #pragma unroll
                 for (int w = 0; w < D / 32; ++w) {
                     // four dimensions of keys (2t, 2t+1) and (2t+8, 2t+9), as pairs of keys
                     uint32_t b0[4], b1[4];
-                    tc::s8x4_half(__byte_perm(b.v[s][0][w], b.v[s][1][w], 0x5140), b0[0], b0[1]);
-                    tc::s8x4_half(__byte_perm(b.v[s][0][w], b.v[s][1][w], 0x7362), b0[2], b0[3]);
-                    tc::s8x4_half(__byte_perm(b.v[s][2][w], b.v[s][3][w], 0x5140), b1[0], b1[1]);
-                    tc::s8x4_half(__byte_perm(b.v[s][2][w], b.v[s][3][w], 0x7362), b1[2], b1[3]);
+                    tc::s8x4_half(__byte_perm(vr[s][0][w], vr[s][1][w], 0x5140), b0[0], b0[1]);
+                    tc::s8x4_half(__byte_perm(vr[s][0][w], vr[s][1][w], 0x7362), b0[2], b0[3]);
+                    tc::s8x4_half(__byte_perm(vr[s][2][w], vr[s][3][w], 0x5140), b1[0], b1[1]);
+                    tc::s8x4_half(__byte_perm(vr[s][2][w], vr[s][3][w], 0x7362), b1[2], b1[3]);
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         mma16816(o[4 * w + x], ph, b0[x], b1[x]);
@@ -437,23 +471,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_rows_kernel(const KvView c, c
                     }
                 }
             }
-        };
-        {
-            constexpr int BT = 32 / NSUB;                                       // tiles of a batch
-            Tile<D> buf[2];
-            if (mine > 0) {
-                fetch_batch(0);
-                load_tile(buf[0], 0);
-            }
-            for (int t = 0; t < mine; t += 2) {
-                if (t + 1 < mine) load_tile(buf[1], t + 1);                     // t + 1 is odd: same batch as t
-                use_tile(buf[0]);
-                if (t + 2 < mine) {
-                    if ((t + 2) % BT == 0) fetch_batch(t + 2);
-                    load_tile(buf[0], t + 2);
-                }
-                if (t + 1 < mine) use_tile(buf[1]);
-            }
+            if (more) load_v(t + 1);
         }
 
         // ---- the warps' parts of the piece
@@ -551,7 +569,7 @@ cudaError_t launch_rows_t(const DeviceInfo& dev, const KvView& c, const AttnArgs
     if (smem > dev.smem_optin) return cudaErrorInvalidConfiguration;
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_rows_kernel<T, D>), smem);
     if (e != cudaSuccess) return e;
-    const int ctas = std::min(dev.sm_count, ATTN_MAX_CTAS);
+    const int ctas = std::min(dev.sm_count * CTAS, ATTN_MAX_CTAS);
     return launch_kernel(attn_rows_kernel<T, D>, dim3(static_cast<unsigned>(ctas)), dim3(THREADS), static_cast<size_t>(smem), s, c, a, pl);
 }
 
