@@ -11,7 +11,7 @@ namespace cq {
 
 // CTAs that share the partial results of a call: the workspace has two slots
 // and a counter for each.
-constexpr int ATTN_MAX_CTAS = 512;
+constexpr int ATTN_MAX_CTAS = 640;
 
 struct RowsPlan {
     int* count;          // [ATTN_MAX_CTAS], zero between calls

@@ -10,15 +10,16 @@
 // only when a score passes it by 8: P_j then stays below 2^15, and a value
 // that is small against the largest keeps its 11 bits down to 2^-21 of it.
 //
-// Both products are mma.sync m16n8k16: 16 query rows (token, head of the kv
-// head's group) against 8 keys, and against 8 head dimensions. The cache is
-// read once, straight from global memory into the B fragments' registers: a
-// key row's 16-byte piece holds four k-steps of its lane, a value row's piece
-// one dimension of each of 16 (8 for D = 64) column tiles, so no shared memory
-// or shuffle stands between the load and the product. fp32 queries and
+// Both products are mma.sync m16n8k16 with the cache as the A operand: 16 keys
+// against 8 query rows (token, head of the kv head's group), and 16 head
+// dimensions against the 8 rows, so one decoded token of up to eight heads wastes
+// no row. The cache is read once, straight from global memory into the A
+// fragments' registers: a key row's 16-byte piece holds four k-steps of its lane,
+// a value row's piece its lane's dimensions of all row tiles. Only the
+// probabilities change lanes (one 8 x 8 transpose for 8 keys). fp32 queries and
 // probabilities enter as two binary16 parts (22 bits).
 //
-// Work: every (request, kv head, row tile) is a group of units of 64 keys; the
+// Work: every (request, kv head, tile of 8 or 16 rows) is a group of units of 64 keys; the
 // units of all groups, in order, are split evenly over the CTAs, whatever the
 // lengths. A CTA's warps take its piece's tiles in turn and merge in shared
 // memory; pieces of a group that several CTAs share go to the workspace, and the
@@ -36,7 +37,6 @@ namespace cq {
 namespace {
 
 constexpr int NW = 4;                     // warps a CTA
-constexpr int CTAS = 3;                   // CTAs an SM: one's merge hides behind the others' loads
 constexpr int THREADS = NW * 32;
 constexpr int UNIT = 64;                  // keys of a work unit
 constexpr int MIN_UNITS = 2;              // a CTA is worth at least so many
@@ -99,22 +99,40 @@ __device__ __forceinline__ int request_units(const AttnArgs& a, int n, int kv) {
     return max(u, 1);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(THREADS, CTAS) attn_rows_kernel(const KvView c, const AttnArgs a, const RowsPlan pl) {
+// Transposes an 8 x 8 matrix of 16-bit values held as fragments (lane: row
+// lane / 4, columns 2 (lane % 4), 2 (lane % 4) + 1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <typename T, int D, int NB> struct Rows {
+    static constexpr bool F32 = std::is_same<T, float>::value;
+    static constexpr int RT = 8 * NB;                       // rows of a tile
+    static constexpr int CTAS = NB == 1 && !F32 ? 4 : 3;    // an SM's CTAs (registers): one's merge hides behind the others' loads
+    static constexpr int ROWF = D + 4;                      // floats of a merge row
+    static constexpr int QF = (F32 ? 2 : 1) * NB * (D / 16) * 32;   // query fragments, 8 bytes each
+    static int smem(int R) { return (((R + 1) * 8 + 15) & ~15) + QF * 8 + RT * 4 + NW * RT * (ROWF + 2) * 4; }
+};
+
+template <typename T, int D, int NB>
+__global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kernel(const KvView c, const AttnArgs a, const RowsPlan pl) {
     pdl_trigger();
     pdl_wait();
-    constexpr bool F32 = std::is_same<T, float>::value;
+    using W = Rows<T, D, NB>;
+    constexpr bool F32 = W::F32;
     constexpr bool SPLIT_P = !std::is_same<T, __nv_bfloat16>::value;
-    constexpr int NSUB = 128 / D, KST = D / 16, NT = D / 8;     // a tile: NSUB blocks of 16 keys, 2 KB of keys
-    constexpr int TK = 16 * NSUB;                     // keys of a tile
-    constexpr int ROWF = D + 4;                       // floats of a merge row
+    constexpr int RT = W::RT, ROWF = W::ROWF;
+    constexpr int NSUB = 128 / D, KST = D / 16, MT = D / 16;      // a tile: NSUB blocks of 16 keys, 2 KB of keys
+    constexpr int TK = 16 * NSUB;                                 // keys of a tile
+    constexpr int BT = 32 / NSUB;                                 // tiles of a batch of page ids
     extern __shared__ __align__(16) uint8_t rows_smem[];
     int64_t* cum = reinterpret_cast<int64_t*>(rows_smem);                     // [R + 1] first unit of each request
-    const int cum_bytes = ((a.R + 1) * 8 + 15) & ~15;
-    uint4* qf = reinterpret_cast<uint4*>(rows_smem + cum_bytes);              // [1 or 2][KST][32] A fragments
-    float* rowf = reinterpret_cast<float*>(qf + (F32 ? 2 : 1) * KST * 32);    // [16] factor of each row's scores
-    float* merge = rowf + 16;                                                 // [NW][16][ROWF]
-    float* ml = merge + NW * 16 * ROWF;                                       // [NW][16][2]
+    uint2* qf = reinterpret_cast<uint2*>(rows_smem + (((a.R + 1) * 8 + 15) & ~15));   // [1 or 2][KST][NB][32] B fragments
+    float* merge = reinterpret_cast<float*>(qf + W::QF);                      // [NW][RT][ROWF]
+    float* ml = merge + NW * RT * ROWF;                                       // [NW][RT][2]
+    float* rowf = ml + NW * RT * 2;                                           // [RT] factor of each row's scores
     __shared__ int64_t wsum[NW];
     __shared__ int last_flag;
     __shared__ int known[KNOWN][3];
@@ -130,7 +148,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) attn_rows_kernel(const KvView c
             int first, n, kv;
             request_of(c, a, r, first, n, kv);
             if (r < KNOWN) { known[r][0] = first; known[r][1] = n; known[r][2] = kv; }
-            if (rows_take(pl, n, G)) x = static_cast<int64_t>(request_units(a, n, kv)) * c.heads * ((static_cast<int64_t>(n) * G + 15) / 16);
+            if (rows_take(pl, n, G)) x = static_cast<int64_t>(request_units(a, n, kv)) * c.heads * ((static_cast<int64_t>(n) * G + RT - 1) / RT);
         }
         int64_t s = x;
 #pragma unroll
@@ -181,75 +199,19 @@ __global__ void __launch_bounds__(THREADS, CTAS) attn_rows_kernel(const KvView c
         gr.units = request_units(a, gr.n, gr.kv);
         const int64_t in = u - cum[gr.r], gi = in / gr.units;
         const int piece0 = static_cast<int>(in - gi * gr.units);
-        const int nrt = (gr.n * G + 15) / 16;
+        const int nrt = (gr.n * G + RT - 1) / RT;
         gr.h = static_cast<int>(gi / nrt);
         gr.i = static_cast<int>(gi - static_cast<int64_t>(gr.h) * nrt);
         const int64_t group_u = u - piece0;                       // the group's first unit
         const int piece1 = static_cast<int>(min(static_cast<int64_t>(gr.units), u_end - group_u));
-        const int rows = min(16, gr.n * G - 16 * gr.i);           // of this tile
-        // what this lane's two rows see, and what the tile's rows see together
-        int rfrom[2], rstop[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int rho = 16 * gr.i + g + 8 * e;
-            row_range(a, gr.n, gr.kv, rho / G, rfrom[e], rstop[e]);
-            if (g + 8 * e >= rows) rfrom[e] = rstop[e] = 0;
-        }
+        const int rows = min(RT, gr.n * G - RT * gr.i);           // of this tile
         int tfrom, tstop, x0, x1;
-        row_range(a, gr.n, gr.kv, (16 * gr.i) / G, tfrom, x0);
-        row_range(a, gr.n, gr.kv, (16 * gr.i + rows - 1) / G, x1, tstop);
+        row_range(a, gr.n, gr.kv, (RT * gr.i) / G, tfrom, x0);
+        row_range(a, gr.n, gr.kv, (RT * gr.i + rows - 1) / G, x1, tstop);
         // keys that every row sees: from the last row's first to the first row's last
         const int all_from = x1, all_stop = x0;
 
-        // ---- query fragments: k-step (j, s) of lane (g, t) holds dimensions 64j + 16t + 4s + 0..3
-        __syncthreads();                                          // the previous piece's readers are done
-        for (int row = warp; row < 16; row += NW) {
-            constexpr int PER = D / 32;                           // consecutive dimensions of a lane
-            float q[PER];
-            const int rho = 16 * gr.i + row;
-            const int64_t tok = gr.first + rho / G;
-            const int head = gr.h * G + rho % G;
-            const bool on = row < rows;
-#pragma unroll
-            for (int i = 0; i < PER; i += 2) {
-                float2 v = make_float2(0.0f, 0.0f);
-                if (on) v = load2(static_cast<const T*>(a.q) + tok * a.q_stride + head * D + lane * PER + i);
-                q[i] = v.x;
-                q[i + 1] = v.y;
-            }
-            // A power of two brings the row's largest value to [2^8, 2^9): exact, and
-            // nothing that matters is below binary16's range. NaN for a row that is not finite.
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) top = max(top, __float_as_uint(fabsf(q[i])));
-            top = __reduce_max_sync(0xffffffffu, top);
-            float mul, back;
-            row_scale(top, mul, back);
-            if (a.scale < 0.0f) mul = -mul;
-            if (lane == 0) rowf[row] = back * lscale;
-#pragma unroll
-            for (int i = 0; i < PER; i += 2) {
-                const int d = lane * PER + i;
-                const int j = d >> 6, t = (d >> 4) & 3, s = (d >> 2) & 3, half = (d >> 1) & 1;
-                const float v0 = q[i] * mul, v1 = q[i + 1] * mul;
-                const __half2 hi = __floats2half2_rn(v0, v1);
-                uint32_t* dst = reinterpret_cast<uint32_t*>(qf + (4 * j + s) * 32 + 4 * (row & 7) + t) + (row >> 3) + 2 * half;
-                *dst = *reinterpret_cast<const uint32_t*>(&hi);
-                if constexpr (F32) {
-                    const float2 back2 = __half22float2(hi);
-                    const __half2 lo = __floats2half2_rn(v0 - back2.x, v1 - back2.y);
-                    dst[KST * 32 * 4] = *reinterpret_cast<const uint32_t*>(&lo);
-                }
-            }
-        }
-        __syncthreads();
-        const float rf[2] = {rowf[g], rowf[g + 8]};
-
         // ---- the piece's tiles, one warp after another
-        float o[NT][4];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-        float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
         const int k_begin = max(gr.u0 + piece0 * UNIT, (tfrom / TK) * TK);
         const int k_end = min(gr.u0 + piece1 * UNIT, tstop);
         const int ntile = k_end > k_begin ? (k_end - k_begin + TK - 1) / TK : 0;
@@ -257,9 +219,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) attn_rows_kernel(const KvView c
         const int32_t* table = a.table + static_cast<int64_t>(gr.r) * a.max_blocks;
         const int64_t head_off = static_cast<int64_t>(gr.h) * c.page_size * D;
 
-        // Lane b of a batch holds the page and scales of sub-block b of the warp's next 32.
-        constexpr int BT = 32 / NSUB;                                           // tiles of a batch
-        // Lane b's page and scales of the batch after it (n_) are on their way meanwhile.
+        // Lane b of a batch holds the place and scales of sub-block b of the warp's
+        // next 32; its page and scales of the batch after it (n_) are on their way meanwhile.
         int n_page = -1;
         float n_ks = 0.0f, n_vs = 0.0f;
         int64_t b_at = -1;                                                      // offset of the sub-block's keys (and values)
@@ -282,8 +243,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) attn_rows_kernel(const KvView c
         auto offset_of = [&](int page, int j0) {
             return page * c.page_stride + head_off + static_cast<int64_t>(j0 & (c.page_size - 1)) * D;
         };
-        auto next_batch = [&](int t0) {
-            b_at = n_page >= 0 ? offset_of(n_page, place(t0 + lane / NSUB)) : -1;
+        auto next_place = [&](int t0) { b_at = n_page >= 0 ? offset_of(n_page, place(t0 + lane / NSUB)) : -1; };
+        auto next_scales = [&]() {
             b_ks = n_ks;
             b_lv = n_vs == 0.0f ? 0.0f : log2f(n_vs);
             b_rv = n_vs == 0.0f ? 1.0f : __frcp_rn(n_vs);
@@ -294,7 +255,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) attn_rows_kernel(const KvView c
             const int64_t at = !next ? b_at : n_page >= 0 ? offset_of(n_page, place(t)) : -1;
             if (at >= 0) { bulk_prefetch_l2(c.k + at, 16 * D); bulk_prefetch_l2(c.v + at, 16 * D); }
         };
-        uint4 kr[NSUB][2][D / 64];          // [sub-block][8 keys][64 dimensions]
+        uint4 kr[NSUB][2][D / 64];          // [sub-block][key g, g + 8][64 dimensions]
         uint32_t vr[NSUB][4][D / 32];       // [sub-block][its keys 2t, 2t+1, 2t+8, 2t+9][words]
         auto load_k = [&](int t) {
             const int at = (t % BT) * NSUB;
@@ -329,13 +290,85 @@ __global__ void __launch_bounds__(THREADS, CTAS) attn_rows_kernel(const KvView c
                 }
             }
         };
+        if (mine > 0) fetch_batch(0);
+
+        // ---- query fragments: k-step (j, s) of lane (g, t) holds dimensions 64j + 16t + 4s + 0..3 of row g
+        constexpr int PER = D / 32, WR = RT / NW;                  // consecutive dimensions of a lane, rows of a warp
+        float q[WR][PER];
+#pragma unroll
+        for (int w = 0; w < WR; ++w) {
+            const int row = warp + w * NW, rho = RT * gr.i + row;
+            const int64_t tok = gr.first + rho / G;
+            const T* src = static_cast<const T*>(a.q) + tok * a.q_stride + (gr.h * G + rho % G) * D + lane * PER;
+#pragma unroll
+            for (int i = 0; i < PER; i += 2) {
+                const float2 v = row < rows ? load2(src + i) : make_float2(0.0f, 0.0f);
+                q[w][i] = v.x;
+                q[w][i + 1] = v.y;
+            }
+        }
         if (mine > 0) {
-            fetch_batch(0);
-            next_batch(0);
+            next_place(0);
             load_k(0);
             load_v(0);
             for (int t = 1; t < AHEAD; ++t) prefetch(t, false);
+            next_scales();
         }
+        __syncthreads();                                          // the previous piece's readers are done
+#pragma unroll
+        for (int w = 0; w < WR; ++w) {
+            const int row = warp + w * NW;
+            // A power of two brings the row's largest value to [2^8, 2^9): exact, and
+            // nothing that matters is below binary16's range. NaN for a row that is not finite.
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) top = max(top, __float_as_uint(fabsf(q[w][i])));
+            top = __reduce_max_sync(0xffffffffu, top);
+            float mul, back;
+            row_scale(top, mul, back);
+            if (a.scale < 0.0f) mul = -mul;
+            if (lane == 0) rowf[row] = back * lscale;
+#pragma unroll
+            for (int i = 0; i < PER; i += 2) {
+                const int d = lane * PER + i;
+                const int j = d >> 6, t = (d >> 4) & 3, s = (d >> 2) & 3, half = (d >> 1) & 1;
+                const float v0 = q[w][i] * mul, v1 = q[w][i + 1] * mul;
+                const __half2 hi = __floats2half2_rn(v0, v1);
+                uint32_t* dst = reinterpret_cast<uint32_t*>(qf + ((4 * j + s) * NB + (row >> 3)) * 32 + 4 * (row & 7) + t) + half;
+                *dst = *reinterpret_cast<const uint32_t*>(&hi);
+                if constexpr (F32) {
+                    const float2 back2 = __half22float2(hi);
+                    const __half2 lo = __floats2half2_rn(v0 - back2.x, v1 - back2.y);
+                    dst[KST * NB * 32 * 2] = *reinterpret_cast<const uint32_t*>(&lo);
+                }
+            }
+        }
+        __syncthreads();
+        // this lane's rows, 8b + 2t + e: what they see, their scores' factors, running reference and sum
+        int rfrom[NB][2], rstop[NB][2];
+        float rf[NB][2], M[NB][2], l[NB][2];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = 8 * b + 2 * tq + e;
+                row_range(a, gr.n, gr.kv, (RT * gr.i + row) / G, rfrom[b][e], rstop[b][e]);
+                if (row >= rows) rfrom[b][e] = rstop[b][e] = 0;
+                rf[b][e] = rowf[row];
+                M[b][e] = -INFINITY;
+                l[b][e] = 0.0f;
+            }
+        uint2 qh[NB == 1 ? KST : 1];                              // one block's fragments stay in registers
+        if constexpr (NB == 1) {
+#pragma unroll
+            for (int ks = 0; ks < KST; ++ks) qh[ks] = qf[ks * 32 + lane];
+        }
+        float o[NB][MT][4];                                       // dimensions (D / 8) g + 2i (0, 1) and + 2i + 1 (2, 3) of rows 2t, 2t + 1
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.0f;
+
         for (int t = 0; t < mine; ++t) {
             // what belongs to this tile, before the batch moves on
             bool on[NSUB];
@@ -350,122 +383,151 @@ __global__ void __launch_bounds__(THREADS, CTAS) attn_rows_kernel(const KvView c
             }
             if (t % BT == BT / 2) fetch_batch(t - BT / 2 + BT);
             prefetch(t + AHEAD, t % BT + AHEAD >= BT);
-            float sc[NSUB][2][4] = {};
+            float sc[NSUB][NB][4] = {};
 #pragma unroll
             for (int ks = 0; ks < KST; ++ks) {
-                uint32_t qh[4], ql[4];
-                {
-                    const uint4 x = qf[ks * 32 + lane];
-                    qh[0] = x.x; qh[1] = x.y; qh[2] = x.z; qh[3] = x.w;
-                }
-                if constexpr (F32) {
-                    const uint4 x = qf[(KST + ks) * 32 + lane];
-                    ql[0] = x.x; ql[1] = x.y; ql[2] = x.z; ql[3] = x.w;
+                uint2 qa[NB], ql[NB];
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    if constexpr (NB == 1) qa[b] = qh[ks];
+                    else qa[b] = qf[(ks * NB + b) * 32 + lane];
+                    if constexpr (F32) ql[b] = qf[((KST + ks) * NB + b) * 32 + lane];
                 }
 #pragma unroll
-                for (int s = 0; s < NSUB; ++s)
+                for (int s = 0; s < NSUB; ++s) {
+                    uint32_t w[2], ka[4];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint4& kk = kr[s][i][ks >> 2];
-                        const uint32_t w = (ks & 3) == 0 ? kk.x : (ks & 3) == 1 ? kk.y : (ks & 3) == 2 ? kk.z : kk.w;
-                        uint32_t b0, b1;
-                        tc::s8x4_half(w, b0, b1);
-                        mma16816(sc[s][i], qh, b0, b1);
-                        if constexpr (F32) mma16816(sc[s][i], ql, b0, b1);
+                        w[i] = (ks & 3) == 0 ? kk.x : (ks & 3) == 1 ? kk.y : (ks & 3) == 2 ? kk.z : kk.w;
+                        tc::s8x4_half(w[i], ka[i], ka[2 + i]);
                     }
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        mma16816(sc[s][b], ka, qa[b].x, qa[b].y);
+                        if constexpr (F32) mma16816(sc[s][b], ka, ql[b].x, ql[b].y);
+                    }
+                }
             }
             // the next tile's keys come in behind the softmax and the second product, its values behind the next scores
             const bool more = t + 1 < mine;
             if (more) {
-                if ((t + 1) % BT == 0) next_batch(t + 1);
+                if ((t + 1) % BT == 0) { next_place(t + 1); next_scales(); }
                 load_k(t + 1);
             }
-            #pragma unroll
+#pragma unroll
             for (int s = 0; s < NSUB; ++s) {
                 if (!on[s]) continue;                                           // warp-uniform
                 const int j0 = k_begin + (warp + t * NW) * TK + s * 16;
                 // x_j, hidden keys at -inf
                 const bool whole = j0 >= all_from && j0 + 16 <= all_stop;
-                const float f0 = ks_[s] * rf[0], f1 = ks_[s] * rf[1];
-                float top[2] = {-INFINITY, -INFINITY};
+                bool raise = false;
+                float top[NB][2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int b = 0; b < NB; ++b) {
+                    const float f[2] = {ks_[s] * rf[b][0], ks_[s] * rf[b][1]};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = fmaf(sc[s][i][e], e < 2 ? f0 : f1, lv_[s]);
+                    for (int e = 0; e < 4; ++e) {                               // key g + 8 (e / 2), row 2t + e % 2
+                        float x = fmaf(sc[s][b][e], f[e & 1], lv_[s]);
                         if (!whole) {
-                            const int j = j0 + 8 * i + 2 * tq + (e & 1);
-                            if (j < rfrom[e >> 1] || j >= rstop[e >> 1]) x = -INFINITY;
+                            const int j = j0 + g + 8 * (e >> 1);
+                            if (j < rfrom[b][e & 1] || j >= rstop[b][e & 1]) x = -INFINITY;
                         }
-                        sc[s][i][e] = x;
-                        top[e >> 1] = fmaxf(top[e >> 1], x);
+                        sc[s][b][e] = x;
                     }
-                if (__any_sync(0xffffffffu, top[0] > M[0] + RAISE || top[1] > M[1] + RAISE)) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float m = top[e];
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                        const float old = M[e];
-                        if (m > old + RAISE) {                                  // the row's own, the same in its four lanes
-                            M[e] = m;
-                            const float f = exp2_approx(old - m);               // 0 from -inf
-                            l[e] *= f;
+                        top[b][e] = fmaxf(sc[s][b][e], sc[s][b][2 + e]);
+                        raise |= top[b][e] > M[b][e] + RAISE;
+                    }
+                }
+                if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-                            for (int i = 0; i < NT; ++i) { o[i][2 * e] *= f; o[i][2 * e + 1] *= f; }
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float m = top[b][e];
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                            const float old = M[b][e];
+                            if (m > old + RAISE) {                              // the row's own, the same in its eight lanes
+                                M[b][e] = m;
+                                const float f = exp2_approx(old - m);           // 0 from -inf
+                                l[b][e] *= f;
+#pragma unroll
+                                for (int i = 0; i < MT; ++i) { o[b][i][e] *= f; o[b][i][2 + e] *= f; }
+                            }
+                        }
+                }
+                uint2 ph[NB], plo[NB], ps[NB], pt[NB];
+                bool small = false;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    float p[4], sm[4];
+                    float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float m = M[b][e & 1], base = m == -INFINITY ? 0.0f : m - OFF;
+                        p[e] = exp2_approx(sc[s][b][e] - base);
+                        sum[e & 1] += p[e];                                     // unrounded: lse is held to fp32
+                        if constexpr (F32) {
+                            sm[e] = p[e] < SMALL ? p[e] : 0.0f;
+                            small |= sm[e] > 0.0f;
+                            p[e] -= sm[e];
+                        }
+                    }
+                    // a row that sees nothing here must not meet a scale that is not finite
+                    l[b][0] += sum[0] != 0.0f ? sum[0] * rv_[s] : 0.0f;
+                    l[b][1] += sum[1] != 0.0f ? sum[1] * rv_[s] : 0.0f;
+                    const __half2 h0 = __floats2half2_rn(p[0], p[1]), h1 = __floats2half2_rn(p[2], p[3]);
+                    ph[b] = make_uint2(transpose8(*reinterpret_cast<const uint32_t*>(&h0)),
+                                       transpose8(*reinterpret_cast<const uint32_t*>(&h1)));
+                    if constexpr (SPLIT_P) {
+                        const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+                        const __half2 l0 = __floats2half2_rn(p[0] - f0.x, p[1] - f0.y), l1 = __floats2half2_rn(p[2] - f1.x, p[3] - f1.y);
+                        plo[b] = make_uint2(transpose8(*reinterpret_cast<const uint32_t*>(&l0)),
+                                            transpose8(*reinterpret_cast<const uint32_t*>(&l1)));
+                    }
+                    if constexpr (F32) {
+                        const uint32_t s0 = bf16_pair(sm[0], sm[1]), s1 = bf16_pair(sm[2], sm[3]);
+                        const uint32_t t0 = bf16_pair(sm[0] - __uint_as_float(s0 << 16), sm[1] - __uint_as_float(s0 & 0xffff0000u));
+                        const uint32_t t1 = bf16_pair(sm[2] - __uint_as_float(s1 << 16), sm[3] - __uint_as_float(s1 & 0xffff0000u));
+                        small = __any_sync(0xffffffffu, small);
+                        if (small) {
+                            ps[b] = make_uint2(transpose8(s0), transpose8(s1));
+                            pt[b] = make_uint2(transpose8(t0), transpose8(t1));
+                        } else {
+                            ps[b] = pt[b] = make_uint2(0, 0);
                         }
                     }
                 }
-                const float base0 = M[0] == -INFINITY ? 0.0f : M[0] - OFF, base1 = M[1] == -INFINITY ? 0.0f : M[1] - OFF;
-                uint32_t ph[4], plo[4], ps[4], pt[4];
-                bool small = false;
-                float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float base = e ? base1 : base0;
-                        float p0 = exp2_approx(sc[s][i][2 * e] - base), p1 = exp2_approx(sc[s][i][2 * e + 1] - base);
-                        sum[e] += p0 + p1;                  // unrounded: lse is held to fp32
-                        if constexpr (F32) {
-                            const float s0 = p0 < SMALL ? p0 : 0.0f, s1 = p1 < SMALL ? p1 : 0.0f;
-                            small |= s0 > 0.0f || s1 > 0.0f;
-                            p0 -= s0;
-                            p1 -= s1;
-                            const uint32_t hi = bf16_pair(s0, s1);
-                            ps[2 * i + e] = hi;
-                            pt[2 * i + e] = bf16_pair(s0 - __uint_as_float(hi << 16), s1 - __uint_as_float(hi & 0xffff0000u));
-                        }
-                        const __half2 hi = __floats2half2_rn(p0, p1);
-                        ph[2 * i + e] = *reinterpret_cast<const uint32_t*>(&hi);
-                        if constexpr (SPLIT_P) {
-                            const float2 hf = __half22float2(hi);
-                            const __half2 lo = __floats2half2_rn(p0 - hf.x, p1 - hf.y);
-                            plo[2 * i + e] = *reinterpret_cast<const uint32_t*>(&lo);
-                        }
-                    }
-                if constexpr (F32) small = __any_sync(0xffffffffu, small);
-                // a row that sees nothing here must not meet a scale that is not finite
-                l[0] += sum[0] != 0.0f ? sum[0] * rv_[s] : 0.0f;
-                l[1] += sum[1] != 0.0f ? sum[1] * rv_[s] : 0.0f;
                 // The second product follows at once: a later sub-block may raise M.
 #pragma unroll
                 for (int w = 0; w < D / 32; ++w) {
-                    // four dimensions of keys (2t, 2t+1) and (2t+8, 2t+9), as pairs of keys
-                    uint32_t b0[4], b1[4];
-                    tc::s8x4_half(__byte_perm(vr[s][0][w], vr[s][1][w], 0x5140), b0[0], b0[1]);
-                    tc::s8x4_half(__byte_perm(vr[s][0][w], vr[s][1][w], 0x7362), b0[2], b0[3]);
-                    tc::s8x4_half(__byte_perm(vr[s][2][w], vr[s][3][w], 0x5140), b1[0], b1[1]);
-                    tc::s8x4_half(__byte_perm(vr[s][2][w], vr[s][3][w], 0x7362), b1[2], b1[3]);
+                    // four dimensions of keys (2t, 2t+1) and (2t+8, 2t+9), as pairs of keys: two row tiles
+                    uint32_t va[2][4];
+                    tc::s8x4_half(__byte_perm(vr[s][0][w], vr[s][1][w], 0x5140), va[0][0], va[0][1]);
+                    tc::s8x4_half(__byte_perm(vr[s][0][w], vr[s][1][w], 0x7362), va[1][0], va[1][1]);
+                    tc::s8x4_half(__byte_perm(vr[s][2][w], vr[s][3][w], 0x5140), va[0][2], va[0][3]);
+                    tc::s8x4_half(__byte_perm(vr[s][2][w], vr[s][3][w], 0x7362), va[1][2], va[1][3]);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        mma16816(o[4 * w + x], ph, b0[x], b1[x]);
-                        if constexpr (SPLIT_P) mma16816(o[4 * w + x], plo, b0[x], b1[x]);
+                    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            mma16816(o[b][2 * w + x], va[x], ph[b].x, ph[b].y);
+                            if constexpr (SPLIT_P) mma16816(o[b][2 * w + x], va[x], plo[b].x, plo[b].y);
+                        }
                         if constexpr (F32) {
                             if (small) {
-                                const uint32_t c0 = half_to_bf16(b0[x]), c1 = half_to_bf16(b1[x]);
-                                mma16816_bf16(o[4 * w + x], ps, c0, c1);
-                                mma16816_bf16(o[4 * w + x], pt, c0, c1);
+                                uint32_t vb[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) vb[i] = half_to_bf16(va[x][i]);
+#pragma unroll
+                                for (int b = 0; b < NB; ++b) {
+                                    mma16816_bf16(o[b][2 * w + x], vb, ps[b].x, ps[b].y);
+                                    mma16816_bf16(o[b][2 * w + x], vb, pt[b].x, pt[b].y);
+                                }
                             }
                         }
                     }
@@ -476,22 +538,22 @@ __global__ void __launch_bounds__(THREADS, CTAS) attn_rows_kernel(const KvView c
 
         // ---- the warps' parts of the piece
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-            const int row = g + 8 * e;
-            if (row < rows) {
-                if (tq == 0) { ml[(warp * 16 + row) * 2] = M[e]; ml[(warp * 16 + row) * 2 + 1] = l[e]; }
-                // this lane's columns: dimensions of group 2t (c0) and 2t + 1 (c1), D / 8 each, NT of them
-                float* dst = merge + (warp * 16 + row) * ROWF + 2 * tq * (D / 8);
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int i = 0; i < NT; i += 4) {
-                    *reinterpret_cast<float4*>(dst + i) = make_float4(o[i][2 * e], o[i + 1][2 * e], o[i + 2][2 * e], o[i + 3][2 * e]);
-                    *reinterpret_cast<float4*>(dst + D / 8 + i) =
-                        make_float4(o[i][2 * e + 1], o[i + 1][2 * e + 1], o[i + 2][2 * e + 1], o[i + 3][2 * e + 1]);
+            for (int e = 0; e < 2; ++e) {
+                float lt = l[b][e];
+                lt += __shfl_xor_sync(0xffffffffu, lt, 4);
+                lt += __shfl_xor_sync(0xffffffffu, lt, 8);
+                lt += __shfl_xor_sync(0xffffffffu, lt, 16);
+                const int row = 8 * b + 2 * tq + e;
+                if (row < rows) {
+                    if (g == 0) { ml[(warp * RT + row) * 2] = M[b][e]; ml[(warp * RT + row) * 2 + 1] = lt; }
+                    float* dst = merge + (warp * RT + row) * ROWF + g * (D / 8);
+#pragma unroll
+                    for (int i = 0; i < MT; i += 2)
+                        *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(o[b][i][e], o[b][i][2 + e], o[b][i + 1][e], o[b][i + 1][2 + e]);
                 }
             }
-        }
         __syncthreads();
         const int used = min(NW, max(ntile, 1));                               // warps that had a tile (warp 0 always counts)
         const bool whole = piece0 == 0 && piece1 == gr.units;
@@ -500,21 +562,21 @@ __global__ void __launch_bounds__(THREADS, CTAS) attn_rows_kernel(const KvView c
         for (int x = tid; x < rows * (D / 4); x += THREADS) {
             const int row = x / (D / 4), col = (x % (D / 4)) * 4;
             float m = -INFINITY;
-            for (int w = 0; w < used; ++w) m = fmaxf(m, ml[(w * 16 + row) * 2]);
+            for (int w = 0; w < used; ++w) m = fmaxf(m, ml[(w * RT + row) * 2]);
             const float base = m == -INFINITY ? 0.0f : m;
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             float lt = 0.0f;
             for (int w = 0; w < used; ++w) {
-                const float f = exp2_approx(ml[(w * 16 + row) * 2] - base);
-                const float4 v = *reinterpret_cast<const float4*>(merge + (w * 16 + row) * ROWF + col);
-                lt = fmaf(ml[(w * 16 + row) * 2 + 1], f, lt);
+                const float f = exp2_approx(ml[(w * RT + row) * 2] - base);
+                const float4 v = *reinterpret_cast<const float4*>(merge + (w * RT + row) * ROWF + col);
+                lt = fmaf(ml[(w * RT + row) * 2 + 1], f, lt);
                 acc.x = fmaf(v.x, f, acc.x);
                 acc.y = fmaf(v.y, f, acc.y);
                 acc.z = fmaf(v.z, f, acc.z);
                 acc.w = fmaf(v.w, f, acc.w);
             }
             if (whole) {
-                write_row<T, D>(a, gr.first, gr.h, G, 16 * gr.i + row, col, acc, m, lt, OFF);
+                write_row<T, D>(a, gr.first, gr.h, G, RT * gr.i + row, col, acc, m, lt, OFF);
             } else {
                 *reinterpret_cast<float4*>(part + row * ROWF + col) = acc;
                 if (col == 0) { part[row * ROWF + D] = m; part[row * ROWF + D + 1] = lt; }
@@ -553,7 +615,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) attn_rows_kernel(const KvView c
                         acc.w = acc.w * f + v.w * fc;
                         m = m2;
                     }
-                    write_row<T, D>(a, gr.first, gr.h, G, 16 * gr.i + row, col, acc, m, lt, OFF);
+                    write_row<T, D>(a, gr.first, gr.h, G, RT * gr.i + row, col, acc, m, lt, OFF);
                 }
             }
         }
@@ -561,16 +623,22 @@ __global__ void __launch_bounds__(THREADS, CTAS) attn_rows_kernel(const KvView c
     }
 }
 
+template <typename T, int D, int NB>
+cudaError_t launch_rows_n(const DeviceInfo& dev, const KvView& c, const AttnArgs& a, const RowsPlan& pl, cudaStream_t s) {
+    using W = Rows<T, D, NB>;
+    const int smem = W::smem(a.R);
+    if (smem > dev.smem_optin) return cudaErrorInvalidConfiguration;
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_rows_kernel<T, D, NB>), smem);
+    if (e != cudaSuccess) return e;
+    const int ctas = std::min(dev.sm_count * W::CTAS, ATTN_MAX_CTAS);
+    return launch_kernel(attn_rows_kernel<T, D, NB>, dim3(static_cast<unsigned>(ctas)), dim3(THREADS), static_cast<size_t>(smem), s, c, a, pl);
+}
+
+// Tiles of 8 rows where a request's rows of one kv head fit them, else of 16: the
+// conversion of the cache's bytes is then shared by two row blocks.
 template <typename T, int D>
 cudaError_t launch_rows_t(const DeviceInfo& dev, const KvView& c, const AttnArgs& a, const RowsPlan& pl, cudaStream_t s) {
-    constexpr bool F32 = std::is_same<T, float>::value;
-    const int smem = (((a.R + 1) * 8 + 15) & ~15) + (F32 ? 2 : 1) * (D / 16) * 32 * 16 + 16 * 4 + NW * 16 * (D + 4) * 4 +
-                     NW * 16 * 2 * 4;
-    if (smem > dev.smem_optin) return cudaErrorInvalidConfiguration;
-    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_rows_kernel<T, D>), smem);
-    if (e != cudaSuccess) return e;
-    const int ctas = std::min(dev.sm_count * CTAS, ATTN_MAX_CTAS);
-    return launch_kernel(attn_rows_kernel<T, D>, dim3(static_cast<unsigned>(ctas)), dim3(THREADS), static_cast<size_t>(smem), s, c, a, pl);
+    return a.max_new * (a.heads / c.heads) <= 8 ? launch_rows_n<T, D, 1>(dev, c, a, pl, s) : launch_rows_n<T, D, 2>(dev, c, a, pl, s);
 }
 
 }  // namespace
