@@ -40,6 +40,7 @@ constexpr int NW = 4;                     // warps a CTA
 constexpr int THREADS = NW * 32;
 constexpr int UNIT = 64;                  // keys of a work unit
 constexpr int MIN_UNITS = 2;              // a CTA is worth at least so many
+constexpr int JOIN = 8;                   // partial results joined at a time
 constexpr int AHEAD = 4;                  // tiles that a warp has on their way into L2
 constexpr int KNOWN = THREADS;            // requests whose lengths stay in shared memory
 constexpr float OFF = 7.0f, RAISE = 8.0f;
@@ -73,13 +74,15 @@ __device__ __forceinline__ uint32_t half_to_bf16(uint32_t h) {
     return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
 }
 
-// What the rows of one group see, and its units.
-struct Group {
+// A CTA's part of one group: what its rows are and see, and the keys to read.
+struct Piece {
     int r, h, i;             // request, kv head, row tile
-    int first;               // first token of the request
-    int n, kv;               // its new tokens and its length
-    int u0;                  // first key of the group's units (a multiple of UNIT)
-    int units;
+    int first, n, kv;        // the request's first token, new tokens, length
+    int rows;                // of the tile
+    int units, piece0, piece1;      // the group's units, and the piece's among them
+    int all_from, all_stop;  // keys that every row sees
+    int k_begin, k_end, ntile;
+    int64_t group_u;         // the group's first unit
 };
 
 // Keys [from, stop) that some row of the request sees.
@@ -136,6 +139,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
     __shared__ int64_t wsum[NW];
     __shared__ int last_flag;
     __shared__ int known[KNOWN][3];
+    __shared__ Piece pieces[2];                                               // this one and the next
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
     const int G = a.heads / c.heads;
 
@@ -180,133 +184,145 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
     const float lscale = fabsf(a.scale) * 1.4426950408889634f;
     bool first_piece = true;
 
-    while (u < u_end) {
-        // ---- the group that unit u belongs to
-        Group gr;
-        {
-            int lo = 0, hi = a.R;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (cum[mid] <= u) lo = mid; else hi = mid;
-            }
-            gr.r = lo;
+    // The piece that begins at unit u.
+    auto locate = [&](int64_t u, Piece& pc) {
+        int lo = 0, hi = a.R;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cum[mid] <= u) lo = mid; else hi = mid;
         }
-        if (gr.r < KNOWN) { gr.first = known[gr.r][0]; gr.n = known[gr.r][1]; gr.kv = known[gr.r][2]; }
-        else request_of(c, a, gr.r, gr.first, gr.n, gr.kv);
+        pc.r = lo;
+        if (lo < KNOWN) { pc.first = known[lo][0]; pc.n = known[lo][1]; pc.kv = known[lo][2]; }
+        else request_of(c, a, lo, pc.first, pc.n, pc.kv);
         int from, stop;
-        request_range(a, gr.n, gr.kv, from, stop);
-        gr.u0 = (from / UNIT) * UNIT;
-        gr.units = request_units(a, gr.n, gr.kv);
-        const int64_t in = u - cum[gr.r], gi = in / gr.units;
-        const int piece0 = static_cast<int>(in - gi * gr.units);
-        const int nrt = (gr.n * G + RT - 1) / RT;
-        gr.h = static_cast<int>(gi / nrt);
-        gr.i = static_cast<int>(gi - static_cast<int64_t>(gr.h) * nrt);
-        const int64_t group_u = u - piece0;                       // the group's first unit
-        const int piece1 = static_cast<int>(min(static_cast<int64_t>(gr.units), u_end - group_u));
-        const int rows = min(RT, gr.n * G - RT * gr.i);           // of this tile
-        int tfrom, tstop, x0, x1;
-        row_range(a, gr.n, gr.kv, (RT * gr.i) / G, tfrom, x0);
-        row_range(a, gr.n, gr.kv, (RT * gr.i + rows - 1) / G, x1, tstop);
-        // keys that every row sees: from the last row's first to the first row's last
-        const int all_from = x1, all_stop = x0;
-
-        // ---- the piece's tiles, one warp after another
-        const int k_begin = max(gr.u0 + piece0 * UNIT, (tfrom / TK) * TK);
-        const int k_end = min(gr.u0 + piece1 * UNIT, tstop);
-        const int ntile = k_end > k_begin ? (k_end - k_begin + TK - 1) / TK : 0;
-        const int mine = ntile > warp ? (ntile - warp + NW - 1) / NW : 0;       // tiles warp, warp + NW, ...
-        const int32_t* table = a.table + static_cast<int64_t>(gr.r) * a.max_blocks;
-        const int64_t head_off = static_cast<int64_t>(gr.h) * c.page_size * D;
-
-        // Lane b of a batch holds the place and scales of sub-block b of the warp's
-        // next 32; its page and scales of the batch after it (n_) are on their way meanwhile.
-        int n_page = -1;
-        float n_ks = 0.0f, n_vs = 0.0f;
-        int64_t b_at = -1;                                                      // offset of the sub-block's keys (and values)
-        float b_ks = 0.0f, b_lv = 0.0f, b_rv = 0.0f;
-        auto place = [&](int tl) { return k_begin + (warp + tl * NW) * TK + (lane % NSUB) * 16; };
-        auto fetch_batch = [&](int t0) {
-            const int tl = t0 + lane / NSUB, j0 = place(tl);                    // the warp's tile, its first key
-            n_page = -1;
-            if (tl < mine && j0 < k_end) {
-                const int page = table[j0 >> c.page_shift];
-                if (page >= 0 && page < c.num_pages) {
-                    n_page = page;
-                    n_ks = c.k_scale[page * c.scale_stride + gr.h];
-                    n_vs = c.v_scale[page * c.scale_stride + gr.h];
+        request_range(a, pc.n, pc.kv, from, stop);
+        const int u0 = (from / UNIT) * UNIT;
+        pc.units = request_units(a, pc.n, pc.kv);
+        const int64_t in = u - cum[lo], gi = in / pc.units;
+        pc.piece0 = static_cast<int>(in - gi * pc.units);
+        const int nrt = (pc.n * G + RT - 1) / RT;
+        pc.h = static_cast<int>(gi / nrt);
+        pc.i = static_cast<int>(gi - static_cast<int64_t>(pc.h) * nrt);
+        pc.group_u = u - pc.piece0;
+        pc.piece1 = static_cast<int>(min(static_cast<int64_t>(pc.units), u_end - pc.group_u));
+        pc.rows = min(RT, pc.n * G - RT * pc.i);
+        // from the last row's first key to the first row's last
+        int tfrom, tstop;
+        row_range(a, pc.n, pc.kv, (RT * pc.i) / G, tfrom, pc.all_stop);
+        row_range(a, pc.n, pc.kv, (RT * pc.i + pc.rows - 1) / G, pc.all_from, tstop);
+        pc.k_begin = max(u0 + pc.piece0 * UNIT, (tfrom / TK) * TK);
+        pc.k_end = min(u0 + pc.piece1 * UNIT, tstop);
+        pc.ntile = pc.k_end > pc.k_begin ? (pc.k_end - pc.k_begin + TK - 1) / TK : 0;
+    };
+    // What the loop over the tiles needs of its piece; the rest waits in shared memory.
+    int k_begin = 0, k_end = 0, all_from = 0, all_stop = 0, turn = 0;
+    int mine = 0;                                                 // the warp's tiles: warp, warp + NW, ...
+    // Lane b of a batch holds the place and scales of sub-block b of the warp's
+    // next 32; its page and scales of the batch after it (n_) are on their way meanwhile.
+    int64_t head_off = 0;
+    int n_page = -1;
+    float n_ks = 0.0f, n_vs = 0.0f;
+    int64_t b_at = -1;                                                      // offset of the sub-block's keys (and values)
+    float b_ks = 0.0f, b_lv = 0.0f, b_rv = 0.0f;
+    auto place = [&](int tl) { return k_begin + (warp + tl * NW) * TK + (lane % NSUB) * 16; };
+    auto fetch_batch = [&](const Piece& pc, int t0) {
+        const int tl = t0 + lane / NSUB, j0 = place(tl);                    // the warp's tile, its first key
+        n_page = -1;
+        if (tl < mine && j0 < k_end) {
+            const int page = a.table[pc.r * a.max_blocks + (j0 >> c.page_shift)];
+            if (page >= 0 && page < c.num_pages) {
+                n_page = page;
+                n_ks = c.k_scale[page * c.scale_stride + pc.h];
+                n_vs = c.v_scale[page * c.scale_stride + pc.h];
+            } else {
+                atomicOr(a.status, CQ_DEV_KV_PAGE);
+            }
+        }
+    };
+    auto offset_of = [&](int page, int j0) {
+        return page * c.page_stride + head_off + static_cast<int64_t>(j0 & (c.page_size - 1)) * D;
+    };
+    auto next_place = [&](int t0) { b_at = n_page >= 0 ? offset_of(n_page, place(t0 + lane / NSUB)) : -1; };
+    auto next_scales = [&]() {
+        b_ks = n_ks;
+        b_lv = n_vs == 0.0f ? 0.0f : log2f(n_vs);
+        b_rv = n_vs == 0.0f ? 1.0f : __frcp_rn(n_vs);
+    };
+    // Tile t begins its way into L2: the lanes that hold it in its batch.
+    auto prefetch = [&](int t, bool next) {
+        if (lane / NSUB != t % BT) return;
+        const int64_t at = !next ? b_at : n_page >= 0 ? offset_of(n_page, place(t)) : -1;
+        if (at >= 0) { bulk_prefetch_l2(c.k + at, 16 * D); bulk_prefetch_l2(c.v + at, 16 * D); }
+    };
+    uint4 kr[NSUB][2][D / 64];          // [sub-block][key g, g + 8][64 dimensions]
+    uint32_t vr[NSUB][4][D / 32];       // [sub-block][its keys 2t, 2t+1, 2t+8, 2t+9][words]
+    auto load_k = [&](int t) {
+        const int at = (t % BT) * NSUB;
+#pragma unroll
+        for (int s = 0; s < NSUB; ++s) {
+            const int64_t off = __shfl_sync(0xffffffffu, b_at, at + s);
+            if (off < 0) continue;
+            const int8_t* p = c.k + off + g * D + 16 * tq;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j) kr[s][i][j] = ldg_stream16(p + 8 * i * D + 64 * j);
+        }
+    };
+    auto load_v = [&](int t) {
+        const int at = (t % BT) * NSUB;
+#pragma unroll
+        for (int s = 0; s < NSUB; ++s) {
+            const int64_t off = __shfl_sync(0xffffffffu, b_at, at + s);
+            if (off < 0) continue;
+            const int8_t* p = c.v + off + 2 * tq * D + g * (D / 8);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int8_t* q = p + ((i & 1) + 8 * (i >> 1)) * D;
+                if constexpr (D == 128) {
+                    const uint4 x = ldg_stream16(q);
+                    vr[s][i][0] = x.x; vr[s][i][1] = x.y; vr[s][i][2] = x.z; vr[s][i][3] = x.w;
                 } else {
-                    atomicOr(a.status, CQ_DEV_KV_PAGE);
+                    const uint2 x = ldg_stream8(q);
+                    vr[s][i][0] = x.x; vr[s][i][1] = x.y;
                 }
             }
-        };
-        auto offset_of = [&](int page, int j0) {
-            return page * c.page_stride + head_off + static_cast<int64_t>(j0 & (c.page_size - 1)) * D;
-        };
-        auto next_place = [&](int t0) { b_at = n_page >= 0 ? offset_of(n_page, place(t0 + lane / NSUB)) : -1; };
-        auto next_scales = [&]() {
-            b_ks = n_ks;
-            b_lv = n_vs == 0.0f ? 0.0f : log2f(n_vs);
-            b_rv = n_vs == 0.0f ? 1.0f : __frcp_rn(n_vs);
-        };
-        // Tile t begins its way into L2: the lanes that hold it in its batch.
-        auto prefetch = [&](int t, bool next) {
-            if (lane / NSUB != t % BT) return;
-            const int64_t at = !next ? b_at : n_page >= 0 ? offset_of(n_page, place(t)) : -1;
-            if (at >= 0) { bulk_prefetch_l2(c.k + at, 16 * D); bulk_prefetch_l2(c.v + at, 16 * D); }
-        };
-        uint4 kr[NSUB][2][D / 64];          // [sub-block][key g, g + 8][64 dimensions]
-        uint32_t vr[NSUB][4][D / 32];       // [sub-block][its keys 2t, 2t+1, 2t+8, 2t+9][words]
-        auto load_k = [&](int t) {
-            const int at = (t % BT) * NSUB;
-#pragma unroll
-            for (int s = 0; s < NSUB; ++s) {
-                const int64_t off = __shfl_sync(0xffffffffu, b_at, at + s);
-                if (off < 0) continue;
-                const int8_t* p = c.k + off + g * D + 16 * tq;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < D / 64; ++j) kr[s][i][j] = ldg_stream16(p + 8 * i * D + 64 * j);
-            }
-        };
-        auto load_v = [&](int t) {
-            const int at = (t % BT) * NSUB;
-#pragma unroll
-            for (int s = 0; s < NSUB; ++s) {
-                const int64_t off = __shfl_sync(0xffffffffu, b_at, at + s);
-                if (off < 0) continue;
-                const int8_t* p = c.v + off + 2 * tq * D + g * (D / 8);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int8_t* q = p + ((i & 1) + 8 * (i >> 1)) * D;
-                    if constexpr (D == 128) {
-                        const uint4 x = ldg_stream16(q);
-                        vr[s][i][0] = x.x; vr[s][i][1] = x.y; vr[s][i][2] = x.z; vr[s][i][3] = x.w;
-                    } else {
-                        const uint2 x = ldg_stream8(q);
-                        vr[s][i][0] = x.x; vr[s][i][1] = x.y;
-                    }
-                }
-            }
-        };
-        if (mine > 0) fetch_batch(0);
-
-        // ---- query fragments: k-step (j, s) of lane (g, t) holds dimensions 64j + 16t + 4s + 0..3 of row g
-        constexpr int PER = D / 32, WR = RT / NW;                  // consecutive dimensions of a lane, rows of a warp
-        float q[WR][PER];
+        }
+    };
+    // The query rows of the piece: consecutive dimensions of a lane, rows of a warp.
+    constexpr int PER = D / 32, WR = RT / NW;
+    float q[WR][PER];
+    auto load_q = [&](const Piece& pc) {
 #pragma unroll
         for (int w = 0; w < WR; ++w) {
-            const int row = warp + w * NW, rho = RT * gr.i + row;
-            const int64_t tok = gr.first + rho / G;
-            const T* src = static_cast<const T*>(a.q) + tok * a.q_stride + (gr.h * G + rho % G) * D + lane * PER;
+            const int row = warp + w * NW, rho = RT * pc.i + row;
+            const int64_t tok = pc.first + rho / G;
+            const T* src = static_cast<const T*>(a.q) + tok * a.q_stride + (pc.h * G + rho % G) * D + lane * PER;
 #pragma unroll
             for (int i = 0; i < PER; i += 2) {
-                const float2 v = row < rows ? load2(src + i) : make_float2(0.0f, 0.0f);
+                const float2 v = row < pc.rows ? load2(src + i) : make_float2(0.0f, 0.0f);
                 q[w][i] = v.x;
                 q[w][i + 1] = v.y;
             }
         }
+    };
+    // A piece's first loads, all on their way before anything is waited for: the
+    // next piece's while this one is merged.
+    auto begin = [&](int64_t u) {
+        Piece pc;
+        locate(u, pc);
+        k_begin = pc.k_begin;
+        k_end = pc.k_end;
+        all_from = pc.all_from;
+        all_stop = pc.all_stop;
+        head_off = static_cast<int64_t>(pc.h) * c.page_size * D;
+        mine = pc.ntile > warp ? (pc.ntile - warp + NW - 1) / NW : 0;
+        if (mine > 0) fetch_batch(pc, 0);
+        load_q(pc);
+        turn ^= 1;
+        if (tid == 0) pieces[turn] = pc;
+    };
+    auto begin_tiles = [&]() {
         if (mine > 0) {
             next_place(0);
             load_k(0);
@@ -314,7 +330,13 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
             for (int t = 1; t < AHEAD; ++t) prefetch(t, false);
             next_scales();
         }
-        __syncthreads();                                          // the previous piece's readers are done
+    };
+    begin(u);
+    begin_tiles();
+
+    for (;;) {
+        // ---- query fragments: k-step (j, s) of lane (g, t) holds dimensions 64j + 16t + 4s + 0..3 of row g
+        // (the barrier at the previous piece's merge is behind the last reader of its fragments)
 #pragma unroll
         for (int w = 0; w < WR; ++w) {
             const int row = warp + w * NW;
@@ -352,8 +374,9 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row = 8 * b + 2 * tq + e;
-                row_range(a, gr.n, gr.kv, (RT * gr.i + row) / G, rfrom[b][e], rstop[b][e]);
-                if (row >= rows) rfrom[b][e] = rstop[b][e] = 0;
+                const Piece& pc = pieces[turn];
+                row_range(a, pc.n, pc.kv, (RT * pc.i + row) / G, rfrom[b][e], rstop[b][e]);
+                if (row >= pc.rows) rfrom[b][e] = rstop[b][e] = 0;
                 rf[b][e] = rowf[row];
                 M[b][e] = -INFINITY;
                 l[b][e] = 0.0f;
@@ -381,7 +404,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
                 lv_[s] = __shfl_sync(0xffffffffu, b_lv, at);
                 rv_[s] = __shfl_sync(0xffffffffu, b_rv, at);
             }
-            if (t % BT == BT / 2) fetch_batch(t - BT / 2 + BT);
+            if (t % BT == BT / 2) fetch_batch(pieces[turn], t - BT / 2 + BT);
             prefetch(t + AHEAD, t % BT + AHEAD >= BT);
             float sc[NSUB][NB][4] = {};
 #pragma unroll
@@ -546,7 +569,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
                 lt += __shfl_xor_sync(0xffffffffu, lt, 8);
                 lt += __shfl_xor_sync(0xffffffffu, lt, 16);
                 const int row = 8 * b + 2 * tq + e;
-                if (row < rows) {
+                if (row < pieces[turn].rows) {
                     if (g == 0) { ml[(warp * RT + row) * 2] = M[b][e]; ml[(warp * RT + row) * 2 + 1] = lt; }
                     float* dst = merge + (warp * RT + row) * ROWF + g * (D / 8);
 #pragma unroll
@@ -554,9 +577,15 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
                         *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(o[b][i][e], o[b][i][2 + e], o[b][i + 1][e], o[b][i + 1][2 + e]);
                 }
             }
+        const Piece& done = pieces[turn];
+        const int rows = done.rows;
+        u = done.group_u + done.piece1;
+        const bool more = u < u_end;
+        if (more) begin(u);
         __syncthreads();
-        const int used = min(NW, max(ntile, 1));                               // warps that had a tile (warp 0 always counts)
-        const bool whole = piece0 == 0 && piece1 == gr.units;
+        if (more) begin_tiles();
+        const int used = min(NW, max(done.ntile, 1));                               // warps that had a tile (warp 0 always counts)
+        const bool whole = done.piece0 == 0 && done.piece1 == done.units;
         float* part = pl.part + (me * 2 + (first_piece ? 0 : 1)) * (16 * ROWF);
         first_piece = false;
         for (int x = tid; x < rows * (D / 4); x += THREADS) {
@@ -576,7 +605,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
                 acc.w = fmaf(v.w, f, acc.w);
             }
             if (whole) {
-                write_row<T, D>(a, gr.first, gr.h, G, RT * gr.i + row, col, acc, m, lt, OFF);
+                write_row<T, D>(a, done.first, done.h, G, RT * done.i + row, col, acc, m, lt, OFF);
             } else {
                 *reinterpret_cast<float4*>(part + row * ROWF + col) = acc;
                 if (col == 0) { part[row * ROWF + D] = m; part[row * ROWF + D + 1] = lt; }
@@ -584,7 +613,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
         }
         if (!whole) {
             // ---- the group's pieces lie with CTAs c0..c1; the last of them to arrive joins them
-            const int64_t c0 = ((group_u + 1) * nact - 1) / U, c1 = ((group_u + gr.units) * nact - 1) / U;
+            const int64_t c0 = ((done.group_u + 1) * nact - 1) / U, c1 = ((done.group_u + done.units) * nact - 1) / U;
             __threadfence();
             __syncthreads();
             if (tid == 0) {
@@ -600,26 +629,40 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
                     float m = -INFINITY;
                     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     float lt = 0.0f;
-                    for (int64_t cc = c0; cc <= c1; ++cc) {
-                        // a CTA's second slot holds its last piece unless that is its first too
-                        const int64_t cta_u = cc * U / nact;
-                        const float* src = pl.part + (cc * 2 + (cta_u < group_u ? 1 : 0)) * (16 * ROWF) + row * ROWF;
-                        const float mc = __ldcg(src + D), lc = __ldcg(src + D + 1);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(src + col));
-                        const float m2 = fmaxf(m, mc), base = m2 == -INFINITY ? 0.0f : m2;
-                        const float f = exp2_approx(m - base), fc = exp2_approx(mc - base);
-                        lt = lt * f + lc * fc;
-                        acc.x = acc.x * f + v.x * fc;
-                        acc.y = acc.y * f + v.y * fc;
-                        acc.z = acc.z * f + v.z * fc;
-                        acc.w = acc.w * f + v.w * fc;
-                        m = m2;
+                    // The first CTA holds the group in its second slot unless the group begins with it; the others
+                    // begin inside the group: their first. Eight at a time, their loads in flight together.
+                    for (int64_t cb = c0; cb <= c1; cb += JOIN) {
+                        float mc[JOIN], lc[JOIN];
+                        float4 v[JOIN];
+#pragma unroll
+                        for (int k = 0; k < JOIN; ++k) {
+                            const int64_t cc = min(cb + k, c1);
+                            const int slot = cc == c0 && c0 * U / nact < done.group_u;
+                            const float* src = pl.part + (cc * 2 + slot) * (16 * ROWF) + row * ROWF;
+                            mc[k] = cb + k <= c1 ? __ldcg(src + D) : -INFINITY;
+                            lc[k] = __ldcg(src + D + 1);
+                            v[k] = __ldcg(reinterpret_cast<const float4*>(src + col));
+                        }
+#pragma unroll
+                        for (int k = 0; k < JOIN; ++k) {
+                            const float m2 = fmaxf(m, mc[k]), base = m2 == -INFINITY ? 0.0f : m2;
+                            if (cb + k > c1) continue;
+                            const float f = exp2_approx(m - base), fc = exp2_approx(mc[k] - base);
+                            lt = lt * f + lc[k] * fc;
+                            acc.x = acc.x * f + v[k].x * fc;
+                            acc.y = acc.y * f + v[k].y * fc;
+                            acc.z = acc.z * f + v[k].z * fc;
+                            acc.w = acc.w * f + v[k].w * fc;
+                            m = m2;
+                        }
                     }
-                    write_row<T, D>(a, gr.first, gr.h, G, RT * gr.i + row, col, acc, m, lt, OFF);
+                    write_row<T, D>(a, done.first, done.h, G, RT * done.i + row, col, acc, m, lt, OFF);
                 }
             }
         }
-        u = group_u + piece1;
+        if (!more) break;
+        // the merge region and the fragments are free once every warp is here
+        __syncthreads();
     }
 }
 
