@@ -40,8 +40,9 @@ constexpr int NW = 4;                     // warps a CTA
 constexpr int THREADS = NW * 32;
 constexpr int UNIT = 64;                  // keys of a work unit
 constexpr int MIN_UNITS = 2;              // a CTA is worth at least so many
+constexpr int SETUP = 3;                  // units that beginning and merging a group is worth
 constexpr int JOIN = 8;                   // partial results joined at a time
-constexpr int AHEAD = 4;                  // tiles that a warp has on their way into L2
+constexpr int AHEAD = 2;                  // tiles that a warp has on their way into L2
 constexpr int KNOWN = THREADS;            // requests whose lengths stay in shared memory
 constexpr float OFF = 7.0f, RAISE = 8.0f;
 // fp32: probabilities below this leave binary16's range before they have given
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
             int first, n, kv;
             request_of(c, a, r, first, n, kv);
             if (r < KNOWN) { known[r][0] = first; known[r][1] = n; known[r][2] = kv; }
-            if (rows_take(pl, n, G)) x = static_cast<int64_t>(request_units(a, n, kv)) * c.heads * ((static_cast<int64_t>(n) * G + RT - 1) / RT);
+            if (rows_take(pl, n, G)) x = static_cast<int64_t>(SETUP + request_units(a, n, kv)) * c.heads * ((static_cast<int64_t>(n) * G + RT - 1) / RT);
         }
         int64_t s = x;
 #pragma unroll
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
     __syncthreads();
     const int64_t U = carry;
     if (U == 0) return;
-    const int64_t nact = min(static_cast<int64_t>(gridDim.x), (U + MIN_UNITS - 1) / MIN_UNITS);
+    const int64_t nact = min(static_cast<int64_t>(gridDim.x), (U + SETUP + MIN_UNITS - 1) / (SETUP + MIN_UNITS));
     const int64_t me = blockIdx.x;
     if (me >= nact) return;
     int64_t u = me * U / nact;
@@ -198,13 +199,13 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
         request_range(a, pc.n, pc.kv, from, stop);
         const int u0 = (from / UNIT) * UNIT;
         pc.units = request_units(a, pc.n, pc.kv);
-        const int64_t in = u - cum[lo], gi = in / pc.units;
-        pc.piece0 = static_cast<int>(in - gi * pc.units);
+        const int64_t in = u - cum[lo], gi = in / (SETUP + pc.units);
+        pc.group_u = u - (in - gi * (SETUP + pc.units));
+        pc.piece0 = static_cast<int>(max(u - pc.group_u - SETUP, int64_t(0)));
         const int nrt = (pc.n * G + RT - 1) / RT;
         pc.h = static_cast<int>(gi / nrt);
         pc.i = static_cast<int>(gi - static_cast<int64_t>(pc.h) * nrt);
-        pc.group_u = u - pc.piece0;
-        pc.piece1 = static_cast<int>(min(static_cast<int64_t>(pc.units), u_end - pc.group_u));
+        pc.piece1 = static_cast<int>(min(static_cast<int64_t>(pc.units), u_end - pc.group_u - SETUP));
         pc.rows = min(RT, pc.n * G - RT * pc.i);
         // from the last row's first key to the first row's last
         int tfrom, tstop;
@@ -321,6 +322,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
         load_q(pc);
         turn ^= 1;
         if (tid == 0) pieces[turn] = pc;
+        return pc.piece1 > pc.piece0;
     };
     auto begin_tiles = [&]() {
         if (mine > 0) {
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
             next_scales();
         }
     };
-    begin(u);
+    if (!begin(u)) return;                                        // a part of one group's setup
     begin_tiles();
 
     for (;;) {
@@ -579,9 +581,9 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
             }
         const Piece& done = pieces[turn];
         const int rows = done.rows;
-        u = done.group_u + done.piece1;
-        const bool more = u < u_end;
-        if (more) begin(u);
+        u = done.group_u + SETUP + done.piece1;
+        const bool more = u + SETUP < u_end;                       // u begins a group, or u_end was in this one
+        if (more) (void)begin(u);
         __syncthreads();
         if (more) begin_tiles();
         const int used = min(NW, max(done.ntile, 1));                               // warps that had a tile (warp 0 always counts)
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
         }
         if (!whole) {
             // ---- the group's pieces lie with CTAs c0..c1; the last of them to arrive joins them
-            const int64_t c0 = ((done.group_u + 1) * nact - 1) / U, c1 = ((done.group_u + done.units) * nact - 1) / U;
+            const int64_t c0 = ((done.group_u + SETUP + 1) * nact - 1) / U, c1 = ((done.group_u + SETUP + done.units) * nact - 1) / U;
             __threadfence();
             __syncthreads();
             if (tid == 0) {
