@@ -16,10 +16,12 @@ constexpr int ATTN_MAX_CTAS = 640;
 struct RowsPlan {
     int* count;          // [ATTN_MAX_CTAS], zero between calls
     float* part;         // [ATTN_MAX_CTAS][2][16][head_dim + 4]
+    int tile_rows;       // a request with at least so many rows of a kv head is attn_tiles.cu's; INT_MAX: none is
 };
 
-// Requests that the row-tile kernel takes.
-__device__ __forceinline__ bool rows_take(const RowsPlan&, int n, int) { return n > 0; }
+// Requests that each kernel takes: n new tokens, G query heads a kv head.
+__device__ __forceinline__ bool tiles_take(const RowsPlan& pl, int n, int G) { return static_cast<int64_t>(n) * G >= pl.tile_rows; }
+__device__ __forceinline__ bool rows_take(const RowsPlan& pl, int n, int G) { return n > 0 && !tiles_take(pl, n, G); }
 
 // First token, new tokens (clipped to T) and length (clipped to the table) of request r.
 __device__ __forceinline__ void request_of(const KvView& c, const AttnArgs& a, int r, int& first, int& n, int& kv) {
@@ -55,6 +57,29 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// Two binary16 integers of at most 8 bits as bfloat16 (exact).
+__device__ __forceinline__ uint32_t half_to_bf16(uint32_t h) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+}
+
+// Four signed bytes as bfloat16 integers, in byte order: each flipped to 128 + b
+// under the exponent of 2^23, the offset taken away, the upper halves kept.
+__device__ __forceinline__ void s8x4_bf16(uint32_t w, uint32_t& o0, uint32_t& o1) {
+    const uint32_t u = w ^ 0x80808080u;
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + i)) - 8388736.0f;
+    o0 = __byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x7632);
+    o1 = __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x7632);
+}
+
 __device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
 __device__ __forceinline__ float2 load2(const __half* p) { return __half22float2(*reinterpret_cast<const __half2*>(p)); }
 __device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
@@ -88,6 +113,8 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int first, int h, i
         a.lse[tok * a.heads + head] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m - off + log2f(l));
 }
 
+cudaError_t launch_attn_tiles(const DeviceInfo& dev, const KvView& c, int dtype, const AttnArgs& a, const RowsPlan& pl,
+                              cudaStream_t s);
 cudaError_t launch_attn_rows(const DeviceInfo& dev, const KvView& c, int dtype, const AttnArgs& a, const RowsPlan& pl,
                              cudaStream_t s);
 

@@ -69,12 +69,6 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&x);
 }
 
-// Two binary16 integers of at most 8 bits as bfloat16 (exact).
-__device__ __forceinline__ uint32_t half_to_bf16(uint32_t h) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
-}
-
 // A CTA's part of one group: what its rows are and see, and the keys to read.
 struct Piece {
     int r, h, i;             // request, kv head, row tile

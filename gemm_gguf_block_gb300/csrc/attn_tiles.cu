@@ -1,0 +1,581 @@
+// Attention over the 8-bit paged cache for many query rows a (request, kv head):
+// prompts and chunks of them (cq_attn_paged in include/cq.h).
+//
+// The mathematics is attn_rows.cu's: x_j = log2(e) scale s_k (q . k_j) + log2(s_v),
+// P_j = 2^(x_j - M + OFF), out = sum P_j v_j / sum (P_j / s_v). Here the products
+// run on tcgen05 with the accumulators in tensor memory: a CTA takes 256 rows
+// (token, head of the kv head's group) as two tiles of 128 -- fp32: 128 rows --
+// against 128 keys at a time.
+//   S = Q K^T: both from shared memory, K-major, 128-byte swizzle; K the stored
+//     integers as binary16 (exact). fp32 queries are two binary16 parts, two MMAs.
+//   O += P V: P from tensor memory over its scores' columns, V from shared memory as
+//     it lies in the cache (keys as rows, MN-major). fp32: P is three bfloat16 parts
+//     (24 bits over fp32's whole range) beside the scores, and V bfloat16.
+// Warps: 0-7 softmax, a thread to a row (fp32: two threads, 64 keys each); 8-11
+// convert the cache's bytes to operands, two stages of keys and two of values;
+// 12 issues the MMAs. While one tile's softmax runs, the other tile's MMAs do.
+// A block of 16 keys carries (s_k, log2 s_v, 1 / s_v) in shared memory; a block
+// outside the cache or the request's keys is stored as zeros with log2 s_v = -inf.
+#include <algorithm>
+#include <type_traits>
+
+#include "attn_common.cuh"
+#include "cq_device.cuh"
+#include "cq_internal.h"
+#include "kv.cuh"
+#include "tc.cuh"
+
+namespace cq {
+namespace {
+
+constexpr int KEYS = 128;                 // keys of a step
+constexpr int SOFT = 256;                 // softmax threads
+constexpr int CONV = 128;                 // converter threads
+constexpr int THREADS = SOFT + CONV + 32;
+constexpr float OFF = 7.0f, RAISE = 8.0f;
+constexpr int INFO = 4;                   // steps whose scales are kept
+
+enum { B_Q = 0, B_K_FULL = 1, B_K_EMPTY = 3, B_V_FULL = 5, B_V_EMPTY = 7, B_S = 9, B_P = 11, B_O = 13, B_INFO = 15, B_X = 19 };
+
+template <typename T, int D> struct Tiles {
+    static constexpr bool F32 = std::is_same<T, float>::value;
+    static constexpr int MT = F32 ? 1 : 2;                 // row tiles
+    static constexpr int ROWS = 128 * MT;
+    static constexpr int QB = 128 * D * 2;                 // one query operand
+    static constexpr int KB = KEYS * D * 2;
+    static constexpr int OFF_Q = 1024;
+    static constexpr int OFF_K = OFF_Q + 2 * QB;
+    static constexpr int OFF_V = OFF_K + 2 * KB;
+    static constexpr int SMEM = OFF_V + 2 * KB + 1024;     // + alignment slack of the dynamic base
+    // tensor memory columns
+    static constexpr uint32_t S0 = 0;
+    static constexpr uint32_t SP = 128;                    // 16-bit types: the second tile's scores; fp32: P's parts, 64 columns each
+    static constexpr uint32_t O0 = F32 ? 320 : 256;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, const AttnArgs a, const RowsPlan pl) {
+    pdl_trigger();
+    pdl_wait();
+    using W = Tiles<T, D>;
+    constexpr bool F32 = W::F32;
+    constexpr int MT = W::MT, ROWS = W::ROWS;
+    extern __shared__ uint8_t tiles_smem[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tiles_smem) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
+    __shared__ uint32_t tmem_holder;
+    __shared__ int abort_word;
+    __shared__ int item[4];                                // request, its first token, new tokens, length
+    __shared__ int item_at;                                // index inside the request
+    __shared__ int scan[THREADS / 32];
+    __shared__ float4 info[INFO][KEYS / 16];
+    __shared__ float exch[F32 ? 2 : 1][F32 ? 128 : 1];
+    const SmemFlag abort_flag{smem_u32(&abort_word)};
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = a.heads / c.heads;
+
+    // ---- this CTA's item: requests in order; inside one the last rows (the longest) first, heads together
+    if (tid == 0) { item_at = -1; abort_word = 0; }
+    __syncthreads();
+    {
+        int64_t carry = 0;
+        for (int r0 = 0; r0 < a.R && carry <= blockIdx.x; r0 += THREADS) {
+            const int r = r0 + tid;
+            int first = 0, n = 0, kv = 0, x = 0;
+            if (r < a.R) {
+                request_of(c, a, r, first, n, kv);
+                if (tiles_take(pl, n, G)) x = static_cast<int>((static_cast<int64_t>(n) * G + ROWS - 1) / ROWS) * c.heads;
+            }
+            int s = x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += up;
+            }
+            if (lane == 31) scan[warp] = s;
+            __syncthreads();
+            int64_t before = carry, all = 0;
+            for (int w = 0; w < THREADS / 32; ++w) {
+                if (w < warp) before += scan[w];
+                all += scan[w];
+            }
+            const int64_t mine = static_cast<int64_t>(blockIdx.x) - (before + s - x);
+            if (mine >= 0 && mine < x) {
+                item[0] = r; item[1] = first; item[2] = n; item[3] = kv;
+                item_at = static_cast<int>(mine);
+            }
+            carry += all;
+            __syncthreads();
+        }
+    }
+    if (item_at < 0) return;
+    const int r = item[0], first = item[1], n = item[2], kv = item[3];
+    const int h = item_at % c.heads;
+    const int row0 = ((static_cast<int>((static_cast<int64_t>(n) * G + ROWS - 1) / ROWS)) - 1 - item_at / c.heads) * ROWS;
+    const int rows = min(ROWS, n * G - row0);
+    // keys that some row sees, and those that all rows see
+    int tfrom, tstop, all_from, all_stop;
+    row_range(a, n, kv, row0 / G, tfrom, all_stop);
+    row_range(a, n, kv, (row0 + rows - 1) / G, all_from, tstop);
+    const int key0 = (tfrom / KEYS) * KEYS;
+    const int steps = tstop > key0 ? (tstop - key0 + KEYS - 1) / KEYS : 0;
+
+    if (tid == 0) {
+        mbar_init(&bars[B_Q], SOFT);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars[B_K_FULL + i], CONV);
+            mbar_init(&bars[B_K_EMPTY + i], 1);
+            mbar_init(&bars[B_V_FULL + i], CONV);
+            mbar_init(&bars[B_V_EMPTY + i], 1);
+            mbar_init(&bars[B_S + i], 1);
+            mbar_init(&bars[B_P + i], F32 ? SOFT : SOFT / 2);
+            mbar_init(&bars[B_O + i], 1);
+        }
+        for (int i = 0; i < INFO; ++i) mbar_init(&bars[B_INFO + i], CONV / 32);
+        mbar_init(&bars[B_X], SOFT);
+        fence_mbar_init();
+    }
+    if (warp == THREADS / 32 - 1) {
+        tc::tmem_alloc(&tmem_holder, 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = tmem_holder;
+
+    if (warp < SOFT / 32) {
+        // ------------------------------------------------------------ softmax
+        const int wg = warp >> 2;                           // 16-bit types: the row tile; fp32: which 64 keys
+        const int lrow = (warp & 3) * 32 + lane;            // row of the tile, lane of tensor memory
+        const int row = (F32 ? 0 : 128 * wg) + lrow;        // of the item
+        const int rho = row0 + row;
+        const int64_t tok = first + rho / G;
+        const int head = h * G + rho % G;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        float rf = 0.0f;
+        {
+            // The row as operand: scaled to [2^8, 2^9) by a power of two. fp32: the first
+            // warpgroup writes the upper parts, the second the lower.
+            const T* src = static_cast<const T*>(a.q) + tok * a.q_stride + head * D;
+            uint32_t top = 0;
+            if (row < rows)
+#pragma unroll 4
+                for (int d = 0; d < D; d += 4) {
+                    const float4 v = load4(src + d);
+                    top = max(max(top, max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y)))),
+                              max(__float_as_uint(fabsf(v.z)), __float_as_uint(fabsf(v.w))));
+                }
+            float mul, back;
+            row_scale(top, mul, back);
+            if (a.scale < 0.0f) mul = -mul;
+            rf = back * fabsf(a.scale) * 1.4426950408889634f;
+            uint8_t* dst = smem + W::OFF_Q + wg * W::QB;
+#pragma unroll 4
+            for (int d = 0; d < D; d += 8) {
+                float4 v[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+                if (row < rows) { v[0] = load4(src + d); v[1] = load4(src + d + 4); }
+                uint32_t o[4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float x[4] = {v[i].x * mul, v[i].y * mul, v[i].z * mul, v[i].w * mul};
+                    __half2 h0 = __floats2half2_rn(x[0], x[1]), h1 = __floats2half2_rn(x[2], x[3]);
+                    if (F32 && wg == 1) {
+                        const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+                        h0 = __floats2half2_rn(x[0] - f0.x, x[1] - f0.y);
+                        h1 = __floats2half2_rn(x[2] - f1.x, x[3] - f1.y);
+                    }
+                    o[2 * i] = *reinterpret_cast<const uint32_t*>(&h0);
+                    o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                }
+                *reinterpret_cast<uint4*>(dst + tc::tile_off_sw128(lrow, d, 128)) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            fence_proxy_async_smem();
+            tc::mbar_arrive(&bars[B_Q]);
+        }
+        int from = 0, stop = 0;
+        if (row < rows) row_range(a, n, kv, rho / G, from, stop);
+        const int mt = F32 ? 0 : wg;
+        const uint32_t s_col = tmem + lanes + (F32 ? W::S0 + 64 * wg : mt == 0 ? W::S0 : W::SP);
+        const uint32_t p_col = F32 ? tmem + lanes + W::SP + 32 * wg : s_col;
+        const uint32_t o_col = tmem + lanes + W::O0 + mt * 128;
+        constexpr int CHUNKS = F32 ? 2 : 4;                 // of 32 keys
+        float M = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int j = 0; j < steps && ok; ++j) {
+            ok = mbar_wait_bounded(&bars[B_S + mt], j & 1, WAIT_LIMIT_NS) &&
+                 mbar_wait_bounded(&bars[B_INFO + j % INFO], (j / INFO) & 1, WAIT_LIMIT_NS);
+            ok = __all_sync(0xffffffffu, ok) && !abort_flag.get();
+            if (!ok) break;
+            tc::fence_after();
+            const float4* inf = info[j % INFO] + (F32 ? 4 * wg : 0);
+            const int k0 = key0 + j * KEYS + (F32 ? 64 * wg : 0);
+            const bool whole = k0 >= all_from && k0 + 32 * CHUNKS <= all_stop;
+            // the largest x: a block's from its largest score, since its factor is not negative
+            float top = -INFINITY;
+#pragma unroll
+            for (int ch = 0; ch < CHUNKS; ++ch) {
+                uint32_t sr[32];
+                tc::ld32(s_col + 32 * ch, sr);
+                tc::wait_ld();
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const float4 in = inf[2 * ch + b];
+                    const float f = in.x * rf;
+                    float m = -INFINITY;
+                    if (whole) {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) m = max3(m, __uint_as_float(sr[16 * b + i]), __uint_as_float(sr[16 * b + i + 1]));
+                        m = fmaf(m, f, in.y);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int key = k0 + 32 * ch + 16 * b + i;
+                            if (key >= from && key < stop) m = fmaxf(m, fmaf(__uint_as_float(sr[16 * b + i]), f, in.y));
+                        }
+                    }
+                    top = fmaxf(top, m);
+                }
+            }
+            if constexpr (F32) {
+                // the other half's; it has read this one's before the next scores come, which wait for its P
+                exch[wg][lrow] = top;
+                tc::mbar_arrive(&bars[B_X]);
+                ok = mbar_wait_bounded(&bars[B_X], j & 1, WAIT_LIMIT_NS);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                top = fmaxf(top, exch[wg ^ 1][lrow]);
+            }
+            const bool raise = top > M + RAISE;
+            bool o_known = false;
+            if (__any_sync(0xffffffffu, raise)) {
+                const float old = M;
+                if (raise) M = top;
+                const float f = raise ? exp2_approx(old - M) : 1.0f;             // 0 from -inf
+                l *= f;
+                if (j > 0) {
+                    ok = mbar_wait_bounded(&bars[B_O + mt], (j - 1) & 1, WAIT_LIMIT_NS);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    o_known = true;
+                    tc::fence_after();
+                    constexpr int OC = F32 ? D / 2 : D;                          // fp32: half of the columns each
+#pragma unroll
+                    for (int ch = 0; ch < OC / 16; ++ch) {
+                        uint32_t orr[16];
+                        const uint32_t at = o_col + (F32 ? wg * OC : 0) + 16 * ch;
+                        tc::ld16(at, orr);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) orr[i] = __float_as_uint(__uint_as_float(orr[i]) * f);
+                        tc::st16(at, orr);
+                    }
+                    tc::wait_st();
+                }
+            }
+            if constexpr (F32) {
+                // P has columns of its own: the product of the step before has to be done with them
+                if (j > 0 && !o_known) {
+                    ok = mbar_wait_bounded(&bars[B_O], (j - 1) & 1, WAIT_LIMIT_NS);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc::fence_after();
+                }
+            }
+            const float base = M == -INFINITY ? 0.0f : M - OFF;
+#pragma unroll
+            for (int ch = 0; ch < CHUNKS; ++ch) {
+                uint32_t sr[32];
+                tc::ld32(s_col + 32 * ch, sr);
+                tc::wait_ld();
+                float p[32];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const float4 in = inf[2 * ch + b];
+                    const float f = in.x * rf, lb = in.y - base;
+                    uint64_t sum2 = 0;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const uint64_t x2 = tc::fma2(tc::pk(__uint_as_float(sr[16 * b + i]), __uint_as_float(sr[16 * b + i + 1])),
+                                                     tc::pk(f, f), tc::pk(lb, lb));
+                        float x0, x1;
+                        tc::upk(x2, x0, x1);
+                        if (!whole) {
+                            const int key = k0 + 32 * ch + 16 * b + i;
+                            if (key < from || key >= stop) x0 = -INFINITY;
+                            if (key + 1 < from || key + 1 >= stop) x1 = -INFINITY;
+                        }
+                        p[16 * b + i] = exp2_approx(x0);
+                        p[16 * b + i + 1] = exp2_approx(x1);
+                        sum2 = tc::add2(sum2, tc::pk(p[16 * b + i], p[16 * b + i + 1]));
+                    }
+                    float s0, s1;
+                    tc::upk(sum2, s0, s1);
+                    const float sum = s0 + s1;
+                    // a row that sees nothing here must not meet a scale that is not finite
+                    l += sum != 0.0f ? sum * in.z : 0.0f;
+                }
+                uint32_t pr[16];
+                if constexpr (F32) {
+#pragma unroll
+                    for (int part = 0; part < 3; ++part) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const __nv_bfloat162 x = __floats2bfloat162_rn(p[2 * i], p[2 * i + 1]);
+                            pr[i] = *reinterpret_cast<const uint32_t*>(&x);
+                            p[2 * i] -= __uint_as_float(pr[i] << 16);
+                            p[2 * i + 1] -= __uint_as_float(pr[i] & 0xffff0000u);
+                        }
+                        tc::st16(p_col + 64 * part + 16 * ch, pr);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const __half2 x = __floats2half2_rn(p[2 * i], p[2 * i + 1]);
+                        pr[i] = *reinterpret_cast<const uint32_t*>(&x);
+                    }
+                    tc::st16(p_col + 16 * ch, pr);
+                }
+            }
+            tc::wait_st();
+            tc::fence_before();
+            tc::mbar_arrive(&bars[B_P + mt]);
+        }
+        // ---- the rows
+        if (ok && steps > 0) {
+            ok = mbar_wait_bounded(&bars[B_O + mt], (steps - 1) & 1, WAIT_LIMIT_NS);
+            ok = __all_sync(0xffffffffu, ok);
+            tc::fence_after();
+        }
+        if constexpr (F32) {
+            if (ok) {
+                exch[wg][lrow] = l;
+                tc::mbar_arrive(&bars[B_X]);
+                ok = mbar_wait_bounded(&bars[B_X], steps & 1, WAIT_LIMIT_NS);
+                ok = __all_sync(0xffffffffu, ok);
+                l = exch[0][lrow] + exch[1][lrow];
+            }
+        }
+        if (ok) {
+            constexpr int OC = F32 ? D / 2 : D;
+#pragma unroll
+            for (int ch = 0; ch < OC / 16; ++ch) {
+                uint32_t orr[16];
+                const int col = (F32 ? wg * OC : 0) + 16 * ch;
+                if (steps > 0) {
+                    tc::ld16(o_col + col, orr);
+                    tc::wait_ld();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) orr[i] = 0;
+                }
+                if (row < rows)
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        write_row<T, D>(a, first, h, G, rho, col + i,
+                                        make_float4(__uint_as_float(orr[i]), __uint_as_float(orr[i + 1]),
+                                                    __uint_as_float(orr[i + 2]), __uint_as_float(orr[i + 3])),
+                                        M, l, OFF);
+            }
+        } else if (lane == 0) {
+            abort_flag.set(1);
+            atomicOr(a.status, CQ_DEV_WAIT_TIMEOUT);
+        }
+    } else if (warp < (SOFT + CONV) / 32) {
+        // ---------------------------------------------------------- converters
+        // A lane takes 16 dimensions of a key: lanes 0-7 eight keys (the eight chunk
+        // positions of the swizzle), lanes / 8 the piece of 16 dimensions.
+        const int cw = warp - SOFT / 32;
+        const int ck = lane & 7, piece = lane >> 3;         // + 4 for the second half of D = 128
+        constexpr int NL = D / 64;                          // loads a lane and 8 keys
+        constexpr int GROUPS = KEYS / 8 / 4;                // groups of 8 keys of a warp: 4, keys 32 cw ..
+        const int32_t* table = a.table + static_cast<int64_t>(r) * a.max_blocks;
+        const int64_t head_off = static_cast<int64_t>(h) * c.page_size * D;
+        // The warp's two blocks of 16 keys of step j: lanes 0 and 1 look them up.
+        int page = -1;
+        float p_ks = 0.0f, p_vs = 0.0f;
+        auto look = [&](int j) {
+            const int k = key0 + j * KEYS + 32 * cw + 16 * lane;
+            page = -1;
+            if (lane < 2 && j < steps && k < tstop) {
+                page = table[k >> c.page_shift];
+                if (page >= 0 && page < c.num_pages) {
+                    p_ks = c.k_scale[page * c.scale_stride + h];
+                    p_vs = c.v_scale[page * c.scale_stride + h];
+                } else {
+                    page = -1;
+                    atomicOr(a.status, CQ_DEV_KV_PAGE);
+                }
+            }
+        };
+        uint4 kr[GROUPS][NL], vr[GROUPS][NL];
+        auto load = [&](const int8_t* src, uint4 (&x)[GROUPS][NL], int j, const int64_t (&at)[2]) {
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+                for (int i = 0; i < NL; ++i) {
+                    x[g][i] = make_uint4(0, 0, 0, 0);
+                    if (at[g >> 1] >= 0)
+                        x[g][i] = *reinterpret_cast<const uint4*>(src + at[g >> 1] + (8 * (g & 1) + ck) * D + 16 * (piece + 4 * i));
+                }
+        };
+        auto store = [&](uint8_t* dst, const uint4 (&x)[GROUPS][NL], bool bf) {
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+                for (int i = 0; i < NL; ++i) {
+                    const int key = 32 * cw + 8 * g + ck, d = 16 * (piece + 4 * i);
+                    const uint32_t w[4] = {x[g][i].x, x[g][i].y, x[g][i].z, x[g][i].w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (bf) s8x4_bf16(w[k], o[2 * k], o[2 * k + 1]);
+                        else tc::s8x4_half(w[k], o[2 * k], o[2 * k + 1]);
+                    }
+                    *reinterpret_cast<uint4*>(dst + tc::tile_off_sw128(key, d, KEYS)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(dst + tc::tile_off_sw128(key, d + 8, KEYS)) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+        };
+        look(0);
+        for (int j = 0; j < steps; ++j) {
+            int64_t at[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int pg = __shfl_sync(0xffffffffu, page, b);
+                const int k = key0 + j * KEYS + 32 * cw + 16 * b;
+                at[b] = pg >= 0 ? pg * c.page_stride + head_off + static_cast<int64_t>(k & (c.page_size - 1)) * D : -1;
+            }
+            load(c.k, kr, j, at);
+            load(c.v, vr, j, at);
+            float4 in = make_float4(0.0f, -INFINITY, 1.0f, 0.0f);
+            if (page >= 0) {
+                in.x = p_ks;
+                in.y = p_vs == 0.0f ? 0.0f : log2f(p_vs);
+                in.z = p_vs == 0.0f ? 1.0f : __frcp_rn(p_vs);
+            }
+            look(j + 1);
+            const int st = j & 1;
+            if (__any_sync(0xffffffffu, abort_flag.get())) break;
+            // (the whole warp leaves or none of it: it shuffles)
+            if (!__all_sync(0xffffffffu, tc::wait_or_abort_sleep(&bars[B_K_EMPTY + st], ((j >> 1) & 1) ^ 1, abort_flag, a.status))) break;
+            // the step that used this entry before is past its softmax: the scores of two steps ago were its next
+            if (lane < 2) info[j % INFO][2 * cw + lane] = in;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bars[B_INFO + j % INFO]);
+            store(smem + W::OFF_K + st * W::KB, kr, false);
+            fence_proxy_async_smem();
+            tc::mbar_arrive(&bars[B_K_FULL + st]);
+            if (!__all_sync(0xffffffffu, tc::wait_or_abort_sleep(&bars[B_V_EMPTY + st], ((j >> 1) & 1) ^ 1, abort_flag, a.status))) break;
+            store(smem + W::OFF_V + st * W::KB, vr, F32);
+            fence_proxy_async_smem();
+            tc::mbar_arrive(&bars[B_V_FULL + st]);
+        }
+    } else if (lane == 0 && steps > 0) {
+        // --------------------------------------------------------- MMA issuer
+        const uint32_t q0 = smem_u32(smem + W::OFF_Q), k0 = smem_u32(smem + W::OFF_K), v0 = smem_u32(smem + W::OFF_V);
+        constexpr uint32_t ID_S = tc::idesc_f16_f32(128, KEYS);
+        constexpr uint32_t ID_O = tc::idesc_f16_f32(128, D) | tc::IDESC_B_MN | (F32 ? tc::IDESC_BF16 : 0u);
+        // A k-step of 16 values adds 32 bytes inside a 128-byte row; 64 values on is the next block of rows.
+        auto scores = [&](int m, int st) {
+#pragma unroll
+            for (int part = 0; part < (F32 ? 2 : 1); ++part)
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32;
+                    tc::mma_f16(tmem + (m == 0 ? W::S0 : W::SP), tc::smem_desc_sw128(q0 + (F32 ? part : m) * W::QB + off, 1024),
+                                tc::smem_desc_sw128(k0 + st * W::KB + off, 1024), ID_S, part > 0 || k > 0);
+                }
+        };
+        auto product = [&](int m, int st, bool add) {
+#pragma unroll
+            for (int part = 0; part < (F32 ? 3 : 1); ++part)
+#pragma unroll
+                for (int k = 0; k < KEYS / 16; ++k)
+                    tc::mma_f16_ts(tmem + W::O0 + m * 128,
+                                   tmem + (F32 ? W::SP + 64 * part : m == 0 ? W::S0 : W::SP) + 8 * k,
+                                   tc::smem_desc_sw128_mn(v0 + st * W::KB + k * 2048, KEYS * 128, 1024), ID_O,
+                                   add || part > 0 || k > 0);
+        };
+        auto wait = [&](int bar, int parity) {
+            if (!tc::wait_or_abort(&bars[bar], parity, abort_flag, a.status)) return false;
+            tc::fence_after();
+            return true;
+        };
+        bool ok = wait(B_Q, 0) && wait(B_K_FULL, 0);
+        if (ok) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                scores(m, 0);
+                tc::commit(&bars[B_S + m]);
+            }
+            tc::commit(&bars[B_K_EMPTY]);
+        }
+        for (int j = 0; j < steps && ok && !abort_flag.get(); ++j) {
+            const int st = j & 1, nst = st ^ 1;
+            const bool next = j + 1 < steps;
+#pragma unroll
+            for (int m = 0; m < MT && ok; ++m) {
+                ok = wait(B_P + m, j & 1);
+                if (!ok) break;
+                if (F32 && next) {
+                    // the scores' columns are free, P has its own: the next scores first
+                    ok = wait(B_K_FULL + nst, ((j + 1) >> 1) & 1);
+                    if (!ok) break;
+                    scores(0, nst);
+                    tc::commit(&bars[B_S]);
+                    tc::commit(&bars[B_K_EMPTY + nst]);
+                }
+                if (m == 0) ok = wait(B_V_FULL + st, (j >> 1) & 1);
+                if (!ok) break;
+                product(m, st, j > 0);
+                tc::commit(&bars[B_O + m]);
+                if (m == MT - 1) tc::commit(&bars[B_V_EMPTY + st]);
+                if (!F32 && next) {
+                    // P's columns are the scores': the MMAs run in the order they were issued in
+                    if (m == 0) ok = wait(B_K_FULL + nst, ((j + 1) >> 1) & 1);
+                    if (!ok) break;
+                    scores(m, nst);
+                    tc::commit(&bars[B_S + m]);
+                    if (m == MT - 1) tc::commit(&bars[B_K_EMPTY + nst]);
+                }
+            }
+        }
+    }
+    // ---- every role has left its loop; no MMA is in flight before the tensor memory goes
+    tc::fence_before();
+    __syncthreads();
+    if (abort_flag.get() && tid == 0)
+        for (int i = 0; i < MT; ++i) (void)mbar_wait_bounded(&bars[B_O + i], 0, WAIT_LIMIT_NS / 8);
+    __syncthreads();
+    tc::fence_after();
+    if (warp == THREADS / 32 - 1) tc::tmem_dealloc(tmem, 512);
+}
+
+template <typename T, int D>
+cudaError_t launch_tiles_t(const DeviceInfo& dev, const KvView& c, const AttnArgs& a, const RowsPlan& pl, cudaStream_t s) {
+    using W = Tiles<T, D>;
+    if (W::SMEM > dev.smem_optin) return cudaErrorInvalidConfiguration;
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_tiles_kernel<T, D>), W::SMEM);
+    if (e != cudaSuccess) return e;
+    const int64_t G = a.heads / c.heads;
+    // Each request that this kernel takes has at most one part-filled item more than its rows make
+    const int64_t items = (a.T * G / W::ROWS + std::min<int64_t>(a.R, a.T * G / pl.tile_rows + 1)) * c.heads;
+    if (items > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    return launch_kernel(attn_tiles_kernel<T, D>, dim3(static_cast<unsigned>(items)), dim3(THREADS), W::SMEM, s, c, a, pl);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tiles(const DeviceInfo& dev, const KvView& c, int dtype, const AttnArgs& a, const RowsPlan& pl,
+                              cudaStream_t s) {
+    const bool d64 = c.dim == 64;
+    switch (dtype) {
+    case CQ_F32: return d64 ? launch_tiles_t<float, 64>(dev, c, a, pl, s) : launch_tiles_t<float, 128>(dev, c, a, pl, s);
+    case CQ_F16: return d64 ? launch_tiles_t<__half, 64>(dev, c, a, pl, s) : launch_tiles_t<__half, 128>(dev, c, a, pl, s);
+    case CQ_BF16:
+        return d64 ? launch_tiles_t<__nv_bfloat16, 64>(dev, c, a, pl, s) : launch_tiles_t<__nv_bfloat16, 128>(dev, c, a, pl, s);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace cq
