@@ -213,30 +213,38 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             const bool whole = k0 >= all_from && k0 + 32 * CHUNKS <= all_stop;
             // the largest x: a block's from its largest score, since its factor is not negative
             float top = -INFINITY;
+            auto largest = [&](auto whole_) {
+                constexpr bool WHOLE = decltype(whole_)::value;
+                uint32_t sr[2][32];
+                tc::ld32(s_col, sr[0]);
 #pragma unroll
-            for (int ch = 0; ch < CHUNKS; ++ch) {
-                uint32_t sr[32];
-                tc::ld32(s_col + 32 * ch, sr);
-                tc::wait_ld();
+                for (int ch = 0; ch < CHUNKS; ++ch) {
+                    tc::wait_ld();
+                    if (ch + 1 < CHUNKS) tc::ld32(s_col + 32 * (ch + 1), sr[(ch + 1) & 1]);
+                    const uint32_t (&v)[32] = sr[ch & 1];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const float4 in = inf[2 * ch + b];
-                    const float f = in.x * rf;
-                    float m = -INFINITY;
-                    if (whole) {
+                    for (int b = 0; b < 2; ++b) {
+                        const float4 in = inf[2 * ch + b];
+                        const float f = in.x * rf;
+                        float m = -INFINITY;
+                        if constexpr (WHOLE) {
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) m = max3(m, __uint_as_float(sr[16 * b + i]), __uint_as_float(sr[16 * b + i + 1]));
-                        m = fmaf(m, f, in.y);
-                    } else {
+                            for (int i = 0; i < 16; i += 2) m = max3(m, __uint_as_float(v[16 * b + i]), __uint_as_float(v[16 * b + i + 1]));
+                            m = fmaf(m, f, in.y);
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int key = k0 + 32 * ch + 16 * b + i;
-                            if (key >= from && key < stop) m = fmaxf(m, fmaf(__uint_as_float(sr[16 * b + i]), f, in.y));
+                            for (int i = 0; i < 16; ++i) {
+                                const int key = k0 + 32 * ch + 16 * b + i;
+                                const float x = fmaf(__uint_as_float(v[16 * b + i]), f, in.y);
+                                m = fmaxf(m, key >= from && key < stop ? x : -INFINITY);
+                            }
                         }
+                        top = fmaxf(top, m);
                     }
-                    top = fmaxf(top, m);
                 }
-            }
+            };
+            if (whole) largest(std::true_type{});
+            else largest(std::false_type{});
             if constexpr (F32) {
                 // the other half's; it has read this one's before the next scores come, which wait for its P
                 exch[wg][lrow] = top;
@@ -283,60 +291,69 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                 }
             }
             const float base = M == -INFINITY ? 0.0f : M - OFF;
+            auto probabilities = [&](auto whole_) {
+                constexpr bool WHOLE = decltype(whole_)::value;
+                uint32_t sr[2][32];
+                tc::ld32(s_col, sr[0]);
 #pragma unroll
-            for (int ch = 0; ch < CHUNKS; ++ch) {
-                uint32_t sr[32];
-                tc::ld32(s_col + 32 * ch, sr);
-                tc::wait_ld();
-                float p[32];
+                for (int ch = 0; ch < CHUNKS; ++ch) {
+                    tc::wait_ld();
+                    // (P's columns overlay scores that are in registers by then)
+                    if (ch + 1 < CHUNKS) tc::ld32(s_col + 32 * (ch + 1), sr[(ch + 1) & 1]);
+                    uint32_t (&v)[32] = sr[ch & 1];
+                    uint32_t pr[16];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const float4 in = inf[2 * ch + b];
-                    const float f = in.x * rf, lb = in.y - base;
-                    uint64_t sum2 = 0;
+                    for (int b = 0; b < 2; ++b) {
+                        const float4 in = inf[2 * ch + b];
+                        const float f = in.x * rf, lb = in.y - base;
+                        const uint64_t f2 = tc::pk(f, f), lb2 = tc::pk(lb, lb);
+                        uint64_t sum2 = 0;
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const uint64_t x2 = tc::fma2(tc::pk(__uint_as_float(sr[16 * b + i]), __uint_as_float(sr[16 * b + i + 1])),
-                                                     tc::pk(f, f), tc::pk(lb, lb));
-                        float x0, x1;
-                        tc::upk(x2, x0, x1);
-                        if (!whole) {
-                            const int key = k0 + 32 * ch + 16 * b + i;
-                            if (key < from || key >= stop) x0 = -INFINITY;
-                            if (key + 1 < from || key + 1 >= stop) x1 = -INFINITY;
+                        for (int i = 0; i < 16; i += 2) {
+                            const uint64_t x2 = tc::fma2(tc::pk(__uint_as_float(v[16 * b + i]), __uint_as_float(v[16 * b + i + 1])), f2, lb2);
+                            float x0, x1;
+                            tc::upk(x2, x0, x1);
+                            if constexpr (!WHOLE) {
+                                const int key = k0 + 32 * ch + 16 * b + i;
+                                x0 = key >= from && key < stop ? x0 : -INFINITY;
+                                x1 = key + 1 >= from && key + 1 < stop ? x1 : -INFINITY;
+                            }
+                            const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
+                            sum2 = tc::add2(sum2, tc::pk(p0, p1));
+                            if constexpr (F32) {
+                                v[16 * b + i] = __float_as_uint(p0);
+                                v[16 * b + i + 1] = __float_as_uint(p1);
+                            } else {
+                                const __half2 x = __floats2half2_rn(p0, p1);
+                                pr[8 * b + i / 2] = *reinterpret_cast<const uint32_t*>(&x);
+                            }
                         }
-                        p[16 * b + i] = exp2_approx(x0);
-                        p[16 * b + i + 1] = exp2_approx(x1);
-                        sum2 = tc::add2(sum2, tc::pk(p[16 * b + i], p[16 * b + i + 1]));
+                        float s0, s1;
+                        tc::upk(sum2, s0, s1);
+                        const float sum = s0 + s1;
+                        // a row that sees nothing here must not meet a scale that is not finite
+                        l += sum != 0.0f ? sum * in.z : 0.0f;
                     }
-                    float s0, s1;
-                    tc::upk(sum2, s0, s1);
-                    const float sum = s0 + s1;
-                    // a row that sees nothing here must not meet a scale that is not finite
-                    l += sum != 0.0f ? sum * in.z : 0.0f;
-                }
-                uint32_t pr[16];
-                if constexpr (F32) {
+                    if constexpr (F32) {
 #pragma unroll
-                    for (int part = 0; part < 3; ++part) {
+                        for (int part = 0; part < 3; ++part) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const __nv_bfloat162 x = __floats2bfloat162_rn(p[2 * i], p[2 * i + 1]);
-                            pr[i] = *reinterpret_cast<const uint32_t*>(&x);
-                            p[2 * i] -= __uint_as_float(pr[i] << 16);
-                            p[2 * i + 1] -= __uint_as_float(pr[i] & 0xffff0000u);
+                            for (int i = 0; i < 16; ++i) {
+                                const float p0 = __uint_as_float(v[2 * i]), p1 = __uint_as_float(v[2 * i + 1]);
+                                const __nv_bfloat162 x = __floats2bfloat162_rn(p0, p1);
+                                pr[i] = *reinterpret_cast<const uint32_t*>(&x);
+                                v[2 * i] = __float_as_uint(p0 - __uint_as_float(pr[i] << 16));
+                                v[2 * i + 1] = __float_as_uint(p1 - __uint_as_float(pr[i] & 0xffff0000u));
+                            }
+                            tc::st16(p_col + 64 * part + 16 * ch, pr);
                         }
-                        tc::st16(p_col + 64 * part + 16 * ch, pr);
+                    } else {
+                        tc::st16(p_col + 16 * ch, pr);
                     }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const __half2 x = __floats2half2_rn(p[2 * i], p[2 * i + 1]);
-                        pr[i] = *reinterpret_cast<const uint32_t*>(&x);
-                    }
-                    tc::st16(p_col + 16 * ch, pr);
                 }
-            }
+            };
+            if (whole) probabilities(std::true_type{});
+            else probabilities(std::false_type{});
             tc::wait_st();
             tc::fence_before();
             tc::mbar_arrive(&bars[B_P + mt]);
