@@ -17,6 +17,7 @@
 // A block of 16 keys carries (s_k, log2 s_v, 1 / s_v) in shared memory; a block
 // outside the cache or the request's keys is stored as zeros with log2 s_v = -inf.
 #include <algorithm>
+#include <climits>
 #include <type_traits>
 
 #include "attn_common.cuh"
@@ -408,32 +409,42 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         constexpr int GROUPS = KEYS / 8 / 4;                // groups of 8 keys of a warp: 4, keys 32 cw ..
         const int32_t* table = a.table + static_cast<int64_t>(r) * a.max_blocks;
         const int64_t head_off = static_cast<int64_t>(h) * c.page_size * D;
-        // The warp's two blocks of 16 keys of step j: lanes 0 and 1 look them up.
-        int page = -1;
-        float p_ks = 0.0f, p_vs = 0.0f;
-        auto look = [&](int j) {
+        // The warp's two blocks of 16 keys of a step: lanes 0 and 1 look them up. A step's
+        // table entries are fetched two steps ahead, its scales and bytes one: no lookup
+        // is waited for in the loop, and a step's loads run behind the one before's stores.
+        auto entry = [&](int j) {
             const int k = key0 + j * KEYS + 32 * cw + 16 * lane;
-            page = -1;
-            if (lane < 2 && j < steps && k < tstop) {
-                page = table[k >> c.page_shift];
-                if (page >= 0 && page < c.num_pages) {
-                    p_ks = c.k_scale[page * c.scale_stride + h];
-                    p_vs = c.v_scale[page * c.scale_stride + h];
-                } else {
-                    page = -1;
-                    atomicOr(a.status, CQ_DEV_KV_PAGE);
-                }
+            return lane < 2 && j < steps && k < tstop ? table[k >> c.page_shift] : INT_MIN;     // INT_MIN: no keys
+        };
+        auto checked = [&](int e) {
+            if (e >= 0 && e < c.num_pages) return e;
+            if (e != INT_MIN) atomicOr(a.status, CQ_DEV_KV_PAGE);
+            return -1;
+        };
+        int64_t at[2];
+        auto place = [&](int page, int j) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int pg = __shfl_sync(0xffffffffu, page, b);
+                const int k = key0 + j * KEYS + 32 * cw + 16 * b;
+                at[b] = pg >= 0 ? pg * c.page_stride + head_off + static_cast<int64_t>(k & (c.page_size - 1)) * D : -1;
             }
         };
+        float p_ks = 0.0f, p_vs = 0.0f;
+        auto scales = [&](int page) {
+            if (page < 0) return;
+            p_ks = c.k_scale[page * c.scale_stride + h];
+            p_vs = c.v_scale[page * c.scale_stride + h];
+        };
         uint4 kr[GROUPS][NL], vr[GROUPS][NL];
-        auto load = [&](const int8_t* src, uint4 (&x)[GROUPS][NL], int j, const int64_t (&at)[2]) {
+        auto load = [&](const int8_t* src, uint4 (&x)[GROUPS][NL]) {
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
                 for (int i = 0; i < NL; ++i) {
                     x[g][i] = make_uint4(0, 0, 0, 0);
                     if (at[g >> 1] >= 0)
-                        x[g][i] = *reinterpret_cast<const uint4*>(src + at[g >> 1] + (8 * (g & 1) + ck) * D + 16 * (piece + 4 * i));
+                        x[g][i] = ldg_stream16(src + at[g >> 1] + (8 * (g & 1) + ck) * D + 16 * (piece + 4 * i));
                 }
         };
         auto store = [&](uint8_t* dst, const uint4 (&x)[GROUPS][NL], bool bf) {
@@ -453,24 +464,22 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                     *reinterpret_cast<uint4*>(dst + tc::tile_off_sw128(key, d + 8, KEYS)) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
         };
-        look(0);
+        int page = checked(entry(0)), ahead = entry(1);
+        scales(page);
+        place(page, 0);
+        load(c.k, kr);
+        load(c.v, vr);
         for (int j = 0; j < steps; ++j) {
-            int64_t at[2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int pg = __shfl_sync(0xffffffffu, page, b);
-                const int k = key0 + j * KEYS + 32 * cw + 16 * b;
-                at[b] = pg >= 0 ? pg * c.page_stride + head_off + static_cast<int64_t>(k & (c.page_size - 1)) * D : -1;
-            }
-            load(c.k, kr, j, at);
-            load(c.v, vr, j, at);
             float4 in = make_float4(0.0f, -INFINITY, 1.0f, 0.0f);
             if (page >= 0) {
                 in.x = p_ks;
                 in.y = p_vs == 0.0f ? 0.0f : log2f(p_vs);
                 in.z = p_vs == 0.0f ? 1.0f : __frcp_rn(p_vs);
             }
-            look(j + 1);
+            page = checked(ahead);
+            ahead = entry(j + 2);
+            scales(page);
+            place(page, j + 1);
             const int st = j & 1;
             if (__any_sync(0xffffffffu, abort_flag.get())) break;
             // (the whole warp leaves or none of it: it shuffles)
@@ -480,10 +489,12 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars[B_INFO + j % INFO]);
             store(smem + W::OFF_K + st * W::KB, kr, false);
+            load(c.k, kr);
             fence_proxy_async_smem();
             tc::mbar_arrive(&bars[B_K_FULL + st]);
             if (!__all_sync(0xffffffffu, tc::wait_or_abort_sleep(&bars[B_V_EMPTY + st], ((j >> 1) & 1) ^ 1, abort_flag, a.status))) break;
             store(smem + W::OFF_V + st * W::KB, vr, F32);
+            load(c.v, vr);
             fence_proxy_async_smem();
             tc::mbar_arrive(&bars[B_V_FULL + st]);
         }
