@@ -87,6 +87,26 @@ __device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
+// Eight consecutive values, 16-byte aligned (fp32: 32 bytes of them).
+__device__ __forceinline__ void load8(const float* p, float4& a, float4& b) {
+    a = load4(p);
+    b = load4(p + 4);
+}
+__device__ __forceinline__ void load8(const __half* p, float4& a, float4& b) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const float2 f[4] = {__half22float2(*reinterpret_cast<const __half2*>(&u.x)), __half22float2(*reinterpret_cast<const __half2*>(&u.y)),
+                         __half22float2(*reinterpret_cast<const __half2*>(&u.z)), __half22float2(*reinterpret_cast<const __half2*>(&u.w))};
+    a = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    b = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float4& a, float4& b) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    a = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                    __uint_as_float(u.y & 0xffff0000u));
+    b = make_float4(__uint_as_float(u.z << 16), __uint_as_float(u.z & 0xffff0000u), __uint_as_float(u.w << 16),
+                    __uint_as_float(u.w & 0xffff0000u));
+}
+
 // Cache rows are read once: past L1.
 __device__ __forceinline__ uint4 ldg_stream16(const void* p) {
     uint4 v;

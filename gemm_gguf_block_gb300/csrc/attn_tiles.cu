@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
     __shared__ int item_at;                                // index inside the request
     __shared__ int scan[THREADS / 32];
     __shared__ float4 info[INFO][KEYS / 16];
+    __shared__ float rowf[ROWS];                           // the rows' factors
     __shared__ float exch[F32 ? 2 : 1][F32 ? 128 : 1];
     const SmemFlag abort_flag{smem_u32(&abort_word)};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -154,46 +155,56 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         const int64_t tok = first + rho / G;
         const int head = h * G + rho % G;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        float rf = 0.0f;
         {
-            // The row as operand: scaled to [2^8, 2^9) by a power of two. fp32: the first
-            // warpgroup writes the upper parts, the second the lower.
-            const T* src = static_cast<const T*>(a.q) + tok * a.q_stride + head * D;
-            uint32_t top = 0;
-            if (row < rows)
-#pragma unroll 4
-                for (int d = 0; d < D; d += 4) {
-                    const float4 v = load4(src + d);
-                    top = max(max(top, max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y)))),
-                              max(__float_as_uint(fabsf(v.z)), __float_as_uint(fabsf(v.w))));
-                }
-            float mul, back;
-            row_scale(top, mul, back);
-            if (a.scale < 0.0f) mul = -mul;
-            rf = back * fabsf(a.scale) * 1.4426950408889634f;
-            uint8_t* dst = smem + W::OFF_Q + wg * W::QB;
-#pragma unroll 4
-            for (int d = 0; d < D; d += 8) {
-                float4 v[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-                if (row < rows) { v[0] = load4(src + d); v[1] = load4(src + d + 4); }
-                uint32_t o[4];
+            // The rows as operand, each scaled to [2^8, 2^9) by a power of two: 8 values a
+            // lane, so a row's chunks go to one 128-byte row of the tile side by side.
+            constexpr int LR = D / 8, RW = 32 / LR, PASS = ROWS / (SOFT / 32) / RW;    // lanes a row, rows a load, loads
+            constexpr int BATCH = 4;
+            const int w0 = warp * (ROWS / (SOFT / 32)) + lane / LR, d = (lane % LR) * 8;
+            for (int b0 = 0; b0 < PASS; b0 += BATCH) {
+                float4 v[BATCH][2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float x[4] = {v[i].x * mul, v[i].y * mul, v[i].z * mul, v[i].w * mul};
-                    __half2 h0 = __floats2half2_rn(x[0], x[1]), h1 = __floats2half2_rn(x[2], x[3]);
-                    if (F32 && wg == 1) {
-                        const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-                        h0 = __floats2half2_rn(x[0] - f0.x, x[1] - f0.y);
-                        h1 = __floats2half2_rn(x[2] - f1.x, x[3] - f1.y);
-                    }
-                    o[2 * i] = *reinterpret_cast<const uint32_t*>(&h0);
-                    o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                for (int b = 0; b < BATCH; ++b) {
+                    const int rr = w0 + (b0 + b) * RW, rh = row0 + rr;
+                    const T* src = static_cast<const T*>(a.q) + static_cast<int64_t>(first + rh / G) * a.q_stride + (h * G + rh % G) * D + d;
+                    v[b][0] = v[b][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (rr < rows) load8(src, v[b][0], v[b][1]);
                 }
-                *reinterpret_cast<uint4*>(dst + tc::tile_off_sw128(lrow, d, 128)) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+                for (int b = 0; b < BATCH; ++b) {
+                    const int rr = w0 + (b0 + b) * RW;
+                    const float x[8] = {v[b][0].x, v[b][0].y, v[b][0].z, v[b][0].w, v[b][1].x, v[b][1].y, v[b][1].z, v[b][1].w};
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(fabsf(x[i])));
+#pragma unroll
+                    for (int o = LR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    float mul, back;
+                    row_scale(top, mul, back);
+                    if (a.scale < 0.0f) mul = -mul;
+                    if (d == 0) rowf[rr] = back * fabsf(a.scale) * 1.4426950408889634f;
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float y0 = x[2 * i] * mul, y1 = x[2 * i + 1] * mul;
+                        const __half2 hh = __floats2half2_rn(y0, y1);
+                        hi[i] = *reinterpret_cast<const uint32_t*>(&hh);
+                        if constexpr (F32) {
+                            const float2 f = __half22float2(hh);
+                            const __half2 hl = __floats2half2_rn(y0 - f.x, y1 - f.y);
+                            lo[i] = *reinterpret_cast<const uint32_t*>(&hl);
+                        }
+                    }
+                    uint8_t* dst = smem + W::OFF_Q + (rr >> 7) * W::QB + tc::tile_off_sw128(rr & 127, d, 128);
+                    *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    if constexpr (F32) *reinterpret_cast<uint4*>(dst + W::QB) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
             }
             fence_proxy_async_smem();
             tc::mbar_arrive(&bars[B_Q]);
         }
+        if (!mbar_wait_bounded(&bars[B_Q], 0, WAIT_LIMIT_NS)) abort_flag.set(1);     // rowf is every warp's work
+        const float rf = rowf[row];
         int from = 0, stop = 0;
         if (row < rows) row_range(a, n, kv, rho / G, from, stop);
         const int mt = F32 ? 0 : wg;
@@ -213,39 +224,47 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             const int k0 = key0 + j * KEYS + (F32 ? 64 * wg : 0);
             const bool whole = k0 >= all_from && k0 + 32 * CHUNKS <= all_stop;
             // the largest x: a block's from its largest score, since its factor is not negative
-            float top = -INFINITY;
-            auto largest = [&](auto whole_) {
-                constexpr bool WHOLE = decltype(whole_)::value;
-                uint32_t sr[2][32];
-                tc::ld32(s_col, sr[0]);
-#pragma unroll
-                for (int ch = 0; ch < CHUNKS; ++ch) {
+            // Chunks of 32 keys, one's scores on their way while the other's are used. The loops
+            // stay rolled up: the roles' code together has to fit the instruction cache.
+            uint32_t sa[32], sb[32];
+            auto chunks = [&](auto&& use) {
+                tc::ld32(s_col, sa);
+#pragma unroll 1
+                for (int ch = 0; ch < CHUNKS; ch += 2) {
                     tc::wait_ld();
-                    if (ch + 1 < CHUNKS) tc::ld32(s_col + 32 * (ch + 1), sr[(ch + 1) & 1]);
-                    const uint32_t (&v)[32] = sr[ch & 1];
+                    tc::ld32(s_col + 32 * (ch + 1), sb);
+                    use(sa, ch);
+                    tc::wait_ld();
+                    if (ch + 2 < CHUNKS) tc::ld32(s_col + 32 * (ch + 2), sa);
+                    use(sb, ch + 1);
+                }
+            };
+            float top = -INFINITY;
+            if (whole) {
+                chunks([&](uint32_t (&v)[32], int ch) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const float4 in = inf[2 * ch + b];
+                        float m = __uint_as_float(v[16 * b]);
+#pragma unroll
+                        for (int i = 1; i < 15; i += 2) m = max3(m, __uint_as_float(v[16 * b + i]), __uint_as_float(v[16 * b + i + 1]));
+                        m = fmaxf(m, __uint_as_float(v[16 * b + 15]));
+                        top = fmaxf(top, fmaf(m, in.x * rf, in.y));
+                    }
+                });
+            } else {
+                chunks([&](uint32_t (&v)[32], int ch) {
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const float4 in = inf[2 * ch + b];
                         const float f = in.x * rf;
-                        float m = -INFINITY;
-                        if constexpr (WHOLE) {
+                        const int key = k0 + 32 * ch + 16 * b;
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2) m = max3(m, __uint_as_float(v[16 * b + i]), __uint_as_float(v[16 * b + i + 1]));
-                            m = fmaf(m, f, in.y);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const int key = k0 + 32 * ch + 16 * b + i;
-                                const float x = fmaf(__uint_as_float(v[16 * b + i]), f, in.y);
-                                m = fmaxf(m, key >= from && key < stop ? x : -INFINITY);
-                            }
-                        }
-                        top = fmaxf(top, m);
+                        for (int i = 0; i < 16; ++i)
+                            if (key + i >= from && key + i < stop) top = fmaxf(top, fmaf(__uint_as_float(v[16 * b + i]), f, in.y));
                     }
-                }
-            };
-            if (whole) largest(std::true_type{});
-            else largest(std::false_type{});
+                });
+            }
             if constexpr (F32) {
                 // the other half's; it has read this one's before the next scores come, which wait for its P
                 exch[wg][lrow] = top;
@@ -292,69 +311,60 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                 }
             }
             const float base = M == -INFINITY ? 0.0f : M - OFF;
-            auto probabilities = [&](auto whole_) {
-                constexpr bool WHOLE = decltype(whole_)::value;
-                uint32_t sr[2][32];
-                tc::ld32(s_col, sr[0]);
+            // (P's columns overlay scores that are in registers by then)
+            auto probabilities = [&](uint32_t (&v)[32], int ch, auto whole_) {
+                uint32_t pr[16];
 #pragma unroll
-                for (int ch = 0; ch < CHUNKS; ++ch) {
-                    tc::wait_ld();
-                    // (P's columns overlay scores that are in registers by then)
-                    if (ch + 1 < CHUNKS) tc::ld32(s_col + 32 * (ch + 1), sr[(ch + 1) & 1]);
-                    uint32_t (&v)[32] = sr[ch & 1];
-                    uint32_t pr[16];
+                for (int b = 0; b < 2; ++b) {
+                    const float4 in = inf[2 * ch + b];
+                    const float f = in.x * rf, lb = in.y - base;
+                    const uint64_t f2 = tc::pk(f, f), lb2 = tc::pk(lb, lb);
+                    uint64_t sum2 = 0;
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const float4 in = inf[2 * ch + b];
-                        const float f = in.x * rf, lb = in.y - base;
-                        const uint64_t f2 = tc::pk(f, f), lb2 = tc::pk(lb, lb);
-                        uint64_t sum2 = 0;
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const uint64_t x2 = tc::fma2(tc::pk(__uint_as_float(v[16 * b + i]), __uint_as_float(v[16 * b + i + 1])), f2, lb2);
-                            float x0, x1;
-                            tc::upk(x2, x0, x1);
-                            if constexpr (!WHOLE) {
-                                const int key = k0 + 32 * ch + 16 * b + i;
-                                x0 = key >= from && key < stop ? x0 : -INFINITY;
-                                x1 = key + 1 >= from && key + 1 < stop ? x1 : -INFINITY;
-                            }
-                            const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
-                            sum2 = tc::add2(sum2, tc::pk(p0, p1));
-                            if constexpr (F32) {
-                                v[16 * b + i] = __float_as_uint(p0);
-                                v[16 * b + i + 1] = __float_as_uint(p1);
-                            } else {
-                                const __half2 x = __floats2half2_rn(p0, p1);
-                                pr[8 * b + i / 2] = *reinterpret_cast<const uint32_t*>(&x);
-                            }
+                    for (int i = 0; i < 16; i += 2) {
+                        const uint64_t x2 = tc::fma2(tc::pk(__uint_as_float(v[16 * b + i]), __uint_as_float(v[16 * b + i + 1])), f2, lb2);
+                        float x0, x1;
+                        tc::upk(x2, x0, x1);
+                        if constexpr (!decltype(whole_)::value) {
+                            const int key = k0 + 32 * ch + 16 * b + i;
+                            x0 = key >= from && key < stop ? x0 : -INFINITY;
+                            x1 = key + 1 >= from && key + 1 < stop ? x1 : -INFINITY;
                         }
-                        float s0, s1;
-                        tc::upk(sum2, s0, s1);
-                        const float sum = s0 + s1;
-                        // a row that sees nothing here must not meet a scale that is not finite
-                        l += sum != 0.0f ? sum * in.z : 0.0f;
-                    }
-                    if constexpr (F32) {
-#pragma unroll
-                        for (int part = 0; part < 3; ++part) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float p0 = __uint_as_float(v[2 * i]), p1 = __uint_as_float(v[2 * i + 1]);
-                                const __nv_bfloat162 x = __floats2bfloat162_rn(p0, p1);
-                                pr[i] = *reinterpret_cast<const uint32_t*>(&x);
-                                v[2 * i] = __float_as_uint(p0 - __uint_as_float(pr[i] << 16));
-                                v[2 * i + 1] = __float_as_uint(p1 - __uint_as_float(pr[i] & 0xffff0000u));
-                            }
-                            tc::st16(p_col + 64 * part + 16 * ch, pr);
+                        const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
+                        sum2 = tc::add2(sum2, tc::pk(p0, p1));
+                        if constexpr (F32) {
+                            v[16 * b + i] = __float_as_uint(p0);
+                            v[16 * b + i + 1] = __float_as_uint(p1);
+                        } else {
+                            const __half2 x = __floats2half2_rn(p0, p1);
+                            pr[8 * b + i / 2] = *reinterpret_cast<const uint32_t*>(&x);
                         }
-                    } else {
-                        tc::st16(p_col + 16 * ch, pr);
                     }
+                    float s0, s1;
+                    tc::upk(sum2, s0, s1);
+                    const float sum = s0 + s1;
+                    // a row that sees nothing here must not meet a scale that is not finite
+                    l += sum != 0.0f ? sum * in.z : 0.0f;
+                }
+                if constexpr (F32) {
+#pragma unroll
+                    for (int part = 0; part < 3; ++part) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float p0 = __uint_as_float(v[2 * i]), p1 = __uint_as_float(v[2 * i + 1]);
+                            const __nv_bfloat162 x = __floats2bfloat162_rn(p0, p1);
+                            pr[i] = *reinterpret_cast<const uint32_t*>(&x);
+                            v[2 * i] = __float_as_uint(p0 - __uint_as_float(pr[i] << 16));
+                            v[2 * i + 1] = __float_as_uint(p1 - __uint_as_float(pr[i] & 0xffff0000u));
+                        }
+                        tc::st16(p_col + 64 * part + 16 * ch, pr);
+                    }
+                } else {
+                    tc::st16(p_col + 16 * ch, pr);
                 }
             };
-            if (whole) probabilities(std::true_type{});
-            else probabilities(std::false_type{});
+            if (whole) chunks([&](uint32_t (&v)[32], int ch) { probabilities(v, ch, std::true_type{}); });
+            else chunks([&](uint32_t (&v)[32], int ch) { probabilities(v, ch, std::false_type{}); });
             tc::wait_st();
             tc::fence_before();
             tc::mbar_arrive(&bars[B_P + mt]);
@@ -375,25 +385,41 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             }
         }
         if (ok) {
-            constexpr int OC = F32 ? D / 2 : D;
+            // A row a thread in tensor memory, but a row a few lanes in global memory: the
+            // warp's rows change hands in the query operand's place, which no MMA reads any more.
+            constexpr int OC = F32 ? D / 2 : D;                              // columns of this warp (fp32: half of the row's)
+            constexpr int CH = 16 / sizeof(T), NC = OC / CH;                 // values and number of 16-byte chunks of a row
+            uint8_t* mine = smem + W::OFF_Q + warp * (32 * OC * sizeof(T));
+            const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);               // 0 only where nothing was seen
 #pragma unroll
             for (int ch = 0; ch < OC / 16; ++ch) {
                 uint32_t orr[16];
-                const int col = (F32 ? wg * OC : 0) + 16 * ch;
                 if (steps > 0) {
-                    tc::ld16(o_col + col, orr);
+                    tc::ld16(o_col + (F32 ? wg * OC : 0) + 16 * ch, orr);
                     tc::wait_ld();
                 } else {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) orr[i] = 0;
                 }
-                if (row < rows)
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4)
-                        write_row<T, D>(a, first, h, G, rho, col + i,
-                                        make_float4(__uint_as_float(orr[i]), __uint_as_float(orr[i + 1]),
-                                                    __uint_as_float(orr[i + 2]), __uint_as_float(orr[i + 3])),
-                                        M, l, OFF);
+                for (int i = 0; i < 16; i += CH) {
+                    T* dst = reinterpret_cast<T*>(mine + lane * (OC * sizeof(T)) + (((16 * ch + i) / CH) ^ (lane & 7)) * 16);
+#pragma unroll
+                    for (int k = 0; k < CH; k += 4)
+                        store4(dst + k, make_float4(__uint_as_float(orr[i + k]) * inv, __uint_as_float(orr[i + k + 1]) * inv,
+                                                    __uint_as_float(orr[i + k + 2]) * inv, __uint_as_float(orr[i + k + 3]) * inv));
+                }
+            }
+            if (a.lse != nullptr && row < rows && (!F32 || wg == 0))
+                a.lse[tok * a.heads + head] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (M - OFF + log2f(l));
+            __syncwarp();
+#pragma unroll 4
+            for (int x = lane; x < 32 * NC; x += 32) {
+                const int lr = x / NC, cc = x % NC, rr = (F32 ? 0 : 128 * wg) + (warp & 3) * 32 + lr, rh = row0 + rr;
+                if (rr < rows)
+                    *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + static_cast<int64_t>(first + rh / G) * a.out_stride +
+                                              (h * G + rh % G) * D + (F32 ? wg * OC : 0) + cc * CH) =
+                        *reinterpret_cast<const uint4*>(mine + lr * (OC * sizeof(T)) + ((cc ^ (lr & 7)) * 16));
             }
         } else if (lane == 0) {
             abort_flag.set(1);
@@ -447,7 +473,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                         x[g][i] = ldg_stream16(src + at[g >> 1] + (8 * (g & 1) + ck) * D + 16 * (piece + 4 * i));
                 }
         };
-        auto store = [&](uint8_t* dst, const uint4 (&x)[GROUPS][NL], bool bf) {
+        auto store = [&](uint8_t* dst, const uint4 (&x)[GROUPS][NL], bool bf) {      // bf: bfloat16
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
