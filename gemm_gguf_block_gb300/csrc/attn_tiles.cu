@@ -427,10 +427,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         }
     } else if (warp < (SOFT + CONV) / 32) {
         // ---------------------------------------------------------- converters
-        // A lane takes 16 dimensions of a key: lanes 0-7 eight keys (the eight chunk
-        // positions of the swizzle), lanes / 8 the piece of 16 dimensions.
+        // A load takes 16 dimensions a lane of 8 keys. Eight lanes (a phase of a 16-byte
+        // access) hold four pieces of an even key and four of the odd one after it; at D = 128
+        // the other half of the row: the bytes then come from different banks of the lines,
+        // and the chunks go to different banks of the swizzled rows (8-way conflicts on both
+        // sides otherwise measured 2300 cycles a step).
         const int cw = warp - SOFT / 32;
-        const int ck = lane & 7, piece = lane >> 3;         // + 4 for the second half of D = 128
+        const int odd = (lane >> 2) & 1, ck = 2 * (lane >> 3) + odd;
+        auto piece = [&](int i) { return (lane & 3) + (D == 128 ? 4 * (odd ^ i) : 0); };
         constexpr int NL = D / 64;                          // loads a lane and 8 keys
         constexpr int GROUPS = KEYS / 8 / 4;                // groups of 8 keys of a warp: 4, keys 32 cw ..
         const int32_t* table = a.table + static_cast<int64_t>(r) * a.max_blocks;
@@ -470,7 +474,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                 for (int i = 0; i < NL; ++i) {
                     x[g][i] = make_uint4(0, 0, 0, 0);
                     if (at[g >> 1] >= 0)
-                        x[g][i] = ldg_stream16(src + at[g >> 1] + (8 * (g & 1) + ck) * D + 16 * (piece + 4 * i));
+                        x[g][i] = ldg_stream16(src + at[g >> 1] + (8 * (g & 1) + ck) * D + 16 * piece(i));
                 }
         };
         auto store = [&](uint8_t* dst, const uint4 (&x)[GROUPS][NL], bool bf) {      // bf: bfloat16
@@ -478,7 +482,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
                 for (int i = 0; i < NL; ++i) {
-                    const int key = 32 * cw + 8 * g + ck, d = 16 * (piece + 4 * i);
+                    const int key = 32 * cw + 8 * g + ck, d = 16 * piece(i);
                     const uint32_t w[4] = {x[g][i].x, x[g][i].y, x[g][i].z, x[g][i].w};
                     uint32_t o[8];
 #pragma unroll
