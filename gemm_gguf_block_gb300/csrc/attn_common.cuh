@@ -2,6 +2,7 @@
 // scaling, streaming loads, output rows.
 #pragma once
 #include <cstdint>
+#include <type_traits>
 
 #include "cq_device.cuh"
 #include "cq_internal.h"
@@ -87,25 +88,33 @@ __device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
-// Eight consecutive values, 16-byte aligned (fp32: 32 bytes of them).
-__device__ __forceinline__ void load8(const float* p, float4& a, float4& b) {
-    a = load4(p);
-    b = load4(p + 4);
-}
-__device__ __forceinline__ void load8(const __half* p, float4& a, float4& b) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const float2 f[4] = {__half22float2(*reinterpret_cast<const __half2*>(&u.x)), __half22float2(*reinterpret_cast<const __half2*>(&u.y)),
-                         __half22float2(*reinterpret_cast<const __half2*>(&u.z)), __half22float2(*reinterpret_cast<const __half2*>(&u.w))};
-    a = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-    b = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float4& a, float4& b) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    a = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                    __uint_as_float(u.y & 0xffff0000u));
-    b = make_float4(__uint_as_float(u.z << 16), __uint_as_float(u.z & 0xffff0000u), __uint_as_float(u.w << 16),
-                    __uint_as_float(u.w & 0xffff0000u));
-}
+// Eight consecutive values, 16-byte aligned, as they were loaded: converted only
+// when they are used, so that several loads can be in flight.
+template <typename T> struct Raw8 {
+    uint4 u[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+    __device__ __forceinline__ void values(float (&x)[8]) const {
+        const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                const uint32_t z[4] = {u[1].x, u[1].y, u[1].z, u[1].w};
+                x[i] = __uint_as_float(w[i]);
+                x[4 + i] = __uint_as_float(z[i]);
+            } else if constexpr (std::is_same<T, __half>::value) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                x[2 * i] = f.x;
+                x[2 * i + 1] = f.y;
+            } else {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
+};
 
 // Cache rows are read once: past L1.
 __device__ __forceinline__ uint4 ldg_stream16(const void* p) {

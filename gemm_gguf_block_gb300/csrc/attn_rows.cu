@@ -290,12 +290,12 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
     auto load_q = [&](const Piece& pc) {
 #pragma unroll
         for (int w = 0; w < WR; ++w) {
-            const int row = warp + w * NW, rho = RT * pc.i + row;
+            const int rho = RT * pc.i + min(warp + w * NW, pc.rows - 1);     // rows past the last are the last
             const int64_t tok = pc.first + rho / G;
             const T* src = static_cast<const T*>(a.q) + tok * a.q_stride + (pc.h * G + rho % G) * D + lane * PER;
 #pragma unroll
             for (int i = 0; i < PER; i += 2) {
-                const float2 v = row < pc.rows ? load2(src + i) : make_float2(0.0f, 0.0f);
+                const float2 v = load2(src + i);
                 q[w][i] = v.x;
                 q[w][i + 1] = v.y;
             }

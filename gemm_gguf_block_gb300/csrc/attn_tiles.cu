@@ -159,21 +159,22 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             // The rows as operand, each scaled to [2^8, 2^9) by a power of two: 8 values a
             // lane, so a row's chunks go to one 128-byte row of the tile side by side.
             constexpr int LR = D / 8, RW = 32 / LR, PASS = ROWS / (SOFT / 32) / RW;    // lanes a row, rows a load, loads
-            constexpr int BATCH = 4;
+            constexpr int BATCH = F32 ? 4 : 8;
             const int w0 = warp * (ROWS / (SOFT / 32)) + lane / LR, d = (lane % LR) * 8;
             for (int b0 = 0; b0 < PASS; b0 += BATCH) {
-                float4 v[BATCH][2];
+                Raw8<T> v[BATCH];                              // a batch of loads in flight; rows past the last are the last
 #pragma unroll
                 for (int b = 0; b < BATCH; ++b) {
-                    const int rr = w0 + (b0 + b) * RW, rh = row0 + rr;
-                    const T* src = static_cast<const T*>(a.q) + static_cast<int64_t>(first + rh / G) * a.q_stride + (h * G + rh % G) * D + d;
-                    v[b][0] = v[b][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (rr < rows) load8(src, v[b][0], v[b][1]);
+                    const int rh = row0 + min(w0 + (b0 + b) * RW, rows - 1);
+                    v[b].load(static_cast<const T*>(a.q) + static_cast<int64_t>(first + rh / G) * a.q_stride + (h * G + rh % G) * D + d);
                 }
 #pragma unroll
                 for (int b = 0; b < BATCH; ++b) {
                     const int rr = w0 + (b0 + b) * RW;
-                    const float x[8] = {v[b][0].x, v[b][0].y, v[b][0].z, v[b][0].w, v[b][1].x, v[b][1].y, v[b][1].z, v[b][1].w};
+                    float x[8];
+                    v[b].values(x);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = rr < rows ? x[i] : 0.0f;
                     uint32_t top = 0;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(fabsf(x[i])));
