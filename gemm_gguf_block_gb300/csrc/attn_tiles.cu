@@ -11,9 +11,12 @@
 //   O += P V: P from tensor memory over its scores' columns, V from shared memory as
 //     it lies in the cache (keys as rows, MN-major). fp32: P is three bfloat16 parts
 //     (24 bits over fp32's whole range) beside the scores, and V bfloat16.
-// Warps: 0-7 softmax, a thread to a row (fp32: two threads, 64 keys each); 8-11
-// convert the cache's bytes to operands, two stages of keys and two of values;
-// 12 issues the MMAs. While one tile's softmax runs, the other tile's MMAs do.
+// Warps: 0-15 softmax, two threads to a row (fp32: four), each with its part of the
+// keys; 16-19 convert the cache's bytes to operands, two stages of keys and two of
+// values; 20 issues the MMAs. While one tile's softmax runs, the other tile's MMAs do:
+// a tile's scores wait for its own softmax and two MMAs, so the softmax is spread
+// over as many threads as the registers carry (one thread a row measured 600 us where
+// two take less: see the numbers at the kernel).
 // A block of 16 keys carries (s_k, log2 s_v, 1 / s_v) in shared memory; a block
 // outside the cache or the request's keys is stored as zeros with log2 s_v = -inf.
 #include <algorithm>
@@ -30,18 +33,24 @@ namespace cq {
 namespace {
 
 constexpr int KEYS = 128;                 // keys of a step
-constexpr int SOFT = 256;                 // softmax threads
+constexpr int SOFT = 512;                 // softmax threads
 constexpr int CONV = 128;                 // converter threads
-constexpr int THREADS = SOFT + CONV + 32;
+constexpr int THREADS = SOFT + CONV + 128;   // the last four warps: one issues the MMAs
+// Registers a thread of each role; 768 threads are launched with 80 each, and the
+// roles' sum is that: 512 * 80 + 128 * 112 + 128 * 48 = 768 * 80.
+constexpr int REGS_CONV = 112, REGS_MMA = 48;
 constexpr float OFF = 7.0f, RAISE = 8.0f;
 constexpr int INFO = 4;                   // steps whose scales are kept
 
-enum { B_Q = 0, B_K_FULL = 1, B_K_EMPTY = 3, B_V_FULL = 5, B_V_EMPTY = 7, B_S = 9, B_P = 11, B_O = 13, B_INFO = 15, B_X = 19 };
+enum { B_Q = 0, B_K_FULL = 1, B_K_EMPTY = 3, B_V_FULL = 5, B_V_EMPTY = 7, B_S = 9, B_P = 11, B_O = 13, B_INFO = 15 };
 
 template <typename T, int D> struct Tiles {
     static constexpr bool F32 = std::is_same<T, float>::value;
     static constexpr int MT = F32 ? 1 : 2;                 // row tiles
     static constexpr int ROWS = 128 * MT;
+    static constexpr int SPLIT = 4 / MT;                   // softmax threads of a row
+    static constexpr int KT = KEYS / SPLIT;                // their keys
+    static constexpr int OC = D / SPLIT;                   // and their columns of the result
     static constexpr int QB = 128 * D * 2;                 // one query operand
     static constexpr int KB = KEYS * D * 2;
     static constexpr int OFF_Q = 1024;
@@ -60,7 +69,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
     pdl_wait();
     using W = Tiles<T, D>;
     constexpr bool F32 = W::F32;
-    constexpr int MT = W::MT, ROWS = W::ROWS;
+    constexpr int MT = W::MT, ROWS = W::ROWS, SPLIT = W::SPLIT, KT = W::KT, OC = W::OC;
     extern __shared__ uint8_t tiles_smem[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tiles_smem) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
@@ -71,7 +80,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
     __shared__ int scan[THREADS / 32];
     __shared__ float4 info[INFO][KEYS / 16];
     __shared__ float rowf[ROWS];                           // the rows' factors
-    __shared__ float exch[F32 ? 2 : 1][F32 ? 128 : 1];
+    __shared__ float exch[2][SPLIT][ROWS];                 // [step's parity]
     const SmemFlag abort_flag{smem_u32(&abort_word)};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = a.heads / c.heads;
@@ -130,14 +139,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             mbar_init(&bars[B_V_FULL + i], CONV);
             mbar_init(&bars[B_V_EMPTY + i], 1);
             mbar_init(&bars[B_S + i], 1);
-            mbar_init(&bars[B_P + i], F32 ? SOFT : SOFT / 2);
+            mbar_init(&bars[B_P + i], SOFT / 32 / MT);
             mbar_init(&bars[B_O + i], 1);
         }
         for (int i = 0; i < INFO; ++i) mbar_init(&bars[B_INFO + i], CONV / 32);
-        mbar_init(&bars[B_X], SOFT);
         fence_mbar_init();
     }
-    if (warp == THREADS / 32 - 1) {
+    if (warp == (SOFT + CONV) / 32) {
         tc::tmem_alloc(&tmem_holder, 512);
         tc::tmem_relinquish();
     }
@@ -148,9 +156,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
 
     if (warp < SOFT / 32) {
         // ------------------------------------------------------------ softmax
-        const int wg = warp >> 2;                           // 16-bit types: the row tile; fp32: which 64 keys
+        const int mt = (warp >> 2) / SPLIT, part = (warp >> 2) % SPLIT;      // row tile, part of the keys
         const int lrow = (warp & 3) * 32 + lane;            // row of the tile, lane of tensor memory
-        const int row = (F32 ? 0 : 128 * wg) + lrow;        // of the item
+        const int row = 128 * mt + lrow;                    // of the item
+        // the warps that share these 32 rows meet here (the same number of times each, come what may)
+        auto meet = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + 4 * mt + (warp & 3)), "n"(32 * SPLIT) : "memory"); };
         const int rho = row0 + row;
         const int64_t tok = first + rho / G;
         const int head = h * G + rho % G;
@@ -159,7 +169,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             // The rows as operand, each scaled to [2^8, 2^9) by a power of two: 8 values a
             // lane, so a row's chunks go to one 128-byte row of the tile side by side.
             constexpr int LR = D / 8, RW = 32 / LR, PASS = ROWS / (SOFT / 32) / RW;    // lanes a row, rows a load, loads
-            constexpr int BATCH = F32 ? 4 : 8;
+            constexpr int BATCH = PASS < 8 ? PASS : 8;
             const int w0 = warp * (ROWS / (SOFT / 32)) + lane / LR, d = (lane % LR) * 8;
             for (int b0 = 0; b0 < PASS; b0 += BATCH) {
                 Raw8<T> v[BATCH];                              // a batch of loads in flight; rows past the last are the last
@@ -208,41 +218,34 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         const float rf = rowf[row];
         int from = 0, stop = 0;
         if (row < rows) row_range(a, n, kv, rho / G, from, stop);
-        const int mt = F32 ? 0 : wg;
-        const uint32_t s_col = tmem + lanes + (F32 ? W::S0 + 64 * wg : mt == 0 ? W::S0 : W::SP);
-        const uint32_t p_col = F32 ? tmem + lanes + W::SP + 32 * wg : s_col;
-        const uint32_t o_col = tmem + lanes + W::O0 + mt * 128;
-        constexpr int CHUNKS = F32 ? 2 : 4;                 // of 32 keys
+        const uint32_t tile_col = tmem + lanes + (mt == 0 ? W::S0 : W::SP);
+        const uint32_t s_col = tile_col + KT * part;
+        const uint32_t p_col = F32 ? tmem + lanes + W::SP + KT / 2 * part : s_col;
+        const uint32_t o_col = tmem + lanes + W::O0 + mt * 128 + OC * part;
+        constexpr int CHUNKS = KT / 32;
         float M = -INFINITY, l = 0.0f;
         bool ok = true;
-        for (int j = 0; j < steps && ok; ++j) {
-            ok = mbar_wait_bounded(&bars[B_S + mt], j & 1, WAIT_LIMIT_NS) &&
-                 mbar_wait_bounded(&bars[B_INFO + j % INFO], (j / INFO) & 1, WAIT_LIMIT_NS);
-            ok = __all_sync(0xffffffffu, ok) && !abort_flag.get();
-            if (!ok) break;
+        // After a wait that ran out (ok false) the loop goes on without waiting: the meetings stay paired.
+        auto wait = [&](int bar, int parity) {
+            if (ok && !mbar_wait_bounded(&bars[bar], parity, WAIT_LIMIT_NS)) ok = false;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) abort_flag.set(1);
             tc::fence_after();
-            const float4* inf = info[j % INFO] + (F32 ? 4 * wg : 0);
-            const int k0 = key0 + j * KEYS + (F32 ? 64 * wg : 0);
-            const bool whole = k0 >= all_from && k0 + 32 * CHUNKS <= all_stop;
+        };
+        for (int j = 0; j < steps; ++j) {
+            wait(B_S + mt, j & 1);
+            wait(B_INFO + j % INFO, (j / INFO) & 1);
+            const float4* inf = info[j % INFO] + KT / 16 * part;
+            const int k0 = key0 + j * KEYS + KT * part;
+            const bool whole = k0 >= all_from && k0 + KT <= all_stop;
             // the largest x: a block's from its largest score, since its factor is not negative
-            // Chunks of 32 keys, one's scores on their way while the other's are used. The loops
-            // stay rolled up: the roles' code together has to fit the instruction cache.
-            uint32_t sa[32], sb[32];
-            auto chunks = [&](auto&& use) {
-                tc::ld32(s_col, sa);
-#pragma unroll 1
-                for (int ch = 0; ch < CHUNKS; ch += 2) {
-                    tc::wait_ld();
-                    tc::ld32(s_col + 32 * (ch + 1), sb);
-                    use(sa, ch);
-                    tc::wait_ld();
-                    if (ch + 2 < CHUNKS) tc::ld32(s_col + 32 * (ch + 2), sa);
-                    use(sb, ch + 1);
-                }
-            };
             float top = -INFINITY;
-            if (whole) {
-                chunks([&](uint32_t (&v)[32], int ch) {
+#pragma unroll 1
+            for (int ch = 0; ch < CHUNKS; ++ch) {
+                uint32_t v[32];
+                tc::ld32(s_col + 32 * ch, v);
+                tc::wait_ld();
+                if (whole) {
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const float4 in = inf[2 * ch + b];
@@ -252,9 +255,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                         m = fmaxf(m, __uint_as_float(v[16 * b + 15]));
                         top = fmaxf(top, fmaf(m, in.x * rf, in.y));
                     }
-                });
-            } else {
-                chunks([&](uint32_t (&v)[32], int ch) {
+                } else {
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const float4 in = inf[2 * ch + b];
@@ -264,55 +265,38 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                         for (int i = 0; i < 16; ++i)
                             if (key + i >= from && key + i < stop) top = fmaxf(top, fmaf(__uint_as_float(v[16 * b + i]), f, in.y));
                     }
-                });
+                }
             }
-            if constexpr (F32) {
-                // the other half's; it has read this one's before the next scores come, which wait for its P
-                exch[wg][lrow] = top;
-                tc::mbar_arrive(&bars[B_X]);
-                ok = mbar_wait_bounded(&bars[B_X], j & 1, WAIT_LIMIT_NS);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                top = fmaxf(top, exch[wg ^ 1][lrow]);
-            }
+            // the row's other parts (a slot is written again two steps on, after the next meeting)
+            exch[j & 1][part][row] = top;
+            meet();
+#pragma unroll
+            for (int i = 0; i < SPLIT; ++i) top = fmaxf(top, exch[j & 1][i][row]);
             const bool raise = top > M + RAISE;
-            bool o_known = false;
+            bool o_known = j == 0;
             if (__any_sync(0xffffffffu, raise)) {
                 const float old = M;
                 if (raise) M = top;
                 const float f = raise ? exp2_approx(old - M) : 1.0f;             // 0 from -inf
                 l *= f;
                 if (j > 0) {
-                    ok = mbar_wait_bounded(&bars[B_O + mt], (j - 1) & 1, WAIT_LIMIT_NS);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
+                    wait(B_O + mt, (j - 1) & 1);
                     o_known = true;
-                    tc::fence_after();
-                    constexpr int OC = F32 ? D / 2 : D;                          // fp32: half of the columns each
-#pragma unroll
-                    for (int ch = 0; ch < OC / 16; ++ch) {
+#pragma unroll 1
+                    for (int ch = 0; ch < OC / 16; ++ch) {                       // its share of the row's columns
                         uint32_t orr[16];
-                        const uint32_t at = o_col + (F32 ? wg * OC : 0) + 16 * ch;
-                        tc::ld16(at, orr);
+                        tc::ld16(o_col + 16 * ch, orr);
                         tc::wait_ld();
 #pragma unroll
                         for (int i = 0; i < 16; ++i) orr[i] = __float_as_uint(__uint_as_float(orr[i]) * f);
-                        tc::st16(at, orr);
+                        tc::st16(o_col + 16 * ch, orr);
                     }
-                    tc::wait_st();
                 }
             }
-            if constexpr (F32) {
-                // P has columns of its own: the product of the step before has to be done with them
-                if (j > 0 && !o_known) {
-                    ok = mbar_wait_bounded(&bars[B_O], (j - 1) & 1, WAIT_LIMIT_NS);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    tc::fence_after();
-                }
-            }
+            // fp32: P has columns of its own, the product of the step before has to be done with them
+            if (F32 && !o_known) wait(B_O, (j - 1) & 1);
             const float base = M == -INFINITY ? 0.0f : M - OFF;
-            // (P's columns overlay scores that are in registers by then)
+            // (16-bit types: each part's P overlays its own scores, those that are in registers by then)
             auto probabilities = [&](uint32_t (&v)[32], int ch, auto whole_) {
                 uint32_t pr[16];
 #pragma unroll
@@ -364,39 +348,38 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                     tc::st16(p_col + 16 * ch, pr);
                 }
             };
-            if (whole) chunks([&](uint32_t (&v)[32], int ch) { probabilities(v, ch, std::true_type{}); });
-            else chunks([&](uint32_t (&v)[32], int ch) { probabilities(v, ch, std::false_type{}); });
+#pragma unroll 1
+            for (int ch = 0; ch < CHUNKS; ++ch) {
+                uint32_t v[32];
+                tc::ld32(s_col + 32 * ch, v);
+                tc::wait_ld();
+                if (whole) probabilities(v, ch, std::true_type{});
+                else probabilities(v, ch, std::false_type{});
+            }
             tc::wait_st();
             tc::fence_before();
-            tc::mbar_arrive(&bars[B_P + mt]);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bars[B_P + mt]);
         }
         // ---- the rows
-        if (ok && steps > 0) {
-            ok = mbar_wait_bounded(&bars[B_O + mt], (steps - 1) & 1, WAIT_LIMIT_NS);
-            ok = __all_sync(0xffffffffu, ok);
-            tc::fence_after();
-        }
-        if constexpr (F32) {
-            if (ok) {
-                exch[wg][lrow] = l;
-                tc::mbar_arrive(&bars[B_X]);
-                ok = mbar_wait_bounded(&bars[B_X], steps & 1, WAIT_LIMIT_NS);
-                ok = __all_sync(0xffffffffu, ok);
-                l = exch[0][lrow] + exch[1][lrow];
-            }
-        }
+        if (steps > 0) wait(B_O + mt, (steps - 1) & 1);
+        exch[steps & 1][part][row] = l;
+        meet();
+        l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < SPLIT; ++i) l += exch[steps & 1][i][row];
         if (ok) {
             // A row a thread in tensor memory, but a row a few lanes in global memory: the
             // warp's rows change hands in the query operand's place, which no MMA reads any more.
-            constexpr int OC = F32 ? D / 2 : D;                              // columns of this warp (fp32: half of the row's)
-            constexpr int CH = 16 / sizeof(T), NC = OC / CH;                 // values and number of 16-byte chunks of a row
+            constexpr int CH = 16 / sizeof(T), NC = OC / CH;                 // values of a 16-byte chunk, chunks of the warp's columns
+            constexpr int SW = (NC < 8 ? NC : 8) - 1;
             uint8_t* mine = smem + W::OFF_Q + warp * (32 * OC * sizeof(T));
             const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);               // 0 only where nothing was seen
 #pragma unroll
             for (int ch = 0; ch < OC / 16; ++ch) {
                 uint32_t orr[16];
                 if (steps > 0) {
-                    tc::ld16(o_col + (F32 ? wg * OC : 0) + 16 * ch, orr);
+                    tc::ld16(o_col + 16 * ch, orr);
                     tc::wait_ld();
                 } else {
 #pragma unroll
@@ -404,29 +387,29 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                 }
 #pragma unroll
                 for (int i = 0; i < 16; i += CH) {
-                    T* dst = reinterpret_cast<T*>(mine + lane * (OC * sizeof(T)) + (((16 * ch + i) / CH) ^ (lane & 7)) * 16);
+                    T* dst = reinterpret_cast<T*>(mine + lane * (OC * sizeof(T)) + (((16 * ch + i) / CH) ^ (lane & SW)) * 16);
 #pragma unroll
                     for (int k = 0; k < CH; k += 4)
                         store4(dst + k, make_float4(__uint_as_float(orr[i + k]) * inv, __uint_as_float(orr[i + k + 1]) * inv,
                                                     __uint_as_float(orr[i + k + 2]) * inv, __uint_as_float(orr[i + k + 3]) * inv));
                 }
             }
-            if (a.lse != nullptr && row < rows && (!F32 || wg == 0))
+            if (a.lse != nullptr && row < rows && part == 0)
                 a.lse[tok * a.heads + head] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (M - OFF + log2f(l));
             __syncwarp();
 #pragma unroll 4
             for (int x = lane; x < 32 * NC; x += 32) {
-                const int lr = x / NC, cc = x % NC, rr = (F32 ? 0 : 128 * wg) + (warp & 3) * 32 + lr, rh = row0 + rr;
+                const int lr = x / NC, cc = x % NC, rr = 128 * mt + (warp & 3) * 32 + lr, rh = row0 + rr;
                 if (rr < rows)
                     *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + static_cast<int64_t>(first + rh / G) * a.out_stride +
-                                              (h * G + rh % G) * D + (F32 ? wg * OC : 0) + cc * CH) =
-                        *reinterpret_cast<const uint4*>(mine + lr * (OC * sizeof(T)) + ((cc ^ (lr & 7)) * 16));
+                                              (h * G + rh % G) * D + OC * part + cc * CH) =
+                        *reinterpret_cast<const uint4*>(mine + lr * (OC * sizeof(T)) + ((cc ^ (lr & SW)) * 16));
             }
         } else if (lane == 0) {
-            abort_flag.set(1);
             atomicOr(a.status, CQ_DEV_WAIT_TIMEOUT);
         }
     } else if (warp < (SOFT + CONV) / 32) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_CONV));
         // ---------------------------------------------------------- converters
         // A load takes 16 dimensions a lane of 8 keys. Eight lanes (a phase of a 16-byte
         // access) hold four pieces of an even key and four of the odd one after it; at D = 128
@@ -529,47 +512,58 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             fence_proxy_async_smem();
             tc::mbar_arrive(&bars[B_V_FULL + st]);
         }
-    } else if (lane == 0 && steps > 0) {
+    } else {
         // --------------------------------------------------------- MMA issuer
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_MMA));
+        if (warp == (SOFT + CONV) / 32 && steps > 0) {
+        const uint32_t lead = tc::elect_one();
         const uint32_t q0 = smem_u32(smem + W::OFF_Q), k0 = smem_u32(smem + W::OFF_K), v0 = smem_u32(smem + W::OFF_V);
         constexpr uint32_t ID_S = tc::idesc_f16_f32(128, KEYS);
         constexpr uint32_t ID_O = tc::idesc_f16_f32(128, D) | tc::IDESC_B_MN | (F32 ? tc::IDESC_BF16 : 0u);
-        // A k-step of 16 values adds 32 bytes inside a 128-byte row; 64 values on is the next block of rows.
+        // One warp issues all MMAs between busy ones, so an MMA is to cost it few
+        // instructions: the warp runs as one, one lane issues, descriptors are a base and a constant. A k-step of 16 values adds 32
+        // bytes inside a 128-byte row, 64 values on is the next block of rows; 16 keys of
+        // values are 16 rows of 128 bytes.
+        const uint64_t qd = tc::smem_desc_sw128(q0, 1024), kd = tc::smem_desc_sw128(k0, 1024),
+                       vd = tc::smem_desc_sw128_mn(v0, KEYS * 128, 1024);
         auto scores = [&](int m, int st) {
+            const uint32_t d = tmem + (m == 0 ? W::S0 : W::SP);
+            const uint64_t bd = kd + st * (W::KB >> 4);
 #pragma unroll
-            for (int part = 0; part < (F32 ? 2 : 1); ++part)
+            for (int part = 0; part < (F32 ? 2 : 1); ++part) {
+                const uint64_t ad = qd + (F32 ? part : m) * (W::QB >> 4);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32;
-                    tc::mma_f16(tmem + (m == 0 ? W::S0 : W::SP), tc::smem_desc_sw128(q0 + (F32 ? part : m) * W::QB + off, 1024),
-                                tc::smem_desc_sw128(k0 + st * W::KB + off, 1024), ID_S, part > 0 || k > 0);
+                    const uint32_t off = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+                    tc::mma_f16_lead(d, ad + off, bd + off, ID_S, part > 0 || k > 0, lead);
                 }
+            }
         };
         auto product = [&](int m, int st, bool add) {
+            const uint32_t d = tmem + W::O0 + m * 128;
+            const uint64_t bd = vd + st * (W::KB >> 4);
 #pragma unroll
             for (int part = 0; part < (F32 ? 3 : 1); ++part)
 #pragma unroll
                 for (int k = 0; k < KEYS / 16; ++k)
-                    tc::mma_f16_ts(tmem + W::O0 + m * 128,
-                                   tmem + (F32 ? W::SP + 64 * part : m == 0 ? W::S0 : W::SP) + 8 * k,
-                                   tc::smem_desc_sw128_mn(v0 + st * W::KB + k * 2048, KEYS * 128, 1024), ID_O,
-                                   add || part > 0 || k > 0);
+                    tc::mma_f16_ts_lead(d, tmem + (F32 ? W::SP + 64 * part + 8 * k : (m == 0 ? W::S0 : W::SP) + (k >> 2) * 64 + (k & 3) * 8),
+                                   bd + k * (2048 >> 4), ID_O, part > 0 || k > 0 ? 1u : add, lead);
         };
         auto wait = [&](int bar, int parity) {
-            if (!tc::wait_or_abort(&bars[bar], parity, abort_flag, a.status)) return false;
+            const bool got = tc::wait_or_abort(&bars[bar], parity, abort_flag, a.status);
             tc::fence_after();
-            return true;
+            return __all_sync(0xffffffffu, got) != 0;
         };
         bool ok = wait(B_Q, 0) && wait(B_K_FULL, 0);
         if (ok) {
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 scores(m, 0);
-                tc::commit(&bars[B_S + m]);
+                tc::commit_lead(&bars[B_S + m], lead);
             }
-            tc::commit(&bars[B_K_EMPTY]);
+            tc::commit_lead(&bars[B_K_EMPTY], lead);
         }
-        for (int j = 0; j < steps && ok && !abort_flag.get(); ++j) {
+        for (int j = 0; j < steps && ok && !__any_sync(0xffffffffu, abort_flag.get()); ++j) {
             const int st = j & 1, nst = st ^ 1;
             const bool next = j + 1 < steps;
 #pragma unroll
@@ -581,23 +575,24 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                     ok = wait(B_K_FULL + nst, ((j + 1) >> 1) & 1);
                     if (!ok) break;
                     scores(0, nst);
-                    tc::commit(&bars[B_S]);
-                    tc::commit(&bars[B_K_EMPTY + nst]);
+                    tc::commit_lead(&bars[B_S], lead);
+                    tc::commit_lead(&bars[B_K_EMPTY + nst], lead);
                 }
                 if (m == 0) ok = wait(B_V_FULL + st, (j >> 1) & 1);
                 if (!ok) break;
                 product(m, st, j > 0);
-                tc::commit(&bars[B_O + m]);
-                if (m == MT - 1) tc::commit(&bars[B_V_EMPTY + st]);
+                tc::commit_lead(&bars[B_O + m], lead);
+                if (m == MT - 1) tc::commit_lead(&bars[B_V_EMPTY + st], lead);
                 if (!F32 && next) {
                     // P's columns are the scores': the MMAs run in the order they were issued in
                     if (m == 0) ok = wait(B_K_FULL + nst, ((j + 1) >> 1) & 1);
                     if (!ok) break;
                     scores(m, nst);
-                    tc::commit(&bars[B_S + m]);
-                    if (m == MT - 1) tc::commit(&bars[B_K_EMPTY + nst]);
+                    tc::commit_lead(&bars[B_S + m], lead);
+                    if (m == MT - 1) tc::commit_lead(&bars[B_K_EMPTY + nst], lead);
                 }
             }
+        }
         }
     }
     // ---- every role has left its loop; no MMA is in flight before the tensor memory goes
@@ -607,7 +602,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         for (int i = 0; i < MT; ++i) (void)mbar_wait_bounded(&bars[B_O + i], 0, WAIT_LIMIT_NS / 8);
     __syncthreads();
     tc::fence_after();
-    if (warp == THREADS / 32 - 1) tc::tmem_dealloc(tmem, 512);
+    if (warp == (SOFT + CONV) / 32) tc::tmem_dealloc(tmem, 512);
 }
 
 template <typename T, int D>
