@@ -11,12 +11,11 @@
 //   O += P V: P from tensor memory over its scores' columns, V from shared memory as
 //     it lies in the cache (keys as rows, MN-major). fp32: P is three bfloat16 parts
 //     (24 bits over fp32's whole range) beside the scores, and V bfloat16.
-// Warps: 0-15 softmax, two threads to a row (fp32: four), each with its part of the
-// keys; 16-19 convert the cache's bytes to operands, two stages of keys and two of
-// values; 20 issues the MMAs. While one tile's softmax runs, the other tile's MMAs do:
-// a tile's scores wait for its own softmax and two MMAs, so the softmax is spread
-// over as many threads as the registers carry (one thread a row measured 600 us where
-// two take less: see the numbers at the kernel).
+// Warps: 0-7 softmax, a thread to a row (fp32: two threads, 64 keys each); 8-11
+// convert the cache's bytes to operands, two stages of keys and two of values;
+// 12 issues the MMAs. While one tile's softmax runs, the other tile's MMAs do. (Two
+// threads a row, 16 softmax warps, measured the same: what the shorter loops gain, the
+// exchange of the rows' largest costs.)
 // A block of 16 keys carries (s_k, log2 s_v, 1 / s_v) in shared memory; a block
 // outside the cache or the request's keys is stored as zeros with log2 s_v = -inf.
 #include <algorithm>
@@ -33,12 +32,9 @@ namespace cq {
 namespace {
 
 constexpr int KEYS = 128;                 // keys of a step
-constexpr int SOFT = 512;                 // softmax threads
+constexpr int SOFT = 256;                 // softmax threads
 constexpr int CONV = 128;                 // converter threads
-constexpr int THREADS = SOFT + CONV + 128;   // the last four warps: one issues the MMAs
-// Registers a thread of each role; 768 threads are launched with 80 each, and the
-// roles' sum is that: 512 * 80 + 128 * 112 + 128 * 48 = 768 * 80.
-constexpr int REGS_CONV = 112, REGS_MMA = 48;
+constexpr int THREADS = SOFT + CONV + 32;
 constexpr float OFF = 7.0f, RAISE = 8.0f;
 constexpr int INFO = 4;                   // steps whose scales are kept
 
@@ -48,7 +44,7 @@ template <typename T, int D> struct Tiles {
     static constexpr bool F32 = std::is_same<T, float>::value;
     static constexpr int MT = F32 ? 1 : 2;                 // row tiles
     static constexpr int ROWS = 128 * MT;
-    static constexpr int SPLIT = 4 / MT;                   // softmax threads of a row
+    static constexpr int SPLIT = SOFT / (128 * MT);        // softmax threads of a row
     static constexpr int KT = KEYS / SPLIT;                // their keys
     static constexpr int OC = D / SPLIT;                   // and their columns of the result
     static constexpr int QB = 128 * D * 2;                 // one query operand
@@ -159,7 +155,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         const int mt = (warp >> 2) / SPLIT, part = (warp >> 2) % SPLIT;      // row tile, part of the keys
         const int lrow = (warp & 3) * 32 + lane;            // row of the tile, lane of tensor memory
         const int row = 128 * mt + lrow;                    // of the item
-        // the warps that share these 32 rows meet here (the same number of times each, come what may)
+        // fp32: the warps that share these 32 rows meet here (the same number of times each, come what may)
         auto meet = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + 4 * mt + (warp & 3)), "n"(32 * SPLIT) : "memory"); };
         const int rho = row0 + row;
         const int64_t tok = first + rho / G;
@@ -238,14 +234,25 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             const float4* inf = info[j % INFO] + KT / 16 * part;
             const int k0 = key0 + j * KEYS + KT * part;
             const bool whole = k0 >= all_from && k0 + KT <= all_stop;
+            // Chunks of 32 keys, one's scores on their way while the other's are used (loops stay
+            // rolled up: the roles' code together has to fit the instruction cache).
+            uint32_t sa[32], sb[32];
+            auto chunks = [&](auto&& use) {
+                tc::ld32(s_col, sa);
+#pragma unroll 1
+                for (int ch = 0; ch < CHUNKS; ch += 2) {
+                    tc::wait_ld();
+                    tc::ld32(s_col + 32 * (ch + 1), sb);
+                    use(sa, ch);
+                    tc::wait_ld();
+                    if (ch + 2 < CHUNKS) tc::ld32(s_col + 32 * (ch + 2), sa);
+                    use(sb, ch + 1);
+                }
+            };
             // the largest x: a block's from its largest score, since its factor is not negative
             float top = -INFINITY;
-#pragma unroll 1
-            for (int ch = 0; ch < CHUNKS; ++ch) {
-                uint32_t v[32];
-                tc::ld32(s_col + 32 * ch, v);
-                tc::wait_ld();
-                if (whole) {
+            if (whole) {
+                chunks([&](uint32_t (&v)[32], int ch) {
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const float4 in = inf[2 * ch + b];
@@ -255,7 +262,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                         m = fmaxf(m, __uint_as_float(v[16 * b + 15]));
                         top = fmaxf(top, fmaf(m, in.x * rf, in.y));
                     }
-                } else {
+                });
+            } else {
+                chunks([&](uint32_t (&v)[32], int ch) {
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const float4 in = inf[2 * ch + b];
@@ -265,13 +274,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                         for (int i = 0; i < 16; ++i)
                             if (key + i >= from && key + i < stop) top = fmaxf(top, fmaf(__uint_as_float(v[16 * b + i]), f, in.y));
                     }
-                }
+                });
             }
             // the row's other parts (a slot is written again two steps on, after the next meeting)
-            exch[j & 1][part][row] = top;
-            meet();
+            if constexpr (SPLIT > 1) {
+                exch[j & 1][part][row] = top;
+                meet();
 #pragma unroll
-            for (int i = 0; i < SPLIT; ++i) top = fmaxf(top, exch[j & 1][i][row]);
+                for (int i = 0; i < SPLIT; ++i) top = fmaxf(top, exch[j & 1][i][row]);
+            }
             const bool raise = top > M + RAISE;
             bool o_known = j == 0;
             if (__any_sync(0xffffffffu, raise)) {
@@ -348,14 +359,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                     tc::st16(p_col + 16 * ch, pr);
                 }
             };
-#pragma unroll 1
-            for (int ch = 0; ch < CHUNKS; ++ch) {
-                uint32_t v[32];
-                tc::ld32(s_col + 32 * ch, v);
-                tc::wait_ld();
-                if (whole) probabilities(v, ch, std::true_type{});
-                else probabilities(v, ch, std::false_type{});
-            }
+            if (whole) chunks([&](uint32_t (&v)[32], int ch) { probabilities(v, ch, std::true_type{}); });
+            else chunks([&](uint32_t (&v)[32], int ch) { probabilities(v, ch, std::false_type{}); });
             tc::wait_st();
             tc::fence_before();
             __syncwarp();
@@ -363,11 +368,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         }
         // ---- the rows
         if (steps > 0) wait(B_O + mt, (steps - 1) & 1);
-        exch[steps & 1][part][row] = l;
-        meet();
-        l = 0.0f;
+        if constexpr (SPLIT > 1) {
+            exch[steps & 1][part][row] = l;
+            meet();
+            l = 0.0f;
 #pragma unroll
-        for (int i = 0; i < SPLIT; ++i) l += exch[steps & 1][i][row];
+            for (int i = 0; i < SPLIT; ++i) l += exch[steps & 1][i][row];
+        }
         if (ok) {
             // A row a thread in tensor memory, but a row a few lanes in global memory: the
             // warp's rows change hands in the query operand's place, which no MMA reads any more.
@@ -409,7 +416,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             atomicOr(a.status, CQ_DEV_WAIT_TIMEOUT);
         }
     } else if (warp < (SOFT + CONV) / 32) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_CONV));
         // ---------------------------------------------------------- converters
         // A load takes 16 dimensions a lane of 8 keys. Eight lanes (a phase of a 16-byte
         // access) hold four pieces of an even key and four of the odd one after it; at D = 128
@@ -514,7 +520,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         }
     } else {
         // --------------------------------------------------------- MMA issuer
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_MMA));
         if (warp == (SOFT + CONV) / 32 && steps > 0) {
         const uint32_t lead = tc::elect_one();
         const uint32_t q0 = smem_u32(smem + W::OFF_Q), k0 = smem_u32(smem + W::OFF_K), v0 = smem_u32(smem + W::OFF_V);
@@ -546,7 +551,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             for (int part = 0; part < (F32 ? 3 : 1); ++part)
 #pragma unroll
                 for (int k = 0; k < KEYS / 16; ++k)
-                    tc::mma_f16_ts_lead(d, tmem + (F32 ? W::SP + 64 * part + 8 * k : (m == 0 ? W::S0 : W::SP) + (k >> 2) * 64 + (k & 3) * 8),
+                    tc::mma_f16_ts_lead(d, tmem + (F32 ? W::SP + 64 * part + 8 * k : (m == 0 ? W::S0 : W::SP) + k / (KT / 16) * KT + k % (KT / 16) * 8),
                                    bd + k * (2048 >> 4), ID_O, part > 0 || k > 0 ? 1u : add, lead);
         };
         auto wait = [&](int bar, int parity) {
