@@ -453,15 +453,15 @@ def kv_plan_t(past_len, new_len, block_table, free_pages, page_size: int, num_pa
     past, new, free = _vec(fn, past_len, i32, R), _vec(fn, new_len, i32, R), _vec(fn, free_pages, i32, n_free)
     stream = _stream_of(past_len, raw)
     dev = past_len.device
-    words = torch.empty(2 * R + 1 + tokens + 2, dtype=i32, device=dev)
-    slots = torch.empty(tokens, dtype=i64, device=dev)
-    base = words.data_ptr()
-    st = (_lib or lib()).cq_kv_plan(R, page_size, wide, num_pages, past, new, free, n_free, tp, tokens, base,
-                                    base + 4 * R, slots.data_ptr(), base + 4 * (2 * R + 1),
-                                    base + 4 * (2 * R + 1 + tokens), stream)
+    # (an allocation each costs the host less than views of one)
+    kv_len, q_start = torch.empty(R, dtype=i32, device=dev), torch.empty(R + 1, dtype=i32, device=dev)
+    slots, positions = torch.empty(tokens, dtype=i64, device=dev), torch.empty(tokens, dtype=i32, device=dev)
+    used = torch.empty(2, dtype=i32, device=dev)
+    st = (_lib or lib()).cq_kv_plan(R, page_size, wide, num_pages, past, new, free, n_free, tp, tokens,
+                                    kv_len.data_ptr(), q_start.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+                                    used.data_ptr(), stream)
     if st:
         raise CqError(fn, st)
-    kv_len, q_start, positions, used = words.split((R, R + 1, tokens, 2))
     return kv_len, q_start, slots, positions, used
 
 

@@ -2,6 +2,7 @@
 // lengths, writing and reading rows (include/cq.h: cq_kv_plan, cq_kv_append,
 // cq_kv_read).
 #include <algorithm>
+#include <type_traits>
 
 #include "cq_device.cuh"
 #include "cq_internal.h"
@@ -156,19 +157,16 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_plan_kernel(const PlanParams 
     }
 }
 
-__device__ __forceinline__ float warp_max_bits(float a) {
-    // |x| as an integer keeps the order of the values and puts infinities and NaN on top
-    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
-}
-
 template <typename T>
 struct AppendParams {
     KvView c;
-    const T* x[2];           // keys, values
-    int64_t stride[2];       // elements
+    const T* xk;
+    const T* xv;
+    int64_t k_stride, v_stride;      // elements
     const int64_t* slots;
     int* status;
     int T_;
+    int slice;               // tokens whose runs one CTA takes, at most 128
 };
 
 __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
@@ -176,116 +174,212 @@ __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
            ((static_cast<uint32_t>(c) & 0xffu) << 16) | (static_cast<uint32_t>(d) << 24);
 }
 
-// A warp takes one (run of tokens that share a page, head, keys or values): it
-// owns that block's scale and rows, so nothing is shared between warps. A run
-// begins at a token whose slot does not follow its neighbour's or begins a
-// page; the warps of the other tokens leave at once.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams<T> p) {
-    pdl_trigger();
-    pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    const int per = 2 * p.c.heads;
-    const int64_t t0 = unit / per;
-    if (t0 >= p.T_) return;
-    const int which = static_cast<int>(unit - t0 * per) & 1, head = static_cast<int>(unit - t0 * per) >> 1;
-    const int P = p.c.page_size;
-    const int64_t slot = p.slots[t0];
-    if (slot < 0) return;
-    const int64_t page = slot >> p.c.page_shift;
-    const int off = static_cast<int>(slot & (P - 1));
-    if (page >= p.c.num_pages) {
-        if (lane == 0) atomicOr(p.status, CQ_DEV_KV_PAGE);
-        return;
-    }
-    if (off != 0 && t0 > 0 && p.slots[t0 - 1] == slot - 1) return;
-    int n = 1;
-    for (bool on = true; on && off + n < P;) {
-        const bool next = off + n + lane < P && t0 + n + lane < p.T_ && p.slots[t0 + n + lane] == slot + n + lane;
-        const uint32_t m = __ballot_sync(0xffffffffu, next);
-        const int got = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
-        n += got;
-        on = got == 32;
-    }
-    // Four values a lane: a row of 128 is a warp's width, two rows of 64 are.
-    constexpr int RPW = 128 / D;
-    const int sub = lane / (D / 4), col = (lane % (D / 4)) * 4;
-    const T* x = p.x[which] + t0 * p.stride[which] + head * D + col;
-    const int64_t xs = p.stride[which];
-    float a = 0.0f;
-    for (int i = sub; i < n; i += RPW) {
-        const float4 v = load4(x + i * xs);
-        const uint32_t u = max(max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y))),
-                               max(__float_as_uint(fabsf(v.z)), __float_as_uint(fabsf(v.w))));
-        a = __uint_as_float(max(__float_as_uint(a), u));
-    }
-    a = warp_max_bits(a);
-    float* sp = (which ? p.c.v_scale : p.c.k_scale) + page * p.c.scale_stride + head;
-    int8_t* q = (which ? p.c.v : p.c.k) + page * p.c.page_stride + (static_cast<int64_t>(head) * P) * D + col;
-    const float old = off == 0 ? 0.0f : *sp;
-    float want = q8_scale(a);
-    if (want < 1.17549435e-38f) want = 0.0f;
-    float s = fmaxf(old, want);
-    if (!(a < INFINITY) || old != old) s = __uint_as_float(0x7fffffffu);
-    const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;      // 0 for NaN too: the rows hold zeros then
-    if (s != old && off > 0) {
-        const float ratio = s > 0.0f ? __fdiv_rn(old, s) : 0.0f;
-        for (int i = sub; i < off; i += RPW) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(q + i * D);
-            int r[4];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const float h = static_cast<float>(static_cast<int8_t>(w >> (8 * b)));
-                r[b] = static_cast<int>(roundf(__fmul_rn(h, ratio)));
-            }
-            *reinterpret_cast<uint32_t*>(q + i * D) = pack4(r[0], r[1], r[2], r[3]);
+// Four consecutive values as they were loaded, converted when they are used.
+template <typename T> struct Raw4 {
+    uint32_t u[sizeof(T)];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (sizeof(T) == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p);
+            u[0] = v.x; u[1] = v.y; u[2] = v.z; u[3] = v.w;
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            u[0] = v.x; u[1] = v.y;
         }
     }
-    for (int i = sub; i < n; i += RPW) {
-        const float4 v = load4(x + i * xs);
-        const uint32_t w = inv > 0.0f ? pack4(quant_q8(v.x, inv), quant_q8(v.y, inv), quant_q8(v.z, inv), quant_q8(v.w, inv)) : 0u;
-        *reinterpret_cast<uint32_t*>(q + (off + i) * D) = w;
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) u[i] = 0;
     }
-    __syncwarp();
-    if (lane == 0) *sp = s;
+    __device__ __forceinline__ float4 value() const {
+        if constexpr (sizeof(T) == 4) {
+            return make_float4(__uint_as_float(u[0]), __uint_as_float(u[1]), __uint_as_float(u[2]), __uint_as_float(u[3]));
+        } else if constexpr (std::is_same<T, __half>::value) {
+            const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u[0]));
+            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u[1]));
+            return make_float4(a.x, a.y, b.x, b.y);
+        } else {
+            return make_float4(__uint_as_float(u[0] << 16), __uint_as_float(u[0] & 0xffff0000u), __uint_as_float(u[1] << 16),
+                               __uint_as_float(u[1] & 0xffff0000u));
+        }
+    }
+};
+
+constexpr int APPEND_WARPS = 8;
+
+// A run is a stretch of tokens that lie one after another in one page: it begins
+// at a token whose slot does not follow its neighbour's or begins a page. A CTA
+// takes the runs that begin in a slice of tokens, for one head's keys or values:
+// it alone changes those blocks' scales and rows. A run belongs to one warp for
+// every 16 tokens of a page, each holding its 16 rows in registers between the
+// largest value and the rounding, so that the new rows are read once, all of
+// a warp's loads in flight together (8 KB at fp32).
+template <typename T, int D>
+__global__ void __launch_bounds__(APPEND_WARPS * 32) kv_append_kernel(const AppendParams<T> p) {
+    pdl_trigger();
+    pdl_wait();
+    __shared__ int64_t slot_of[2 * 128 + 1];   // slots of tokens t0 - 1 .. t0 + slice + P - 1
+    __shared__ int16_t start[128];             // the runs' first tokens, from t0
+    __shared__ int runs;
+    __shared__ uint32_t top[APPEND_WARPS];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int P = p.c.page_size, head = blockIdx.y >> 1, which = blockIdx.y & 1;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.slice, stride = which ? p.v_stride : p.k_stride;
+    for (int i = tid; i <= p.slice + P; i += APPEND_WARPS * 32) {
+        const int64_t t = t0 - 1 + i;
+        slot_of[i] = t >= 0 && t < p.T_ ? p.slots[t] : -2;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int count = 0;
+        for (int i0 = 0; i0 < p.slice; i0 += 32) {
+            const int i = i0 + lane;
+            bool begins = false;
+            if (i < p.slice) {
+                const int64_t s = slot_of[i + 1];
+                const bool inside = s >= 0 && (s >> p.c.page_shift) < p.c.num_pages;
+                begins = inside && ((s & (P - 1)) == 0 || slot_of[i] != s - 1);
+                if (s >= 0 && !inside) atomicOr(p.status, CQ_DEV_KV_PAGE);
+            }
+            const uint32_t m = __ballot_sync(0xffffffffu, begins);
+            if (begins) start[count + __popc(m & ((1u << lane) - 1))] = static_cast<int16_t>(i);
+            count += __popc(m);
+        }
+        if (lane == 0) runs = count;
+    }
+    __syncthreads();
+    const int wpr = P / 16;                                     // warps of a run
+    const int group = warp / wpr, part = warp % wpr, groups = APPEND_WARPS / wpr;
+    constexpr int RPW = 128 / D, NL = 16 / RPW;                 // rows of a load, loads
+    const int sub = lane / (D / 4), col = (lane % (D / 4)) * 4;
+    for (int r = group; r < runs; r += groups) {
+        const int i0 = start[r];
+        const int64_t slot = slot_of[i0 + 1], page = slot >> p.c.page_shift;
+        const int off = static_cast<int>(slot & (P - 1));
+        int n = 1;                                              // tokens of the run
+        for (bool on = true; on && off + n < P;) {
+            const bool next = off + n + lane < P && slot_of[i0 + 1 + min(n + lane, P)] == slot + n + lane;
+            const uint32_t m = __ballot_sync(0xffffffffu, next);
+            const int got = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+            n += got;
+            on = got == 32;
+        }
+        float* sp = (which ? p.c.v_scale : p.c.k_scale) + page * p.c.scale_stride + head;
+        const float old = off == 0 ? 0.0f : *sp;
+        const T* x = (which ? p.xv : p.xk) + (t0 + i0) * stride + head * D + col;
+        Raw4<T> v[NL];
+        uint32_t a = 0;                                         // |x| as an integer keeps the order and puts infinities and NaN on top
+        const int row0 = 16 * part + sub;
+#pragma unroll
+        for (int k = 0; k < NL; ++k) {
+            v[k].zero();
+            if (row0 + k * RPW < n) v[k].load(x + (row0 + k * RPW) * stride);
+        }
+#pragma unroll
+        for (int k = 0; k < NL; ++k) {
+            const float4 f = v[k].value();
+            a = max(max(a, max(__float_as_uint(fabsf(f.x)), __float_as_uint(fabsf(f.y)))),
+                    max(__float_as_uint(fabsf(f.z)), __float_as_uint(fabsf(f.w))));
+        }
+        a = __reduce_max_sync(0xffffffffu, a);
+        if (wpr > 1) {
+            if (lane == 0) top[warp] = a;
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * wpr) : "memory");
+            for (int w = 0; w < wpr; ++w) a = max(a, top[group * wpr + w]);
+        }
+        float want = q8_scale(__uint_as_float(a));
+        if (want < 1.17549435e-38f) want = 0.0f;
+        float s = fmaxf(old, want);
+        if (a >= 0x7f800000u || old != old) s = __uint_as_float(0x7fffffffu);
+        const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;       // 0 for NaN too: the rows hold zeros then
+        int8_t* q = (which ? p.c.v : p.c.k) + page * p.c.page_stride + static_cast<int64_t>(head) * P * D + col;
+        if (s != old && off > 0) {
+            const float ratio = s > 0.0f ? __fdiv_rn(old, s) : 0.0f;
+            for (int i = row0; i < min(off, 16 * part + 16); i += RPW) {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(q + i * D);
+                int z[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const float h = static_cast<float>(static_cast<int8_t>(w >> (8 * b)));
+                    z[b] = static_cast<int>(roundf(__fmul_rn(h, ratio)));
+                }
+                *reinterpret_cast<uint32_t*>(q + i * D) = pack4(z[0], z[1], z[2], z[3]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NL; ++k) {
+            const int i = row0 + k * RPW;
+            const float4 f = v[k].value();
+            const uint32_t w = inv > 0.0f ? pack4(quant_q8(f.x, inv), quant_q8(f.y, inv), quant_q8(f.z, inv), quant_q8(f.w, inv)) : 0u;
+            if (i < n) *reinterpret_cast<uint32_t*>(q + (off + i) * D) = w;
+        }
+        // every warp has the old scale before it is replaced, and the largest values before the next run's
+        if (wpr > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * wpr) : "memory");
+        if (part == 0 && lane == 0) *sp = s;
+    }
 }
 
 template <typename T>
 struct ReadParams {
     KvView c;
-    T* out[2];
+    T* k_out;
+    T* v_out;
     const int64_t* slots;
     int* status;
-    int64_t n4;              // groups of four values in one output
+    int T_;
 };
 
+// A thread keeps its place in a row (head, four dimensions) and goes down the tokens,
+// four of them in flight: rows are read and written whole by neighbouring threads.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv_read_kernel(const ReadParams<T> p) {
     pdl_trigger();
     pdl_wait();
+    constexpr int BATCH = 4;
     const int row4 = p.c.heads * (D / 4);
-    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < p.n4; i += step) {
-        const int64_t t = i / row4;
-        const int in = static_cast<int>(i - t * row4), head = in / (D / 4), col = (in % (D / 4)) * 4;
-        const int64_t slot = p.slots[t];
-        const int64_t page = slot >> p.c.page_shift;
-        const bool on = slot >= 0 && page < p.c.num_pages;
-        if (slot >= 0 && !on) atomicOr(p.status, CQ_DEV_KV_PAGE);
+    const int per = row4 < 256 ? 256 / row4 : 1;                // tokens of a CTA side by side
+    const int sub = row4 < 256 ? threadIdx.x / row4 : 0;
+    if (sub >= per) return;
+    const int shift = p.c.page_shift, mask = p.c.page_size - 1;
+    for (int in = row4 < 256 ? threadIdx.x - sub * row4 : threadIdx.x; in < row4; in += 256) {
+        const int head = in / (D / 4), col = (in % (D / 4)) * 4;
+        for (int64_t tb = static_cast<int64_t>(blockIdx.x) * per * BATCH + sub; tb < p.T_; tb += static_cast<int64_t>(gridDim.x) * per * BATCH) {
+            int64_t slot[BATCH];
+            uint32_t u[2][BATCH];
+            float sc[2][BATCH];
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            if (p.out[w] == nullptr) continue;
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (on) {
-                const int row = static_cast<int>(slot & (p.c.page_size - 1));
-                const int8_t* q = (w ? p.c.v : p.c.k) + page * p.c.page_stride + (static_cast<int64_t>(head) * p.c.page_size + row) * D + col;
-                const uint32_t u = *reinterpret_cast<const uint32_t*>(q);
-                const float s = (w ? p.c.v_scale : p.c.k_scale)[page * p.c.scale_stride + head];
-                v = make_float4(s * static_cast<int8_t>(u), s * static_cast<int8_t>(u >> 8),
-                                s * static_cast<int8_t>(u >> 16), s * static_cast<int8_t>(u >> 24));
+            for (int b = 0; b < BATCH; ++b) {
+                const int64_t t = tb + b * per;
+                slot[b] = t < p.T_ ? p.slots[t] : -1;
+                if (slot[b] >= 0 && (slot[b] >> shift) >= p.c.num_pages) {
+                    atomicOr(p.status, CQ_DEV_KV_PAGE);
+                    slot[b] = -1;
+                }
             }
-            store4(p.out[w] + i * 4, v);
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                const int64_t page = slot[b] >> shift;
+                const int64_t at = page * p.c.page_stride + (static_cast<int64_t>(head) * p.c.page_size + (slot[b] & mask)) * D + col;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    u[w][b] = 0;
+                    sc[w][b] = 0.0f;
+                    if (slot[b] >= 0 && (w ? p.v_out : p.k_out) != nullptr) {
+                        u[w][b] = *reinterpret_cast<const uint32_t*>((w ? p.c.v : p.c.k) + at);
+                        sc[w][b] = (w ? p.c.v_scale : p.c.k_scale)[page * p.c.scale_stride + head];
+                    }
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                const int64_t t = tb + b * per;
+                if (t >= p.T_) continue;
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
+                    if ((w ? p.v_out : p.k_out) != nullptr)
+                        store4((w ? p.v_out : p.k_out) + t * (row4 * 4) + in * 4,
+                               make_float4(sc[w][b] * static_cast<int8_t>(u[w][b]), sc[w][b] * static_cast<int8_t>(u[w][b] >> 8),
+                                           sc[w][b] * static_cast<int8_t>(u[w][b] >> 16), sc[w][b] * static_cast<int8_t>(u[w][b] >> 24)));
+            }
         }
     }
 }
@@ -293,19 +387,22 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const ReadParams<T> p) {
 template <typename T>
 cudaError_t append_t(const DeviceInfo& dev, const KvView& c, int64_t T_, const void* k, int64_t ks, const void* v,
                      int64_t vs, const int64_t* slots, cudaStream_t s) {
-    AppendParams<T> p{c, {static_cast<const T*>(k), static_cast<const T*>(v)}, {ks, vs}, slots, dev.status,
-                      static_cast<int>(T_)};
-    const int64_t ctas = (T_ * 2 * c.heads + 7) / 8;
-    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    // Runs for all of a CTA's warps: 128 tokens where there are plenty (a page for each group of
+    // warps); with few tokens, whose runs are short, a token for each group.
+    const int groups = APPEND_WARPS / (c.page_size / 16);
+    const int slice = (T_ + 127) / 128 * 2 * c.heads >= dev.sm_count ? 128 : groups;
+    AppendParams<T> p{c, static_cast<const T*>(k), static_cast<const T*>(v), ks, vs, slots, dev.status,
+                      static_cast<int>(T_), slice};
     return launch_kernel(c.dim == 64 ? kv_append_kernel<T, 64> : kv_append_kernel<T, 128>,
-                         dim3(static_cast<unsigned>(ctas)), dim3(256), 0, s, p);
+                         dim3(static_cast<unsigned>((T_ + slice - 1) / slice), 2 * c.heads), dim3(APPEND_WARPS * 32), 0, s, p);
 }
 
 template <typename T>
 cudaError_t read_t(const DeviceInfo& dev, const KvView& c, int64_t T_, const int64_t* slots, void* k, void* v,
                    cudaStream_t s) {
-    ReadParams<T> p{c, {static_cast<T*>(k), static_cast<T*>(v)}, slots, dev.status, T_ * c.heads * (c.dim / 4)};
-    const int64_t ctas = std::min<int64_t>((p.n4 + 255) / 256, static_cast<int64_t>(dev.sm_count) * 64);
+    ReadParams<T> p{c, static_cast<T*>(k), static_cast<T*>(v), slots, dev.status, static_cast<int>(T_)};
+    const int row4 = c.heads * (c.dim / 4), per = row4 < 256 ? 256 / row4 : 1;
+    const int64_t ctas = std::min<int64_t>((T_ + per * 4 - 1) / (per * 4), static_cast<int64_t>(dev.sm_count) * 32);
     return launch_kernel(c.dim == 64 ? kv_read_kernel<T, 64> : kv_read_kernel<T, 128>,
                          dim3(static_cast<unsigned>(ctas)), dim3(256), 0, s, p);
 }
