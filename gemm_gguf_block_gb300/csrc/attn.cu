@@ -27,6 +27,7 @@ cudaError_t launch_attn(const DeviceInfo& dev, const KvView& c, int dtype, const
     // only says whether there may be any for the tiles.
     const bool tiles = a.max_new * G >= TILE_ROWS;
     pl.tile_rows = tiles ? TILE_ROWS : INT_MAX;
+    pl.after_tiles = tiles;
     if (tiles) {
         const cudaError_t e = launch_attn_tiles(dev, c, dtype, a, pl, s);
         if (e != cudaSuccess) return e;

@@ -17,12 +17,19 @@ constexpr int ATTN_MAX_CTAS = 640;
 struct RowsPlan {
     int* count;          // [ATTN_MAX_CTAS], zero between calls
     float* part;         // [ATTN_MAX_CTAS][2][16][head_dim + 4]
+    int after_tiles;     // the rows kernel follows the tiles kernel and runs beside it
     int tile_rows;       // a request with at least so many rows of a kv head is attn_tiles.cu's; INT_MAX: none is
 };
 
 // Requests that each kernel takes: n new tokens, G query heads a kv head.
 __device__ __forceinline__ bool tiles_take(const RowsPlan& pl, int n, int G) { return static_cast<int64_t>(n) * G >= pl.tile_rows; }
 __device__ __forceinline__ bool rows_take(const RowsPlan& pl, int n, int G) { return n > 0 && !tiles_take(pl, n, G); }
+
+// a / b for 0 <= a, 0 < b, by a 32-bit division where both allow it.
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
 
 // First token, new tokens (clipped to T) and length (clipped to the table) of request r.
 __device__ __forceinline__ void request_of(const KvView& c, const AttnArgs& a, int r, int& first, int& n, int& kv) {

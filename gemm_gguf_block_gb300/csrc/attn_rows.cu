@@ -117,7 +117,12 @@ template <typename T, int D, int NB> struct Rows {
 template <typename T, int D, int NB>
 __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kernel(const KvView c, const AttnArgs a, const RowsPlan pl) {
     pdl_trigger();
-    pdl_wait();
+    // Behind the tiles kernel this one runs beside it: every CTA of that one has waited for what
+    // came before (see its first lines), and each CTA of this one waits for its end before it
+    // leaves, so that this grid's end is the end of both.
+    if (pl.after_tiles) __threadfence();
+    else pdl_wait();
+    auto leave = [&]() { if (pl.after_tiles) pdl_wait(); };
     using W = Rows<T, D, NB>;
     constexpr bool F32 = W::F32;
     constexpr bool SPLIT_P = !std::is_same<T, __nv_bfloat16>::value;
@@ -170,12 +175,12 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
     if (tid == 0) cum[a.R] = carry;
     __syncthreads();
     const int64_t U = carry;
-    if (U == 0) return;
-    const int64_t nact = min(static_cast<int64_t>(gridDim.x), (U + SETUP + MIN_UNITS - 1) / (SETUP + MIN_UNITS));
+    if (U == 0) return leave();
+    const int64_t nact = min(static_cast<int64_t>(gridDim.x), (U + MIN_UNITS - 1) / MIN_UNITS);
     const int64_t me = blockIdx.x;
-    if (me >= nact) return;
-    int64_t u = me * U / nact;
-    const int64_t u_end = (me + 1) * U / nact;
+    if (me >= nact) return leave();
+    int64_t u = quot(me * U, nact);
+    const int64_t u_end = quot((me + 1) * U, nact);
     const float lscale = fabsf(a.scale) * 1.4426950408889634f;
     bool first_piece = true;
 
@@ -193,11 +198,11 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
         request_range(a, pc.n, pc.kv, from, stop);
         const int u0 = (from / UNIT) * UNIT;
         pc.units = request_units(a, pc.n, pc.kv);
-        const int64_t in = u - cum[lo], gi = in / (SETUP + pc.units);
+        const int64_t in = u - cum[lo], gi = quot(in, SETUP + pc.units);
         pc.group_u = u - (in - gi * (SETUP + pc.units));
         pc.piece0 = static_cast<int>(max(u - pc.group_u - SETUP, int64_t(0)));
         const int nrt = (pc.n * G + RT - 1) / RT;
-        pc.h = static_cast<int>(gi / nrt);
+        pc.h = static_cast<int>(quot(gi, nrt));
         pc.i = static_cast<int>(gi - static_cast<int64_t>(pc.h) * nrt);
         pc.piece1 = static_cast<int>(min(static_cast<int64_t>(pc.units), u_end - pc.group_u - SETUP));
         pc.rows = min(RT, pc.n * G - RT * pc.i);
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
             next_scales();
         }
     };
-    if (!begin(u)) return;                                        // a part of one group's setup
+    if (!begin(u)) return leave();                                        // a part of one group's setup
     begin_tiles();
 
     for (;;) {
@@ -402,7 +407,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
             }
             if (t % BT == BT / 2) fetch_batch(pieces[turn], t - BT / 2 + BT);
             prefetch(t + AHEAD, t % BT + AHEAD >= BT);
-            float sc[NSUB][NB][4] = {};
+            float sc[NSUB][NB][4] = {}, sl[F32 ? NSUB : 1][F32 ? NB : 1][4] = {};    // fp32: the lower parts' scores, a chain of their own
 #pragma unroll
             for (int ks = 0; ks < KST; ++ks) {
                 uint2 qa[NB], ql[NB];
@@ -424,7 +429,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
                         mma16816(sc[s][b], ka, qa[b].x, qa[b].y);
-                        if constexpr (F32) mma16816(sc[s][b], ka, ql[b].x, ql[b].y);
+                        if constexpr (F32) mma16816(sl[s][b], ka, ql[b].x, ql[b].y);
                     }
                 }
             }
@@ -447,6 +452,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
                     const float f[2] = {ks_[s] * rf[b][0], ks_[s] * rf[b][1]};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {                               // key g + 8 (e / 2), row 2t + e % 2
+                        if constexpr (F32) sc[s][b][e] += sl[s][b][e];
                         float x = fmaf(sc[s][b][e], f[e & 1], lv_[s]);
                         if (!whole) {
                             const int j = j0 + g + 8 * (e >> 1);
@@ -609,17 +615,17 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
         }
         if (!whole) {
             // ---- the group's pieces lie with CTAs c0..c1; the last of them to arrive joins them
-            const int64_t c0 = ((done.group_u + SETUP + 1) * nact - 1) / U, c1 = ((done.group_u + SETUP + done.units) * nact - 1) / U;
-            __threadfence();
+            const int64_t c0 = quot((done.group_u + SETUP + 1) * nact - 1, U), c1 = quot((done.group_u + SETUP + done.units) * nact - 1, U);
             __syncthreads();
             if (tid == 0) {
+                __threadfence();                                               // the CTA's, after the barrier
                 const int before = atomicAdd(pl.count + c0, 1);
                 last_flag = before == static_cast<int>(c1 - c0);
                 if (last_flag) pl.count[c0] = 0;                               // as the next call wants it
+                __threadfence();
             }
             __syncthreads();
             if (last_flag) {
-                __threadfence();
                 for (int x = tid; x < rows * (D / 4); x += THREADS) {
                     const int row = x / (D / 4), col = (x % (D / 4)) * 4;
                     float m = -INFINITY;
@@ -633,7 +639,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
 #pragma unroll
                         for (int k = 0; k < JOIN; ++k) {
                             const int64_t cc = min(cb + k, c1);
-                            const int slot = cc == c0 && c0 * U / nact < done.group_u;
+                            const int slot = cc == c0 && quot(c0 * U, nact) < done.group_u;
                             const float* src = pl.part + (cc * 2 + slot) * (16 * ROWF) + row * ROWF;
                             mc[k] = cb + k <= c1 ? __ldcg(src + D) : -INFINITY;
                             lc[k] = __ldcg(src + D + 1);
@@ -656,7 +662,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
                 }
             }
         }
-        if (!more) break;
+        if (!more) return leave();
         // the merge region and the fragments are free once every warp is here
         __syncthreads();
     }

@@ -40,6 +40,20 @@ constexpr int INFO = 4;                   // steps whose scales are kept
 
 enum { B_Q = 0, B_K_FULL = 1, B_K_EMPTY = 3, B_V_FULL = 5, B_V_EMPTY = 7, B_S = 9, B_P = 11, B_O = 13, B_INFO = 15 };
 
+// Token and head of a kv head's group of an item's rows: rows count on from row0 = tok0 * G +
+// head0. The quotient by G <= 1024 of a number below 1280, by a reciprocal in 21 bits: exact,
+// since the number times the reciprocal's error (below G) stays under 2^21.
+struct RowMap {
+    int tok0, head0, G;
+    uint32_t inv;
+    __device__ __forceinline__ RowMap(int row0, int g) : tok0(row0 / g), head0(row0 % g), G(g), inv(((1u << 21) + g - 1) / g) {}
+    __device__ __forceinline__ void of(int row, int& tok, int& head) const {
+        const int x = head0 + row, t = static_cast<int>((x * inv) >> 21);
+        tok = tok0 + t;
+        head = x - t * G;
+    }
+};
+
 template <typename T, int D> struct Tiles {
     static constexpr bool F32 = std::is_same<T, float>::value;
     static constexpr int MT = F32 ? 1 : 2;                 // row tiles
@@ -53,19 +67,24 @@ template <typename T, int D> struct Tiles {
     static constexpr int OFF_K = OFF_Q + 2 * QB;
     static constexpr int OFF_V = OFF_K + 2 * KB;
     static constexpr int SMEM = OFF_V + 2 * KB + 1024;     // + alignment slack of the dynamic base
-    // tensor memory columns
-    static constexpr uint32_t S0 = 0;
-    static constexpr uint32_t SP = 128;                    // 16-bit types: the second tile's scores; fp32: P's parts, 64 columns each
-    static constexpr uint32_t O0 = F32 ? 320 : 256;
+    // Tensor memory columns. 16-bit types: the two tiles' scores (P overlays them) and results.
+    // fp32: scores -- two steps' where that fits, so that one step's are there before the
+    // other's softmax is done --, P's three parts of 64 columns, the result.
+    static constexpr int SBUF = F32 && D == 64 ? 2 : 1;
+    static constexpr uint32_t S0 = 0, S1 = 128;
+    static constexpr uint32_t SP = 128 * SBUF;             // fp32: P
+    static constexpr uint32_t O0 = F32 ? SP + 192 : 256;
 };
 
 template <typename T, int D>
 __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, const AttnArgs a, const RowsPlan pl) {
-    pdl_trigger();
+    // The rows kernel that follows begins when every CTA of this one has passed here, and
+    // does not wait for the end of it: what both read is complete by then.
     pdl_wait();
+    pdl_trigger();
     using W = Tiles<T, D>;
     constexpr bool F32 = W::F32;
-    constexpr int MT = W::MT, ROWS = W::ROWS, SPLIT = W::SPLIT, KT = W::KT, OC = W::OC;
+    constexpr int MT = W::MT, ROWS = W::ROWS, SPLIT = W::SPLIT, KT = W::KT, OC = W::OC, SBUF = W::SBUF;
     extern __shared__ uint8_t tiles_smem[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tiles_smem) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
@@ -157,54 +176,61 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         const int row = 128 * mt + lrow;                    // of the item
         // fp32: the warps that share these 32 rows meet here (the same number of times each, come what may)
         auto meet = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + 4 * mt + (warp & 3)), "n"(32 * SPLIT) : "memory"); };
-        const int rho = row0 + row;
-        const int64_t tok = first + rho / G;
-        const int head = h * G + rho % G;
+        const RowMap map(row0, G);
+        int my_tok, my_head;
+        map.of(row, my_tok, my_head);
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         {
-            // The rows as operand, each scaled to [2^8, 2^9) by a power of two: 8 values a
-            // lane, so a row's chunks go to one 128-byte row of the tile side by side.
-            constexpr int LR = D / 8, RW = 32 / LR, PASS = ROWS / (SOFT / 32) / RW;    // lanes a row, rows a load, loads
-            constexpr int BATCH = PASS < 8 ? PASS : 8;
-            const int w0 = warp * (ROWS / (SOFT / 32)) + lane / LR, d = (lane % LR) * 8;
-            for (int b0 = 0; b0 < PASS; b0 += BATCH) {
-                Raw8<T> v[BATCH];                              // a batch of loads in flight; rows past the last are the last
+            // The rows as operand, each scaled to [2^8, 2^9) by a power of two: four lanes a
+            // row, each with every fourth chunk of 8 values; all of a warp's loads in flight.
+            constexpr int NCH = D / 32, PASS = ROWS / (SOFT / 32) / 8;
+            const int quad = lane & 3, w0 = warp * (ROWS / (SOFT / 32)) + (lane >> 2);
+            Raw8<T> v[PASS][NCH];                              // rows past the last are the last
 #pragma unroll
-                for (int b = 0; b < BATCH; ++b) {
-                    const int rh = row0 + min(w0 + (b0 + b) * RW, rows - 1);
-                    v[b].load(static_cast<const T*>(a.q) + static_cast<int64_t>(first + rh / G) * a.q_stride + (h * G + rh % G) * D + d);
+            for (int b = 0; b < PASS; ++b) {
+                int tk, hd;
+                map.of(min(w0 + 8 * b, rows - 1), tk, hd);
+                const T* src = static_cast<const T*>(a.q) + static_cast<int64_t>(first + tk) * a.q_stride + (h * G + hd) * D + quad * 8;
+#pragma unroll
+                for (int i = 0; i < NCH; ++i) v[b][i].load(src + 32 * i);
+            }
+            const float lscale = fabsf(a.scale) * 1.4426950408889634f;
+#pragma unroll
+            for (int b = 0; b < PASS; ++b) {
+                const int rr = w0 + 8 * b;
+                float x[NCH][8];
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < NCH; ++i) {
+                    v[b][i].values(x[i]);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(fabsf(x[i][k])));
                 }
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                float mul, back;
+                row_scale(rr < rows ? top : 0, mul, back);
+                if (quad == 0) rowf[rr] = back * lscale;
+                if (a.scale < 0.0f) mul = -mul;
+                if (rr >= rows) mul = 0.0f;
+                uint8_t* dst = smem + W::OFF_Q + (rr >> 7) * W::QB;
 #pragma unroll
-                for (int b = 0; b < BATCH; ++b) {
-                    const int rr = w0 + (b0 + b) * RW;
-                    float x[8];
-                    v[b].values(x);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = rr < rows ? x[i] : 0.0f;
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(fabsf(x[i])));
-#pragma unroll
-                    for (int o = LR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    float mul, back;
-                    row_scale(top, mul, back);
-                    if (a.scale < 0.0f) mul = -mul;
-                    if (d == 0) rowf[rr] = back * fabsf(a.scale) * 1.4426950408889634f;
+                for (int i = 0; i < NCH; ++i) {
                     uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float y0 = x[2 * i] * mul, y1 = x[2 * i + 1] * mul;
+                    for (int k = 0; k < 4; ++k) {
+                        const float y0 = x[i][2 * k] * mul, y1 = x[i][2 * k + 1] * mul;
                         const __half2 hh = __floats2half2_rn(y0, y1);
-                        hi[i] = *reinterpret_cast<const uint32_t*>(&hh);
+                        hi[k] = *reinterpret_cast<const uint32_t*>(&hh);
                         if constexpr (F32) {
                             const float2 f = __half22float2(hh);
                             const __half2 hl = __floats2half2_rn(y0 - f.x, y1 - f.y);
-                            lo[i] = *reinterpret_cast<const uint32_t*>(&hl);
+                            lo[k] = *reinterpret_cast<const uint32_t*>(&hl);
                         }
                     }
-                    uint8_t* dst = smem + W::OFF_Q + (rr >> 7) * W::QB + tc::tile_off_sw128(rr & 127, d, 128);
-                    *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    if constexpr (F32) *reinterpret_cast<uint4*>(dst + W::QB) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    const int off = tc::tile_off_sw128(rr & 127, 8 * (quad + 4 * i), 128);
+                    *reinterpret_cast<uint4*>(dst + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    if constexpr (F32) *reinterpret_cast<uint4*>(dst + W::QB + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
             fence_proxy_async_smem();
@@ -213,10 +239,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         if (!mbar_wait_bounded(&bars[B_Q], 0, WAIT_LIMIT_NS)) abort_flag.set(1);     // rowf is every warp's work
         const float rf = rowf[row];
         int from = 0, stop = 0;
-        if (row < rows) row_range(a, n, kv, rho / G, from, stop);
-        const uint32_t tile_col = tmem + lanes + (mt == 0 ? W::S0 : W::SP);
-        const uint32_t s_col = tile_col + KT * part;
-        const uint32_t p_col = F32 ? tmem + lanes + W::SP + KT / 2 * part : s_col;
+        if (row < rows) row_range(a, n, kv, my_tok, from, stop);
+        const uint32_t s_col0 = tmem + lanes + (mt == 0 ? W::S0 : W::S1) + KT * part;
+        const uint32_t p_col = F32 ? tmem + lanes + W::SP + KT / 2 * part : s_col0;
         const uint32_t o_col = tmem + lanes + W::O0 + mt * 128 + OC * part;
         constexpr int CHUNKS = KT / 32;
         float M = -INFINITY, l = 0.0f;
@@ -229,7 +254,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             tc::fence_after();
         };
         for (int j = 0; j < steps; ++j) {
-            wait(B_S + mt, j & 1);
+            if constexpr (SBUF == 2) wait(B_S + (j & 1), (j >> 1) & 1);
+            else wait(B_S + mt, j & 1);
+            const uint32_t s_col = s_col0 + (SBUF == 2 ? (j & 1) * (W::S1 - W::S0) : 0);
             wait(B_INFO + j % INFO, (j / INFO) & 1);
             const float4* inf = info[j % INFO] + KT / 16 * part;
             const int k0 = key0 + j * KEYS + KT * part;
@@ -382,19 +409,20 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             constexpr int SW = (NC < 8 ? NC : 8) - 1;
             uint8_t* mine = smem + W::OFF_Q + warp * (32 * OC * sizeof(T));
             const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);               // 0 only where nothing was seen
+            static_assert(OC % 32 == 0, "columns in chunks of 32");
 #pragma unroll
-            for (int ch = 0; ch < OC / 16; ++ch) {
-                uint32_t orr[16];
+            for (int ch = 0; ch < OC / 32; ++ch) {
+                uint32_t orr[32];
                 if (steps > 0) {
-                    tc::ld16(o_col + 16 * ch, orr);
+                    tc::ld32(o_col + 32 * ch, orr);
                     tc::wait_ld();
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) orr[i] = 0;
+                    for (int i = 0; i < 32; ++i) orr[i] = 0;
                 }
 #pragma unroll
-                for (int i = 0; i < 16; i += CH) {
-                    T* dst = reinterpret_cast<T*>(mine + lane * (OC * sizeof(T)) + (((16 * ch + i) / CH) ^ (lane & SW)) * 16);
+                for (int i = 0; i < 32; i += CH) {
+                    T* dst = reinterpret_cast<T*>(mine + lane * (OC * sizeof(T)) + (((32 * ch + i) / CH) ^ (lane & SW)) * 16);
 #pragma unroll
                     for (int k = 0; k < CH; k += 4)
                         store4(dst + k, make_float4(__uint_as_float(orr[i + k]) * inv, __uint_as_float(orr[i + k + 1]) * inv,
@@ -402,15 +430,19 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                 }
             }
             if (a.lse != nullptr && row < rows && part == 0)
-                a.lse[tok * a.heads + head] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (M - OFF + log2f(l));
+                a.lse[static_cast<int64_t>(first + my_tok) * a.heads + h * G + my_head] =
+                    l == 0.0f ? -INFINITY : 0.6931471805599453f * (M - OFF + log2f(l));
             __syncwarp();
+            const int cc = lane % NC;
 #pragma unroll 4
-            for (int x = lane; x < 32 * NC; x += 32) {
-                const int lr = x / NC, cc = x % NC, rr = 128 * mt + (warp & 3) * 32 + lr, rh = row0 + rr;
+            for (int lr = lane / NC; lr < 32; lr += 32 / NC) {
+                const int rr = 128 * mt + (warp & 3) * 32 + lr;
+                int tk, hd;
+                map.of(rr, tk, hd);
+                const uint4 x = *reinterpret_cast<const uint4*>(mine + lr * (OC * sizeof(T)) + ((cc ^ (lr & SW)) * 16));
                 if (rr < rows)
-                    *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + static_cast<int64_t>(first + rh / G) * a.out_stride +
-                                              (h * G + rh % G) * D + OC * part + cc * CH) =
-                        *reinterpret_cast<const uint4*>(mine + lr * (OC * sizeof(T)) + ((cc ^ (lr & SW)) * 16));
+                    *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + static_cast<int64_t>(first + tk) * a.out_stride +
+                                              (h * G + hd) * D + OC * part + cc * CH) = x;
             }
         } else if (lane == 0) {
             atomicOr(a.status, CQ_DEV_WAIT_TIMEOUT);
@@ -531,8 +563,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         // values are 16 rows of 128 bytes.
         const uint64_t qd = tc::smem_desc_sw128(q0, 1024), kd = tc::smem_desc_sw128(k0, 1024),
                        vd = tc::smem_desc_sw128_mn(v0, KEYS * 128, 1024);
-        auto scores = [&](int m, int st) {
-            const uint32_t d = tmem + (m == 0 ? W::S0 : W::SP);
+        auto scores = [&](int m, int st) {                  // fp32: m is the buffer
+            const uint32_t d = tmem + (m == 0 ? W::S0 : W::S1);
             const uint64_t bd = kd + st * (W::KB >> 4);
 #pragma unroll
             for (int part = 0; part < (F32 ? 2 : 1); ++part) {
@@ -551,7 +583,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             for (int part = 0; part < (F32 ? 3 : 1); ++part)
 #pragma unroll
                 for (int k = 0; k < KEYS / 16; ++k)
-                    tc::mma_f16_ts_lead(d, tmem + (F32 ? W::SP + 64 * part + 8 * k : (m == 0 ? W::S0 : W::SP) + k / (KT / 16) * KT + k % (KT / 16) * 8),
+                    tc::mma_f16_ts_lead(d, tmem + (F32 ? W::SP + 64 * part + 8 * k : (m == 0 ? W::S0 : W::S1) + k / (KT / 16) * KT + k % (KT / 16) * 8),
                                    bd + k * (2048 >> 4), ID_O, part > 0 || k > 0 ? 1u : add, lead);
         };
         auto wait = [&](int bar, int parity) {
@@ -573,9 +605,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             const bool next = j + 1 < steps;
 #pragma unroll
             for (int m = 0; m < MT && ok; ++m) {
+                if (SBUF == 2 && next) {
+                    // the other buffer's scores: its softmax was waited for a step ago
+                    ok = wait(B_K_FULL + nst, ((j + 1) >> 1) & 1);
+                    if (!ok) break;
+                    scores(nst, nst);
+                    tc::commit_lead(&bars[B_S + nst], lead);
+                    tc::commit_lead(&bars[B_K_EMPTY + nst], lead);
+                }
                 ok = wait(B_P + m, j & 1);
                 if (!ok) break;
-                if (F32 && next) {
+                if (F32 && SBUF == 1 && next) {
                     // the scores' columns are free, P has its own: the next scores first
                     ok = wait(B_K_FULL + nst, ((j + 1) >> 1) & 1);
                     if (!ok) break;
