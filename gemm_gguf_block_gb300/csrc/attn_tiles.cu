@@ -10,7 +10,7 @@
 //     integers as binary16 (exact). fp32 queries are two binary16 parts, two MMAs.
 //   O += P V: P from tensor memory over its scores' columns, V from shared memory as
 //     it lies in the cache (keys as rows, MN-major). fp32: P is three bfloat16 parts
-//     (24 bits over fp32's whole range) beside the scores, and V bfloat16.
+//     (24 bits over fp32's whole range), and V bfloat16.
 // Warps: 0-7 softmax, a thread to a row (fp32: two threads, 64 keys each); 8-11
 // convert the cache's bytes to operands, two stages of keys and two of values;
 // 12 issues the MMAs. While one tile's softmax runs, the other tile's MMAs do. (Two
@@ -69,11 +69,16 @@ template <typename T, int D> struct Tiles {
     static constexpr int SMEM = OFF_V + 2 * KB + 1024;     // + alignment slack of the dynamic base
     // Tensor memory columns. 16-bit types: the two tiles' scores (P overlays them) and results.
     // fp32: scores -- two steps' where that fits, so that one step's are there before the
-    // other's softmax is done --, P's three parts of 64 columns, the result.
+    // other's softmax is done --, overlaid by the first two parts of P, the third part, and two
+    // results: of P's first part and of the other two. (The MMAs' sums are cut off, not rounded:
+    // the small parts' 16 additions a step would cost a sum of full size as much as the first
+    // part's 8.)
     static constexpr int SBUF = F32 && D == 64 ? 2 : 1;
     static constexpr uint32_t S0 = 0, S1 = 128;
-    static constexpr uint32_t SP = 128 * SBUF;             // fp32: P
-    static constexpr uint32_t O0 = F32 ? SP + 192 : 256;
+    static constexpr uint32_t SP = 128 * SBUF;             // fp32: P's third part
+    static constexpr uint32_t O0 = F32 ? SP + 64 : 256;
+    static constexpr uint32_t O1 = O0 + (F32 ? D : 128);   // fp32: the smaller result; else the second tile's
+    static_assert(O1 + D <= 512, "tensor memory");
 };
 
 template <typename T, int D>
@@ -241,8 +246,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         int from = 0, stop = 0;
         if (row < rows) row_range(a, n, kv, my_tok, from, stop);
         const uint32_t s_col0 = tmem + lanes + (mt == 0 ? W::S0 : W::S1) + KT * part;
-        const uint32_t p_col = F32 ? tmem + lanes + W::SP + KT / 2 * part : s_col0;
-        const uint32_t o_col = tmem + lanes + W::O0 + mt * 128 + OC * part;
+        const uint32_t p3_col = tmem + lanes + W::SP + KT / 2 * part;
+        const uint32_t o_col = tmem + lanes + (mt == 0 ? W::O0 : W::O1) + OC * part;
         constexpr int CHUNKS = KT / 32;
         float M = -INFINITY, l = 0.0f;
         bool ok = true;
@@ -321,17 +326,18 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                     wait(B_O + mt, (j - 1) & 1);
                     o_known = true;
 #pragma unroll 1
-                    for (int ch = 0; ch < OC / 16; ++ch) {                       // its share of the row's columns
+                    for (int ch = 0; ch < (F32 ? 2 : 1) * (OC / 16); ++ch) {     // its share of the row's columns
                         uint32_t orr[16];
-                        tc::ld16(o_col + 16 * ch, orr);
+                        const uint32_t at = o_col + (ch % (OC / 16)) * 16 + (ch < OC / 16 ? 0 : W::O1 - W::O0);
+                        tc::ld16(at, orr);
                         tc::wait_ld();
 #pragma unroll
                         for (int i = 0; i < 16; ++i) orr[i] = __float_as_uint(__uint_as_float(orr[i]) * f);
-                        tc::st16(o_col + 16 * ch, orr);
+                        tc::st16(at, orr);
                     }
                 }
             }
-            // fp32: P has columns of its own, the product of the step before has to be done with them
+            // fp32: P's third part has columns of its own, the product of the step before has to be done with them
             if (F32 && !o_known) wait(B_O, (j - 1) & 1);
             const float base = M == -INFINITY ? 0.0f : M - OFF;
             // (16-bit types: each part's P overlays its own scores, those that are in registers by then)
@@ -370,6 +376,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                     l += sum != 0.0f ? sum * in.z : 0.0f;
                 }
                 if constexpr (F32) {
+                    tc::wait_ld();                           // the other chunk's scores are in registers too
 #pragma unroll
                     for (int part = 0; part < 3; ++part) {
 #pragma unroll
@@ -380,10 +387,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                             v[2 * i] = __float_as_uint(p0 - __uint_as_float(pr[i] << 16));
                             v[2 * i + 1] = __float_as_uint(p1 - __uint_as_float(pr[i] & 0xffff0000u));
                         }
-                        tc::st16(p_col + 64 * part + 16 * ch, pr);
+                        tc::st16(part < 2 ? s_col + KT / 2 * part + 16 * ch : p3_col + 16 * ch, pr);
                     }
                 } else {
-                    tc::st16(p_col + 16 * ch, pr);
+                    tc::st16(s_col + 16 * ch, pr);
                 }
             };
             if (whole) chunks([&](uint32_t (&v)[32], int ch) { probabilities(v, ch, std::true_type{}); });
@@ -416,6 +423,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                 if (steps > 0) {
                     tc::ld32(o_col + 32 * ch, orr);
                     tc::wait_ld();
+                    if constexpr (F32) {
+                        uint32_t os[32];
+                        tc::ld32(o_col + (W::O1 - W::O0) + 32 * ch, os);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) orr[i] = __float_as_uint(__uint_as_float(orr[i]) + __uint_as_float(os[i]));
+                    }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) orr[i] = 0;
@@ -568,7 +582,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             const uint64_t bd = kd + st * (W::KB >> 4);
 #pragma unroll
             for (int part = 0; part < (F32 ? 2 : 1); ++part) {
-                const uint64_t ad = qd + (F32 ? part : m) * (W::QB >> 4);
+                const uint64_t ad = qd + (F32 ? 1 - part : m) * (W::QB >> 4);      // fp32: the lower parts first, while the sums are small
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t off = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
@@ -576,15 +590,18 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                 }
             }
         };
-        auto product = [&](int m, int st, bool add) {
-            const uint32_t d = tmem + W::O0 + m * 128;
+        auto product = [&](int m, int st, bool add) {       // m: the tile; fp32: the scores' buffer
             const uint64_t bd = vd + st * (W::KB >> 4);
+            const uint32_t p0 = tmem + (m == 0 ? W::S0 : W::S1);
 #pragma unroll
             for (int part = 0; part < (F32 ? 3 : 1); ++part)
 #pragma unroll
-                for (int k = 0; k < KEYS / 16; ++k)
-                    tc::mma_f16_ts_lead(d, tmem + (F32 ? W::SP + 64 * part + 8 * k : (m == 0 ? W::S0 : W::S1) + k / (KT / 16) * KT + k % (KT / 16) * 8),
-                                   bd + k * (2048 >> 4), ID_O, part > 0 || k > 0 ? 1u : add, lead);
+                for (int k = 0; k < KEYS / 16; ++k) {
+                    const uint32_t own = k / (KT / 16) * KT + k % (KT / 16) * 8;      // P in its thread's scores
+                    const uint32_t d = F32 ? (part == 0 ? W::O0 : W::O1) : m == 0 ? W::O0 : W::O1;
+                    tc::mma_f16_ts_lead(tmem + d, part < 2 ? p0 + KT / 2 * part + own : tmem + W::SP + 8 * k,
+                                        bd + k * (2048 >> 4), ID_O, part > 1 || k > 0 ? 1u : add, lead);
+                }
         };
         auto wait = [&](int bar, int parity) {
             const bool got = tc::wait_or_abort(&bars[bar], parity, abort_flag, a.status);
@@ -615,20 +632,12 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                 }
                 ok = wait(B_P + m, j & 1);
                 if (!ok) break;
-                if (F32 && SBUF == 1 && next) {
-                    // the scores' columns are free, P has its own: the next scores first
-                    ok = wait(B_K_FULL + nst, ((j + 1) >> 1) & 1);
-                    if (!ok) break;
-                    scores(0, nst);
-                    tc::commit_lead(&bars[B_S], lead);
-                    tc::commit_lead(&bars[B_K_EMPTY + nst], lead);
-                }
                 if (m == 0) ok = wait(B_V_FULL + st, (j >> 1) & 1);
                 if (!ok) break;
-                product(m, st, j > 0);
+                product(SBUF == 2 ? st : m, st, j > 0);
                 tc::commit_lead(&bars[B_O + m], lead);
                 if (m == MT - 1) tc::commit_lead(&bars[B_V_EMPTY + st], lead);
-                if (!F32 && next) {
+                if (SBUF == 1 && next) {
                     // P's columns are the scores': the MMAs run in the order they were issued in
                     if (m == 0) ok = wait(B_K_FULL + nst, ((j + 1) >> 1) & 1);
                     if (!ok) break;
