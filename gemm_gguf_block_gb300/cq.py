@@ -1,4 +1,4 @@
-"""Python binding of libcq (include/cq.h): argument marshalling only.
+"""Python binding of libcq (include/cq.h, include/cq_kv.h): argument marshalling only.
 
 The raw functions carry the C names and arguments (integers for pointers and
 the stream) and return the integer cq_status. The ``*_t`` helpers take torch
@@ -30,7 +30,7 @@ DEV_BAD_EXPERT_ID, DEV_DUP_EXPERT_ID, DEV_WAIT_TIMEOUT = 0x1, 0x2, 0x4
 DEV_KV_LENGTH, DEV_KV_BLOCKS, DEV_KV_PAGES, DEV_KV_TOKENS, DEV_KV_PAGE = 0x08, 0x10, 0x20, 0x40, 0x80
 F32, F16, BF16 = 0, 1, 30      # value types of keys, values and queries (cq_dtype)
 
-# Every symbol include/cq.h declares, with (restype, argtypes).
+# Every symbol include/cq.h and include/cq_kv.h declare, with (restype, argtypes).
 _P, _I64, _I, _SZ, _F = C.c_void_p, C.c_int64, C.c_int, C.c_size_t, C.c_float
 SIGNATURES = {
     "cq_quantize_act": (_I, [_I, _I64, _I64, _P, _P, _P]),
@@ -65,7 +65,7 @@ SIGNATURES = {
 
 
 class cq_kv_cache(C.Structure):
-    """The C struct of an 8-bit paged key/value cache (include/cq.h)."""
+    """The C struct of an 8-bit paged key/value cache (include/cq_kv.h)."""
     _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("num_pages", _I64), ("page_stride", _I64),
                 ("scale_stride", _I64), ("page_size", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32),
                 ("reserved", C.c_int32)]

@@ -1,5 +1,5 @@
 // Dispatch of the attention over the 8-bit paged cache (cq_attn_paged in
-// include/cq.h) and its workspace.
+// include/cq_kv.h) and its workspace.
 #include <climits>
 
 #include "attn_common.cuh"
@@ -16,7 +16,7 @@ size_t part_bytes(int64_t head_dim) { return size_t(ATTN_MAX_CTAS) * 2 * 16 * (h
 
 }  // namespace
 
-size_t attn_workspace_size(int64_t, int64_t, int64_t head_dim) { return COUNT_BYTES + part_bytes(head_dim); }
+size_t attn_workspace_size(int64_t head_dim) { return COUNT_BYTES + part_bytes(head_dim); }
 
 cudaError_t launch_attn(const DeviceInfo& dev, const KvView& c, int dtype, const AttnArgs& a, cudaStream_t s) {
     RowsPlan pl{};

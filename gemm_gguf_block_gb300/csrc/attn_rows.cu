@@ -1,5 +1,5 @@
 // Attention over the 8-bit paged cache for few query rows a (request, kv head):
-// decoding and verification (cq_attn_paged in include/cq.h).
+// decoding and verification (cq_attn_paged in include/cq_kv.h).
 //
 // With x_j = log2(e) * scale * s_k * (q . k_j) + log2(s_v), the int8 values k_j, v_j
 // and their blocks' scales s_k, s_v:

@@ -1,5 +1,5 @@
 // Attention over the 8-bit paged cache for many query rows a (request, kv head):
-// prompts and chunks of them (cq_attn_paged in include/cq.h).
+// prompts and chunks of them (cq_attn_paged in include/cq_kv.h).
 //
 // The mathematics is attn_rows.cu's: x_j = log2(e) scale s_k (q . k_j) + log2(s_v),
 // P_j = 2^(x_j - M + OFF), out = sum P_j v_j / sum (P_j / s_v). Here the products

@@ -1,6 +1,6 @@
 // C ABI of libcq: argument validation and dispatch to the kernel launchers.
 // Every check runs before any launch, so an error return means that nothing
-// was launched and nothing was written. See include/cq.h for the contract.
+// was launched and nothing was written. See include/cq.h and include/cq_kv.h for the contract.
 #include <cstdint>
 #include <atomic>
 #include <map>
@@ -522,7 +522,7 @@ cq_status cq_kv_read(const cq_kv_cache* cache, cq_dtype dtype, int64_t T, const 
 size_t cq_attn_workspace_size(int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
     if (kv_heads < 1 || q_heads < 1 || q_heads > 1024 || q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128))
         return 0;
-    return cq::attn_workspace_size(q_heads, kv_heads, head_dim);
+    return cq::attn_workspace_size(head_dim);
 }
 
 cq_status cq_attn_paged(const cq_kv_cache* cache, cq_dtype dtype, int64_t R, int64_t T, int64_t q_heads,
@@ -539,14 +539,14 @@ cq_status cq_attn_paged(const cq_kv_cache* cache, cq_dtype dtype, int64_t R, int
     cq_status st = check_cache(cache, &c);
     if (st != CQ_OK) return st;
     if (q_heads < 1 || q_heads > 1024 || q_heads % c.heads != 0 || R > 16384 || T > INT_LIMIT ||
-        max_blocks > (INT_LIMIT >> c.page_shift))
+        max_blocks > (INT_LIMIT >> c.page_shift) || T * (q_heads / c.heads) > (int64_t(1) << 30))
         return CQ_ERR_SHAPE;
     if (R == 0 || T == 0) return CQ_OK;
     const int64_t width = q_heads * c.dim;
     if ((st = check_rows(q, q_stride, width, bytes)) != CQ_OK) return st;
     if ((st = check_rows(out, out_stride, width, bytes)) != CQ_OK) return st;
     if (kv_len == nullptr || q_start == nullptr || (max_blocks > 0 && block_table == nullptr)) return CQ_ERR_INVALID_ARG;
-    const size_t need = cq::attn_workspace_size(q_heads, c.heads, c.dim);
+    const size_t need = cq::attn_workspace_size(c.dim);
     if (workspace == nullptr || workspace_bytes < need) return CQ_ERR_WORKSPACE;
     if (!aligned4(kv_len) || !aligned4(q_start) || !aligned4(block_table) || !aligned4(lse) || !aligned_to(workspace, 256))
         return CQ_ERR_ALIGNMENT;

@@ -146,34 +146,4 @@ cudaError_t launch_moe(const DeviceInfo& dev, int T, int K, int F, int E, int to
                        const void* Wu, const void* Wd, const int32_t* ids, const float* rw, const void* xq,
                        float* y, void* ws, cudaStream_t s);
 
-// The 8-bit paged key/value cache and attention over it (kv.cu, attn.cu).
-struct KvView;
-cudaError_t launch_kv_plan(const DeviceInfo& dev, int R, int page_shift, int64_t max_blocks, int64_t num_pages,
-                           const int32_t* past, const int32_t* fresh, const int32_t* free_pages, int n_free,
-                           int32_t* table, int T, int32_t* kv_len, int32_t* q_start, int64_t* slots,
-                           int32_t* positions, int32_t* used, cudaStream_t s);
-cudaError_t launch_kv_append(const DeviceInfo& dev, const KvView& c, int dtype, int64_t T, const void* k, int64_t ks,
-                             const void* v, int64_t vs, const int64_t* slots, cudaStream_t s);
-cudaError_t launch_kv_read(const DeviceInfo& dev, const KvView& c, int dtype, int64_t T, const int64_t* slots,
-                           void* k, void* v, cudaStream_t s);
-
-// Attention arguments past the cache view (cq_attn_paged).
-struct AttnArgs {
-    const void* q;
-    void* out;
-    float* lse;
-    const int32_t* table;
-    const int32_t* kv_len;
-    const int32_t* q_start;
-    int* status;
-    void* ws;
-    int64_t q_stride, out_stride;   // elements
-    int64_t max_blocks, window;
-    int64_t max_new, max_kv;
-    float scale;
-    int R, T, heads, causal;        // heads: query heads
-};
-size_t attn_workspace_size(int64_t q_heads, int64_t kv_heads, int64_t head_dim);
-cudaError_t launch_attn(const DeviceInfo& dev, const KvView& c, int dtype, const AttnArgs& a, cudaStream_t s);
-
 }  // namespace cq

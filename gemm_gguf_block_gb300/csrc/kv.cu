@@ -1,5 +1,5 @@
 // The 8-bit paged key/value cache: block tables and slot maps from request
-// lengths, writing and reading rows (include/cq.h: cq_kv_plan, cq_kv_append,
+// lengths, writing and reading rows (include/cq_kv.h: cq_kv_plan, cq_kv_append,
 // cq_kv_read).
 #include <algorithm>
 #include <type_traits>

@@ -1,5 +1,6 @@
-// Device views of the 8-bit paged key/value cache (cq_kv_cache in
-// include/cq.h) and conversions of the activation types its kernels take.
+// The 8-bit paged key/value cache inside the library: its view (cq_kv_cache in
+// include/cq_kv.h), the launchers of its kernels and of the attention over it, and
+// the conversions of the value types they take.
 #pragma once
 #include <cstdint>
 
@@ -7,6 +8,8 @@
 #include <cuda_fp16.h>
 
 #include "cq_device.cuh"
+#include "cq_internal.h"
+#include "cq_kv.h"
 
 namespace cq {
 
@@ -24,24 +27,34 @@ struct KvView {
     int dim;
 };
 
-template <int DT> struct DType;
-template <> struct DType<CQ_F32> { using T = float; };
-template <> struct DType<CQ_F16> { using T = __half; };
-template <> struct DType<CQ_BF16> { using T = __nv_bfloat16; };
+cudaError_t launch_kv_plan(const DeviceInfo& dev, int R, int page_shift, int64_t max_blocks, int64_t num_pages,
+                           const int32_t* past, const int32_t* fresh, const int32_t* free_pages, int n_free,
+                           int32_t* table, int T, int32_t* kv_len, int32_t* q_start, int64_t* slots,
+                           int32_t* positions, int32_t* used, cudaStream_t s);
+cudaError_t launch_kv_append(const DeviceInfo& dev, const KvView& c, int dtype, int64_t T, const void* k, int64_t ks,
+                             const void* v, int64_t vs, const int64_t* slots, cudaStream_t s);
+cudaError_t launch_kv_read(const DeviceInfo& dev, const KvView& c, int dtype, int64_t T, const int64_t* slots,
+                           void* k, void* v, cudaStream_t s);
 
-// Four consecutive values (16 or 8 bytes, aligned) as fp32, exact.
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __half* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
-}
+// Attention arguments past the cache view (cq_attn_paged).
+struct AttnArgs {
+    const void* q;
+    void* out;
+    float* lse;
+    const int32_t* table;
+    const int32_t* kv_len;
+    const int32_t* q_start;
+    int* status;
+    void* ws;
+    int64_t q_stride, out_stride;   // elements
+    int64_t max_blocks, window;
+    int64_t max_new, max_kv;
+    float scale;
+    int R, T, heads, causal;        // heads: query heads
+};
+size_t attn_workspace_size(int64_t head_dim);
+cudaError_t launch_attn(const DeviceInfo& dev, const KvView& c, int dtype, const AttnArgs& a, cudaStream_t s);
+
 // Four fp32 values rounded to nearest even, stored as 16 or 8 bytes.
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 __device__ __forceinline__ void store4(__half* p, float4 v) {
@@ -54,8 +67,4 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
     *reinterpret_cast<uint2*>(p) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-
 }  // namespace cq

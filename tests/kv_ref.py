@@ -1,6 +1,6 @@
 """Plain implementations of the cache and attention calls in 64 bits (numpy), and the error bounds of the results.
 
-The stored integers and scales follow the fp32 rule of include/cq.h and are compared exactly; attention is compared
+The stored integers and scales follow the fp32 rule of include/cq_kv.h and are compared exactly; attention is compared
 with its formula in 64 bits.
 """
 import numpy as np

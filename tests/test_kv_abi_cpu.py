@@ -1,5 +1,7 @@
 """The cache and attention calls without a GPU: arguments that they refuse before any launch."""
 import ctypes as C
+import os
+import re
 
 import pytest
 
@@ -28,6 +30,15 @@ BAD_CACHES = [(dict(k=None), cq.ERR_INVALID_ARG), (dict(v_scale=None), cq.ERR_IN
               (dict(reserved=1), cq.ERR_SHAPE), (dict(page_stride=4 * 16 * 64 - 16), cq.ERR_SHAPE),
               (dict(scale_stride=3), cq.ERR_SHAPE), (dict(page_stride=4 * 16 * 64 + 8), cq.ERR_ALIGNMENT),
               (dict(k=A + 8), cq.ERR_ALIGNMENT), (dict(v=A + 4), cq.ERR_ALIGNMENT), (dict(k_scale=A + 2), cq.ERR_ALIGNMENT)]
+
+
+def test_every_declared_symbol_is_exported(L):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "cq_kv.h")).read()
+    names = set(re.findall(r"^(?:cq_status|size_t) (cq_[a-z_]+)\(", text, re.M))
+    assert len(names) == 5
+    for n in names:
+        assert hasattr(L, n) and n in cq.SIGNATURES, n
 
 
 def test_struct_layout(L):
@@ -109,7 +120,7 @@ def test_attn_refusals(L):
     for kw in (dict(cc=None), dict(R=-1), dict(T=-1), dict(hq=-8), dict(mn=-1), dict(mk=-1), dict(mb=-1), dict(window=-1),
                dict(causal=2), dict(q=None), dict(out=None), dict(table=None), dict(kv=None), dict(start=None)):
         assert call(**kw) == cq.ERR_INVALID_ARG, kw
-    for kw in (dict(hq=0), dict(hq=9), dict(hq=1028), dict(R=16385), dict(T=1 << 31), dict(qs=511), dict(os=8),
+    for kw in (dict(hq=0), dict(hq=9), dict(hq=1028), dict(R=16385), dict(T=1 << 31), dict(T=(1 << 29) + 1), dict(qs=511), dict(os=8),
                dict(mb=1 << 27)):
         assert call(**kw) == cq.ERR_SHAPE, kw
     for kw in (dict(q=A + 8), dict(out=A + 4), dict(qs=513), dict(dt=cq.F16, os=516), dict(kv=A + 1), dict(start=A + 2),
