@@ -88,15 +88,27 @@ __device__ __forceinline__ void s8x4_bf16(uint32_t w, uint32_t& o0, uint32_t& o1
     o1 = __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x7632);
 }
 
-__device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
-__device__ __forceinline__ float2 load2(const __half* p) { return __half22float2(*reinterpret_cast<const __half2*>(p)); }
-__device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
-    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
-    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-}
+// Two consecutive values as they were loaded: converted only when they are used, so
+// that several loads can be in flight.
+template <typename T> struct Raw2 {
+    uint32_t u[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (sizeof(T) == 4) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            u[0] = v.x;
+            u[1] = v.y;
+        } else {
+            u[0] = *reinterpret_cast<const uint32_t*>(p);
+        }
+    }
+    __device__ __forceinline__ float2 value() const {
+        if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(u[0]), __uint_as_float(u[1]));
+        else if constexpr (std::is_same<T, __half>::value) return __half22float2(*reinterpret_cast<const __half2*>(&u[0]));
+        else return make_float2(__uint_as_float(u[0] << 16), __uint_as_float(u[0] & 0xffff0000u));
+    }
+};
 
-// Eight consecutive values, 16-byte aligned, as they were loaded: converted only
-// when they are used, so that several loads can be in flight.
+// Eight of them, 16-byte aligned.
 template <typename T> struct Raw8 {
     uint4 u[sizeof(T) / 2];
     __device__ __forceinline__ void load(const T* p) {

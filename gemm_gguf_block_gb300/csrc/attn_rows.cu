@@ -40,7 +40,7 @@ constexpr int NW = 4;                     // warps a CTA
 constexpr int THREADS = NW * 32;
 constexpr int UNIT = 64;                  // keys of a work unit
 constexpr int MIN_UNITS = 2;              // a CTA is worth at least so many
-constexpr int SETUP = 3;                  // units that beginning and merging a group is worth
+constexpr int SETUP = 4;                  // units that beginning and merging a group is worth
 constexpr int JOIN = 8;                   // partial results joined at a time
 constexpr int AHEAD = 2;                  // tiles that a warp has on their way into L2
 constexpr int KNOWN = THREADS;            // requests whose lengths stay in shared memory
@@ -137,12 +137,15 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
     float* ml = merge + NW * RT * ROWF;                                       // [NW][RT][2]
     float* rowf = ml + NW * RT * 2;                                           // [RT] factor of each row's scores
     __shared__ int64_t wsum[NW];
-    __shared__ int last_flag;
+    __shared__ int last_flag[2];
+    __shared__ Piece held[2];                                                 // pieces of groups that other CTAs share
+    __shared__ int held_on[2];
     __shared__ int known[KNOWN][3];
     __shared__ Piece pieces[2];                                               // this one and the next
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
     const int G = a.heads / c.heads;
 
+    if (tid < 2) held_on[tid] = 0;
     // ---- every CTA counts all requests' units
     int64_t carry = 0;
     for (int r0 = 0; r0 < a.R; r0 += THREADS) {
@@ -291,7 +294,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
     };
     // The query rows of the piece: consecutive dimensions of a lane, rows of a warp.
     constexpr int PER = D / 32, WR = RT / NW;
-    float q[WR][PER];
+    Raw2<T> q[WR][PER / 2];                                       // as loaded: converted when the piece begins
     auto load_q = [&](const Piece& pc) {
 #pragma unroll
         for (int w = 0; w < WR; ++w) {
@@ -299,11 +302,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
             const int64_t tok = pc.first + rho / G;
             const T* src = static_cast<const T*>(a.q) + tok * a.q_stride + (pc.h * G + rho % G) * D + lane * PER;
 #pragma unroll
-            for (int i = 0; i < PER; i += 2) {
-                const float2 v = load2(src + i);
-                q[w][i] = v.x;
-                q[w][i + 1] = v.y;
-            }
+            for (int i = 0; i < PER / 2; ++i) q[w][i].load(src + 2 * i);
         }
     };
     // A piece's first loads, all on their way before anything is waited for: the
@@ -317,8 +316,8 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
         all_stop = pc.all_stop;
         head_off = static_cast<int64_t>(pc.h) * c.page_size * D;
         mine = pc.ntile > warp ? (pc.ntile - warp + NW - 1) / NW : 0;
-        if (mine > 0) fetch_batch(pc, 0);
         load_q(pc);
+        if (mine > 0) fetch_batch(pc, 0);
         turn ^= 1;
         if (tid == 0) pieces[turn] = pc;
         return pc.piece1 > pc.piece0;
@@ -344,8 +343,12 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
             // A power of two brings the row's largest value to [2^8, 2^9): exact, and
             // nothing that matters is below binary16's range. NaN for a row that is not finite.
             uint32_t top = 0;
+            float2 x[PER / 2];
 #pragma unroll
-            for (int i = 0; i < PER; ++i) top = max(top, __float_as_uint(fabsf(q[w][i])));
+            for (int i = 0; i < PER / 2; ++i) {
+                x[i] = q[w][i].value();
+                top = max(top, max(__float_as_uint(fabsf(x[i].x)), __float_as_uint(fabsf(x[i].y))));
+            }
             top = __reduce_max_sync(0xffffffffu, top);
             float mul, back;
             row_scale(top, mul, back);
@@ -355,7 +358,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
             for (int i = 0; i < PER; i += 2) {
                 const int d = lane * PER + i;
                 const int j = d >> 6, t = (d >> 4) & 3, s = (d >> 2) & 3, half = (d >> 1) & 1;
-                const float v0 = q[w][i] * mul, v1 = q[w][i + 1] * mul;
+                const float v0 = x[i / 2].x * mul, v1 = x[i / 2].y * mul;
                 const __half2 hi = __floats2half2_rn(v0, v1);
                 uint32_t* dst = reinterpret_cast<uint32_t*>(qf + ((4 * j + s) * NB + (row >> 3)) * 32 + 4 * (row & 7) + t) + half;
                 *dst = *reinterpret_cast<const uint32_t*>(&hi);
@@ -588,8 +591,10 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
         if (more) begin_tiles();
         const int used = min(NW, max(done.ntile, 1));                               // warps that had a tile (warp 0 always counts)
         const bool whole = done.piece0 == 0 && done.piece1 == done.units;
-        float* part = pl.part + (me * 2 + (first_piece ? 0 : 1)) * (16 * ROWF);
+        const int slot = first_piece ? 0 : 1;                                  // only a first and a last piece may be parts
+        float* part = pl.part + (me * 2 + slot) * (16 * ROWF);
         first_piece = false;
+        if (!whole && tid == 0) { held[slot] = done; held_on[slot] = 1; }
         for (int x = tid; x < rows * (D / 4); x += THREADS) {
             const int row = x / (D / 4), col = (x % (D / 4)) * 4;
             float m = -INFINITY;
@@ -613,59 +618,69 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
                 if (col == 0) { part[row * ROWF + D] = m; part[row * ROWF + D + 1] = lt; }
             }
         }
-        if (!whole) {
-            // ---- the group's pieces lie with CTAs c0..c1; the last of them to arrive joins them
-            const int64_t c0 = quot((done.group_u + SETUP + 1) * nact - 1, U), c1 = quot((done.group_u + SETUP + done.units) * nact - 1, U);
-            __syncthreads();
-            if (tid == 0) {
-                __threadfence();                                               // the CTA's, after the barrier
-                const int before = atomicAdd(pl.count + c0, 1);
-                last_flag = before == static_cast<int>(c1 - c0);
-                if (last_flag) pl.count[c0] = 0;                               // as the next call wants it
-                __threadfence();
-            }
-            __syncthreads();
-            if (last_flag) {
-                for (int x = tid; x < rows * (D / 4); x += THREADS) {
-                    const int row = x / (D / 4), col = (x % (D / 4)) * 4;
-                    float m = -INFINITY;
-                    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    float lt = 0.0f;
-                    // The first CTA holds the group in its second slot unless the group begins with it; the others
-                    // begin inside the group: their first. Eight at a time, their loads in flight together.
-                    for (int64_t cb = c0; cb <= c1; cb += JOIN) {
-                        float mc[JOIN], lc[JOIN];
-                        float4 v[JOIN];
-#pragma unroll
-                        for (int k = 0; k < JOIN; ++k) {
-                            const int64_t cc = min(cb + k, c1);
-                            const int slot = cc == c0 && quot(c0 * U, nact) < done.group_u;
-                            const float* src = pl.part + (cc * 2 + slot) * (16 * ROWF) + row * ROWF;
-                            mc[k] = cb + k <= c1 ? __ldcg(src + D) : -INFINITY;
-                            lc[k] = __ldcg(src + D + 1);
-                            v[k] = __ldcg(reinterpret_cast<const float4*>(src + col));
-                        }
-#pragma unroll
-                        for (int k = 0; k < JOIN; ++k) {
-                            const float m2 = fmaxf(m, mc[k]), base = m2 == -INFINITY ? 0.0f : m2;
-                            if (cb + k > c1) continue;
-                            const float f = exp2_approx(m - base), fc = exp2_approx(mc[k] - base);
-                            lt = lt * f + lc[k] * fc;
-                            acc.x = acc.x * f + v[k].x * fc;
-                            acc.y = acc.y * f + v[k].y * fc;
-                            acc.z = acc.z * f + v[k].z * fc;
-                            acc.w = acc.w * f + v[k].w * fc;
-                            m = m2;
-                        }
-                    }
-                    write_row<T, D>(a, done.first, done.h, G, RT * done.i + row, col, acc, m, lt, OFF);
-                }
-            }
-        }
-        if (!more) return leave();
+        if (!more) break;
         // the merge region and the fragments are free once every warp is here
         __syncthreads();
     }
+
+    // ---- Groups that this CTA has a part of lie with CTAs c0..c1; the last of them to arrive at
+    // the group's counter joins the parts. Both of this CTA's arrive here, together: the fence and
+    // the counters' latency are paid once.
+    __syncthreads();
+    auto first_cta = [&](const Piece& pc) { return quot((pc.group_u + SETUP + 1) * nact - 1, U); };
+    auto last_cta = [&](const Piece& pc) { return quot((pc.group_u + SETUP + pc.units) * nact - 1, U); };
+    if (tid < 2) {
+        last_flag[tid] = 0;
+        if (held_on[tid]) {
+            const int64_t c0 = first_cta(held[tid]), c1 = last_cta(held[tid]);
+            __threadfence();                                                   // the CTA's, after the barrier
+            last_flag[tid] = atomicAdd(pl.count + c0, 1) == static_cast<int>(c1 - c0);
+            if (last_flag[tid]) pl.count[c0] = 0;                              // as the next call wants it
+            __threadfence();
+        }
+    }
+    __syncthreads();
+    for (int hs = 0; hs < 2; ++hs) {
+        if (!last_flag[hs]) continue;
+        const Piece& pc = held[hs];
+        const int64_t c0 = first_cta(pc), c1 = last_cta(pc);
+        // The first CTA holds the group in its second slot unless the group begins with it; the others
+        // begin inside the group: their first.
+        const int slot0 = quot(c0 * U, nact) < pc.group_u;
+        for (int x = tid; x < pc.rows * (D / 4); x += THREADS) {
+            const int row = x / (D / 4), col = (x % (D / 4)) * 4;
+            float m = -INFINITY;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float lt = 0.0f;
+            // in order, so that the result does not depend on who joins; eight at a time, their loads in flight together
+            for (int64_t cb = c0; cb <= c1; cb += JOIN) {
+                float mc[JOIN], lc[JOIN];
+                float4 v[JOIN];
+#pragma unroll
+                for (int k = 0; k < JOIN; ++k) {
+                    const int64_t cc = min(cb + k, c1);
+                    const float* src = pl.part + (cc * 2 + (cc == c0 ? slot0 : 0)) * (16 * ROWF) + row * ROWF;
+                    mc[k] = cb + k <= c1 ? __ldcg(src + D) : -INFINITY;
+                    lc[k] = __ldcg(src + D + 1);
+                    v[k] = __ldcg(reinterpret_cast<const float4*>(src + col));
+                }
+#pragma unroll
+                for (int k = 0; k < JOIN; ++k) {
+                    if (cb + k > c1) continue;
+                    const float m2 = fmaxf(m, mc[k]), base = m2 == -INFINITY ? 0.0f : m2;
+                    const float f = exp2_approx(m - base), fc = exp2_approx(mc[k] - base);
+                    lt = lt * f + lc[k] * fc;
+                    acc.x = acc.x * f + v[k].x * fc;
+                    acc.y = acc.y * f + v[k].y * fc;
+                    acc.z = acc.z * f + v[k].z * fc;
+                    acc.w = acc.w * f + v[k].w * fc;
+                    m = m2;
+                }
+            }
+            write_row<T, D>(a, pc.first, pc.h, G, RT * pc.i + row, col, acc, m, lt, OFF);
+        }
+    }
+    leave();
 }
 
 template <typename T, int D, int NB>
