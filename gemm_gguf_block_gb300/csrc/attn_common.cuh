@@ -14,9 +14,25 @@ namespace cq {
 // and a counter for each.
 constexpr int ATTN_MAX_CTAS = 640;
 
+// CTAs of the tiles kernel when it splits its items over the keys (one an SM at
+// most), the reference offset of its results, and what a shared item's first
+// CTA writes down for the join.
+constexpr int ATTN_TILE_CTAS = 256;
+constexpr float TILES_OFF = 7.0f;
+struct TileShare {
+    int parts;           // CTAs that share the item; below 2: none
+    int rows, row0;      // its rows, and the first among its request's rows of the kv head
+    int first, h;        // the request's first token, the kv head
+    int any;             // whether the call splits items at all
+    int pad[2];
+};
+
 struct RowsPlan {
     int* count;          // [ATTN_MAX_CTAS], zero between calls
     float* part;         // [ATTN_MAX_CTAS][2][16][head_dim + 4]
+    TileShare* share;    // [ATTN_TILE_CTAS]
+    float* tile_part;    // [ATTN_TILE_CTAS][256][head_dim + 4]
+    int sms;             // CTAs that the tiles kernel may split its items into
     int after_tiles;     // the rows kernel follows the tiles kernel and runs beside it
     int tile_rows;       // a request with at least so many rows of a kv head is attn_tiles.cu's; INT_MAX: none is
 };

@@ -7,7 +7,7 @@
 //   lse = ln 2 * (M - OFF + log2(sum_j P_j / s_v)),
 // so both scales cost one fused multiply-add a score and the tensor cores see
 // the stored integers (exact in binary16). M is a running reference, raised
-// only when a score passes it by 8: P_j then stays below 2^15, and a value
+// only when a score passes it by RAISE: P_j then stays below 2^15, and a value
 // that is small against the largest keeps its 11 bits down to 2^-21 of it.
 //
 // Both products are mma.sync m16n8k16 with the cache as the A operand: 16 keys
@@ -44,11 +44,10 @@ constexpr int SETUP = 4;                  // units that beginning and merging a 
 constexpr int JOIN = 8;                   // partial results joined at a time
 constexpr int AHEAD = 2;                  // tiles that a warp has on their way into L2
 constexpr int KNOWN = THREADS;            // requests whose lengths stay in shared memory
-constexpr float OFF = 7.0f, RAISE = 8.0f;
-// fp32: probabilities below this leave binary16's range before they have given
-// 22 bits. They enter as two bfloat16 parts instead, in the tiles that have any
-// (2^-20 of the largest: rare unless the softmax is very peaked).
-constexpr float SMALL = 1.0f / 8192.0f;
+// fp32: probabilities below this would be held to less than 17 bits by two binary16
+// parts (which end at 2^-25). They enter as two bfloat16 parts instead, in the tiles that
+// have any: 2^-20 of the largest and less, rare unless the softmax is very peaked.
+constexpr float SMALL = 1.0f / 256.0f;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -97,6 +96,12 @@ __device__ __forceinline__ int request_units(const AttnArgs& a, int n, int kv) {
     return max(u, 1);
 }
 
+__device__ __forceinline__ int atomic_inc_acq_rel(int* p) {
+    int v;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
 // Transposes an 8 x 8 matrix of 16-bit values held as fragments (lane: row
 // lane / 4, columns 2 (lane % 4), 2 (lane % 4) + 1).
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -105,9 +110,48 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
+// The items that the tiles kernel split over their keys, 16 rows of one at a time, over
+// this grid's CTAs: parts in order, weighted by their references.
+template <typename T, int D>
+__device__ __forceinline__ void join_tiles(const AttnArgs& a, const RowsPlan& pl, int G) {
+    constexpr int ROWF = D + 4;
+    if (__ldcg(&pl.share->any) == 0) return;
+    for (int w = blockIdx.x; w < pl.sms * 16; w += gridDim.x) {
+        const int b = w >> 4, chunk = (w & 15) * 16;
+        const int4* sp = reinterpret_cast<const int4*>(pl.share + b);
+        const int4 s0 = __ldcg(sp), s1 = __ldcg(sp + 1);
+        const TileShare sh{s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, {0, 0}};
+        if (sh.parts < 2 || chunk >= sh.rows) continue;
+        for (int x = threadIdx.x; x < min(16, sh.rows - chunk) * (D / 4); x += THREADS) {
+            const int row = chunk + x / (D / 4), col = (x % (D / 4)) * 4;
+            const float* src = pl.tile_part + static_cast<int64_t>(b) * (256 * ROWF) + row * ROWF;
+            float m = -INFINITY;
+            for (int k = 0; k < sh.parts; ++k) m = fmaxf(m, __ldcg(src + static_cast<int64_t>(k) * (256 * ROWF) + D));
+            const float base = m == -INFINITY ? 0.0f : m;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float lt = 0.0f;
+#pragma unroll 4
+            for (int k = 0; k < sh.parts; ++k) {
+                const float* p = src + static_cast<int64_t>(k) * (256 * ROWF);
+                const float f = exp2_approx(__ldcg(p + D) - base);
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(p + col));
+                lt = fmaf(__ldcg(p + D + 1), f, lt);
+                acc.x = fmaf(v.x, f, acc.x);
+                acc.y = fmaf(v.y, f, acc.y);
+                acc.z = fmaf(v.z, f, acc.z);
+                acc.w = fmaf(v.w, f, acc.w);
+            }
+            write_row<T, D>(a, sh.first, sh.h, G, sh.row0 + row, col, acc, m, lt, TILES_OFF);
+        }
+    }
+}
+
 template <typename T, int D, int NB> struct Rows {
     static constexpr bool F32 = std::is_same<T, float>::value;
     static constexpr int RT = 8 * NB;                       // rows of a tile
+    // The largest probability lies between 2^OFF and 2^(OFF + RAISE) = 2^15. fp32 raises its
+    // reference sooner, so that fewer are SMALL.
+    static constexpr float OFF = F32 ? 12.0f : 7.0f, RAISE = 15.0f - OFF;
     static constexpr int CTAS = NB == 1 && !F32 ? 4 : 3;    // an SM's CTAs (registers): one's merge hides behind the others' loads
     static constexpr int ROWF = D + 4;                      // floats of a merge row
     static constexpr int QF = (F32 ? 2 : 1) * NB * (D / 16) * 32;   // query fragments, 8 bytes each
@@ -122,11 +166,16 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
     // leaves, so that this grid's end is the end of both.
     if (pl.after_tiles) __threadfence();
     else pdl_wait();
-    auto leave = [&]() { if (pl.after_tiles) pdl_wait(); };
+    auto leave = [&]() {
+        if (!pl.after_tiles) return;
+        pdl_wait();
+        join_tiles<T, D>(a, pl, a.heads / c.heads);
+    };
     using W = Rows<T, D, NB>;
     constexpr bool F32 = W::F32;
     constexpr bool SPLIT_P = !std::is_same<T, __nv_bfloat16>::value;
     constexpr int RT = W::RT, ROWF = W::ROWF;
+    constexpr float OFF = W::OFF, RAISE = W::RAISE;
     constexpr int NSUB = 128 / D, KST = D / 16, MT = D / 16;      // a tile: NSUB blocks of 16 keys, 2 KB of keys
     constexpr int TK = 16 * NSUB;                                 // keys of a tile
     constexpr int BT = 32 / NSUB;                                 // tiles of a batch of page ids
@@ -489,25 +538,44 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
                         }
                 }
                 uint2 ph[NB], plo[NB], ps[NB], pt[NB];
-                bool small = false;
+                bool small = false;                         // (hidden keys' zeros too: the tiles at the edges)
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    float p[4], sm[4];
                     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float m = M[b][e & 1], base = m == -INFINITY ? 0.0f : m - OFF;
-                        p[e] = exp2_approx(sc[s][b][e] - base);
-                        sum[e & 1] += p[e];                                     // unrounded: lse is held to fp32
-                        if constexpr (F32) {
-                            sm[e] = p[e] < SMALL ? p[e] : 0.0f;
-                            small |= sm[e] > 0.0f;
-                            p[e] -= sm[e];
-                        }
+                        const float p = exp2_approx(sc[s][b][e] - base);
+                        sum[e & 1] += p;                                        // unrounded: lse is held to fp32
+                        if constexpr (F32) small |= p < SMALL;
+                        sc[s][b][e] = p;
                     }
                     // a row that sees nothing here must not meet a scale that is not finite
                     l[b][0] += sum[0] != 0.0f ? sum[0] * rv_[s] : 0.0f;
                     l[b][1] += sum[1] != 0.0f ? sum[1] * rv_[s] : 0.0f;
+                }
+                if constexpr (F32) {
+                    small = __any_sync(0xffffffffu, small);
+                    if (small) {
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            float sm[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                sm[e] = sc[s][b][e] < SMALL ? sc[s][b][e] : 0.0f;
+                                sc[s][b][e] -= sm[e];
+                            }
+                            const uint32_t s0 = bf16_pair(sm[0], sm[1]), s1 = bf16_pair(sm[2], sm[3]);
+                            const uint32_t t0 = bf16_pair(sm[0] - __uint_as_float(s0 << 16), sm[1] - __uint_as_float(s0 & 0xffff0000u));
+                            const uint32_t t1 = bf16_pair(sm[2] - __uint_as_float(s1 << 16), sm[3] - __uint_as_float(s1 & 0xffff0000u));
+                            ps[b] = make_uint2(transpose8(s0), transpose8(s1));
+                            pt[b] = make_uint2(transpose8(t0), transpose8(t1));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const float (&p)[4] = sc[s][b];
                     const __half2 h0 = __floats2half2_rn(p[0], p[1]), h1 = __floats2half2_rn(p[2], p[3]);
                     ph[b] = make_uint2(transpose8(*reinterpret_cast<const uint32_t*>(&h0)),
                                        transpose8(*reinterpret_cast<const uint32_t*>(&h1)));
@@ -516,18 +584,6 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
                         const __half2 l0 = __floats2half2_rn(p[0] - f0.x, p[1] - f0.y), l1 = __floats2half2_rn(p[2] - f1.x, p[3] - f1.y);
                         plo[b] = make_uint2(transpose8(*reinterpret_cast<const uint32_t*>(&l0)),
                                             transpose8(*reinterpret_cast<const uint32_t*>(&l1)));
-                    }
-                    if constexpr (F32) {
-                        const uint32_t s0 = bf16_pair(sm[0], sm[1]), s1 = bf16_pair(sm[2], sm[3]);
-                        const uint32_t t0 = bf16_pair(sm[0] - __uint_as_float(s0 << 16), sm[1] - __uint_as_float(s0 & 0xffff0000u));
-                        const uint32_t t1 = bf16_pair(sm[2] - __uint_as_float(s1 << 16), sm[3] - __uint_as_float(s1 & 0xffff0000u));
-                        small = __any_sync(0xffffffffu, small);
-                        if (small) {
-                            ps[b] = make_uint2(transpose8(s0), transpose8(s1));
-                            pt[b] = make_uint2(transpose8(t0), transpose8(t1));
-                        } else {
-                            ps[b] = pt[b] = make_uint2(0, 0);
-                        }
                     }
                 }
                 // The second product follows at once: a later sub-block may raise M.
@@ -633,10 +689,9 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
         last_flag[tid] = 0;
         if (held_on[tid]) {
             const int64_t c0 = first_cta(held[tid]), c1 = last_cta(held[tid]);
-            __threadfence();                                                   // the CTA's, after the barrier
-            last_flag[tid] = atomicAdd(pl.count + c0, 1) == static_cast<int>(c1 - c0);
+            // (releases what the CTA wrote before the barrier, and acquires the others' parts)
+            last_flag[tid] = atomic_inc_acq_rel(pl.count + c0) == static_cast<int>(c1 - c0);
             if (last_flag[tid]) pl.count[c0] = 0;                              // as the next call wants it
-            __threadfence();
         }
     }
     __syncthreads();

@@ -16,6 +16,8 @@
 // 12 issues the MMAs. While one tile's softmax runs, the other tile's MMAs do. (Two
 // threads a row, 16 softmax warps, measured the same: what the shorter loops gain, the
 // exchange of the rows' largest costs.)
+// Few items are split over their keys; the rows kernel, which always follows, joins
+// the parts.
 // A block of 16 keys carries (s_k, log2 s_v, 1 / s_v) in shared memory; a block
 // outside the cache or the request's keys is stored as zeros with log2 s_v = -inf.
 #include <algorithm>
@@ -35,7 +37,8 @@ constexpr int KEYS = 128;                 // keys of a step
 constexpr int SOFT = 256;                 // softmax threads
 constexpr int CONV = 128;                 // converter threads
 constexpr int THREADS = SOFT + CONV + 32;
-constexpr float OFF = 7.0f, RAISE = 8.0f;
+constexpr float OFF = TILES_OFF, RAISE = 8.0f;
+constexpr int MIN_STEPS = 3;              // a part of an item has at least so many, where it has parts
 constexpr int INFO = 4;                   // steps whose scales are kept
 
 enum { B_Q = 0, B_K_FULL = 1, B_K_EMPTY = 3, B_V_FULL = 5, B_V_EMPTY = 7, B_S = 9, B_P = 11, B_O = 13, B_INFO = 15 };
@@ -97,7 +100,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
     __shared__ int abort_word;
     __shared__ int item[4];                                // request, its first token, new tokens, length
     __shared__ int item_at;                                // index inside the request
-    __shared__ int scan[THREADS / 32];
+    __shared__ int64_t scan[THREADS / 32];
     __shared__ float4 info[INFO][KEYS / 16];
     __shared__ float rowf[ROWS];                           // the rows' factors
     __shared__ float exch[2][SPLIT][ROWS];                 // [step's parity]
@@ -105,22 +108,37 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = a.heads / c.heads;
 
-    // ---- this CTA's item: requests in order; inside one the last rows (the longest) first, heads together
-    if (tid == 0) { item_at = -1; abort_word = 0; }
-    __syncthreads();
-    {
+    // ---- this CTA's item: requests in order; inside one the last rows (the longest) first, heads together.
+    // Where the items are too few for half the SMs, each is split over its keys into parts of about
+    // equal length, together one CTA an SM.
+    if (tid == 0) { item[0] = -1; abort_word = 0; }
+    auto items_of = [&](int n_) {
+        return tiles_take(pl, n_, G) ? static_cast<int>((static_cast<int64_t>(n_) * G + ROWS - 1) / ROWS) : 0;
+    };
+    // Keys and steps of row tile i of a request: what some row sees, and what all rows see.
+    auto range_of = [&](int n_, int kv_, int i, int& key0_, int& stop_, int& all_from_, int& all_stop_) {
+        const int last = min((i + 1) * ROWS, n_ * G) - 1;
+        row_range(a, n_, kv_, i * ROWS / G, key0_, all_stop_);
+        row_range(a, n_, kv_, last / G, all_from_, stop_);
+        key0_ = key0_ / KEYS * KEYS;
+        return stop_ > key0_ ? (stop_ - key0_ + KEYS - 1) / KEYS : 0;
+    };
+    // The sum of count(n, kv) over the requests; where the CTA's index falls into a request's
+    // count, notes the request and the index in it.
+    auto over_requests = [&](auto&& count) {
         int64_t carry = 0;
-        for (int r0 = 0; r0 < a.R && carry <= blockIdx.x; r0 += THREADS) {
-            const int r = r0 + tid;
-            int first = 0, n = 0, kv = 0, x = 0;
-            if (r < a.R) {
-                request_of(c, a, r, first, n, kv);
-                if (tiles_take(pl, n, G)) x = static_cast<int>((static_cast<int64_t>(n) * G + ROWS - 1) / ROWS) * c.heads;
+        for (int r0 = 0; r0 < a.R; r0 += THREADS) {
+            const int r_ = r0 + tid;
+            int f_ = 0, n_ = 0, kv_ = 0;
+            int64_t x = 0;
+            if (r_ < a.R) {
+                request_of(c, a, r_, f_, n_, kv_);
+                x = count(n_, kv_);
             }
-            int s = x;
+            int64_t s = x;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int up = __shfl_up_sync(0xffffffffu, s, o);
+                const int64_t up = __shfl_up_sync(0xffffffffu, s, o);
                 if (lane >= o) s += up;
             }
             if (lane == 31) scan[warp] = s;
@@ -130,26 +148,75 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                 if (w < warp) before += scan[w];
                 all += scan[w];
             }
-            const int64_t mine = static_cast<int64_t>(blockIdx.x) - (before + s - x);
-            if (mine >= 0 && mine < x) {
-                item[0] = r; item[1] = first; item[2] = n; item[3] = kv;
-                item_at = static_cast<int>(mine);
+            const int64_t in = static_cast<int64_t>(blockIdx.x) - (before + s - x);
+            if (in >= 0 && in < x) {
+                item[0] = r_; item[1] = f_; item[2] = n_; item[3] = kv_;
+                item_at = static_cast<int>(in);
             }
             carry += all;
             __syncthreads();
         }
+        return carry;
+    };
+    __syncthreads();
+    const int64_t items = over_requests([&](int n_, int) { return static_cast<int64_t>(items_of(n_)) * c.heads; });
+    int parts = 1, mine = 0, tile = 0, h = 0;                   // parts of the item, this one, row tile, kv head
+    const bool split = 2 * items <= pl.sms && items > 0;
+    if (split) {
+        auto steps_of = [&](int n_, int kv_, int per) {         // per > 0: parts of that many steps instead
+            int64_t total = 0;
+            int x[4];
+            for (int i = 0; i < items_of(n_); ++i) {
+                const int st = max(range_of(n_, kv_, i, x[0], x[1], x[2], x[3]), 1);
+                total += per > 0 ? (st + per - 1) / per : st;
+            }
+            return total * c.heads;
+        };
+        // The rows kernel's requests want SMs at the same time: a step takes an SM as long as
+        // about six of its units (64 keys, 16 rows).
+        auto units_of = [&](int n_, int kv_) {
+            if (!rows_take(pl, n_, G)) return int64_t(0);
+            int f0, s0, f1, s1;
+            row_range(a, n_, kv_, 0, f0, s0);
+            row_range(a, n_, kv_, n_ - 1, f1, s1);
+            return static_cast<int64_t>((max(s1 - f0, 0) >> 6) + 1) * ((n_ * G + 15) >> 4) * c.heads;
+        };
+        const int64_t steps_all = over_requests([&](int n_, int kv_) { return steps_of(n_, kv_, 0); });
+        const int64_t units_all = over_requests(units_of);
+        const int64_t share = pl.sms * 6 * steps_all / (6 * steps_all + units_all);
+        const int64_t room = max(share - items, int64_t(1));
+        const int per = max(MIN_STEPS, static_cast<int>(min((steps_all + room - 1) / room, static_cast<int64_t>(INT_MAX / 2))));
+        if (tid == 0) item[0] = -1;
+        __syncthreads();
+        over_requests([&](int n_, int kv_) { return steps_of(n_, kv_, per); });
+        if (item[0] >= 0) {
+            int x[4];
+            mine = item_at;
+            for (tile = items_of(item[2]) - 1;; --tile) {
+                parts = (max(range_of(item[2], item[3], tile, x[0], x[1], x[2], x[3]), 1) + per - 1) / per;
+                if (mine < parts * c.heads || tile == 0) break;
+                mine -= parts * c.heads;
+            }
+            h = mine / parts;
+            mine -= h * parts;
+        }
+    } else if (item[0] >= 0) {
+        tile = items_of(item[2]) - 1 - item_at / c.heads;
+        h = item_at % c.heads;
     }
-    if (item_at < 0) return;
     const int r = item[0], first = item[1], n = item[2], kv = item[3];
-    const int h = item_at % c.heads;
-    const int row0 = ((static_cast<int>((static_cast<int64_t>(n) * G + ROWS - 1) / ROWS)) - 1 - item_at / c.heads) * ROWS;
-    const int rows = min(ROWS, n * G - row0);
-    // keys that some row sees, and those that all rows see
-    int tfrom, tstop, all_from, all_stop;
-    row_range(a, n, kv, row0 / G, tfrom, all_stop);
-    row_range(a, n, kv, (row0 + rows - 1) / G, all_from, tstop);
-    const int key0 = (tfrom / KEYS) * KEYS;
-    const int steps = tstop > key0 ? (tstop - key0 + KEYS - 1) / KEYS : 0;
+    const int row0 = tile * ROWS, rows = min(ROWS, n * G - row0);
+    if (tid == 0 && blockIdx.x < ATTN_TILE_CTAS)
+        pl.share[blockIdx.x] = TileShare{r >= 0 && mine == 0 ? parts : 0, rows, row0, first, h, split, {0, 0}};
+    if (r < 0) return;
+    int key0, tstop, all_from, all_stop;
+    int steps = range_of(n, kv, tile, key0, tstop, all_from, all_stop);
+    if (parts > 1) {
+        const int s0 = static_cast<int>(static_cast<int64_t>(mine) * steps / parts),
+                  s1 = static_cast<int>(static_cast<int64_t>(mine + 1) * steps / parts);
+        key0 += s0 * KEYS;
+        steps = s1 - s0;
+    }
 
     if (tid == 0) {
         mbar_init(&bars[B_Q], SOFT);
@@ -409,7 +476,50 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
 #pragma unroll
             for (int i = 0; i < SPLIT; ++i) l += exch[steps & 1][i][row];
         }
-        if (ok) {
+        auto load_o = [&](uint32_t at, uint32_t (&orr)[32]) {
+            if (steps == 0) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) orr[i] = 0;
+                return;
+            }
+            tc::ld32(at, orr);
+            tc::wait_ld();
+            if constexpr (F32) {
+                uint32_t os[32];
+                tc::ld32(at + (W::O1 - W::O0), os);
+                tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) orr[i] = __float_as_uint(__uint_as_float(orr[i]) + __uint_as_float(os[i]));
+            }
+        };
+        if (ok && parts > 1) {
+            // Sums as they are, fp32, to the workspace: half the columns at a time through the query operand's place.
+            constexpr int PC = D / 2, NC = PC / 4, SW = (NC < 8 ? NC : 8) - 1, ROWF = D + 4;
+            float* mine_ = reinterpret_cast<float*>(smem + W::OFF_Q + warp * (32 * PC * 4));
+            float* dst = pl.tile_part + static_cast<int64_t>(blockIdx.x) * (256 * ROWF) + (128 * mt + (warp & 3) * 32) * ROWF;
+#pragma unroll
+            for (int ps = 0; ps < OC / PC; ++ps) {
+#pragma unroll
+                for (int ch = 0; ch < PC / 32; ++ch) {
+                    uint32_t orr[32];
+                    load_o(o_col + ps * PC + 32 * ch, orr);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<uint4*>(mine_ + lane * PC + (((32 * ch + i) / 4) ^ (lane & SW)) * 4) =
+                            make_uint4(orr[i], orr[i + 1], orr[i + 2], orr[i + 3]);
+                }
+                __syncwarp();
+#pragma unroll 4
+                for (int x = lane; x < 32 * NC; x += 32) {
+                    const int lr = x / NC, cc = x % NC;
+                    if (128 * mt + (warp & 3) * 32 + lr < rows)
+                        *reinterpret_cast<uint4*>(dst + lr * ROWF + OC * part + ps * PC + cc * 4) =
+                            *reinterpret_cast<const uint4*>(mine_ + lr * PC + (cc ^ (lr & SW)) * 4);
+                }
+                __syncwarp();
+            }
+            if (row < rows && part == 0) { dst[lane * ROWF + D] = M; dst[lane * ROWF + D + 1] = l; }
+        } else if (ok) {
             // A row a thread in tensor memory, but a row a few lanes in global memory: the
             // warp's rows change hands in the query operand's place, which no MMA reads any more.
             constexpr int CH = 16 / sizeof(T), NC = OC / CH;                 // values of a 16-byte chunk, chunks of the warp's columns
@@ -420,20 +530,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
 #pragma unroll
             for (int ch = 0; ch < OC / 32; ++ch) {
                 uint32_t orr[32];
-                if (steps > 0) {
-                    tc::ld32(o_col + 32 * ch, orr);
-                    tc::wait_ld();
-                    if constexpr (F32) {
-                        uint32_t os[32];
-                        tc::ld32(o_col + (W::O1 - W::O0) + 32 * ch, os);
-                        tc::wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) orr[i] = __float_as_uint(__uint_as_float(orr[i]) + __uint_as_float(os[i]));
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) orr[i] = 0;
-                }
+                load_o(o_col + 32 * ch, orr);
 #pragma unroll
                 for (int i = 0; i < 32; i += CH) {
                     T* dst = reinterpret_cast<T*>(mine + lane * (OC * sizeof(T)) + (((32 * ch + i) / CH) ^ (lane & SW)) * 16);
@@ -667,8 +764,9 @@ cudaError_t launch_tiles_t(const DeviceInfo& dev, const KvView& c, const AttnArg
     if (e != cudaSuccess) return e;
     const int64_t G = a.heads / c.heads;
     // Each request that this kernel takes has at most one part-filled item more than its rows make
-    const int64_t items = (a.T * G / W::ROWS + std::min<int64_t>(a.R, a.T * G / pl.tile_rows + 1)) * c.heads;
+    int64_t items = (a.T * G / W::ROWS + std::min<int64_t>(a.R, a.T * G / pl.tile_rows + 1)) * c.heads;
     if (items > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    items = std::max<int64_t>(items, pl.sms);              // parts of items
     return launch_kernel(attn_tiles_kernel<T, D>, dim3(static_cast<unsigned>(items)), dim3(THREADS), W::SMEM, s, c, a, pl);
 }
 

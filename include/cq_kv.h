@@ -131,9 +131,9 @@ cq_status cq_kv_read(const cq_kv_cache* cache, cq_dtype dtype, int64_t T, const 
  * A row that sees nothing gets out = 0 and lse = -inf; a hidden key never
  * reaches a row, whatever it or its block's scale holds. Rows of no request
  * (t >= q_start[R]) are not written. Softmax statistics and sums are fp32. fp32 q
- * enters the products with 22 bits and the probabilities with at least as many; 16-bit q
- * enters exactly and the probabilities as binary16 (11 bits; below 2^-31 of the row's
- * largest they add nothing). Scales are not negative; a q that is not finite
+ * enters the products with 22 bits, the probabilities with 22 (those below 2^-15 of the
+ * row's largest with 16 at least); 16-bit q enters exactly and the probabilities as
+ * binary16 (11 bits; below 2^-31 of the row's largest they add nothing). Scales are not negative; a q that is not finite
  * makes its own row NaN.
  * Pages outside [0, num_pages) are hidden and flagged in the library's status
  * word (CQ_DEV_KV_PAGE); lengths are clipped to the table and to T.

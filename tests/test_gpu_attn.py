@@ -297,3 +297,32 @@ def test_offsets_past_32_bits():
     c["table"] = np.where(c["table"] >= 0, np.array(ids)[np.maximum(c["table"], 0)], -1).astype(np.int32)
     got = _run(torch, cq, c)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D,Hq,H,P", [(64, 8, 2, 16), (128, 4, 1, 64), (128, 7, 1, 16), (64, 4, 4, 128)])
+@pytest.mark.parametrize("kv,n", [([3000], [40]), ([5000, 2111], [100, 64]), ([1500, 90, 4100], [70, 90, 1])])
+def test_few_rows_over_long_contexts(dtype, D, Hq, H, P, kv, n):
+    """Chunks of some tens of tokens: work split over the keys and joined."""
+    torch, cq = torch_cuda(), cq_built()
+    c = _case(torch, cq, [D, Hq, kv[0]], dtype, Hq, H, D, P, kv, n)
+    for causal, window in ((True, 0), (True, 700), (False, 0), (False, 2000)):
+        _check(c, *_run(torch, cq, c, causal=causal, window=window), causal=causal, window=window)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_one_chunk_among_many_tokens(dtype):
+    """More requests than a warp looks over at once, one of them a chunk; a workspace used again by another shape."""
+    torch, cq = torch_cuda(), cq_built()
+    rng = np.random.default_rng(7)
+    ws = None
+    for R, at, n in ((70, 66, 150), (500, 3, 60), (2, 0, 50)):
+        kv = rng.integers(1, 400, R)
+        new = np.ones(R, np.int32)
+        kv[at], new[at] = 2500, n
+        c = _case(torch, cq, R, dtype, 8, 2, 64, 16, kv, new)
+        ws = cq.attn_workspace_t(8, 2, 64) if ws is None else ws
+        out, lse = _run(torch, cq, c, ws=ws)
+        _check(c, out, lse)
+        again = _run(torch, cq, c, ws=ws)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
