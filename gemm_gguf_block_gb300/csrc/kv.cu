@@ -170,8 +170,7 @@ struct AppendParams {
 };
 
 __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
-    return (static_cast<uint32_t>(a) & 0xffu) | ((static_cast<uint32_t>(b) & 0xffu) << 8) |
-           ((static_cast<uint32_t>(c) & 0xffu) << 16) | (static_cast<uint32_t>(d) << 24);
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
 // Four consecutive values as they were loaded, converted when they are used.
@@ -203,6 +202,14 @@ template <typename T> struct Raw4 {
         }
     }
 };
+
+// x to the nearest integer, halves away from zero, for |x| < 2^22: half a unit is
+// added away from zero and both the addition and the conversion are cut off, so
+// that nothing is rounded up across an integer. No clamp: |x * (1 / s)| is at most 127 (1 + 2^-22)
+// for every s that is not below the block's largest / 127.
+__device__ __forceinline__ int round_away(float x) {
+    return __float2int_rz(__fadd_rz(x, copysignf(0.5f, x)));
+}
 
 constexpr int APPEND_WARPS = 8;
 
@@ -300,7 +307,7 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) kv_append_kernel(const Appe
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     const float h = static_cast<float>(static_cast<int8_t>(w >> (8 * b)));
-                    z[b] = static_cast<int>(roundf(__fmul_rn(h, ratio)));
+                    z[b] = round_away(__fmul_rn(h, ratio));
                 }
                 *reinterpret_cast<uint32_t*>(q + i * D) = pack4(z[0], z[1], z[2], z[3]);
             }
@@ -309,7 +316,8 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) kv_append_kernel(const Appe
         for (int k = 0; k < NL; ++k) {
             const int i = row0 + k * RPW;
             const float4 f = v[k].value();
-            const uint32_t w = inv > 0.0f ? pack4(quant_q8(f.x, inv), quant_q8(f.y, inv), quant_q8(f.z, inv), quant_q8(f.w, inv)) : 0u;
+            const uint32_t w = inv > 0.0f ? pack4(round_away(__fmul_rn(f.x, inv)), round_away(__fmul_rn(f.y, inv)),
+                                              round_away(__fmul_rn(f.z, inv)), round_away(__fmul_rn(f.w, inv))) : 0u;
             if (i < n) *reinterpret_cast<uint32_t*>(q + (off + i) * D) = w;
         }
         // every warp has the old scale before it is replaced, and the largest values before the next run's
