@@ -211,6 +211,12 @@ __device__ __forceinline__ int round_away(float x) {
     return __float2int_rz(__fadd_rz(x, copysignf(0.5f, x)));
 }
 
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {      // NaN if any is
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 constexpr int APPEND_WARPS = 8;
 
 // A run is a stretch of tokens that lie one after another in one page: it begins
@@ -274,19 +280,21 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) kv_append_kernel(const Appe
         const float old = off == 0 ? 0.0f : *sp;
         const T* x = (which ? p.xv : p.xk) + (t0 + i0) * stride + head * D + col;
         Raw4<T> v[NL];
-        uint32_t a = 0;                                         // |x| as an integer keeps the order and puts infinities and NaN on top
         const int row0 = 16 * part + sub;
+        const T* xr = x + row0 * stride;
 #pragma unroll
         for (int k = 0; k < NL; ++k) {
             v[k].zero();
-            if (row0 + k * RPW < n) v[k].load(x + (row0 + k * RPW) * stride);
+            if (row0 + k * RPW < n) v[k].load(xr);
+            xr += RPW * stride;
         }
+        float far = 0.0f;
 #pragma unroll
         for (int k = 0; k < NL; ++k) {
             const float4 f = v[k].value();
-            a = max(max(a, max(__float_as_uint(fabsf(f.x)), __float_as_uint(fabsf(f.y)))),
-                    max(__float_as_uint(fabsf(f.z)), __float_as_uint(fabsf(f.w))));
+            far = max3_nan(max3_nan(far, fabsf(f.x), fabsf(f.y)), fabsf(f.z), fabsf(f.w));
         }
+        uint32_t a = __float_as_uint(far);                      // as an integer: the same order, infinities and NaN on top
         a = __reduce_max_sync(0xffffffffu, a);
         if (wpr > 1) {
             if (lane == 0) top[warp] = a;
@@ -318,7 +326,7 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) kv_append_kernel(const Appe
             const float4 f = v[k].value();
             const uint32_t w = inv > 0.0f ? pack4(round_away(__fmul_rn(f.x, inv)), round_away(__fmul_rn(f.y, inv)),
                                               round_away(__fmul_rn(f.z, inv)), round_away(__fmul_rn(f.w, inv))) : 0u;
-            if (i < n) *reinterpret_cast<uint32_t*>(q + (off + i) * D) = w;
+            if (i < n) *reinterpret_cast<uint32_t*>(q + static_cast<int64_t>(off + i) * D) = w;
         }
         // every warp has the old scale before it is replaced, and the largest values before the next run's
         if (wpr > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * wpr) : "memory");
