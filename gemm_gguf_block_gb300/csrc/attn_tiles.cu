@@ -36,7 +36,10 @@ namespace {
 constexpr int KEYS = 128;                 // keys of a step
 constexpr int SOFT = 256;                 // softmax threads
 constexpr int CONV = 128;                 // converter threads
-constexpr int THREADS = SOFT + CONV + 32;
+constexpr int THREADS = SOFT + CONV + 128;   // the last four warps: one issues the MMAs
+// Registers a thread of each role. 512 threads are launched with 128 each, and the
+// roles' sum is that: 256 * 176 + 128 * 104 + 128 * 56 = 512 * 128.
+constexpr int REGS_SOFT = 176, REGS_CONV = 104, REGS_MMA = 56;
 constexpr float OFF = TILES_OFF, RAISE = 8.0f;
 constexpr int MIN_STEPS = 3;              // a part of an item has at least so many, where it has parts
 constexpr int INFO = 4;                   // steps whose scales are kept
@@ -243,6 +246,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
 
     if (warp < SOFT / 32) {
         // ------------------------------------------------------------ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
         const int mt = (warp >> 2) / SPLIT, part = (warp >> 2) % SPLIT;      // row tile, part of the keys
         const int lrow = (warp & 3) * 32 + lane;            // row of the tile, lane of tensor memory
         const int row = 128 * mt + lrow;                    // of the item
@@ -333,48 +337,46 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             const float4* inf = info[j % INFO] + KT / 16 * part;
             const int k0 = key0 + j * KEYS + KT * part;
             const bool whole = k0 >= all_from && k0 + KT <= all_stop;
-            // Chunks of 32 keys, one's scores on their way while the other's are used (loops stay
-            // rolled up: the roles' code together has to fit the instruction cache).
-            uint32_t sa[32], sb[32];
-            auto chunks = [&](auto&& use) {
-                tc::ld32(s_col, sa);
-#pragma unroll 1
-                for (int ch = 0; ch < CHUNKS; ch += 2) {
-                    tc::wait_ld();
-                    tc::ld32(s_col + 32 * (ch + 1), sb);
-                    use(sa, ch);
-                    tc::wait_ld();
-                    if (ch + 2 < CHUNKS) tc::ld32(s_col + 32 * (ch + 2), sa);
-                    use(sb, ch + 1);
-                }
-            };
-            // the largest x: a block's from its largest score, since its factor is not negative
-            float top = -INFINITY;
-            if (whole) {
-                chunks([&](uint32_t (&v)[32], int ch) {
+            // The scores are read once and stay in registers: tensor memory gives about 100 bytes a
+            // cycle, and a second reading of 64 KB a tile and step was what the step waited for.
+            uint32_t v[CHUNKS][32];
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const float4 in = inf[2 * ch + b];
-                        float m = __uint_as_float(v[16 * b]);
+            for (int ch = 0; ch < CHUNKS; ++ch) tc::ld32(s_col + 32 * ch, v[ch]);
+            tc::wait_ld();
+            if (!whole) {
+                // x itself, hidden keys at -inf: factor 1 and no offset from here on
 #pragma unroll
-                        for (int i = 1; i < 15; i += 2) m = max3(m, __uint_as_float(v[16 * b + i]), __uint_as_float(v[16 * b + i + 1]));
-                        m = fmaxf(m, __uint_as_float(v[16 * b + 15]));
-                        top = fmaxf(top, fmaf(m, in.x * rf, in.y));
-                    }
-                });
-            } else {
-                chunks([&](uint32_t (&v)[32], int ch) {
+                for (int ch = 0; ch < CHUNKS; ++ch)
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const float4 in = inf[2 * ch + b];
                         const float f = in.x * rf;
                         const int key = k0 + 32 * ch + 16 * b;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (key + i >= from && key + i < stop) top = fmaxf(top, fmaf(__uint_as_float(v[16 * b + i]), f, in.y));
+                        for (int i = 0; i < 16; ++i) {
+                            const float x = fmaf(__uint_as_float(v[ch][16 * b + i]), f, in.y);
+                            v[ch][16 * b + i] = __float_as_uint(key + i >= from && key + i < stop ? x : -INFINITY);
+                        }
                     }
-                });
             }
+            // a block's factor and offset, and the weight of its probabilities in the sum
+            auto block = [&](int b) {
+                const float4 in = inf[b];
+                return make_float3(whole ? in.x * rf : 1.0f, whole ? in.y : 0.0f, in.z);
+            };
+            // the largest x: a block's from its largest score, since its factor is not negative
+            float top = -INFINITY;
+#pragma unroll
+            for (int ch = 0; ch < CHUNKS; ++ch)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const float3 k = block(2 * ch + b);
+                    float m = __uint_as_float(v[ch][16 * b]);
+#pragma unroll
+                    for (int i = 1; i < 15; i += 2) m = max3(m, __uint_as_float(v[ch][16 * b + i]), __uint_as_float(v[ch][16 * b + i + 1]));
+                    m = fmaxf(m, __uint_as_float(v[ch][16 * b + 15]));
+                    top = fmaxf(top, fmaf(m, k.x, k.y));
+                }
             // the row's other parts (a slot is written again two steps on, after the next meeting)
             if constexpr (SPLIT > 1) {
                 exch[j & 1][part][row] = top;
@@ -407,30 +409,26 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             // fp32: P's third part has columns of its own, the product of the step before has to be done with them
             if (F32 && !o_known) wait(B_O, (j - 1) & 1);
             const float base = M == -INFINITY ? 0.0f : M - OFF;
-            // (16-bit types: each part's P overlays its own scores, those that are in registers by then)
-            auto probabilities = [&](uint32_t (&v)[32], int ch, auto whole_) {
+            // (each part's P overlays its own scores, which are in registers)
+#pragma unroll
+            for (int ch = 0; ch < CHUNKS; ++ch) {
                 uint32_t pr[16];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const float4 in = inf[2 * ch + b];
-                    const float f = in.x * rf, lb = in.y - base;
-                    const uint64_t f2 = tc::pk(f, f), lb2 = tc::pk(lb, lb);
+                    const float3 k = block(2 * ch + b);
+                    const float lb = k.y - base;
+                    const uint64_t f2 = tc::pk(k.x, k.x), lb2 = tc::pk(lb, lb);
                     uint64_t sum2 = 0;
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
-                        const uint64_t x2 = tc::fma2(tc::pk(__uint_as_float(v[16 * b + i]), __uint_as_float(v[16 * b + i + 1])), f2, lb2);
+                        uint32_t &v0 = v[ch][16 * b + i], &v1 = v[ch][16 * b + i + 1];
                         float x0, x1;
-                        tc::upk(x2, x0, x1);
-                        if constexpr (!decltype(whole_)::value) {
-                            const int key = k0 + 32 * ch + 16 * b + i;
-                            x0 = key >= from && key < stop ? x0 : -INFINITY;
-                            x1 = key + 1 >= from && key + 1 < stop ? x1 : -INFINITY;
-                        }
+                        tc::upk(tc::fma2(tc::pk(__uint_as_float(v0), __uint_as_float(v1)), f2, lb2), x0, x1);
                         const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
                         sum2 = tc::add2(sum2, tc::pk(p0, p1));
                         if constexpr (F32) {
-                            v[16 * b + i] = __float_as_uint(p0);
-                            v[16 * b + i + 1] = __float_as_uint(p1);
+                            v0 = __float_as_uint(p0);
+                            v1 = __float_as_uint(p1);
                         } else {
                             const __half2 x = __floats2half2_rn(p0, p1);
                             pr[8 * b + i / 2] = *reinterpret_cast<const uint32_t*>(&x);
@@ -440,28 +438,25 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                     tc::upk(sum2, s0, s1);
                     const float sum = s0 + s1;
                     // a row that sees nothing here must not meet a scale that is not finite
-                    l += sum != 0.0f ? sum * in.z : 0.0f;
+                    l += sum != 0.0f ? sum * k.z : 0.0f;
                 }
                 if constexpr (F32) {
-                    tc::wait_ld();                           // the other chunk's scores are in registers too
 #pragma unroll
-                    for (int part = 0; part < 3; ++part) {
+                    for (int p3 = 0; p3 < 3; ++p3) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float p0 = __uint_as_float(v[2 * i]), p1 = __uint_as_float(v[2 * i + 1]);
+                            const float p0 = __uint_as_float(v[ch][2 * i]), p1 = __uint_as_float(v[ch][2 * i + 1]);
                             const __nv_bfloat162 x = __floats2bfloat162_rn(p0, p1);
                             pr[i] = *reinterpret_cast<const uint32_t*>(&x);
-                            v[2 * i] = __float_as_uint(p0 - __uint_as_float(pr[i] << 16));
-                            v[2 * i + 1] = __float_as_uint(p1 - __uint_as_float(pr[i] & 0xffff0000u));
+                            v[ch][2 * i] = __float_as_uint(p0 - __uint_as_float(pr[i] << 16));
+                            v[ch][2 * i + 1] = __float_as_uint(p1 - __uint_as_float(pr[i] & 0xffff0000u));
                         }
-                        tc::st16(part < 2 ? s_col + KT / 2 * part + 16 * ch : p3_col + 16 * ch, pr);
+                        tc::st16(p3 < 2 ? s_col + KT / 2 * p3 + 16 * ch : p3_col + 16 * ch, pr);
                     }
                 } else {
                     tc::st16(s_col + 16 * ch, pr);
                 }
-            };
-            if (whole) chunks([&](uint32_t (&v)[32], int ch) { probabilities(v, ch, std::true_type{}); });
-            else chunks([&](uint32_t (&v)[32], int ch) { probabilities(v, ch, std::false_type{}); });
+            }
             tc::wait_st();
             tc::fence_before();
             __syncwarp();
@@ -560,6 +555,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         }
     } else if (warp < (SOFT + CONV) / 32) {
         // ---------------------------------------------------------- converters
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_CONV));
         // A load takes 16 dimensions a lane of 8 keys. Eight lanes (a phase of a 16-byte
         // access) hold four pieces of an even key and four of the odd one after it; at D = 128
         // the other half of the row: the bytes then come from different banks of the lines,
@@ -663,6 +659,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         }
     } else {
         // --------------------------------------------------------- MMA issuer
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_MMA));
         if (warp == (SOFT + CONV) / 32 && steps > 0) {
         const uint32_t lead = tc::elect_one();
         const uint32_t q0 = smem_u32(smem + W::OFF_Q), k0 = smem_u32(smem + W::OFF_K), v0 = smem_u32(smem + W::OFF_V);
