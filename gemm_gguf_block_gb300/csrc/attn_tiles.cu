@@ -8,12 +8,13 @@
 // against 128 keys at a time.
 //   S = Q K^T: both from shared memory, K-major, 128-byte swizzle; K the stored
 //     integers as binary16 (exact). fp32 queries are two binary16 parts, two MMAs.
-//   O += P V: P from tensor memory over its scores' columns, V from shared memory as
-//     it lies in the cache (keys as rows, MN-major). fp32: P is three bfloat16 parts
-//     (24 bits over fp32's whole range), and V bfloat16.
+//   O += P V: P from tensor memory, V from shared memory as it lies in the cache (keys
+//     as rows, MN-major). fp32: P is three bfloat16 parts (24 bits over fp32's whole
+//     range), and V bfloat16.
 // Warps: 0-7 softmax, a thread to a row (fp32: two threads, 64 keys each); 8-11
 // convert the cache's bytes to operands, two stages of keys and two of values;
-// 12 issues the MMAs. While one tile's softmax runs, the other tile's MMAs do. (Two
+// 12 issues the MMAs, 13-15 only make the registers divisible. While one tile's
+// softmax runs, the other tile's MMAs do. (Two
 // threads a row, 16 softmax warps, measured the same: what the shorter loops gain, the
 // exchange of the rows' largest costs.)
 // Few items are split over their keys; the rows kernel, which always follows, joins
@@ -44,7 +45,7 @@ constexpr float OFF = TILES_OFF, RAISE = 8.0f;
 constexpr int MIN_STEPS = 3;              // a part of an item has at least so many, where it has parts
 constexpr int INFO = 4;                   // steps whose scales are kept
 
-enum { B_Q = 0, B_K_FULL = 1, B_K_EMPTY = 3, B_V_FULL = 5, B_V_EMPTY = 7, B_S = 9, B_P = 11, B_O = 13, B_INFO = 15 };
+enum { B_Q = 0, B_K_FULL = 1, B_K_EMPTY = 3, B_V_FULL = 5, B_V_EMPTY = 7, B_S = 9, B_P = 11, B_O = 13, B_INFO = 15, B_FREE = 19 };
 
 // Token and head of a kv head's group of an item's rows: rows count on from row0 = tok0 * G +
 // head0. The quotient by G <= 1024 of a number below 1280, by a reciprocal in 21 bits: exact,
@@ -73,7 +74,10 @@ template <typename T, int D> struct Tiles {
     static constexpr int OFF_K = OFF_Q + 2 * QB;
     static constexpr int OFF_V = OFF_K + 2 * KB;
     static constexpr int SMEM = OFF_V + 2 * KB + 1024;     // + alignment slack of the dynamic base
-    // Tensor memory columns. 16-bit types: the two tiles' scores (P overlays them) and results.
+    // Tensor memory columns. 16-bit types: the scores of one tile at a time, both tiles' P, both
+    // results. (A tile's scores are there only until its softmax has them in registers, so the
+    // other's next ones follow while the first is at work: no softmax waits for its own P's
+    // product. With 128 columns of scores a tile, P over them: 505 us, for 493 at the 8192-token prompt.)
     // fp32: scores -- two steps' where that fits, so that one step's are there before the
     // other's softmax is done --, overlaid by the first two parts of P, the third part, and two
     // results: of P's first part and of the other two. (The MMAs' sums are cut off, not rounded:
@@ -81,8 +85,8 @@ template <typename T, int D> struct Tiles {
     // part's 8.)
     static constexpr int SBUF = F32 && D == 64 ? 2 : 1;
     static constexpr uint32_t S0 = 0, S1 = 128;
-    static constexpr uint32_t SP = 128 * SBUF;             // fp32: P's third part
-    static constexpr uint32_t O0 = F32 ? SP + 64 : 256;
+    static constexpr uint32_t SP = 128 * SBUF;             // P, 64 columns a tile; fp32: P's third part
+    static constexpr uint32_t O0 = F32 ? SP + 64 : SP + 128;
     static constexpr uint32_t O1 = O0 + (F32 ? D : 128);   // fp32: the smaller result; else the second tile's
     static_assert(O1 + D <= 512, "tensor memory");
 };
@@ -231,6 +235,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             mbar_init(&bars[B_S + i], 1);
             mbar_init(&bars[B_P + i], SOFT / 32 / MT);
             mbar_init(&bars[B_O + i], 1);
+            mbar_init(&bars[B_FREE + i], SOFT / 32 / MT);
         }
         for (int i = 0; i < INFO; ++i) mbar_init(&bars[B_INFO + i], CONV / 32);
         fence_mbar_init();
@@ -316,7 +321,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         const float rf = rowf[row];
         int from = 0, stop = 0;
         if (row < rows) row_range(a, n, kv, my_tok, from, stop);
-        const uint32_t s_col0 = tmem + lanes + (mt == 0 ? W::S0 : W::S1) + KT * part;
+        const uint32_t s_col0 = tmem + lanes + W::S0 + KT * part;
+        const uint32_t p_col = tmem + lanes + W::SP + 64 * mt;                         // 16-bit types
         const uint32_t p3_col = tmem + lanes + W::SP + KT / 2 * part;
         const uint32_t o_col = tmem + lanes + (mt == 0 ? W::O0 : W::O1) + OC * part;
         constexpr int CHUNKS = KT / 32;
@@ -337,12 +343,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             const float4* inf = info[j % INFO] + KT / 16 * part;
             const int k0 = key0 + j * KEYS + KT * part;
             const bool whole = k0 >= all_from && k0 + KT <= all_stop;
-            // The scores are read once and stay in registers: tensor memory gives about 100 bytes a
-            // cycle, and a second reading of 64 KB a tile and step was what the step waited for.
+            // The scores are read once and stay in registers (read twice, 522 us for 501 at the
+            // 8192-token prompt).
             uint32_t v[CHUNKS][32];
 #pragma unroll
             for (int ch = 0; ch < CHUNKS; ++ch) tc::ld32(s_col + 32 * ch, v[ch]);
             tc::wait_ld();
+            if constexpr (MT == 2) {                        // the other tile's scores may come
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars[B_FREE + mt]);
+            }
             if (!whole) {
                 // x itself, hidden keys at -inf: factor 1 and no offset from here on
 #pragma unroll
@@ -406,10 +417,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                     }
                 }
             }
-            // fp32: P's third part has columns of its own, the product of the step before has to be done with them
-            if (F32 && !o_known) wait(B_O, (j - 1) & 1);
+            // P (fp32: its third part) has columns of its own, the product of the step before has to be done with them
+            if (!o_known) wait(B_O + mt, (j - 1) & 1);
             const float base = M == -INFINITY ? 0.0f : M - OFF;
-            // (each part's P overlays its own scores, which are in registers)
+            // (fp32: each part's P overlays its own scores, which are in registers)
 #pragma unroll
             for (int ch = 0; ch < CHUNKS; ++ch) {
                 uint32_t pr[16];
@@ -454,7 +465,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                         tc::st16(p3 < 2 ? s_col + KT / 2 * p3 + 16 * ch : p3_col + 16 * ch, pr);
                     }
                 } else {
-                    tc::st16(s_col + 16 * ch, pr);
+                    tc::st16(p_col + 16 * ch, pr);
                 }
             }
             tc::wait_st();
@@ -629,33 +640,35 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         load(c.k, kr);
         load(c.v, vr);
         for (int j = 0; j < steps; ++j) {
+            const int st = j & 1;
+            if (__any_sync(0xffffffffu, abort_flag.get())) break;
+            // (the whole warp leaves or none of it: it shuffles)
+            if (!__all_sync(0xffffffffu, tc::wait_or_abort_sleep(&bars[B_K_EMPTY + st], ((j >> 1) & 1) ^ 1, abort_flag, a.status))) break;
+            store(smem + W::OFF_K + st * W::KB, kr, false);
+            fence_proxy_async_smem();
+            tc::mbar_arrive(&bars[B_K_FULL + st]);
+            // What was looked up for this step and the next is taken before any load is issued: right
+            // behind the values' loads, this waited for them (1800 cycles a step).
             float4 in = make_float4(0.0f, -INFINITY, 1.0f, 0.0f);
             if (page >= 0) {
                 in.x = p_ks;
                 in.y = p_vs == 0.0f ? 0.0f : log2f(p_vs);
                 in.z = p_vs == 0.0f ? 1.0f : __frcp_rn(p_vs);
             }
-            page = checked(ahead);
-            ahead = entry(j + 2);
-            scales(page);
-            place(page, j + 1);
-            const int st = j & 1;
-            if (__any_sync(0xffffffffu, abort_flag.get())) break;
-            // (the whole warp leaves or none of it: it shuffles)
-            if (!__all_sync(0xffffffffu, tc::wait_or_abort_sleep(&bars[B_K_EMPTY + st], ((j >> 1) & 1) ^ 1, abort_flag, a.status))) break;
             // the step that used this entry before is past its softmax: the scores of two steps ago were its next
             if (lane < 2) info[j % INFO][2 * cw + lane] = in;
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars[B_INFO + j % INFO]);
-            store(smem + W::OFF_K + st * W::KB, kr, false);
+            page = checked(ahead);
+            ahead = entry(j + 2);
+            scales(page);
+            place(page, j + 1);
             load(c.k, kr);
-            fence_proxy_async_smem();
-            tc::mbar_arrive(&bars[B_K_FULL + st]);
             if (!__all_sync(0xffffffffu, tc::wait_or_abort_sleep(&bars[B_V_EMPTY + st], ((j >> 1) & 1) ^ 1, abort_flag, a.status))) break;
             store(smem + W::OFF_V + st * W::KB, vr, F32);
-            load(c.v, vr);
             fence_proxy_async_smem();
             tc::mbar_arrive(&bars[B_V_FULL + st]);
+            load(c.v, vr);
         }
     } else {
         // --------------------------------------------------------- MMA issuer
@@ -672,7 +685,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         const uint64_t qd = tc::smem_desc_sw128(q0, 1024), kd = tc::smem_desc_sw128(k0, 1024),
                        vd = tc::smem_desc_sw128_mn(v0, KEYS * 128, 1024);
         auto scores = [&](int m, int st) {                  // fp32: m is the buffer
-            const uint32_t d = tmem + (m == 0 ? W::S0 : W::S1);
+            const uint32_t d = tmem + (MT == 2 || m == 0 ? W::S0 : W::S1);
             const uint64_t bd = kd + st * (W::KB >> 4);
 #pragma unroll
             for (int part = 0; part < (F32 ? 2 : 1); ++part) {
@@ -686,7 +699,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         };
         auto product = [&](int m, int st, bool add) {       // m: the tile; fp32: the scores' buffer
             const uint64_t bd = vd + st * (W::KB >> 4);
-            const uint32_t p0 = tmem + (m == 0 ? W::S0 : W::S1);
+            const uint32_t p0 = tmem + (MT == 2 ? W::SP + 64 * m : m == 0 ? W::S0 : W::S1);
 #pragma unroll
             for (int part = 0; part < (F32 ? 3 : 1); ++part)
 #pragma unroll
@@ -703,19 +716,28 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             return __all_sync(0xffffffffu, got) != 0;
         };
         bool ok = wait(B_Q, 0) && wait(B_K_FULL, 0);
-        if (ok) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                scores(m, 0);
-                tc::commit_lead(&bars[B_S + m], lead);
-            }
-            tc::commit_lead(&bars[B_K_EMPTY], lead);
+        for (int m = 0; m < MT && ok; ++m) {
+            if (m == 1) ok = wait(B_FREE, 0);
+            if (!ok) break;
+            scores(m, 0);
+            tc::commit_lead(&bars[B_S + m], lead);
+            if (m == MT - 1) tc::commit_lead(&bars[B_K_EMPTY], lead);
         }
         for (int j = 0; j < steps && ok && !__any_sync(0xffffffffu, abort_flag.get()); ++j) {
             const int st = j & 1, nst = st ^ 1;
             const bool next = j + 1 < steps;
 #pragma unroll
             for (int m = 0; m < MT && ok; ++m) {
+                if (MT == 2 && next) {
+                    // the tile's next scores, once the other tile's last are in registers
+                    if (m == 0) ok = wait(B_K_FULL + nst, ((j + 1) >> 1) & 1);
+                    ok = ok && wait(B_FREE + (m ^ 1), (j + m) & 1);
+                    if (!ok) break;
+                    scores(m, nst);
+                    tc::commit_lead(&bars[B_S + m], lead);
+                    if (m == 1) tc::commit_lead(&bars[B_K_EMPTY + nst], lead);
+                }
                 if (SBUF == 2 && next) {
                     // the other buffer's scores: its softmax was waited for a step ago
                     ok = wait(B_K_FULL + nst, ((j + 1) >> 1) & 1);
@@ -731,13 +753,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                 product(SBUF == 2 ? st : m, st, j > 0);
                 tc::commit_lead(&bars[B_O + m], lead);
                 if (m == MT - 1) tc::commit_lead(&bars[B_V_EMPTY + st], lead);
-                if (SBUF == 1 && next) {
+                if (MT == 1 && SBUF == 1 && next) {
                     // P's columns are the scores': the MMAs run in the order they were issued in
-                    if (m == 0) ok = wait(B_K_FULL + nst, ((j + 1) >> 1) & 1);
+                    ok = wait(B_K_FULL + nst, ((j + 1) >> 1) & 1);
                     if (!ok) break;
-                    scores(m, nst);
-                    tc::commit_lead(&bars[B_S + m], lead);
-                    if (m == MT - 1) tc::commit_lead(&bars[B_K_EMPTY + nst], lead);
+                    scores(0, nst);
+                    tc::commit_lead(&bars[B_S], lead);
+                    tc::commit_lead(&bars[B_K_EMPTY + nst], lead);
                 }
             }
         }
