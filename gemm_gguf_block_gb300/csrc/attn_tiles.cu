@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
     __shared__ int item[4];                                // request, its first token, new tokens, length
     __shared__ int item_at;                                // index inside the request
     __shared__ int64_t scan[THREADS / 32];
-    __shared__ float4 info[INFO][KEYS / 16];
+    __shared__ __align__(16) float info[INFO][3][KEYS / 16];   // s_k, log2 s_v, 1 / s_v of a step's blocks
     __shared__ float rowf[ROWS];                           // the rows' factors
     __shared__ float exch[2][SPLIT][ROWS];                 // [step's parity]
     const SmemFlag abort_flag{smem_u32(&abort_word)};
@@ -330,19 +330,33 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         bool ok = true;
         // After a wait that ran out (ok false) the loop goes on without waiting: the meetings stay paired.
         auto wait = [&](int bar, int parity) {
-            if (ok && !mbar_wait_bounded(&bars[bar], parity, WAIT_LIMIT_NS)) ok = false;
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) abort_flag.set(1);
+            if (!ok || !__all_sync(0xffffffffu, mbar_try_wait(&bars[bar], parity))) {
+                if (ok && !mbar_wait_bounded(&bars[bar], parity, WAIT_LIMIT_NS)) ok = false;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) abort_flag.set(1);
+            }
             tc::fence_after();
         };
-        for (int j = 0; j < steps; ++j) {
+        // A step; whole: every row sees all its keys.
+        auto step = [&](const int j, auto whole_) {
+            constexpr bool whole = decltype(whole_)::value;
+            // The blocks' factors and offsets are there before the scores, and stay in registers: a
+            // 16-byte read of one address by all lanes occupies shared memory for four cycles.
+            wait(B_INFO + j % INFO, (j / INFO) & 1);
+            float fk[KT / 16], lv[KT / 16];
+            auto blocks = [&](int what, float (&x)[KT / 16]) {
+#pragma unroll
+                for (int b = 0; b < KT / 16; b += 4)
+                    *reinterpret_cast<float4*>(x + b) = *reinterpret_cast<const float4*>(&info[j % INFO][what][KT / 16 * part + b]);
+            };
+            blocks(0, fk);
+            blocks(1, lv);
+#pragma unroll
+            for (int b = 0; b < KT / 16; ++b) fk[b] *= rf;
             if constexpr (SBUF == 2) wait(B_S + (j & 1), (j >> 1) & 1);
             else wait(B_S + mt, j & 1);
             const uint32_t s_col = s_col0 + (SBUF == 2 ? (j & 1) * (W::S1 - W::S0) : 0);
-            wait(B_INFO + j % INFO, (j / INFO) & 1);
-            const float4* inf = info[j % INFO] + KT / 16 * part;
             const int k0 = key0 + j * KEYS + KT * part;
-            const bool whole = k0 >= all_from && k0 + KT <= all_stop;
             // The scores are read once and stay in registers (read twice, 522 us for 501 at the
             // 8192-token prompt).
             uint32_t v[CHUNKS][32];
@@ -354,39 +368,31 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bars[B_FREE + mt]);
             }
-            if (!whole) {
+            if constexpr (!whole) {
                 // x itself, hidden keys at -inf: factor 1 and no offset from here on
 #pragma unroll
                 for (int ch = 0; ch < CHUNKS; ++ch)
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        const float4 in = inf[2 * ch + b];
-                        const float f = in.x * rf;
                         const int key = k0 + 32 * ch + 16 * b;
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float x = fmaf(__uint_as_float(v[ch][16 * b + i]), f, in.y);
+                            const float x = fmaf(__uint_as_float(v[ch][16 * b + i]), fk[2 * ch + b], lv[2 * ch + b]);
                             v[ch][16 * b + i] = __float_as_uint(key + i >= from && key + i < stop ? x : -INFINITY);
                         }
                     }
             }
-            // a block's factor and offset, and the weight of its probabilities in the sum
-            auto block = [&](int b) {
-                const float4 in = inf[b];
-                return make_float3(whole ? in.x * rf : 1.0f, whole ? in.y : 0.0f, in.z);
-            };
             // the largest x: a block's from its largest score, since its factor is not negative
             float top = -INFINITY;
 #pragma unroll
             for (int ch = 0; ch < CHUNKS; ++ch)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const float3 k = block(2 * ch + b);
                     float m = __uint_as_float(v[ch][16 * b]);
 #pragma unroll
                     for (int i = 1; i < 15; i += 2) m = max3(m, __uint_as_float(v[ch][16 * b + i]), __uint_as_float(v[ch][16 * b + i + 1]));
                     m = fmaxf(m, __uint_as_float(v[ch][16 * b + 15]));
-                    top = fmaxf(top, fmaf(m, k.x, k.y));
+                    top = fmaxf(top, whole ? fmaf(m, fk[2 * ch + b], lv[2 * ch + b]) : m);
                 }
             // the row's other parts (a slot is written again two steps on, after the next meeting)
             if constexpr (SPLIT > 1) {
@@ -421,35 +427,41 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             if (!o_known) wait(B_O + mt, (j - 1) & 1);
             const float base = M == -INFINITY ? 0.0f : M - OFF;
             // (fp32: each part's P overlays its own scores, which are in registers)
+            // A chunk's exponentials all come before their sums and conversions, and no chunk's P is in
+            // another's registers: a pair at a time, one warp took 1100 cycles for its 128 keys, so 710.
+            uint32_t pr[CHUNKS][16];
+            float weight[KT / 16];
+            blocks(2, weight);
 #pragma unroll
             for (int ch = 0; ch < CHUNKS; ++ch) {
-                uint32_t pr[16];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const float3 k = block(2 * ch + b);
-                    const float lb = k.y - base;
-                    const uint64_t f2 = tc::pk(k.x, k.x), lb2 = tc::pk(lb, lb);
-                    uint64_t sum2 = 0;
+                    const float f = whole ? fk[2 * ch + b] : 1.0f, lb = (whole ? lv[2 * ch + b] : 0.0f) - base;
+                    const uint64_t f2 = tc::pk(f, f), lb2 = tc::pk(lb, lb);
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
                         uint32_t &v0 = v[ch][16 * b + i], &v1 = v[ch][16 * b + i + 1];
                         float x0, x1;
                         tc::upk(tc::fma2(tc::pk(__uint_as_float(v0), __uint_as_float(v1)), f2, lb2), x0, x1);
-                        const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
-                        sum2 = tc::add2(sum2, tc::pk(p0, p1));
-                        if constexpr (F32) {
-                            v0 = __float_as_uint(p0);
-                            v1 = __float_as_uint(p1);
-                        } else {
+                        v0 = __float_as_uint(exp2_approx(x0));
+                        v1 = __float_as_uint(exp2_approx(x1));
+                    }
+                }
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    uint64_t sums[2] = {0, 0};
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const float p0 = __uint_as_float(v[ch][16 * b + i]), p1 = __uint_as_float(v[ch][16 * b + i + 1]);
+                        sums[(i >> 1) & 1] = tc::add2(sums[(i >> 1) & 1], tc::pk(p0, p1));
+                        if constexpr (!F32) {
                             const __half2 x = __floats2half2_rn(p0, p1);
-                            pr[8 * b + i / 2] = *reinterpret_cast<const uint32_t*>(&x);
+                            pr[ch][8 * b + i / 2] = *reinterpret_cast<const uint32_t*>(&x);
                         }
                     }
                     float s0, s1;
-                    tc::upk(sum2, s0, s1);
-                    const float sum = s0 + s1;
-                    // a row that sees nothing here must not meet a scale that is not finite
-                    l += sum != 0.0f ? sum * k.z : 0.0f;
+                    tc::upk(tc::add2(sums[0], sums[1]), s0, s1);
+                    l = fmaf(s0 + s1, weight[2 * ch + b], l);        // (a weight is finite, or the sum is not)
                 }
                 if constexpr (F32) {
 #pragma unroll
@@ -458,20 +470,25 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                         for (int i = 0; i < 16; ++i) {
                             const float p0 = __uint_as_float(v[ch][2 * i]), p1 = __uint_as_float(v[ch][2 * i + 1]);
                             const __nv_bfloat162 x = __floats2bfloat162_rn(p0, p1);
-                            pr[i] = *reinterpret_cast<const uint32_t*>(&x);
-                            v[ch][2 * i] = __float_as_uint(p0 - __uint_as_float(pr[i] << 16));
-                            v[ch][2 * i + 1] = __float_as_uint(p1 - __uint_as_float(pr[i] & 0xffff0000u));
+                            pr[ch][i] = *reinterpret_cast<const uint32_t*>(&x);
+                            v[ch][2 * i] = __float_as_uint(p0 - __uint_as_float(pr[ch][i] << 16));
+                            v[ch][2 * i + 1] = __float_as_uint(p1 - __uint_as_float(pr[ch][i] & 0xffff0000u));
                         }
-                        tc::st16(p3 < 2 ? s_col + KT / 2 * p3 + 16 * ch : p3_col + 16 * ch, pr);
+                        tc::st16(p3 < 2 ? s_col + KT / 2 * p3 + 16 * ch : p3_col + 16 * ch, pr[ch]);
                     }
                 } else {
-                    tc::st16(p_col + 16 * ch, pr);
+                    tc::st16(p_col + 16 * ch, pr[ch]);
                 }
             }
             tc::wait_st();
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars[B_P + mt]);
+        };
+        for (int j = 0; j < steps; ++j) {
+            const int k0 = key0 + j * KEYS + KT * part;
+            if (k0 >= all_from && k0 + KT <= all_stop) step(j, std::true_type{});
+            else step(j, std::false_type{});
         }
         // ---- the rows
         if (steps > 0) wait(B_O + mt, (steps - 1) & 1);
@@ -606,23 +623,27 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             p_ks = c.k_scale[page * c.scale_stride + h];
             p_vs = c.v_scale[page * c.scale_stride + h];
         };
-        uint4 kr[GROUPS][NL], vr[GROUPS][NL];
+        uint4 kr[GROUPS][NL] = {}, vr[GROUPS][NL] = {};
         auto load = [&](const int8_t* src, uint4 (&x)[GROUPS][NL]) {
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
                 for (int i = 0; i < NL; ++i) {
-                    x[g][i] = make_uint4(0, 0, 0, 0);
-                    if (at[g >> 1] >= 0)
+                    if (at[g >> 1] >= 0)                    // else what it held: integers that meet a P of zero
                         x[g][i] = ldg_stream16(src + at[g >> 1] + (8 * (g & 1) + ck) * D + 16 * piece(i));
                 }
         };
+        int put[NL][2];                                     // a piece's places in the operand; 8 keys on are 8 rows
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            put[i][0] = tc::tile_off_sw128(32 * cw + ck, 16 * piece(i), KEYS);
+            put[i][1] = tc::tile_off_sw128(32 * cw + ck, 16 * piece(i) + 8, KEYS);
+        }
         auto store = [&](uint8_t* dst, const uint4 (&x)[GROUPS][NL], bool bf) {      // bf: bfloat16
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
                 for (int i = 0; i < NL; ++i) {
-                    const int key = 32 * cw + 8 * g + ck, d = 16 * piece(i);
                     const uint32_t w[4] = {x[g][i].x, x[g][i].y, x[g][i].z, x[g][i].w};
                     uint32_t o[8];
 #pragma unroll
@@ -630,8 +651,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                         if (bf) s8x4_bf16(w[k], o[2 * k], o[2 * k + 1]);
                         else tc::s8x4_half(w[k], o[2 * k], o[2 * k + 1]);
                     }
-                    *reinterpret_cast<uint4*>(dst + tc::tile_off_sw128(key, d, KEYS)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4*>(dst + tc::tile_off_sw128(key, d + 8, KEYS)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    *reinterpret_cast<uint4*>(dst + put[i][0] + 8 * g * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(dst + put[i][1] + 8 * g * 128) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
         };
         int page = checked(entry(0)), ahead = entry(1);
@@ -649,14 +670,18 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             tc::mbar_arrive(&bars[B_K_FULL + st]);
             // What was looked up for this step and the next is taken before any load is issued: right
             // behind the values' loads, this waited for them (1800 cycles a step).
-            float4 in = make_float4(0.0f, -INFINITY, 1.0f, 0.0f);
+            float3 in = make_float3(0.0f, -INFINITY, 1.0f);
             if (page >= 0) {
                 in.x = p_ks;
                 in.y = p_vs == 0.0f ? 0.0f : log2f(p_vs);
-                in.z = p_vs == 0.0f ? 1.0f : __frcp_rn(p_vs);
+                in.z = p_vs == 0.0f ? 1.0f : fminf(__frcp_rn(p_vs), 3.402823466e38f);   // finite: it meets sums of 0
             }
             // the step that used this entry before is past its softmax: the scores of two steps ago were its next
-            if (lane < 2) info[j % INFO][2 * cw + lane] = in;
+            if (lane < 2) {
+                info[j % INFO][0][2 * cw + lane] = in.x;
+                info[j % INFO][1][2 * cw + lane] = in.y;
+                info[j % INFO][2][2 * cw + lane] = in.z;
+            }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars[B_INFO + j % INFO]);
             page = checked(ahead);
