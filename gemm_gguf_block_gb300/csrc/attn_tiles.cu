@@ -66,6 +66,17 @@ struct RowMap {
     }
 };
 
+__device__ __forceinline__ float log2_approx(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 template <typename T, int D> struct Tiles {
     static constexpr bool F32 = std::is_same<T, float>::value;
     static constexpr int MT = F32 ? 1 : 2;                 // row tiles
@@ -615,12 +626,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         };
         int64_t at[2];
         auto place = [&](int page, int j) {
+            const int k = key0 + j * KEYS + 32 * cw + 16 * lane;
+            const int64_t mine = page >= 0 ? page * c.page_stride + head_off + static_cast<int64_t>(k & (c.page_size - 1)) * D : -1;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int pg = __shfl_sync(0xffffffffu, page, b);
-                const int k = key0 + j * KEYS + 32 * cw + 16 * b;
-                at[b] = pg >= 0 ? pg * c.page_stride + head_off + static_cast<int64_t>(k & (c.page_size - 1)) * D : -1;
-            }
+            for (int b = 0; b < 2; ++b) at[b] = __shfl_sync(0xffffffffu, mine, b);
         };
         float p_ks = 0.0f, p_vs = 0.0f;
         auto scales = [&](int page) {
@@ -667,7 +676,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         load(c.v, vr);
         for (int j = 0; j < steps; ++j) {
             const int st = j & 1;
-            if (__any_sync(0xffffffffu, abort_flag.get())) break;
+            if (j % 8 == 0 && __any_sync(0xffffffffu, abort_flag.get())) break;
             // (the whole warp leaves or none of it: it shuffles)
             if (!__all_sync(0xffffffffu, tc::wait_or_abort_sleep(&bars[B_K_EMPTY + st], ((j >> 1) & 1) ^ 1, abort_flag, a.status))) break;
             store(smem + W::OFF_K + st * W::KB, kr, false);
@@ -678,8 +687,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             float3 in = make_float3(0.0f, -INFINITY, 1.0f);
             if (page >= 0) {
                 in.x = p_ks;
-                in.y = p_vs == 0.0f ? 0.0f : log2f(p_vs);
-                in.z = p_vs == 0.0f ? 1.0f : fminf(__frcp_rn(p_vs), 3.402823466e38f);   // finite: it meets sums of 0
+                // (approximations to 2^-22 for the 16-bit types: the converters' time is the step's)
+                in.y = p_vs == 0.0f ? 0.0f : F32 ? log2f(p_vs) : log2_approx(p_vs);
+                in.z = p_vs == 0.0f ? 1.0f : fminf(F32 ? __frcp_rn(p_vs) : rcp_approx(p_vs), 3.402823466e38f);   // finite: it meets sums of 0
             }
             // the step that used this entry before is past its softmax: the scores of two steps ago were its next
             if (lane < 2) {
@@ -754,7 +764,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             tc::commit_lead(&bars[B_S + m], lead);
             if (m == MT - 1) tc::commit_lead(&bars[B_K_EMPTY], lead);
         }
-        for (int j = 0; j < steps && ok && !__any_sync(0xffffffffu, abort_flag.get()); ++j) {
+        for (int j = 0; j < steps && ok && !(j % 8 == 0 && __any_sync(0xffffffffu, abort_flag.get())); ++j) {
             const int st = j & 1, nst = st ^ 1;
             const bool next = j + 1 < steps;
 #pragma unroll
