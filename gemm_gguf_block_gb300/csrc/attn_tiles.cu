@@ -18,9 +18,9 @@
 // (Two threads a row, 16 softmax warps, measured 547 us for 522 at the 8192-token prompt:
 // the exchange of the rows' largest costs what the shorter loops gain. Eight converter
 // warps leave the softmax 168 registers or fewer, and it spills: 563 to 603 for 455.)
-// Measured, 8192 tokens, 32 heads on 8, dim 128, bf16: 455 us, 1.21 PFLOP/s. The softmax
-// (3000 of a step's 3600 cycles) and the converters (all of them) bound it together:
-// without the converters' loads and stores it takes 400, without the exponentials no less.
+// Measured, 8192 tokens, 32 heads on 8, dim 128, bf16: 437 us, 1.26 PFLOP/s. The softmax
+// (3000 of a step's 3500 cycles) and the converters bound it together: at 455 us it took
+// 400 without the converters' loads and stores, and no less without the exponentials.
 // Few items are split over their keys; the rows kernel, which always follows, joins
 // the parts.
 // A block of 16 keys carries (s_k, log2 s_v, 1 / s_v) in shared memory; a block outside
