@@ -124,14 +124,15 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_plan_kernel(const PlanParams 
         if (t < total) {
             const int r = last_le(qs, p.R, t);
             const int past = max(p.past[r], 0);
-            pos = past + (t - qs[r]);
-            const int64_t b0 = (past + int64_t(P1)) >> p.shift, b = pos >> p.shift;
+            const int64_t at = static_cast<int64_t>(past) + (t - qs[r]);         // passes 32 bits where past + new does
+            const int64_t b0 = (past + int64_t(P1)) >> p.shift, b = at >> p.shift;
             int page = -1;
             if (b < p.max_blocks) {
                 if (b < b0) page = p.table[r * p.max_blocks + b];
                 else if (b - b0 < ps[r + 1] - ps[r]) page = p.free_pages[ps[r] + (b - b0)];
             }
-            if (page >= 0 && page < p.num_pages) slot = (static_cast<int64_t>(page) << p.shift) + (pos & P1);
+            if (page >= 0 && page < p.num_pages) slot = (static_cast<int64_t>(page) << p.shift) + (at & P1);
+            if (at <= 0x7fffffff) pos = static_cast<int>(at);
         }
         p.slots[t] = slot;
         p.positions[t] = pos;

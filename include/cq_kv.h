@@ -73,7 +73,8 @@ typedef struct {
  * an earlier call. What does not fit is left out and flagged in used[1]:
  *   CQ_DEV_KV_LENGTH  a negative length, taken as 0
  *   CQ_DEV_KV_BLOCKS  a request longer than max_blocks pages: the tokens past
- *                     them get slot -1, kv_len stops at max_blocks * P
+ *                     them get slot -1, kv_len stops at max_blocks * P; a
+ *                     position past 2^31 - 1 is -1
  *   CQ_DEV_KV_PAGES   free_pages used up: table entry -1, slots -1
  *   CQ_DEV_KV_TOKENS  more than T new tokens: those past T are left out, and
  *                     q_start stops at T
