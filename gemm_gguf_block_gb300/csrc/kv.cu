@@ -111,18 +111,19 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_plan_kernel(const PlanParams 
             for (int64_t b = b0 + (ps[r + 1] - ps[r]); b < b1; ++b) p.table[r * p.max_blocks + b] = -1;
         }
     }
-    for (int j = first; j < pages; j += step) {
-        const int r = last_le(ps, p.R, j);
+    // (indices in 64 bits: pages and T may be near 2^31, where a step more passes 32)
+    for (int64_t j = first; j < pages; j += step) {
+        const int r = last_le(ps, p.R, static_cast<int>(j));
         const int64_t b0 = (max(p.past[r], 0) + int64_t(P1)) >> p.shift;
         int page = p.free_pages[j];
         if (page < 0 || page >= p.num_pages) page = -1;
         p.table[r * p.max_blocks + b0 + (j - ps[r])] = page;
     }
-    for (int t = first; t < p.T; t += step) {
+    for (int64_t t = first; t < p.T; t += step) {
         int64_t slot = -1;
         int pos = -1;
         if (t < total) {
-            const int r = last_le(qs, p.R, t);
+            const int r = last_le(qs, p.R, static_cast<int>(t));
             const int past = max(p.past[r], 0);
             const int64_t at = static_cast<int64_t>(past) + (t - qs[r]);         // passes 32 bits where past + new does
             const int64_t b0 = (past + int64_t(P1)) >> p.shift, b = at >> p.shift;
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_plan_kernel(const PlanParams 
     // it looks over every page id that the step uses.
     if (blockIdx.x == 0) {
         int fault = 0;
-        for (int j = tid; j < pages; j += PLAN_THREADS) {
+        for (int64_t j = tid; j < pages; j += PLAN_THREADS) {
             const int page = p.free_pages[j];
             if (page < 0 || page >= p.num_pages) fault = CQ_DEV_KV_PAGE;
         }
@@ -435,8 +436,8 @@ cudaError_t launch_kv_plan(const DeviceInfo& dev, int R, int page_shift, int64_t
     const int smem = 2 * (R + 1) * 4;
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kv_plan_kernel), smem);
     if (e != cudaSuccess) return e;
-    const int work = std::max(T, R + 1);
-    const int ctas = std::min(dev.sm_count, (work + PLAN_THREADS - 1) / PLAN_THREADS);
+    const int64_t work = std::max(T, R + 1);
+    const int64_t ctas = std::min<int64_t>(dev.sm_count, (work + PLAN_THREADS - 1) / PLAN_THREADS);
     return launch_kernel(kv_plan_kernel, dim3(static_cast<unsigned>(ctas)), dim3(PLAN_THREADS), static_cast<size_t>(smem), s, p);
 }
 

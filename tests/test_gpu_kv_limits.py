@@ -45,3 +45,24 @@ def test_plan_sum_of_two_largest_lengths():
     assert kv.tolist() == [32] and q_start.tolist() == [0, 100]
     assert (slots == -1).all() and pos.tolist() == [INT_MAX] + [-1] * 99
     assert used.tolist() == [0, cq.DEV_KV_BLOCKS | cq.DEV_KV_TOKENS]
+
+
+@pytest.mark.parametrize("T", [INT_MAX, INT_MAX - 3000])
+def test_plan_of_as_many_tokens_as_it_takes(T):
+    """The largest T: every entry is written, the last ones as the first (26 GB of outputs)."""
+    torch, cq = torch_cuda(), cq_built()
+    P = 128
+    past, new = np.array([7, INT_MAX // 2], np.int32), np.array([300, 5], np.int32)
+    table, free = np.array([[0, -1, -1], [0, 0, 0]], np.int32), np.array([2, 1], np.int32)
+    t = dev(torch, table)
+    kv, q_start, slots, pos, used = cq.kv_plan_t(dev(torch, past), dev(torch, new), t, dev(torch, free), P, 3, T)
+    assert t.tolist() == [[0, 2, 1], [0, 0, 0]] and kv.tolist() == [307, 3 * P] and q_start.tolist() == [0, 300, 305]
+    assert used.tolist() == [2, cq.DEV_KV_BLOCKS]
+    at = np.arange(7, 307)
+    assert slots[:305].tolist() == (np.array([0, 2, 1])[at // P] * P + at % P).tolist() + [-1] * 5
+    assert pos[:305].tolist() == at.tolist() + list(range(INT_MAX // 2, INT_MAX // 2 + 5))
+    for x in (slots, pos):
+        for i in range(305, T, 1 << 28):
+            assert bool((x[i:i + (1 << 28)] == -1).all())
+    del slots, pos, x
+    torch.cuda.empty_cache()
