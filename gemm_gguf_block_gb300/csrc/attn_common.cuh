@@ -81,6 +81,13 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
+// A block of zeros (value scale 0) adds to the sum alone. Its P must not set the reference that
+// the other blocks' are held to, whatever their scale, so it takes part as if its scale were
+// 2^ZERO_LOG: at 1, a row whose other blocks have scales of 1e-6 lost its bits in binary16 (85
+// times its error bound at 1e-8, and 0 at 1e-10). Its P stays a normal number beside scales of up
+// to 2^45, with 24 bits below its largest.
+constexpr float ZERO_LOG = -64.0f;
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float y;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));

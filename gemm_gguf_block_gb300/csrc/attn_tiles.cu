@@ -688,8 +688,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             if (page >= 0) {
                 in.x = p_ks;
                 // (approximations to 2^-22 for the 16-bit types: the converters' time is the step's)
-                in.y = p_vs == 0.0f ? 0.0f : F32 ? log2f(p_vs) : log2_approx(p_vs);
-                in.z = p_vs == 0.0f ? 1.0f : fminf(F32 ? __frcp_rn(p_vs) : rcp_approx(p_vs), 3.402823466e38f);   // finite: it meets sums of 0
+                in.y = p_vs == 0.0f ? ZERO_LOG : F32 ? log2f(p_vs) : log2_approx(p_vs);
+                in.z = p_vs == 0.0f ? exp2f(-ZERO_LOG) : fminf(F32 ? __frcp_rn(p_vs) : rcp_approx(p_vs), 3.402823466e38f);   // finite: it meets sums of 0
             }
             // the step that used this entry before is past its softmax: the scores of two steps ago were its next
             if (lane < 2) {

@@ -134,8 +134,9 @@ cq_status cq_kv_read(const cq_kv_cache* cache, cq_dtype dtype, int64_t T, const 
  * (t >= q_start[R]) are not written. Softmax statistics and sums are fp32. fp32 q
  * enters the products with 22 bits, the probabilities with 22 (those below 2^-15 of the
  * row's largest with 16 at least); 16-bit q enters exactly and the probabilities as
- * binary16 (11 bits; below 2^-31 of the row's largest they add nothing). Scales are not negative; a q that is not finite
- * makes its own row NaN.
+ * binary16 (11 bits; times its value scale -- 2^-64 for a block of zeros, scale 0 --, a probability
+ * below 2^-31 of the row's largest adds nothing to out). Scales are not negative, blocks of
+ * scale 0 hold zeros; a q that is not finite makes its own row NaN.
  * Pages outside [0, num_pages) are hidden and flagged in the library's status
  * word (CQ_DEV_KV_PAGE); lengths are clipped to the table and to T.
  * max_new, max_kv: the host's upper bounds of new tokens and of kv_len of any

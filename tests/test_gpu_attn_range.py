@@ -1,0 +1,32 @@
+"""Attention over the 8-bit cache at the ends of its ranges: value scales, windows and lengths."""
+import numpy as np
+import pytest
+
+from helpers import cq_built, dev, torch_cuda
+from test_gpu_attn import _case, _check, _run
+
+pytestmark = pytest.mark.gpu
+
+
+def _value_scales(torch, c, scales):
+    """The cache's value scales, page by page of the table; blocks of scale 0 hold zeros."""
+    pages = [int(p) for row in c["table"] for p in row if p >= 0]
+    for i, page in enumerate(pages):
+        c["vs"][page] = scales[i % len(scales)]
+        if scales[i % len(scales)] == 0.0:
+            c["v"][page] = 0
+    c["cache"].v.copy_(dev(torch, c["v"]))
+    c["cache"].v_scale.copy_(dev(torch, c["vs"]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n", [1, 3, 200])
+@pytest.mark.parametrize("small", [1e-4, 1e-6, 1e-8, 1e-10, 1e-15])
+def test_zero_blocks_beside_small_ones(dtype, n, small):
+    """Blocks of zeros count in the sum alone: the others keep their bits however small their scale (fp16 results of
+    the smallest are zero: of those, lse alone says something)."""
+    torch, cq = torch_cuda(), cq_built()
+    for zeros in ([0.0, small, small], [0.0, small], [small, 0.0, 0.0, 0.0]):
+        c = _case(torch, cq, [n, len(zeros)], dtype, 4, 2, 64, 16, [400], [n])
+        _value_scales(torch, c, zeros)
+        _check(c, *_run(torch, cq, c))
