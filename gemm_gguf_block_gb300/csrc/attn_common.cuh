@@ -88,6 +88,35 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // to 2^45, with 24 bits below its largest.
 constexpr float ZERO_LOG = -64.0f;
 
+// The sums of P / s_v are held without a factor 2^SUM_LOG: for scales down to append's smallest,
+// 2^-126, P up to 2^15 and 2^26 keys they stay below 2^128 (with nothing taken out they were
+// infinite from 2^-116 down), and beside scales of 2^60 they are above 2^-97.
+constexpr float SUM_LOG = 40.0f, SUM_DOWN = 1.0f / 1099511627776.0f;      // 2^-SUM_LOG
+
+__device__ __forceinline__ float log2_approx(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// What a value scale s gives its block: the offset of its scores, log2 s, and the factor of its
+// P in the sums. Finite whatever s is: the factor meets sums of 0 where a row sees nothing.
+template <bool EXACT>
+__device__ __forceinline__ void value_factors(float s, float& offset, float& weight) {
+    if (s == 0.0f) {
+        offset = ZERO_LOG;
+        weight = exp2f(-ZERO_LOG - SUM_LOG);
+        return;
+    }
+    offset = EXACT ? log2f(s) : log2_approx(s);
+    weight = fminf(EXACT ? __frcp_rn(s) : rcp_approx(s), 3.402823466e38f) * SUM_DOWN;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float y;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
@@ -171,7 +200,7 @@ __device__ __forceinline__ uint2 ldg_stream8(const void* p) {
 }
 
 // Four values of an output row from the sums: rho counts the rows (token,
-// head) of the request's kv head; acc, l in units of 2^(m - off).
+// head) of the request's kv head; acc in units of 2^(m - off), l in 2^(m - off + SUM_LOG).
 template <typename T, int D>
 __device__ __forceinline__ void write_row(const AttnArgs& a, int first, int h, int G, int rho, int col, float4 acc,
                                           float m, float l, float off) {
@@ -179,9 +208,9 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int first, int h, i
     const int head = h * G + rho % G;
     const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);      // 0 only where nothing was seen
     store4(static_cast<T*>(a.out) + tok * a.out_stride + head * D + col,
-           make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+           make_float4(acc.x * inv * SUM_DOWN, acc.y * inv * SUM_DOWN, acc.z * inv * SUM_DOWN, acc.w * inv * SUM_DOWN));
     if (col == 0 && a.lse != nullptr)
-        a.lse[tok * a.heads + head] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m - off + log2f(l));
+        a.lse[tok * a.heads + head] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m - off + SUM_LOG + log2f(l));
 }
 
 cudaError_t launch_attn_tiles(const DeviceInfo& dev, const KvView& c, int dtype, const AttnArgs& a, const RowsPlan& pl,

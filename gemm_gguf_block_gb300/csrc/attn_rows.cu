@@ -297,8 +297,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
     auto next_place = [&](int t0) { b_at = n_page >= 0 ? offset_of(n_page, place(t0 + lane / NSUB)) : -1; };
     auto next_scales = [&]() {
         b_ks = n_ks;
-        b_lv = n_vs == 0.0f ? ZERO_LOG : log2f(n_vs);
-        b_rv = n_vs == 0.0f ? exp2f(-ZERO_LOG) : __frcp_rn(n_vs);
+        value_factors<true>(n_vs, b_lv, b_rv);
     };
     // Tile t begins its way into L2: the lanes that hold it in its batch.
     auto prefetch = [&](int t, bool next) {

@@ -66,17 +66,6 @@ struct RowMap {
     }
 };
 
-__device__ __forceinline__ float log2_approx(float x) {
-    float y;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float rcp_approx(float x) {
-    float y;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 template <typename T, int D> struct Tiles {
     static constexpr bool F32 = std::is_same<T, float>::value;
     static constexpr int MT = F32 ? 1 : 2;                 // row tiles
@@ -575,13 +564,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                     T* dst = reinterpret_cast<T*>(mine + lane * (OC * sizeof(T)) + (((32 * ch + i) / CH) ^ (lane & SW)) * 16);
 #pragma unroll
                     for (int k = 0; k < CH; k += 4)
-                        store4(dst + k, make_float4(__uint_as_float(orr[i + k]) * inv, __uint_as_float(orr[i + k + 1]) * inv,
-                                                    __uint_as_float(orr[i + k + 2]) * inv, __uint_as_float(orr[i + k + 3]) * inv));
+                        store4(dst + k, make_float4(__uint_as_float(orr[i + k]) * inv * SUM_DOWN, __uint_as_float(orr[i + k + 1]) * inv * SUM_DOWN,
+                                                    __uint_as_float(orr[i + k + 2]) * inv * SUM_DOWN, __uint_as_float(orr[i + k + 3]) * inv * SUM_DOWN));
                 }
             }
             if (a.lse != nullptr && row < rows && part == 0)
                 a.lse[static_cast<int64_t>(first + my_tok) * a.heads + h * G + my_head] =
-                    l == 0.0f ? -INFINITY : 0.6931471805599453f * (M - OFF + log2f(l));
+                    l == 0.0f ? -INFINITY : 0.6931471805599453f * (M - OFF + SUM_LOG + log2f(l));
             __syncwarp();
             const int cc = lane % NC;
 #pragma unroll 4
@@ -688,8 +677,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             if (page >= 0) {
                 in.x = p_ks;
                 // (approximations to 2^-22 for the 16-bit types: the converters' time is the step's)
-                in.y = p_vs == 0.0f ? ZERO_LOG : F32 ? log2f(p_vs) : log2_approx(p_vs);
-                in.z = p_vs == 0.0f ? exp2f(-ZERO_LOG) : fminf(F32 ? __frcp_rn(p_vs) : rcp_approx(p_vs), 3.402823466e38f);   // finite: it meets sums of 0
+                value_factors<F32>(p_vs, in.y, in.z);
             }
             // the step that used this entry before is past its softmax: the scores of two steps ago were its next
             if (lane < 2) {

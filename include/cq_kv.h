@@ -136,7 +136,9 @@ cq_status cq_kv_read(const cq_kv_cache* cache, cq_dtype dtype, int64_t T, const 
  * row's largest with 16 at least); 16-bit q enters exactly and the probabilities as
  * binary16 (11 bits; times its value scale -- 2^-64 for a block of zeros, scale 0 --, a probability
  * below 2^-31 of the row's largest adds nothing to out). Scales are not negative, blocks of
- * scale 0 hold zeros; a q that is not finite makes its own row NaN.
+ * scale 0 hold zeros; a q that is not finite makes its own row NaN. Value scales are 0 or 2^-126
+ * (the smallest that cq_kv_append writes) to 2^60, and those that one row sees, 2^-64 for 0 among
+ * them, within 2^100 of one another: past that, a block of the smaller ones may lose its weight.
  * Pages outside [0, num_pages) are hidden and flagged in the library's status
  * word (CQ_DEV_KV_PAGE); lengths are clipped to the table and to T.
  * max_new, max_kv: the host's upper bounds of new tokens and of kv_len of any

@@ -30,3 +30,16 @@ def test_zero_blocks_beside_small_ones(dtype, n, small):
         c = _case(torch, cq, [n, len(zeros)], dtype, 4, 2, 64, 16, [400], [n])
         _value_scales(torch, c, zeros)
         _check(c, *_run(torch, cq, c))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Hq,D,kv,n", [(4, 64, [400], [1]), (4, 64, [400], [200]), (8, 128, [9000], [1]),
+                                       (4, 64, [6000], [30]), (8, 128, [300, 5000], [100, 5])])
+@pytest.mark.parametrize("scales", [[2.0 ** -126], [2.0 ** -120, 1.5 * 2.0 ** -118], [2.0 ** -116, 2.0 ** -60, 2.0 ** -30],
+                                    [2.0 ** 60], [2.0 ** 60, 1.0, 2.0 ** -30]])
+def test_value_scales_of_any_size(dtype, Hq, D, kv, n, scales):
+    """The sum of the probabilities does not depend on the values' size."""
+    torch, cq = torch_cuda(), cq_built()
+    c = _case(torch, cq, [D, kv[0]], dtype, Hq, 2, D, 16, kv, n)
+    _value_scales(torch, c, scales)
+    _check(c, *_run(torch, cq, c))
