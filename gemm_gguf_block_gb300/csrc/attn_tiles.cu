@@ -50,7 +50,7 @@ constexpr float OFF = TILES_OFF, RAISE = 8.0f;
 constexpr int MIN_STEPS = 3;              // a part of an item has at least so many, where it has parts
 constexpr int INFO = 4;                   // steps whose scales are kept
 
-enum { B_Q = 0, B_K_FULL = 1, B_K_EMPTY = 3, B_V_FULL = 5, B_V_EMPTY = 7, B_S = 9, B_P = 11, B_O = 13, B_INFO = 15, B_FREE = 19 };
+enum { B_Q = 0, B_K_FULL = 1, B_K_EMPTY = 3, B_V_FULL = 5, B_V_EMPTY = 7, B_S = 9, B_P = 11, B_O = 13, B_INFO = 15, B_FREE = 19, B_DRAINED = 21 };
 
 // Token and head of a kv head's group of an item's rows: rows count on from row0 = tok0 * G +
 // head0. The quotient by G <= 1024 of a number below 1280, by a reciprocal in 21 bits: exact,
@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             mbar_init(&bars[B_FREE + i], SOFT / 32 / MT);
         }
         for (int i = 0; i < INFO; ++i) mbar_init(&bars[B_INFO + i], CONV / 32);
+        mbar_init(&bars[B_DRAINED], 1);
         fence_mbar_init();
     }
     if (warp == (SOFT + CONV) / 32) {
@@ -791,13 +792,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                 }
             }
         }
+        // Wherever the loop was left: all MMAs issued, and their arrivals at the other barriers, are
+        // over before the tensor memory goes and the CTA's shared memory with it.
+        tc::commit_lead(&bars[B_DRAINED], lead);
+        (void)tc::wait_or_abort_sleep(&bars[B_DRAINED], 0, abort_flag, a.status);
         }
     }
-    // ---- every role has left its loop; no MMA is in flight before the tensor memory goes
+    // ---- every role has left its loop, and no MMA is in flight
     tc::fence_before();
-    __syncthreads();
-    if (abort_flag.get() && tid == 0)
-        for (int i = 0; i < MT; ++i) (void)mbar_wait_bounded(&bars[B_O + i], 0, WAIT_LIMIT_NS / 8);
     __syncthreads();
     tc::fence_after();
     if (warp == (SOFT + CONV) / 32) tc::tmem_dealloc(tmem, 512);
