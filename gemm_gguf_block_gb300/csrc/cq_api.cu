@@ -1,6 +1,7 @@
 // C ABI of libcq: argument validation and dispatch to the kernel launchers.
 // Every check runs before any launch, so an error return means that nothing
 // was launched and nothing was written. See include/cq.h and include/cq_kv.h for the contract.
+#include <algorithm>
 #include <cstdint>
 #include <atomic>
 #include <map>
@@ -557,7 +558,8 @@ cq_status cq_attn_paged(const cq_kv_cache* cache, cq_dtype dtype, int64_t R, int
     a.table = block_table; a.kv_len = kv_len; a.q_start = q_start;
     a.status = dev.status; a.ws = workspace;
     a.q_stride = q_stride; a.out_stride = out_stride;
-    a.max_blocks = max_blocks; a.window = window;
+    a.max_blocks = max_blocks;
+    a.window = std::min(window, int64_t(1) << 32);   // wider than any length and position: sums with positions stay in range
     a.max_new = max_new; a.max_kv = max_kv;
     a.scale = scale;
     a.R = static_cast<int>(R); a.T = static_cast<int>(T); a.heads = static_cast<int>(q_heads); a.causal = causal;

@@ -43,3 +43,13 @@ def test_value_scales_of_any_size(dtype, Hq, D, kv, n, scales):
     c = _case(torch, cq, [D, kv[0]], dtype, Hq, 2, D, 16, kv, n)
     _value_scales(torch, c, scales)
     _check(c, *_run(torch, cq, c))
+
+
+@pytest.mark.parametrize("n", [1, 200])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31, 2 ** 63 - 1])
+def test_windows_wider_than_any_length(n, causal, window):
+    """... leave everything to be seen, by tokens in front of the cache's first key too (more new tokens than keys)."""
+    torch, cq = torch_cuda(), cq_built()
+    c = _case(torch, cq, 5, "bf16", 4, 2, 64, 16, [300, 150, 3], [n, 190, 5])
+    _check(c, *_run(torch, cq, c, causal=causal, window=window), causal=causal, window=2 ** 31 - 1)
