@@ -92,8 +92,7 @@ __device__ __forceinline__ void request_range(const AttnArgs& a, int n, int kv, 
 __device__ __forceinline__ int request_units(const AttnArgs& a, int n, int kv) {
     int from, stop;
     request_range(a, n, kv, from, stop);
-    const int u = (stop + UNIT - 1) / UNIT - from / UNIT;
-    return max(u, 1);
+    return max((stop - 1) / UNIT + 1 - from / UNIT, 1);      // (stop may be near 2^31)
 }
 
 __device__ __forceinline__ int atomic_inc_acq_rel(int* p) {
@@ -263,8 +262,8 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
         row_range(a, pc.n, pc.kv, (RT * pc.i) / G, tfrom, pc.all_stop);
         row_range(a, pc.n, pc.kv, (RT * pc.i + pc.rows - 1) / G, pc.all_from, tstop);
         pc.k_begin = max(u0 + pc.piece0 * UNIT, (tfrom / TK) * TK);
-        pc.k_end = min(u0 + pc.piece1 * UNIT, tstop);
-        pc.ntile = pc.k_end > pc.k_begin ? (pc.k_end - pc.k_begin + TK - 1) / TK : 0;
+        pc.k_end = static_cast<int>(min(u0 + static_cast<int64_t>(pc.piece1) * UNIT, static_cast<int64_t>(tstop)));
+        pc.ntile = pc.k_end > pc.k_begin ? (pc.k_end - 1 - pc.k_begin) / TK + 1 : 0;
     };
     // What the loop over the tiles needs of its piece; the rest waits in shared memory.
     int k_begin = 0, k_end = 0, all_from = 0, all_stop = 0, turn = 0;

@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         row_range(a, n_, kv_, i * ROWS / G, key0_, all_stop_);
         row_range(a, n_, kv_, last / G, all_from_, stop_);
         key0_ = key0_ / KEYS * KEYS;
-        return stop_ > key0_ ? (stop_ - key0_ + KEYS - 1) / KEYS : 0;
+        return stop_ > key0_ ? (stop_ - 1 - key0_) / KEYS + 1 : 0;       // (stop may be near 2^31)
     };
     // The sum of count(n, kv) over the requests; where the CTA's index falls into a request's
     // count, notes the request and the index in it.
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         };
         for (int j = 0; j < steps; ++j) {
             const int k0 = key0 + j * KEYS + KT * part;
-            if (k0 >= all_from && k0 + KT <= all_stop) step(j, std::true_type{});
+            if (k0 >= all_from && k0 <= all_stop - KT) step(j, std::true_type{});
             else step(j, std::false_type{});
         }
         // ---- the rows

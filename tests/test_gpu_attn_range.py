@@ -53,3 +53,44 @@ def test_windows_wider_than_any_length(n, causal, window):
     torch, cq = torch_cuda(), cq_built()
     c = _case(torch, cq, 5, "bf16", 4, 2, 64, 16, [300, 150, 3], [n, 190, 5])
     _check(c, *_run(torch, cq, c, causal=causal, window=window), causal=causal, window=2 ** 31 - 1)
+
+
+def _longest(torch, cq, dtype, n, P=16, pages=4096):
+    """A request of as many tokens as a table takes, 2^31 - P, whose pages are a few over and over."""
+    rng = np.random.default_rng([n, pages])
+    blocks = 2 ** 31 // P - 1
+    k = np.clip(np.round(rng.standard_normal((pages, 1, P, 64)) * 36), -127, 127).astype(np.int8)
+    v = np.clip(np.round(rng.standard_normal((pages, 1, P, 64)) * 36), -127, 127).astype(np.int8)
+    s = (0.02 + 0.015 * rng.random((2, pages, 1))).astype(np.float32)
+    cache = cq.KVCache(dev(torch, k), dev(torch, v), dev(torch, s[0]), dev(torch, s[1]))
+    table = (torch.arange(blocks, device="cuda", dtype=torch.int32) % pages)[None]
+    q = dev(torch, (2.0 * rng.standard_normal((n, 1, 64))).astype(np.float32)).to(dtype)
+    lens = dev(torch, np.array([blocks * P], np.int32)), dev(torch, np.array([0, n], np.int32))
+    return q, cache, table, lens, k, v, s, blocks
+
+
+@pytest.mark.parametrize("n", [1, 50, 300])
+@pytest.mark.parametrize("dtype,P", [("float32", 16), ("bfloat16", 16), ("bfloat16", 32)])
+def test_window_at_the_end_of_the_longest_request(dtype, n, P):
+    """The same as a request that holds the last pages alone. (The tiles begin at other keys there: other roundings,
+    of some 1e-6 in fp32; in bfloat16 of 2^-12 in the probabilities, and of a place in the result.)"""
+    torch, cq = torch_cuda(), cq_built()
+    q, cache, table, (kv, start), *_, blocks = _longest(torch, cq, getattr(torch, dtype), n, P)
+    out, lse = cq.attn_paged_t(q, cache, table, kv, start, n, blocks * P, window=100)
+    tail = 1 + (n + 100) // P + 8
+    short = table[:, -tail:].contiguous()
+    want, wl = cq.attn_paged_t(q, cache, short, dev(torch, np.array([tail * P], np.int32)), start, n, tail * P, window=100)
+    tol = dict(atol=1e-5, rtol=1e-5) if dtype == "float32" else dict(atol=2.0 ** -9, rtol=2.0 ** -7)
+    torch.testing.assert_close(out, want, **tol)
+    torch.testing.assert_close(lse, wl, atol=1e-5, rtol=1e-5)
+    assert torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("n", [1, 64])
+def test_every_key_of_the_longest_request_counts(n):
+    """Queries of zero: lse is the logarithm of the number of keys. A CTA adds up to kv / 150 / 16 terms one after
+    another in fp32, each addition off by 2^-24 of the sum at most: 5.4e-2 in all."""
+    torch, cq = torch_cuda(), cq_built()
+    q, cache, table, (kv, start), *_ = _longest(torch, cq, torch.bfloat16, n)
+    _, lse = cq.attn_paged_t(torch.zeros_like(q), cache, table, kv, start, n, 2 ** 31 - 16, causal=False)
+    assert (lse.double() - np.log(2.0 ** 31 - 16)).abs().max().item() <= 5.4e-2
