@@ -376,11 +376,14 @@ def _torch_tables():
     return _tables["all"]
 
 
-def _stream_of(t, raw):
-    """The current stream of the tensor's device; no stream for a host tensor, whose call is refused here."""
-    i = t.get_device()
+def _stream_of(fn, raw, i, *tensors):
+    """The current stream of device i. A call whose tensors are on the host, or not all on that device, is refused here:
+    the library gets their addresses only."""
     if i < 0:
-        raise CqError("cq", ERR_INVALID_ARG)
+        raise CqError(fn, ERR_INVALID_ARG)
+    for t in tensors:
+        if t.get_device() != i:
+            raise CqError(fn, ERR_INVALID_ARG)
     return raw(i)
 
 
@@ -417,7 +420,7 @@ class KVCache:
     """An 8-bit paged key/value cache over the caller's tensors: k, v int8 [pages, kv heads, page tokens, head size]
     (pages may be strided: halves of one allocation), k_scale, v_scale fp32 [pages, kv heads]."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "num_pages", "kv_heads", "page_size", "head_dim", "_c", "addr")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "num_pages", "kv_heads", "page_size", "head_dim", "device", "_c", "addr")
 
     def __init__(self, k, v, k_scale, v_scale):
         torch = _torch()
@@ -428,6 +431,9 @@ class KVCache:
         n, h, p, d = k.shape
         if k.stride()[1:] != (p * d, d, 1) or (h > 1 and k_scale.stride(1) != 1):
             raise CqError("cq_kv_cache", ERR_SHAPE)
+        self.device = k.get_device()                     # -1 on the host: the calls refuse it
+        if any(t.get_device() != self.device for t in (v, k_scale, v_scale)):
+            raise CqError("cq_kv_cache", ERR_INVALID_ARG)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = n, h, p, d
         one = n <= 1     # a single page's strides say nothing
@@ -451,7 +457,7 @@ def kv_plan_t(past_len, new_len, block_table, free_pages, page_size: int, num_pa
     fn, R, n_free = "cq_kv_plan", past_len.shape[0], free_pages.shape[0]
     tp, wide = _table(fn, block_table, i32, R)
     past, new, free = _vec(fn, past_len, i32, R), _vec(fn, new_len, i32, R), _vec(fn, free_pages, i32, n_free)
-    stream = _stream_of(past_len, raw)
+    stream = _stream_of(fn, raw, past_len.get_device(), new_len, block_table, free_pages)
     dev = past_len.device
     # (an allocation each costs the host less than views of one)
     kv_len, q_start = torch.empty(R, dtype=i32, device=dev), torch.empty(R + 1, dtype=i32, device=dev)
@@ -474,7 +480,7 @@ def kv_append_t(cache: KVCache, k, v, slots):
     if Tv != T or v.dtype != dt:
         raise CqError(fn, ERR_SHAPE)
     st = (_lib or lib()).cq_kv_append(cache.addr, dtypes.get(dt, -1), T, kp, ks, vp, vs, _vec(fn, slots, i64, T),
-                                      _stream_of(slots, raw))
+                                      _stream_of(fn, raw, cache.device, k, v, slots))
     if st:
         raise CqError(fn, st)
 
@@ -483,7 +489,7 @@ def kv_read_t(cache: KVCache, slots, dtype=None):
     """cq_kv_read: slots int64 [T] -> keys and values [T, heads, size] of `dtype` (fp32 by default)."""
     torch, _, i64, dtypes, raw = _torch_tables()
     fn, T = "cq_kv_read", slots.shape[0]
-    sp, stream = _vec(fn, slots, i64, T), _stream_of(slots, raw)
+    sp, stream = _vec(fn, slots, i64, T), _stream_of(fn, raw, cache.device, slots)
     dt = dtype or torch.float32
     if dt not in dtypes:
         raise CqError(fn, ERR_UNSUPPORTED_FORMAT)
@@ -519,25 +525,29 @@ def attn_paged_t(q, cache: KVCache, block_table, kv_len, q_start, max_new: int, 
     qp, qs, _ = _rows(fn, q, width)
     tp, wide = _table(fn, block_table, i32, R)
     kvp, sp = _vec(fn, kv_len, i32, R), _vec(fn, q_start, i32, R + 1)
-    stream, dev = _stream_of(q, raw), q.device
+    stream, dev = _stream_of(fn, raw, cache.device, q, block_table, kv_len, q_start), q.device
     if ws is None:
         ws = attn_workspace_t(heads, cache.kv_heads, D, dev)
+    elif ws.get_device() != cache.device or not ws.is_contiguous():
+        raise CqError(fn, ERR_WORKSPACE)
     if out is None:
         out = torch.empty(shape, dtype=dt, device=dev)
         op, os_ = out.data_ptr(), width
     else:
         op, os_, To = _rows(fn, out, width)
-        if To != T or out.dtype != dt:
+        if To != T or out.dtype != dt or out.get_device() != cache.device:
             raise CqError(fn, ERR_SHAPE)
     if lse is True:
         lse = torch.empty((T, heads), dtype=torch.float32, device=dev)
     elif lse is False:
         lse = None
-    elif lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, heads) or not lse.is_contiguous()):
+    elif lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, heads) or not lse.is_contiguous() or
+                              lse.get_device() != cache.device):
         raise CqError(fn, ERR_SHAPE)
     st = (_lib or lib()).cq_attn_paged(cache.addr, dtypes.get(dt, -1), R, T, heads, max_new, max_kv, qp, qs, tp, wide,
                                        kvp, sp, D ** -0.5 if scale is None else scale, 1 if causal else 0, window, op,
-                                       os_, None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), stream)
+                                       os_, None if lse is None else lse.data_ptr(), ws.data_ptr(),
+                                       ws.numel() * ws.element_size(), stream)
     if st:
         raise CqError(fn, st)
     return out, lse
