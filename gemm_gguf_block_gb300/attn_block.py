@@ -39,14 +39,17 @@ class AttentionBlock:
 
     def step(self, x, new):
         """x: fp32 [T, hidden], the new tokens of all requests in order; new: their number for each request (0 for a
-        request that takes no part). Returns fp32 [T, hidden]."""
+        request that takes no part; T in all, at least 1). Returns fp32 [T, hidden]."""
         import torch
+        new = [int(n) for n in new]
+        if len(new) != len(self.past) or min(new, default=0) < 0 or sum(new) < 1 or x.shape != (sum(new), self.hidden):
+            raise cq.CqError("AttentionBlock.step", cq.ERR_SHAPE)
         P, dev = self.cache.page_size, x.device
         need = sum(-(-(a + b) // P) - -(-a // P) for a, b in zip(self.past, new))
         if self.taken + need > self.free.shape[0]:
             raise cq.CqError("AttentionBlock.step", cq.ERR_WORKSPACE)
         past_t = torch.tensor(self.past, dtype=torch.int32, device=dev)
-        new_t = torch.tensor(list(new), dtype=torch.int32, device=dev)
+        new_t = torch.tensor(new, dtype=torch.int32, device=dev)
         kv_len, q_start, slots, self.positions, self.used = cq.kv_plan_t(
             past_t, new_t, self.table, self.free[self.taken:], P, self.cache.num_pages, x.shape[0])
         width, kv_width = self.q_heads * self.head_dim, self.kv_heads * self.head_dim

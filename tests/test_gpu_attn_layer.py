@@ -1,0 +1,21 @@
+"""The attention layer: what it refuses, and how near its attention is."""
+import pytest
+
+from helpers import cq_built, torch_cuda
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("rows,new", [(3, [1, 1]), (1, [1, 1]), (2, [2]), (2, [1, 1, 0]), (0, [0, 0]), (1, [2, -1])])
+def test_token_counts_that_do_not_fit_are_refused(rows, new):
+    """... before anything is written: rows of no request would be left undefined, missing ones would be counted."""
+    torch = torch_cuda()
+    cq_built()
+    from gemm_gguf_block_gb300 import attn_block, cq
+    block, _ = attn_block.demo(hidden=256, q_heads=4, kv_heads=1, head_dim=64, prompts=(5, 20), steps=3)
+    before = block.cache.k.clone(), block.table.clone()
+    with pytest.raises(cq.CqError):
+        block.step(torch.zeros(rows, 256, device="cuda"), new)
+    assert torch.equal(block.cache.k, before[0]) and torch.equal(block.table, before[1])
+    assert block.past == [8, 23]
+    assert torch.isfinite(block.step(torch.zeros(1, 256, device="cuda"), [0, 1])).all() and block.past == [8, 24]
