@@ -105,7 +105,8 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 // What a value scale s gives its block: the offset of its scores, log2 s, and the factor of its
-// P in the sums. Finite whatever s is: the factor meets sums of 0 where a row sees nothing.
+// P in the sums; for the 16-bit types approximations to 2^-22, as the exponentials themselves are,
+// the same in both kernels. Finite whatever s is: the factor meets sums of 0 where a row sees nothing.
 template <bool EXACT>
 __device__ __forceinline__ void value_factors(float s, float& offset, float& weight) {
     if (s == 0.0f) {

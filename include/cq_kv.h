@@ -131,11 +131,17 @@ cq_status cq_kv_read(const cq_kv_cache* cache, cq_dtype dtype, int64_t T, const 
  *   lse[t][head] = log sum_j exp(scale * q . k_j)         (fp32 [T][q_heads]; may be NULL)
  * A row that sees nothing gets out = 0 and lse = -inf; a hidden key never
  * reaches a row, whatever it or its block's scale holds. Rows of no request
- * (t >= q_start[R]) are not written. Softmax statistics and sums are fp32. fp32 q
- * enters the products with 22 bits, the probabilities with 22 (those below 2^-15 of the
- * row's largest with 16 at least); 16-bit q enters exactly and the probabilities as
- * binary16 (11 bits; times its value scale -- 2^-64 for a block of zeros, scale 0 --, a probability
- * below 2^-31 of the row's largest adds nothing to out). Scales are not negative, blocks of
+ * (t >= q_start[R]) are not written. Softmax statistics and sums are fp32,
+ * exponentials and the factors of 16-bit calls' value scales good to 2^-22.
+ * What the products take:
+ *   fp32 q 22 bits, the probabilities 22 (those below 2^-15 of the row's largest 16 at least)
+ *   16-bit q as it is (values below 2^-23 of the row's largest to 2^-34 of it)
+ *   bfloat16 calls' probabilities as binary16, 11 bits
+ *   binary16 calls' probabilities 22 bits in requests of less than 40 rows (tokens times q_heads /
+ *     kv_heads: decoding, drafts), 11 bits in wider ones (prompts, chunks): 2.1e-4 and 2.5e-4 of a
+ *     result, 2-norm, against 64 bits
+ * As one binary16 a probability, times its value scale (2^-64 for a block of zeros, scale 0), that
+ * is below 2^-31 of the row's largest adds nothing to out. Scales are not negative, blocks of
  * scale 0 hold zeros; a q that is not finite makes its own row NaN. Value scales are 0 or 2^-126
  * (the smallest that cq_kv_append writes) to 2^60, and those that one row sees, 2^-64 for 0 among
  * them, within 2^100 of one another: past that, a block of the smaller ones may lose its weight.

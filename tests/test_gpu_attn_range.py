@@ -94,3 +94,20 @@ def test_every_key_of_the_longest_request_counts(n):
     q, cache, table, (kv, start), *_ = _longest(torch, cq, torch.bfloat16, n)
     _, lse = cq.attn_paged_t(torch.zeros_like(q), cache, table, kv, start, n, 2 ** 31 - 16, causal=False)
     assert (lse.double() - np.log(2.0 ** 31 - 16)).abs().max().item() <= 5.4e-2
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_both_kernels_take_the_same_factors_from_a_scale(dtype, D):
+    """Zero queries that see one key each: nothing but the value scale's factors is left in lse, and both kernels (the
+    hint of no new tokens sends wide requests to the one for few rows) have the same bits. (fp32 has another offset in
+    each, which rounds.)"""
+    torch, cq = torch_cuda(), cq_built()
+    R, n = 60, 45
+    c = _case(torch, cq, D, dtype, 4, 4, D, 16, [1] * R, [n] * R)
+    c["q"].zero_()
+    wide = _run(torch, cq, c, causal=False)
+    few = _run(torch, cq, c, causal=False, max_new=0)
+    assert torch.equal(wide[1], few[1])
+    _check(c, *wide, causal=False)
+    _check(c, *few, causal=False)
