@@ -560,7 +560,7 @@ cq_status cq_attn_paged(const cq_kv_cache* cache, cq_dtype dtype, int64_t R, int
     a.q_stride = q_stride; a.out_stride = out_stride;
     a.max_blocks = max_blocks;
     a.window = std::min(window, int64_t(1) << 32);   // wider than any length and position: sums with positions stay in range
-    a.max_new = max_new; a.max_kv = max_kv;
+    a.max_new = std::min(max_new, T);
     a.scale = scale;
     a.R = static_cast<int>(R); a.T = static_cast<int>(T); a.heads = static_cast<int>(q_heads); a.causal = causal;
     return status_of(cq::launch_attn(dev, c, dtype, a, static_cast<cudaStream_t>(stream)));

@@ -48,7 +48,7 @@ struct AttnArgs {
     void* ws;
     int64_t q_stride, out_stride;   // elements
     int64_t max_blocks, window;
-    int64_t max_new, max_kv;
+    int64_t max_new;                // at most T
     float scale;
     int R, T, heads, causal;        // heads: query heads
 };

@@ -147,9 +147,9 @@ cq_status cq_kv_read(const cq_kv_cache* cache, cq_dtype dtype, int64_t T, const 
  * them, within 2^100 of one another: past that, a block of the smaller ones may lose its weight.
  * Pages outside [0, num_pages) are hidden and flagged in the library's status
  * word (CQ_DEV_KV_PAGE); lengths are clipped to the table and to T.
- * max_new, max_kv: the host's upper bounds of new tokens and of kv_len of any
- * request; they choose kernels and grids, and results stay right when they
- * are exceeded.
+ * max_new: the host's upper bound of any request's new tokens. It chooses kernels and their
+ * tiles: too small or too large a bound costs time, results stay right. max_kv: the same of kv_len;
+ * it is checked (>= 0) and otherwise not used yet.
  * q, out 16-byte aligned, strides multiples of 16 bytes; q_heads a multiple of
  * kv_heads, at most 1024; R <= 16384; T * q_heads / kv_heads <= 2^30. workspace: cq_attn_workspace_size
  * bytes (0 for arguments the call does not take), 256-byte aligned, zero-filled

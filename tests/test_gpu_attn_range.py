@@ -111,3 +111,12 @@ def test_both_kernels_take_the_same_factors_from_a_scale(dtype, D):
     assert torch.equal(wide[1], few[1])
     _check(c, *wide, causal=False)
     _check(c, *few, causal=False)
+
+
+@pytest.mark.parametrize("max_new,max_kv", [(2 ** 62, 0), (2 ** 63 - 1, 2 ** 63 - 1)])
+def test_hints_of_any_size(max_new, max_kv):
+    torch, cq = torch_cuda(), cq_built()
+    c = _case(torch, cq, 3, "bf16", 8, 2, 64, 16, [900, 60, 200], [1, 60, 150])
+    want = _run(torch, cq, c)
+    out, lse = _run(torch, cq, c, max_new=max_new, max_kv=max_kv)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
