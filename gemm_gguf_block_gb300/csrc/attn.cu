@@ -14,14 +14,16 @@ namespace {
 // bf16 at 128: 77 / 128 / 182 against 139.
 constexpr int TILE_ROWS = 40;
 
-// The workspace: the rows kernel's counters and parts, then the tiles kernel's.
+// The workspace: the rows kernel's counters (the part that has to be zero) and parts, then the
+// tiles kernel's. All but the counters is written by a call before it is read.
+static_assert(ATTN_MAX_CTAS * sizeof(int) <= CQ_ATTN_WORKSPACE_ZERO, "the counters");
 struct Layout {
     size_t count, part, share, tile_part, total;
 };
 Layout layout(int64_t head_dim) {
     const size_t row = static_cast<size_t>(head_dim + 4) * sizeof(float);
     Layout l{};
-    l.part = ATTN_MAX_CTAS * sizeof(int);
+    l.part = CQ_ATTN_WORKSPACE_ZERO;
     l.share = l.part + size_t(ATTN_MAX_CTAS) * 2 * 16 * row;
     l.tile_part = l.share + ATTN_TILE_CTAS * sizeof(TileShare);
     l.total = l.tile_part + size_t(ATTN_TILE_CTAS) * 256 * row;

@@ -152,11 +152,12 @@ cq_status cq_kv_read(const cq_kv_cache* cache, cq_dtype dtype, int64_t T, const 
  * it is checked (>= 0) and otherwise not used yet.
  * q, out 16-byte aligned, strides multiples of 16 bytes; q_heads a multiple of
  * kv_heads, at most 1024; R <= 16384; T * q_heads / kv_heads <= 2^30. workspace: cq_attn_workspace_size
- * bytes (0 for arguments the call does not take), 256-byte aligned, zero-filled
- * before its first use and left so by every call; calls that may overlap on
- * the GPU need separate ones. Asynchronous, no allocation; results do not
- * depend on timing.
+ * bytes (0 for arguments the call does not take), 256-byte aligned; its first
+ * CQ_ATTN_WORKSPACE_ZERO bytes are zero before its first use, and every call leaves
+ * them so (the others may hold anything). Calls that may overlap on the GPU need
+ * separate ones. Asynchronous, no allocation; results do not depend on timing.
  */
+#define CQ_ATTN_WORKSPACE_ZERO 4096
 size_t cq_attn_workspace_size(int64_t q_heads, int64_t kv_heads, int64_t head_dim);
 cq_status cq_attn_paged(const cq_kv_cache* cache, cq_dtype dtype, int64_t R, int64_t T, int64_t q_heads,
                         int64_t max_new, int64_t max_kv, const void* q, int64_t q_stride, const int32_t* block_table,

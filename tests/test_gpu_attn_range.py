@@ -1,4 +1,6 @@
 """Attention over the 8-bit cache at the ends of its ranges: value scales, windows and lengths."""
+import os
+
 import numpy as np
 import pytest
 
@@ -120,3 +122,23 @@ def test_hints_of_any_size(max_new, max_kv):
     want = _run(torch, cq, c)
     out, lse = _run(torch, cq, c, max_new=max_new, max_kv=max_kv)
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("bf16", 128)])
+def test_a_workspace_holds_anything_behind_its_zeros(dtype, D):
+    """Work shared over the keys in both kernels, and joined: nothing is read that the call has not written. Every byte
+    is 0xff, numbers that are not finite, but for the first ones, which the call leaves zero."""
+    torch, cq = torch_cuda(), cq_built()
+    header = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "cq_kv.h")
+    assert f"#define CQ_ATTN_WORKSPACE_ZERO {cq.ATTN_WORKSPACE_ZERO}\n" in open(header).read()
+    for kv, new in (([40000], [1]), ([9000, 300, 20], [100, 1, 20]), ([3000] * 30, [1] * 30)):
+        c = _case(torch, cq, kv[0], dtype, 8, 2, D, 16, kv, new)
+        ws = cq.attn_workspace_t(8, 2, D)
+        want = _run(torch, cq, c, ws=ws)
+        assert not ws[:cq.ATTN_WORKSPACE_ZERO].any()
+        ws[cq.ATTN_WORKSPACE_ZERO:] = 255
+        for _ in range(2):
+            out, lse = _run(torch, cq, c, ws=ws)
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+            assert not ws[:cq.ATTN_WORKSPACE_ZERO].any()
+        _check(c, out, lse)
