@@ -66,3 +66,33 @@ def test_plan_of_as_many_tokens_as_it_takes(T):
             assert bool((x[i:i + (1 << 28)] == -1).all())
     del slots, pos, x
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("P", [16, 128])
+@pytest.mark.parametrize("growth", [1.0, 1.004, 1.03, 1.2])
+def test_a_page_filled_token_by_token(P, growth):
+    """Every call that raises a page's scale rounds its rows again: bits as the rule has them after each, and what is read
+    back lies within half a step of every scale since its row was stored (fp32's roundings add 2^-15 of it) of what was
+    given."""
+    torch, cq = torch_cuda(), cq_built()
+    rng = np.random.default_rng([P, int(1000 * growth)])
+    H, D = 2, 64
+    x = (np.clip(rng.standard_normal((P, H, D)), -3, 3) * growth ** np.arange(P)[:, None, None]).astype(np.float32)
+    if growth > 1.0:
+        x[:, :, 0] = (3.0 * growth ** np.arange(P))[:, None]
+    cache = cq.KVCache.empty(2, H, P, D)
+    q, s = np.zeros((2, H, P, D), np.int8), np.zeros((2, H), np.float32)
+    slots, tx, bound, raised = np.arange(P, 2 * P), dev(torch, x), np.zeros((P, H)), 0
+    for t in range(P):
+        old = s[1].copy()
+        cq.kv_append_t(cache, tx[t:t + 1], tx[t:t + 1], dev(torch, slots[t:t + 1]))
+        kv_ref.append(q, s, x[t:t + 1], slots[t:t + 1])
+        raised += int(t > 0 and (s[1] > old).all())
+        bound[:t] += np.where(s[1] > old, s[1].astype(np.float64) / 2, 0.0)
+        bound[t] = s[1].astype(np.float64) / 2
+        for got, scale in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+            assert np.array_equal(scale.cpu().numpy(), s) and np.array_equal(got.cpu().numpy(), q)
+    assert raised == P - 1 or growth == 1.0
+    for back in cq.kv_read_t(cache, dev(torch, slots)):
+        off = np.abs(back.cpu().numpy().astype(np.float64) - x)
+        assert (off <= bound[:, :, None] * (1 + 2.0 ** -15)).all()
