@@ -69,10 +69,16 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // own griddepcontrol.wait still waits for this grid to complete). pdl_wait
 // returns once the grids this one depends on have completed and their writes
 // are visible (at once for a grid launched without such a dependency): no
-// kernel reads or writes global memory before it, except the GEMV's weight
-// prefetches -- into L2 always (L2 is coherent, so nothing stale can reach
-// shared memory through it), into shared memory only under the
-// weights-constant option.
+// kernel reads or writes global memory before it, with two exceptions.
+// - The GEMV's weight prefetches: into L2 always (L2 is coherent, so nothing
+//   stale can reach shared memory through it), into shared memory only under
+//   the weights-constant option.
+// - attn_rows_kernel behind attn_tiles_kernel. Each CTA of the tiles kernel
+//   waits first and triggers then, so this grid begins only when everything
+//   before the tiles kernel is complete and visible; the two write different
+//   rows and parts of the workspace. What the tiles kernel writes is read after
+//   the wait, which every CTA makes before it leaves: the next grid waits for
+//   this one, and so for both.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

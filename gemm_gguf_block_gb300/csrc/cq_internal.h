@@ -11,7 +11,8 @@ namespace cq {
 // Programmatic dependent launch: every kernel of the library is launched so that it may start while the previous grid in the
 // stream is still running; each kernel's first act is griddepcontrol.wait
 // (pdl_wait), which returns once the grids it depends on have completed and
-// their memory is visible, before any global memory is read or written. The
+// their memory is visible, before any global memory is read or written (the
+// exceptions, and why they are sound, stand with pdl_wait in cq_device.cuh). The
 // launch latency and the kernel's setup thus overlap the previous kernel's
 // tail, with the same ordering guarantees as a plain launch.
 // CQ_OPT_WEIGHTS_CONST (see include/cq.h).

@@ -345,8 +345,10 @@ cq_status cq_moe_read_status(const void* workspace, int32_t* out_code, void* str
 cq_status cq_read_device_status(const void* workspace, int32_t* out_code, void* stream);
 
 /* Synchronises the current device, then reads (and, if clear != 0, zeroes) the
- * library's own status word, used by kernels that take no workspace (a copy
- * wait that timed out in cq_gemv / cq_gemm). CQ_ERR_TIMEOUT if set. */
+ * library's own status word, used by kernels whose call has no status word of its
+ * own: a device wait that timed out (CQ_DEV_WAIT_TIMEOUT: CQ_ERR_TIMEOUT), or a
+ * page id or slot outside the cache in the calls of cq_kv.h (CQ_DEV_KV_PAGE:
+ * CQ_ERR_DEVICE_STATUS). */
 cq_status cq_read_global_status(int32_t* out_code, int clear);
 
 const char* cq_status_string(cq_status s);
