@@ -15,12 +15,12 @@
 // convert the cache's bytes to operands, two stages of keys and two of values;
 // 12 issues the MMAs, 13-15 only fill the last warpgroup, whose registers the softmax
 // gets. The tiles are half a step apart: while one's softmax runs, the other's MMAs do.
-// (Two threads a row, 16 softmax warps, measured 547 us for 522 at the 8192-token prompt:
-// the exchange of the rows' largest costs what the shorter loops gain. Eight converter
-// warps leave the softmax 168 registers or fewer, and it spills: 563 to 603 for 455.)
+// (Two threads a row, 16 softmax warps, are 5% slower at the prompt below: the exchange of
+// the rows' largest costs more than the shorter loops gain. Eight converter warps leave the
+// softmax 168 registers or fewer, it spills, and the prompt takes a quarter longer.)
 // Measured, 8192 tokens, 32 heads on 8, dim 128, bf16: 437 us, 1.26 PFLOP/s. The softmax
-// (3000 of a step's 3500 cycles) and the converters bound it together: at 455 us it took
-// 400 without the converters' loads and stores, and no less without the exponentials.
+// (3000 of a step's 3500 cycles) and the converters bound it together: without the
+// converters' loads and stores it takes 12% less, without the exponentials no less.
 // Few items are split over their keys; the rows kernel, which always follows, joins
 // the parts.
 // A block of 16 keys carries (s_k, log2 s_v, 1 / s_v) in shared memory; a block outside
@@ -82,7 +82,7 @@ template <typename T, int D> struct Tiles {
     // Tensor memory columns. 16-bit types: the scores of one tile at a time, both tiles' P, both
     // results. (A tile's scores are there only until its softmax has them in registers, so the
     // other's next ones follow while the first is at work: no softmax waits for its own P's
-    // product. With 128 columns of scores a tile, P over them: 505 us, for 493 at the 8192-token prompt.)
+    // product. With 128 columns of scores a tile, P over them, the prompt takes 2% longer.)
     // fp32: scores -- two steps' where that fits, so that one step's are there before the
     // other's softmax is done --, overlaid by the first two parts of P, the third part, and two
     // results: of P's first part and of the other two. (The MMAs' sums are cut off, not rounded:
@@ -363,8 +363,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             else wait(B_S + mt, j & 1);
             const uint32_t s_col = s_col0 + (SBUF == 2 ? (j & 1) * (W::S1 - W::S0) : 0);
             const int k0 = key0 + j * KEYS + KT * part;
-            // The scores are read once and stay in registers (read twice, 522 us for 501 at the
-            // 8192-token prompt).
+            // The scores are read once and stay in registers: tensor memory is what a step would wait for.
             uint32_t v[CHUNKS][32];
 #pragma unroll
             for (int ch = 0; ch < CHUNKS; ++ch) tc::ld32(s_col + 32 * ch, v[ch]);
@@ -434,7 +433,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             const float base = M == -INFINITY ? 0.0f : M - OFF;
             // (fp32: each part's P overlays its own scores, which are in registers)
             // A chunk's exponentials all come before their sums and conversions, and no chunk's P is in
-            // another's registers: a pair at a time, one warp took 1100 cycles for its 128 keys, so 710.
+            // another's registers: a pair at a time takes a warp half as long again.
             uint32_t pr[CHUNKS][16];
             float weight[KT / 16];
             blocks(2, weight);
@@ -594,7 +593,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         // access) hold four pieces of an even key and four of the odd one after it; at D = 128
         // the other half of the row: the bytes then come from different banks of the lines,
         // and the chunks go to different banks of the swizzled rows (8-way conflicts on both
-        // sides otherwise measured 2300 cycles a step).
+        // sides otherwise).
         const int cw = warp - SOFT / 32;
         const int odd = (lane >> 2) & 1, ck = 2 * (lane >> 3) + odd;
         auto piece = [&](int i) { return (lane & 3) + (D == 128 ? 4 * (odd ^ i) : 0); };
@@ -673,7 +672,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             fence_proxy_async_smem();
             tc::mbar_arrive(&bars[B_K_FULL + st]);
             // What was looked up for this step and the next is taken before any load is issued: right
-            // behind the values' loads, this waited for them (1800 cycles a step).
+            // behind the values' loads, this waits for them, half a step.
             float3 in = make_float3(0.0f, -INFINITY, 1.0f);
             if (page >= 0) {
                 in.x = p_ks;
