@@ -89,9 +89,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
 constexpr float ZERO_LOG = -64.0f;
 
 // The sums of P / s_v are held without a factor 2^SUM_LOG: for scales down to append's smallest,
-// 2^-126, P up to 2^15 and 2^26 keys they stay below 2^128 (with nothing taken out they were
-// infinite from 2^-116 down), and beside scales of 2^60 they are above 2^-97.
-constexpr float SUM_LOG = 40.0f, SUM_DOWN = 1.0f / 1099511627776.0f;      // 2^-SUM_LOG
+// 2^-126, P up to 2^15 and 2^20 keys they stay below 2^128 (with nothing taken out they were
+// infinite from 2^-116 down), and up to scales of 2^96 a row's sum is a normal number: its
+// largest P is at least 2^7.
+constexpr float SUM_LOG = 34.0f, SUM_DOWN = 1.0f / 17179869184.0f;        // 2^-SUM_LOG
 
 __device__ __forceinline__ float log2_approx(float x) {
     float y;
@@ -116,6 +117,17 @@ __device__ __forceinline__ void value_factors(float s, float& offset, float& wei
     }
     offset = EXACT ? log2f(s) : log2_approx(s);
     weight = fminf(EXACT ? __frcp_rn(s) : rcp_approx(s), 3.402823466e38f) * SUM_DOWN;
+}
+
+// What a row's result is multiplied by, one factor after the other: 2^-SUM_LOG / l in two steps
+// that neither pass fp32's range nor fall below it where the result does not. 0 for a row that saw nothing.
+__device__ __forceinline__ void row_factors(float l, float& f, float& down) {
+    f = l == 0.0f ? 0.0f : __frcp_rn(l);
+    down = SUM_DOWN;
+    if (f > 1.0f) {
+        f *= SUM_DOWN;
+        down = 1.0f;
+    }
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -207,9 +219,10 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int first, int h, i
                                           float m, float l, float off) {
     const int64_t tok = first + rho / G;
     const int head = h * G + rho % G;
-    const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);      // 0 only where nothing was seen
+    float inv, down;
+    row_factors(l, inv, down);
     store4(static_cast<T*>(a.out) + tok * a.out_stride + head * D + col,
-           make_float4(acc.x * inv * SUM_DOWN, acc.y * inv * SUM_DOWN, acc.z * inv * SUM_DOWN, acc.w * inv * SUM_DOWN));
+           make_float4(acc.x * inv * down, acc.y * inv * down, acc.z * inv * down, acc.w * inv * down));
     if (col == 0 && a.lse != nullptr)
         a.lse[tok * a.heads + head] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m - off + SUM_LOG + log2f(l));
 }

@@ -553,7 +553,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             constexpr int CH = 16 / sizeof(T), NC = OC / CH;                 // values of a 16-byte chunk, chunks of the warp's columns
             constexpr int SW = (NC < 8 ? NC : 8) - 1;
             uint8_t* mine = smem + W::OFF_Q + warp * (32 * OC * sizeof(T));
-            const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);               // 0 only where nothing was seen
+            float inv, down;
+            row_factors(l, inv, down);
             static_assert(OC % 32 == 0, "columns in chunks of 32");
 #pragma unroll
             for (int ch = 0; ch < OC / 32; ++ch) {
@@ -564,8 +565,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                     T* dst = reinterpret_cast<T*>(mine + lane * (OC * sizeof(T)) + (((32 * ch + i) / CH) ^ (lane & SW)) * 16);
 #pragma unroll
                     for (int k = 0; k < CH; k += 4)
-                        store4(dst + k, make_float4(__uint_as_float(orr[i + k]) * inv * SUM_DOWN, __uint_as_float(orr[i + k + 1]) * inv * SUM_DOWN,
-                                                    __uint_as_float(orr[i + k + 2]) * inv * SUM_DOWN, __uint_as_float(orr[i + k + 3]) * inv * SUM_DOWN));
+                        store4(dst + k, make_float4(__uint_as_float(orr[i + k]) * inv * down, __uint_as_float(orr[i + k + 1]) * inv * down,
+                                                    __uint_as_float(orr[i + k + 2]) * inv * down, __uint_as_float(orr[i + k + 3]) * inv * down));
                 }
             }
             if (a.lse != nullptr && row < rows && part == 0)

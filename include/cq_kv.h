@@ -142,7 +142,7 @@ cq_status cq_kv_read(const cq_kv_cache* cache, cq_dtype dtype, int64_t T, const 
  * exponentials and the factors of 16-bit calls' value scales good to 2^-22.
  * What the products take:
  *   fp32 q 22 bits, the probabilities 22 (those below 2^-15 of the row's largest 16 at least)
- *   16-bit q as it is (values below 2^-23 of the row's largest to 2^-34 of it)
+ *   16-bit q as it is (values below 2^-22 of the row's largest to 2^-33 of it)
  *   bfloat16 calls' probabilities as binary16, 11 bits
  *   binary16 calls' probabilities 22 bits in requests of less than 40 rows (tokens times q_heads /
  *     kv_heads: decoding, drafts), 11 bits in wider ones (prompts, chunks): 2.1e-4 and 2.5e-4 of a
@@ -150,7 +150,7 @@ cq_status cq_kv_read(const cq_kv_cache* cache, cq_dtype dtype, int64_t T, const 
  * As one binary16 a probability, times its value scale (2^-64 for a block of zeros, scale 0), that
  * is below 2^-31 of the row's largest adds nothing to out. Scales are not negative, blocks of
  * scale 0 hold zeros; a q that is not finite makes its own row NaN. Value scales are 0 or 2^-126
- * (the smallest that cq_kv_append writes) to 2^60, and those that one row sees, 2^-64 for 0 among
+ * (the smallest that cq_kv_append writes) to 2^96, and those that one row sees, 2^-64 for 0 among
  * them, within 2^100 of one another: past that, a block of the smaller ones may lose its weight.
  * Pages outside [0, num_pages) are hidden and flagged in the library's status
  * word (CQ_DEV_KV_PAGE); lengths are clipped to the table and to T.

@@ -142,3 +142,13 @@ def test_a_workspace_holds_anything_behind_its_zeros(dtype, D):
             assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
             assert not ws[:cq.ATTN_WORKSPACE_ZERO].any()
         _check(c, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Hq,D,kv,n", [(4, 64, [400], [1]), (4, 64, [400], [200]), (4, 64, [6000], [30])])
+@pytest.mark.parametrize("scales", [[2.0 ** 96], [1.7 * 2.0 ** 90, 2.0 ** 60, 2.0 ** 20], [2.0 ** -126, 2.0 ** -90]])
+def test_value_scales_at_the_ends_of_their_range(dtype, Hq, D, kv, n, scales):
+    torch, cq = torch_cuda(), cq_built()
+    c = _case(torch, cq, [D, kv[0], 1], dtype, Hq, 2, D, 16, kv, n)
+    _value_scales(torch, c, scales)
+    _check(c, *_run(torch, cq, c))
