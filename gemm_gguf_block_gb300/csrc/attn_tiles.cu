@@ -605,18 +605,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         // The warp's two blocks of 16 keys of a step: lanes 0 and 1 look them up. A step's
         // table entries are fetched two steps ahead, its scales and bytes one: no lookup
         // is waited for in the loop, and a step's loads run behind the one before's stores.
-        auto entry = [&](int j) {
-            const int k = key0 + j * KEYS + 32 * cw + 16 * lane;
-            return lane < 2 && j < steps && k < tstop ? table[k >> c.page_shift] : INT_MIN;     // INT_MIN: no keys
-        };
-        auto checked = [&](int e) {
+        auto block_at = [&](int j) { return key0 + j * KEYS + 32 * cw + 16 * lane; };
+        auto has_keys = [&](int j) { return lane < 2 && j < steps && block_at(j) < tstop; };
+        auto entry = [&](int j) { return has_keys(j) ? table[block_at(j) >> c.page_shift] : -1; };
+        auto checked = [&](int e, int j) {
             if (e >= 0 && e < c.num_pages) return e;
-            if (e != INT_MIN) atomicOr(a.status, CQ_DEV_KV_PAGE);
+            if (has_keys(j)) atomicOr(a.status, CQ_DEV_KV_PAGE);
             return -1;
         };
         int64_t at[2];
         auto place = [&](int page, int j) {
-            const int k = key0 + j * KEYS + 32 * cw + 16 * lane;
+            const int k = block_at(j);
             const int64_t mine = page >= 0 ? page * c.page_stride + head_off + static_cast<int64_t>(k & (c.page_size - 1)) * D : -1;
 #pragma unroll
             for (int b = 0; b < 2; ++b) at[b] = __shfl_sync(0xffffffffu, mine, b);
@@ -659,7 +658,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                     *reinterpret_cast<uint4*>(dst + put[i][1] + 8 * g * 128) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
         };
-        int page = checked(entry(0)), ahead = entry(1);
+        int page = checked(entry(0), 0), ahead = entry(1);
         scales(page);
         place(page, 0);
         load(c.k, kr);
@@ -688,7 +687,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
             }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars[B_INFO + j % INFO]);
-            page = checked(ahead);
+            page = checked(ahead, j + 1);
             ahead = entry(j + 2);
             scales(page);
             place(page, j + 1);

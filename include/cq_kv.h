@@ -80,6 +80,8 @@ typedef struct {
  *                     q_start stops at T
  *   CQ_DEV_KV_PAGE    a page id outside [0, num_pages) in the free list (entry
  *                     and slots -1) or in a partly filled page's entry (slots -1)
+ * kv_len and the table then count tokens that have no slot: a step with a bit set in used[1] is
+ * planned anew with what fits before it is attended to.
  * R <= 16384 (CQ_ERR_SHAPE beyond), T < 2^31, max_blocks * P < 2^31. R = 0 only
  * writes q_start[0], used and the padding. Asynchronous, one launch, no
  * allocation.

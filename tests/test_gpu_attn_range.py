@@ -152,3 +152,15 @@ def test_value_scales_at_the_ends_of_their_range(dtype, Hq, D, kv, n, scales):
     c = _case(torch, cq, [D, kv[0], 1], dtype, Hq, 2, D, 16, kv, n)
     _value_scales(torch, c, scales)
     _check(c, *_run(torch, cq, c))
+
+
+@pytest.mark.parametrize("n", [1, 150])
+@pytest.mark.parametrize("page", [-1, -2 ** 31, 2 ** 31 - 1])
+def test_any_page_outside_the_cache_is_flagged(n, page):
+    torch, cq = torch_cuda(), cq_built()
+    c = _case(torch, cq, 9, "bf16", 4, 2, 128, 32, [600], [n])
+    c["table"][0, 3] = page
+    cq.cq_read_global_status()
+    out, lse = _run(torch, cq, c)
+    assert cq.cq_read_global_status() == (cq.ERR_DEVICE_STATUS, cq.DEV_KV_PAGE)
+    _check(c, out, lse)
