@@ -8,7 +8,8 @@ one call -- through
     -> cq_quantize_act -> cq_gemv / cq_gemm (output projection).
 
 The plan's positions are what a rotary embedding would take; the library has none, so queries and keys are used as
-they are projected.
+they are projected. It shows the calls together and is no scheduler: requests do not end, pages are not given back, and
+the lengths go to the device with every step.
 
     python -m gemm_gguf_block_gb300.attn_block      two prompts, then single tokens, checked against 64 bits
 """

@@ -18,7 +18,7 @@
 // (Two threads a row, 16 softmax warps, are 5% slower at the prompt below: the exchange of
 // the rows' largest costs more than the shorter loops gain. Eight converter warps leave the
 // softmax 168 registers or fewer, it spills, and the prompt takes a quarter longer.)
-// Measured, 8192 tokens, 32 heads on 8, dim 128, bf16: 433 us, 1.27 PFLOP/s. The softmax
+// Measured, 8192 tokens, 32 heads on 8, dim 128, bf16: 437 us, 1.26 PFLOP/s. The softmax
 // (3000 of a step's 3500 cycles) and the converters bound it together: without the
 // converters' loads and stores it takes 12% less, without the exponentials no less.
 // Few items are split over their keys; the rows kernel, which always follows, joins
