@@ -517,7 +517,7 @@ def attn_paged_t(q, cache: KVCache, block_table, kv_len, q_start, max_new: int, 
     -> (out [T, q heads, size], lse fp32 [T, q heads] or None). block_table int32 [R, max_blocks], kv_len int32 [R],
     q_start int32 [R + 1]; max_new: the most new tokens of any request (it chooses the kernels), max_kv: of kv_len (not
     used yet); scale 1 / sqrt(size) by default; ws: attn_workspace_t's, made here when not given;
-    lse: a tensor, True for a new one, or None."""
+    lse: a tensor, True for a new one, or None. Rows of no request (padding) are not written: undefined in new tensors."""
     torch, i32, _, dtypes, raw = _torch_tables()
     fn, D, dt = "cq_attn_paged", cache.head_dim, q.dtype
     shape = q.shape
