@@ -1,4 +1,4 @@
-"""Python binding of libcq (include/cq.h, include/cq_kv.h): argument marshalling only.
+"""Python binding of libcq (include/cq.h, include/cq_kv.h, include/cq_tree.h): argument marshalling only.
 
 The raw functions carry the C names and arguments (integers for pointers and
 the stream) and return the integer cq_status. The ``*_t`` helpers take torch
@@ -28,10 +28,12 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED_FORMAT, ERR_SHAPE, ERR_ALIGNMENT, ERR_WORKS
     ERR_DEVICE_STATUS, ERR_TIMEOUT = range(9)
 DEV_BAD_EXPERT_ID, DEV_DUP_EXPERT_ID, DEV_WAIT_TIMEOUT = 0x1, 0x2, 0x4
 DEV_KV_LENGTH, DEV_KV_BLOCKS, DEV_KV_PAGES, DEV_KV_TOKENS, DEV_KV_PAGE = 0x08, 0x10, 0x20, 0x40, 0x80
+DEV_TREE, DEV_LOGITS = 0x100, 0x200
+TREE_MAX = 64                  # tokens of a tree
 ATTN_WORKSPACE_ZERO = 4096     # bytes of an attention workspace that are zero before its first use
 F32, F16, BF16 = 0, 1, 30      # value types of keys, values and queries (cq_dtype)
 
-# Every symbol include/cq.h and include/cq_kv.h declare, with (restype, argtypes).
+# Every symbol include/cq.h, include/cq_kv.h and include/cq_tree.h declare, with (restype, argtypes).
 _P, _I64, _I, _SZ, _F = C.c_void_p, C.c_int64, C.c_int, C.c_size_t, C.c_float
 SIGNATURES = {
     "cq_quantize_act": (_I, [_I, _I64, _I64, _P, _P, _P]),
@@ -62,6 +64,13 @@ SIGNATURES = {
     "cq_attn_workspace_size": (_SZ, [_I64, _I64, _I64]),
     "cq_attn_paged": (_I, [_P, _I, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _F, _I, _I64, _P, _I64, _P,
                            _P, _SZ, _P]),
+    "cq_qk_rope": (_I, [_I, _I, _I64, _I64, _I64, _I64, _I64, _I, _P, _I64, _P, _I64, _P, _P, _P, _P, _F, _P, _I64, _P,
+                        _I64, _P]),
+    "cq_tree_plan": (_I, [_I64, _I64, _P, _P, _P, _P, _P, _P]),
+    "cq_attn_tree": (_I, [_P, _I, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _P, _F, _P, _I64, _P, _P, _SZ, _P]),
+    "cq_tree_verify": (_I, [_I64, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _P, _P]),
+    "cq_kv_move": (_I, [_P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _P]),
+    "cq_kv_release": (_I, [_I64, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _P, _P]),
 }
 
 
@@ -177,6 +186,37 @@ def cq_attn_paged(cache, dtype, R, T, q_heads, max_new, max_kv, q, q_stride, blo
                   scale, causal, window, out, out_stride, lse, ws, ws_bytes, stream=0):
     return lib().cq_attn_paged(cache, dtype, R, T, q_heads, max_new, max_kv, q, q_stride, block_table, max_blocks,
                                kv_len, q_start, scale, causal, window, out, out_stride, lse, ws, ws_bytes, stream)
+
+
+def cq_qk_rope(in_dtype, out_dtype, T, q_heads, kv_heads, head_dim, rot_dim, adjacent, q, q_stride, k, k_stride, positions,
+               freqs, q_norm, k_norm, eps, q_out, q_out_stride, k_out, k_out_stride, stream=0):
+    return lib().cq_qk_rope(in_dtype, out_dtype, T, q_heads, kv_heads, head_dim, rot_dim, adjacent, q, q_stride, k, k_stride,
+                            positions, freqs, q_norm, k_norm, eps, q_out, q_out_stride, k_out, k_out_stride, stream)
+
+
+def cq_tree_plan(R, T, kv_len, q_start, parent, mask, positions, stream=0):
+    return lib().cq_tree_plan(R, T, kv_len, q_start, parent, mask, positions, stream)
+
+
+def cq_attn_tree(cache, dtype, R, T, q_heads, max_new, q, q_stride, block_table, max_blocks, kv_len, q_start, mask, scale,
+                 out, out_stride, lse, ws, ws_bytes, stream=0):
+    return lib().cq_attn_tree(cache, dtype, R, T, q_heads, max_new, q, q_stride, block_table, max_blocks, kv_len, q_start,
+                              mask, scale, out, out_stride, lse, ws, ws_bytes, stream)
+
+
+def cq_tree_verify(R, T, V, logits, logits_stride, draft, draft_stride, tokens, parent, q_start, temperature, u_accept,
+                   u_sample, max_path, count, path, next_token, stream=0):
+    return lib().cq_tree_verify(R, T, V, logits, logits_stride, draft, draft_stride, tokens, parent, q_start, temperature,
+                                u_accept, u_sample, max_path, count, path, next_token, stream)
+
+
+def cq_kv_move(cache, R, block_table, max_blocks, kv_len, q_start, count, path, max_path, new_len, stream=0):
+    return lib().cq_kv_move(cache, R, block_table, max_blocks, kv_len, q_start, count, path, max_path, new_len, stream)
+
+
+def cq_kv_release(R, page_size, block_table, max_blocks, num_pages, old_len, new_len, freed, capacity, used, stream=0):
+    return lib().cq_kv_release(R, page_size, block_table, max_blocks, num_pages, old_len, new_len, freed, capacity, used,
+                               stream)
 
 
 def cq_gemm_workspace_size(w_fmt, M, N, K):
@@ -518,8 +558,22 @@ def attn_paged_t(q, cache: KVCache, block_table, kv_len, q_start, max_new: int, 
     q_start int32 [R + 1]; max_new: the most new tokens of any request (it chooses the kernels), max_kv: of kv_len (not
     used yet); scale 1 / sqrt(size) by default; ws: attn_workspace_t's, made here when not given;
     lse: a tensor, True for a new one, or None. Rows of no request (padding) are not written: undefined in new tensors."""
+    fn = "cq_attn_paged"
+    dt, R, T, heads, qp, qs, tp, wide, kvp, sp, ws, out, op, os_, lse, stream = _attn_args(
+        fn, q, cache, block_table, kv_len, q_start, ws, out, lse)
+    st = (_lib or lib()).cq_attn_paged(cache.addr, dt, R, T, heads, max_new, max_kv, qp, qs, tp, wide, kvp, sp,
+                                       cache.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, op,
+                                       os_, None if lse is None else lse.data_ptr(), ws.data_ptr(),
+                                       ws.numel() * ws.element_size(), stream)
+    if st:
+        raise CqError(fn, st)
+    return out, lse
+
+
+def _attn_args(fn, q, cache, block_table, kv_len, q_start, ws, out, lse, mask=None):
+    """What the attention calls have in common: tensors looked over, outputs made where they are not given."""
     torch, i32, _, dtypes, raw = _torch_tables()
-    fn, D, dt = "cq_attn_paged", cache.head_dim, q.dtype
+    D, dt = cache.head_dim, q.dtype
     shape = q.shape
     if len(shape) != 3 or shape[2] != D:
         raise CqError(fn, ERR_SHAPE)
@@ -528,7 +582,11 @@ def attn_paged_t(q, cache: KVCache, block_table, kv_len, q_start, max_new: int, 
     qp, qs, _ = _rows(fn, q, width)
     tp, wide = _table(fn, block_table, i32, R)
     kvp, sp = _vec(fn, kv_len, i32, R), _vec(fn, q_start, i32, R + 1)
-    stream, dev = _stream_of(fn, raw, cache.device, q, block_table, kv_len, q_start), q.device
+    if mask is None:
+        stream = _stream_of(fn, raw, cache.device, q, block_table, kv_len, q_start)
+    else:
+        stream = _stream_of(fn, raw, cache.device, q, block_table, kv_len, q_start, mask)
+    dev = q.device
     if ws is None:
         ws = attn_workspace_t(heads, cache.kv_heads, D, dev)
     elif ws.get_device() != cache.device or not ws.is_contiguous():
@@ -547,10 +605,139 @@ def attn_paged_t(q, cache: KVCache, block_table, kv_len, q_start, max_new: int, 
     elif lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, heads) or not lse.is_contiguous() or
                               lse.get_device() != cache.device):
         raise CqError(fn, ERR_SHAPE)
-    st = (_lib or lib()).cq_attn_paged(cache.addr, dtypes.get(dt, -1), R, T, heads, max_new, max_kv, qp, qs, tp, wide,
-                                       kvp, sp, D ** -0.5 if scale is None else scale, 1 if causal else 0, window, op,
-                                       os_, None if lse is None else lse.data_ptr(), ws.data_ptr(),
-                                       ws.numel() * ws.element_size(), stream)
+    return dtypes.get(dt, -1), R, T, heads, qp, qs, tp, wide, kvp, sp, ws, out, op, os_, lse, stream
+
+
+# ------------------------------------------------- a step of tree decoding
+def qk_rope_t(q, k, positions, freqs, *, q_norm=None, k_norm=None, eps: float = 1e-6, adjacent: bool = False, dtype=None,
+              q_out=None, k_out=None):
+    """cq_qk_rope: q [T, q heads, size], k [T, kv heads, size] (fp32, fp16 or bf16; rows may be strided), positions int32
+    [T], freqs fp64 [rot / 2] (radians a position; an empty tensor or None: no rotation), q_norm, k_norm fp32 [size] or
+    None -> (q, k) normed and turned, new or in q_out, k_out (q and k themselves: in place). dtype: of the outputs, that of
+    q by default; fp32 inputs take any. Rows of negative positions (padding) are not written: undefined in new tensors."""
+    torch, i32, _, dtypes, raw = _torch_tables()
+    fn, shape, kshape, dt = "cq_qk_rope", q.shape, k.shape, q.dtype
+    if len(shape) != 3 or len(kshape) != 3 or kshape[0] != shape[0] or kshape[2] != shape[2] or k.dtype != dt:
+        raise CqError(fn, ERR_SHAPE)
+    T, hq, D = shape
+    hk, i = kshape[1], q.get_device()
+    qp, qs, _ = _rows(fn, q, hq * D)
+    kp, ks, _ = _rows(fn, k, hk * D)
+    pos = _vec(fn, positions, i32, T)
+    half = 0 if freqs is None else freqs.shape[0] if freqs.dim() == 1 else -1
+    fp = None if freqs is None else _vec(fn, freqs, torch.float64, half)
+    ts = [k, positions] + [t for t in (freqs, q_norm, k_norm, q_out, k_out) if t is not None]
+    stream = _stream_of(fn, raw, i, *ts)
+    norms = [None if t is None else _vec(fn, t, torch.float32, D) for t in (q_norm, k_norm)]
+    ot = dtype or (q_out.dtype if q_out is not None else k_out.dtype if k_out is not None else dt)
+    outs = []
+    for x, y, h in ((q, q_out, hq), (k, k_out, hk)):
+        if y is None:
+            y = torch.empty(x.shape, dtype=ot, device=x.device)
+            outs += [y, y.data_ptr(), h * D]
+        else:
+            yp, ys, Ty = _rows(fn, y, h * D)
+            if Ty != T or y.dtype != ot:
+                raise CqError(fn, ERR_SHAPE)
+            outs += [y, yp, ys]
+    qo, qop, qos, ko, kop, kos = outs
+    st = (_lib or lib()).cq_qk_rope(dtypes.get(dt, -1), dtypes.get(ot, -1), T, hq, hk, D, 2 * half, 1 if adjacent else 0, qp,
+                                    qs, kp, ks, pos, fp, norms[0], norms[1], eps, qop, qos, kop, kos, stream)
+    if st:
+        raise CqError(fn, st)
+    return qo, ko
+
+
+def tree_plan_t(kv_len, q_start, parent):
+    """cq_tree_plan: int32 kv_len [R], q_start [R + 1], parent [T] -> (mask int64 [T], positions int32 [T])."""
+    torch, i32, i64, _, raw = _torch_tables()
+    fn, R, T = "cq_tree_plan", kv_len.shape[0], parent.shape[0]
+    kvp, sp, pp = _vec(fn, kv_len, i32, R), _vec(fn, q_start, i32, R + 1), _vec(fn, parent, i32, T)
+    stream = _stream_of(fn, raw, parent.get_device(), kv_len, q_start)
+    dev = parent.device
+    mask, positions = torch.empty(T, dtype=i64, device=dev), torch.empty(T, dtype=i32, device=dev)
+    st = (_lib or lib()).cq_tree_plan(R, T, kvp, sp, pp, mask.data_ptr(), positions.data_ptr(), stream)
+    if st:
+        raise CqError(fn, st)
+    return mask, positions
+
+
+def attn_tree_t(q, cache: KVCache, block_table, kv_len, q_start, mask, max_new: int, *, scale=None, ws=None, out=None,
+                lse=True):
+    """cq_attn_tree: attn_paged_t under the masks of tree_plan_t (int64 [T]); requests of more than TREE_MAX new tokens
+    are causal."""
+    fn = "cq_attn_tree"
+    mp = _vec(fn, mask, _torch_tables()[2], q.shape[0])
+    dt, R, T, heads, qp, qs, tp, wide, kvp, sp, ws, out, op, os_, lse, stream = _attn_args(
+        fn, q, cache, block_table, kv_len, q_start, ws, out, lse, mask)
+    st = (_lib or lib()).cq_attn_tree(cache.addr, dt, R, T, heads, max_new, qp, qs, tp, wide, kvp, sp, mp,
+                                      cache.head_dim ** -0.5 if scale is None else scale, op, os_,
+                                      None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                      stream)
     if st:
         raise CqError(fn, st)
     return out, lse
+
+
+def tree_verify_t(logits, tokens, parent, q_start, temperature, u_accept, u_sample, max_path: int, *, draft=None):
+    """cq_tree_verify: logits fp32 [T, V] (rows may be strided), int32 tokens, parent [T], q_start [R + 1], fp32 temperature
+    [R], u_accept [T], u_sample [R] in [0, 1), draft fp32 [T, V] or None -> int32 (count [R], path [R, max_path], next [R])."""
+    torch, i32, _, _, raw = _torch_tables()
+    fn = "cq_tree_verify"
+    if logits.dim() != 2 or logits.dtype != torch.float32:
+        raise CqError(fn, ERR_SHAPE)
+    (T, V), R, f32 = logits.shape, temperature.shape[0], torch.float32
+    lp, ls, _ = _rows(fn, logits, V)
+    dp, ds = None, 0
+    ptrs = [_vec(fn, tokens, i32, T), _vec(fn, parent, i32, T), _vec(fn, q_start, i32, R + 1),
+            _vec(fn, temperature, f32, R), _vec(fn, u_accept, f32, T), _vec(fn, u_sample, f32, R)]
+    ts = [tokens, parent, q_start, temperature, u_accept, u_sample]
+    if draft is not None:
+        if draft.dim() != 2 or draft.dtype != f32 or draft.shape != logits.shape:
+            raise CqError(fn, ERR_SHAPE)
+        dp, ds, _ = _rows(fn, draft, V)
+        ts.append(draft)
+    stream = _stream_of(fn, raw, logits.get_device(), *ts)
+    dev = logits.device
+    count, token = torch.empty(R, dtype=i32, device=dev), torch.empty(R, dtype=i32, device=dev)
+    path = torch.empty((R, max(max_path, 0)), dtype=i32, device=dev)
+    st = (_lib or lib()).cq_tree_verify(R, T, V, lp, ls, dp, ds, *ptrs, max_path, count.data_ptr(), path.data_ptr(),
+                                        token.data_ptr(), stream)
+    if st:
+        raise CqError(fn, st)
+    return count, path, token
+
+
+def kv_move_t(cache: KVCache, block_table, kv_len, q_start, count, path, new_len=None):
+    """cq_kv_move: int32 block_table [R, max_blocks], kv_len, count [R], q_start [R + 1], path [R, max_path] as
+    tree_verify_t gives them -> new_len int32 [R]."""
+    torch, i32, _, _, raw = _torch_tables()
+    fn, R = "cq_kv_move", kv_len.shape[0]
+    tp, wide = _table(fn, block_table, i32, R)
+    pp, most = _table(fn, path, i32, R)
+    kvp, sp, cp = _vec(fn, kv_len, i32, R), _vec(fn, q_start, i32, R + 1), _vec(fn, count, i32, R)
+    stream = _stream_of(fn, raw, cache.device, block_table, kv_len, q_start, count, path)
+    if new_len is None:
+        new_len = torch.empty(R, dtype=i32, device=kv_len.device)
+    elif new_len.get_device() != cache.device:
+        raise CqError(fn, ERR_INVALID_ARG)
+    st = (_lib or lib()).cq_kv_move(cache.addr, R, tp, wide, kvp, sp, cp, pp, most, _vec(fn, new_len, i32, R), stream)
+    if st:
+        raise CqError(fn, st)
+    return new_len
+
+
+def kv_release_t(block_table, old_len, new_len, page_size: int, num_pages: int, capacity: int):
+    """cq_kv_release: int32 block_table [R, max_blocks], old_len, new_len [R] -> (freed int32 [capacity], used int32 [2])."""
+    torch, i32, _, _, raw = _torch_tables()
+    fn, R = "cq_kv_release", old_len.shape[0]
+    tp, wide = _table(fn, block_table, i32, R)
+    op, np_ = _vec(fn, old_len, i32, R), _vec(fn, new_len, i32, R)
+    stream = _stream_of(fn, raw, block_table.get_device(), old_len, new_len)
+    dev = block_table.device
+    freed, used = torch.empty(max(capacity, 0), dtype=i32, device=dev), torch.empty(2, dtype=i32, device=dev)
+    st = (_lib or lib()).cq_kv_release(R, page_size, tp, wide, num_pages, op, np_, freed.data_ptr(), capacity, used.data_ptr(),
+                                       stream)
+    if st:
+        raise CqError(fn, st)
+    return freed, used

@@ -6,6 +6,7 @@
 
 #include "cq_device.cuh"
 #include "cq_internal.h"
+#include "cq_tree.h"
 #include "kv.cuh"
 
 namespace cq {
@@ -63,6 +64,43 @@ __device__ __forceinline__ void row_range(const AttnArgs& a, int n, int kv, int 
     if (s <= f) s = f = 0;
     from = static_cast<int>(f);
     stop = static_cast<int>(s);
+}
+
+// Trees (cq_attn_tree): a request of at most CQ_TREE_MAX new tokens sees the keys in front of them, and of
+// them those whose bits are set in the row's mask; a longer one is causal.
+__device__ __forceinline__ bool is_tree(int n) { return n <= CQ_TREE_MAX; }
+
+// What token t sees of its own request's new tokens, by their index; 0 where the request is causal.
+__device__ __forceinline__ uint64_t tree_mask(const AttnArgs& a, int first, int n, int t) {
+    if (!is_tree(n)) return 0;
+    const uint64_t m = a.tree[first + t];
+    return n == 64 ? m : m & ((uint64_t(1) << n) - 1);
+}
+
+// Of the request's tokens t0..t1 (t0 <= t1): the first key that one of them may see, the keys [all_from, all_stop) that all see, the
+// end of what one of them may see. A tree's masks are not looked at: its new tokens count as seen by some.
+template <bool TREE>
+__device__ __forceinline__ void tile_range(const AttnArgs& a, int n, int kv, int t0, int t1, int& from, int& all_from,
+                                           int& all_stop, int& stop) {
+    if (TREE && is_tree(n)) {
+        from = all_from = 0;
+        all_stop = max(kv - n, 0);
+        stop = kv;
+        return;
+    }
+    row_range(a, n, kv, t0, from, all_stop);
+    row_range(a, n, kv, t1, all_from, stop);
+}
+
+// Token t's keys [from, stop), those of a tree's mask apart.
+template <bool TREE>
+__device__ __forceinline__ void token_range(const AttnArgs& a, int n, int kv, int t, int& from, int& stop) {
+    if (TREE && is_tree(n)) {
+        from = 0;
+        stop = max(kv - n, 0);
+        return;
+    }
+    row_range(a, n, kv, t, from, stop);
 }
 
 // From the bits of a row's largest |value|: the power of two that brings it to
@@ -227,9 +265,14 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int first, int h, i
         a.lse[tok * a.heads + head] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m - off + SUM_LOG + log2f(l));
 }
 
+// (the kernels under a tree's masks are built by themselves: attn_tree_tiles.cu, attn_tree_rows.cu)
 cudaError_t launch_attn_tiles(const DeviceInfo& dev, const KvView& c, int dtype, const AttnArgs& a, const RowsPlan& pl,
                               cudaStream_t s);
 cudaError_t launch_attn_rows(const DeviceInfo& dev, const KvView& c, int dtype, const AttnArgs& a, const RowsPlan& pl,
                              cudaStream_t s);
+cudaError_t launch_attn_tree_tiles(const DeviceInfo& dev, const KvView& c, int dtype, const AttnArgs& a, const RowsPlan& pl,
+                                   cudaStream_t s);
+cudaError_t launch_attn_tree_rows(const DeviceInfo& dev, const KvView& c, int dtype, const AttnArgs& a, const RowsPlan& pl,
+                                  cudaStream_t s);
 
 }  // namespace cq

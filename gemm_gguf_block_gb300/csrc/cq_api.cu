@@ -1,6 +1,7 @@
 // C ABI of libcq: argument validation and dispatch to the kernel launchers.
 // Every check runs before any launch, so an error return means that nothing
-// was launched and nothing was written. See include/cq.h and include/cq_kv.h for the contract.
+// was launched and nothing was written. See include/cq.h, include/cq_kv.h and include/cq_tree.h
+// for the contract.
 #include <algorithm>
 #include <cstdint>
 #include <atomic>
@@ -13,6 +14,7 @@
 #include "cq.h"
 #include "cq_internal.h"
 #include "kv.cuh"
+#include "tree.cuh"
 
 namespace {
 
@@ -455,6 +457,48 @@ cq_status check_rows(const void* p, int64_t stride, int64_t width, int bytes) {
 
 cq_status status_of(cudaError_t e) { return e == cudaSuccess ? CQ_OK : CQ_ERR_CUDA; }
 
+// cq_attn_paged, and with masks cq_attn_tree.
+cq_status attend(const cq_kv_cache* cache, cq_dtype dtype, int64_t R, int64_t T, int64_t q_heads, int64_t max_new,
+                 const void* q, int64_t q_stride, const int32_t* block_table, int64_t max_blocks, const int32_t* kv_len,
+                 const int32_t* q_start, const uint64_t* tree, bool needs_tree, float scale, int causal, int64_t window,
+                 void* out, int64_t out_stride, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    const int bytes = dtype_bytes(dtype);
+    if (bytes == 0) return CQ_ERR_UNSUPPORTED_FORMAT;
+    if (R < 0 || T < 0 || q_heads < 0 || max_new < 0 || max_blocks < 0 || window < 0 || (causal != 0 && causal != 1))
+        return CQ_ERR_INVALID_ARG;
+    cq::KvView c;
+    cq_status st = check_cache(cache, &c);
+    if (st != CQ_OK) return st;
+    if (q_heads < 1 || q_heads > 1024 || q_heads % c.heads != 0 || R > 16384 || T > INT_LIMIT ||
+        max_blocks > (INT_LIMIT >> c.page_shift) || T * (q_heads / c.heads) > (int64_t(1) << 30))
+        return CQ_ERR_SHAPE;
+    if (R == 0 || T == 0) return CQ_OK;
+    const int64_t width = q_heads * c.dim;
+    if ((st = check_rows(q, q_stride, width, bytes)) != CQ_OK) return st;
+    if ((st = check_rows(out, out_stride, width, bytes)) != CQ_OK) return st;
+    if (kv_len == nullptr || q_start == nullptr || (max_blocks > 0 && block_table == nullptr) || (needs_tree && tree == nullptr))
+        return CQ_ERR_INVALID_ARG;
+    const size_t need = cq::attn_workspace_size(c.dim);
+    if (workspace == nullptr || workspace_bytes < need) return CQ_ERR_WORKSPACE;
+    if (!aligned4(kv_len) || !aligned4(q_start) || !aligned4(block_table) || !aligned4(lse) || !aligned_to(tree, 8) ||
+        !aligned_to(workspace, 256))
+        return CQ_ERR_ALIGNMENT;
+    cq::DeviceInfo dev;
+    if (cq::device_info(&dev) != cudaSuccess) return CQ_ERR_CUDA;
+    cq::AttnArgs a{};
+    a.q = q; a.out = out; a.lse = lse;
+    a.table = block_table; a.kv_len = kv_len; a.q_start = q_start;
+    a.tree = tree;
+    a.status = dev.status; a.ws = workspace;
+    a.q_stride = q_stride; a.out_stride = out_stride;
+    a.max_blocks = max_blocks;
+    a.window = std::min(window, int64_t(1) << 32);   // wider than any length and position: sums with positions stay in range
+    a.max_new = std::min(max_new, T);
+    a.scale = scale;
+    a.R = static_cast<int>(R); a.T = static_cast<int>(T); a.heads = static_cast<int>(q_heads); a.causal = causal;
+    return status_of(cq::launch_attn(dev, c, dtype, a, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -531,39 +575,139 @@ cq_status cq_attn_paged(const cq_kv_cache* cache, cq_dtype dtype, int64_t R, int
                         int64_t max_blocks, const int32_t* kv_len, const int32_t* q_start, float scale, int causal,
                         int64_t window, void* out, int64_t out_stride, float* lse, void* workspace,
                         size_t workspace_bytes, void* stream) {
-    const int bytes = dtype_bytes(dtype);
-    if (bytes == 0) return CQ_ERR_UNSUPPORTED_FORMAT;
-    if (R < 0 || T < 0 || q_heads < 0 || max_new < 0 || max_kv < 0 || max_blocks < 0 || window < 0 ||
-        (causal != 0 && causal != 1))
+    if (dtype_bytes(dtype) == 0) return CQ_ERR_UNSUPPORTED_FORMAT;
+    if (max_kv < 0) return CQ_ERR_INVALID_ARG;
+    return attend(cache, dtype, R, T, q_heads, max_new, q, q_stride, block_table, max_blocks, kv_len, q_start, nullptr, false,
+                  scale, causal, window, out, out_stride, lse, workspace, workspace_bytes, stream);
+}
+
+cq_status cq_attn_tree(const cq_kv_cache* cache, cq_dtype dtype, int64_t R, int64_t T, int64_t q_heads,
+                       int64_t max_new, const void* q, int64_t q_stride, const int32_t* block_table,
+                       int64_t max_blocks, const int32_t* kv_len, const int32_t* q_start, const uint64_t* mask,
+                       float scale, void* out, int64_t out_stride, float* lse, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+    return attend(cache, dtype, R, T, q_heads, max_new, q, q_stride, block_table, max_blocks, kv_len, q_start, mask, true,
+                  scale, 1, 0, out, out_stride, lse, workspace, workspace_bytes, stream);
+}
+
+cq_status cq_qk_rope(cq_dtype in, cq_dtype out, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                     int64_t rot_dim, int adjacent, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                     const int32_t* positions, const double* freqs, const float* q_norm, const float* k_norm, float eps,
+                     void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream) {
+    const int bi = dtype_bytes(in), bo = dtype_bytes(out);
+    if (bi == 0 || bo == 0 || (in != out && in != CQ_F32)) return CQ_ERR_UNSUPPORTED_FORMAT;
+    if (T < 0 || q_heads < 0 || kv_heads < 0 || head_dim < 0 || rot_dim < 0 || (adjacent != 0 && adjacent != 1) || !(eps >= 0.0f))
         return CQ_ERR_INVALID_ARG;
-    cq::KvView c;
-    cq_status st = check_cache(cache, &c);
-    if (st != CQ_OK) return st;
-    if (q_heads < 1 || q_heads > 1024 || q_heads % c.heads != 0 || R > 16384 || T > INT_LIMIT ||
-        max_blocks > (INT_LIMIT >> c.page_shift) || T * (q_heads / c.heads) > (int64_t(1) << 30))
+    if ((head_dim != 64 && head_dim != 128) || rot_dim > head_dim || rot_dim % 8 != 0 || q_heads > 1024 || kv_heads > 1024 ||
+        T > INT_LIMIT)
         return CQ_ERR_SHAPE;
-    if (R == 0 || T == 0) return CQ_OK;
-    const int64_t width = q_heads * c.dim;
-    if ((st = check_rows(q, q_stride, width, bytes)) != CQ_OK) return st;
-    if ((st = check_rows(out, out_stride, width, bytes)) != CQ_OK) return st;
-    if (kv_len == nullptr || q_start == nullptr || (max_blocks > 0 && block_table == nullptr)) return CQ_ERR_INVALID_ARG;
-    const size_t need = cq::attn_workspace_size(c.dim);
-    if (workspace == nullptr || workspace_bytes < need) return CQ_ERR_WORKSPACE;
-    if (!aligned4(kv_len) || !aligned4(q_start) || !aligned4(block_table) || !aligned4(lse) || !aligned_to(workspace, 256))
+    if (T == 0 || q_heads + kv_heads == 0) return CQ_OK;
+    if (positions == nullptr || (rot_dim > 0 && freqs == nullptr)) return CQ_ERR_INVALID_ARG;
+    if (!aligned4(positions) || !aligned_to(freqs, 8)) return CQ_ERR_ALIGNMENT;
+    cq::RopeArgs a{};
+    const void* x[2] = {q, k};
+    void* y[2] = {q_out, k_out};
+    const float* w[2] = {q_norm, k_norm};
+    const int64_t heads[2] = {q_heads, kv_heads}, xs[2] = {q_stride, k_stride}, ys[2] = {q_out_stride, k_out_stride};
+    for (int i = 0; i < 2; ++i) {
+        if (heads[i] == 0) continue;
+        cq_status st = check_rows(x[i], xs[i], heads[i] * head_dim, bi);
+        if (st == CQ_OK) st = check_rows(y[i], ys[i], heads[i] * head_dim, bo);
+        if (st != CQ_OK) return st;
+        if (!aligned16(w[i])) return CQ_ERR_ALIGNMENT;
+        if (x[i] == y[i] && (in != out || xs[i] != ys[i])) return CQ_ERR_INVALID_ARG;
+        a.x[i] = x[i]; a.y[i] = y[i]; a.w[i] = w[i];
+        a.x_stride[i] = xs[i]; a.y_stride[i] = ys[i];
+        a.heads[i] = static_cast<int>(heads[i]);
+    }
+    a.positions = positions; a.freqs = freqs; a.eps = eps;
+    a.T = static_cast<int>(T); a.rot = static_cast<int>(rot_dim); a.adjacent = adjacent;
+    cq::DeviceInfo dev;
+    if (cq::device_info(&dev) != cudaSuccess) return CQ_ERR_CUDA;
+    return status_of(cq::launch_qk_rope(dev, in, out, head_dim, a, static_cast<cudaStream_t>(stream)));
+}
+
+cq_status cq_tree_plan(int64_t R, int64_t T, const int32_t* kv_len, const int32_t* q_start, const int32_t* parent,
+                       uint64_t* mask, int32_t* positions, void* stream) {
+    if (R < 0 || T < 0) return CQ_ERR_INVALID_ARG;
+    if (R > 16384 || T > INT_LIMIT) return CQ_ERR_SHAPE;
+    if (T == 0 || (mask == nullptr && positions == nullptr)) return CQ_OK;
+    if (parent == nullptr || (R > 0 && (kv_len == nullptr || q_start == nullptr))) return CQ_ERR_INVALID_ARG;
+    if (!aligned4(kv_len) || !aligned4(q_start) || !aligned4(parent) || !aligned4(positions) || !aligned_to(mask, 8))
         return CQ_ERR_ALIGNMENT;
     cq::DeviceInfo dev;
     if (cq::device_info(&dev) != cudaSuccess) return CQ_ERR_CUDA;
-    cq::AttnArgs a{};
-    a.q = q; a.out = out; a.lse = lse;
-    a.table = block_table; a.kv_len = kv_len; a.q_start = q_start;
-    a.status = dev.status; a.ws = workspace;
-    a.q_stride = q_stride; a.out_stride = out_stride;
-    a.max_blocks = max_blocks;
-    a.window = std::min(window, int64_t(1) << 32);   // wider than any length and position: sums with positions stay in range
-    a.max_new = std::min(max_new, T);
-    a.scale = scale;
-    a.R = static_cast<int>(R); a.T = static_cast<int>(T); a.heads = static_cast<int>(q_heads); a.causal = causal;
-    return status_of(cq::launch_attn(dev, c, dtype, a, static_cast<cudaStream_t>(stream)));
+    return status_of(cq::launch_tree_plan(dev, static_cast<int>(R), static_cast<int>(T), kv_len, q_start, parent, mask,
+                                          positions, static_cast<cudaStream_t>(stream)));
+}
+
+cq_status cq_tree_verify(int64_t R, int64_t T, int64_t V, const float* logits, int64_t logits_stride, const float* draft,
+                         int64_t draft_stride, const int32_t* tokens, const int32_t* parent, const int32_t* q_start,
+                         const float* temperature, const float* u_accept, const float* u_sample, int64_t max_path,
+                         int32_t* count, int32_t* path, int32_t* next, void* stream) {
+    if (R < 0 || T < 0 || V < 1 || max_path < 1) return CQ_ERR_INVALID_ARG;
+    if (R > 16384 || T > INT_LIMIT || V > 262144 || max_path > CQ_TREE_MAX) return CQ_ERR_SHAPE;
+    if (R == 0) return CQ_OK;
+    if (q_start == nullptr || temperature == nullptr || u_sample == nullptr || count == nullptr || path == nullptr || next == nullptr ||
+        (T > 0 && (logits == nullptr || tokens == nullptr || parent == nullptr || u_accept == nullptr)))
+        return CQ_ERR_INVALID_ARG;
+    const int64_t most = int64_t(1) << 40;
+    if (T > 0 && (logits_stride < V || logits_stride > most || (draft != nullptr && (draft_stride < V || draft_stride > most))))
+        return CQ_ERR_SHAPE;
+    const void* words[] = {logits, draft, tokens, parent, q_start, temperature, u_accept, u_sample, count, path, next};
+    for (const void* p : words)
+        if (!aligned4(p)) return CQ_ERR_ALIGNMENT;
+    cq::DeviceInfo dev;
+    if (cq::device_info(&dev) != cudaSuccess) return CQ_ERR_CUDA;
+    cq::VerifyArgs a{};
+    a.logits = logits; a.draft = draft;
+    a.logits_stride = logits_stride; a.draft_stride = draft_stride;
+    a.tokens = tokens; a.parent = parent; a.q_start = q_start;
+    a.temperature = temperature; a.u_accept = u_accept; a.u_sample = u_sample;
+    a.count = count; a.path = path; a.next = next;
+    a.status = dev.status;
+    a.R = static_cast<int>(R); a.T = static_cast<int>(T); a.V = static_cast<int>(V); a.max_path = static_cast<int>(max_path);
+    return status_of(cq::launch_tree_verify(dev, a, static_cast<cudaStream_t>(stream)));
+}
+
+cq_status cq_kv_move(const cq_kv_cache* cache, int64_t R, const int32_t* block_table, int64_t max_blocks,
+                     const int32_t* kv_len, const int32_t* q_start, const int32_t* count, const int32_t* path,
+                     int64_t max_path, int32_t* new_len, void* stream) {
+    if (R < 0 || max_blocks < 0 || max_path < 1) return CQ_ERR_INVALID_ARG;
+    cq::KvView c;
+    const cq_status st = check_cache(cache, &c);
+    if (st != CQ_OK) return st;
+    if (R > 16384 || max_path > CQ_TREE_MAX || max_blocks > (INT_LIMIT >> c.page_shift)) return CQ_ERR_SHAPE;
+    if (R == 0) return CQ_OK;
+    if (kv_len == nullptr || q_start == nullptr || count == nullptr || path == nullptr || (max_blocks > 0 && block_table == nullptr))
+        return CQ_ERR_INVALID_ARG;
+    const void* words[] = {block_table, kv_len, q_start, count, path, new_len};
+    for (const void* p : words)
+        if (!aligned4(p)) return CQ_ERR_ALIGNMENT;
+    cq::DeviceInfo dev;
+    if (cq::device_info(&dev) != cudaSuccess) return CQ_ERR_CUDA;
+    const cq::MoveArgs a{block_table, kv_len, q_start, count, path, new_len, dev.status, max_blocks, static_cast<int>(R),
+                         static_cast<int>(max_path)};
+    return status_of(cq::launch_kv_move(dev, c, a, static_cast<cudaStream_t>(stream)));
+}
+
+cq_status cq_kv_release(int64_t R, int64_t page_size, const int32_t* block_table, int64_t max_blocks, int64_t num_pages,
+                        const int32_t* old_len, const int32_t* new_len, int32_t* freed, int64_t capacity, int32_t* used,
+                        void* stream) {
+    if (R < 0 || max_blocks < 0 || num_pages < 0 || capacity < 0) return CQ_ERR_INVALID_ARG;
+    const int shift = page_shift(page_size);
+    if (shift < 0 || R > 16384 || capacity > INT_LIMIT || num_pages > INT_LIMIT || max_blocks > (INT_LIMIT >> shift))
+        return CQ_ERR_SHAPE;
+    if (used == nullptr || (capacity > 0 && freed == nullptr) ||
+        (R > 0 && (old_len == nullptr || new_len == nullptr || (max_blocks > 0 && block_table == nullptr))))
+        return CQ_ERR_INVALID_ARG;
+    const void* words[] = {block_table, old_len, new_len, freed, used};
+    for (const void* p : words)
+        if (!aligned4(p)) return CQ_ERR_ALIGNMENT;
+    cq::DeviceInfo dev;
+    if (cq::device_info(&dev) != cudaSuccess) return CQ_ERR_CUDA;
+    return status_of(cq::launch_kv_release(dev, static_cast<int>(R), shift, block_table, max_blocks, num_pages, old_len, new_len,
+                                           freed, static_cast<int>(capacity), used, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

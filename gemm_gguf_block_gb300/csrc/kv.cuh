@@ -3,6 +3,7 @@
 // the conversions of the value types they take.
 #pragma once
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -44,6 +45,7 @@ struct AttnArgs {
     const int32_t* table;
     const int32_t* kv_len;
     const int32_t* q_start;
+    const uint64_t* tree;           // cq_attn_tree: the tokens' masks; else NULL
     int* status;
     void* ws;
     int64_t q_stride, out_stride;   // elements
@@ -67,4 +69,47 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
     *reinterpret_cast<uint2*>(p) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
+
+// Four consecutive values as they were loaded, converted when they are used.
+template <typename T> struct Raw4 {
+    uint32_t u[sizeof(T)];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (sizeof(T) == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p);
+            u[0] = v.x; u[1] = v.y; u[2] = v.z; u[3] = v.w;
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            u[0] = v.x; u[1] = v.y;
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) u[i] = 0;
+    }
+    __device__ __forceinline__ float4 value() const {
+        if constexpr (sizeof(T) == 4) {
+            return make_float4(__uint_as_float(u[0]), __uint_as_float(u[1]), __uint_as_float(u[2]), __uint_as_float(u[3]));
+        } else if constexpr (std::is_same<T, __half>::value) {
+            const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u[0]));
+            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u[1]));
+            return make_float4(a.x, a.y, b.x, b.y);
+        } else {
+            return make_float4(__uint_as_float(u[0] << 16), __uint_as_float(u[0] & 0xffff0000u), __uint_as_float(u[1] << 16),
+                               __uint_as_float(u[1] & 0xffff0000u));
+        }
+    }
+};
+
+// x to the nearest integer, halves away from zero, for |x| < 2^22: half a unit is
+// added away from zero and both the addition and the conversion are cut off, so
+// that nothing is rounded up across an integer. No clamp: |x * (1 / s)| is at most 127 (1 + 2^-22)
+// for every s that is not below the block's largest / 127.
+__device__ __forceinline__ int round_away(float x) {
+    return __float2int_rz(__fadd_rz(x, copysignf(0.5f, x)));
+}
+
+__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
 }  // namespace cq

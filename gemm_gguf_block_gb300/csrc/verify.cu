@@ -1,0 +1,440 @@
+// Verification of drafted tokens (cq_tree_verify in include/cq_tree.h).
+//
+// A cluster of CTAs walks one request's tree from its first token: only the rows on the path of
+// kept tokens are read, each CTA its slice of the vocabulary, which stays in shared memory for as
+// long as the row is looked at. Probabilities are whole numbers,
+//   w_v = 2^46 * 2^((z_v - max z) log2(e) / temperature), rounded,
+// so that sums are exact whatever their order, W = sum w < 2^64 for 2^18 values, and the
+// rounding moves a value of the distribution function by 2^-46 sqrt(V) of the largest, not by
+// fp32's 2^-24: a random number that falls near a border of a 10^5-value distribution still gives
+// the token that 64 bits give. The exponential of fp32 units would not do, and fp64 runs at a
+// sixty-fourth of fp32's rate; whole-number arithmetic costs about 45 instructions a value.
+//
+// After k rejected children the distribution is r_k = max(w - q A_k, 0) with A_k = R_0 + .. +
+// R_(k-1), R_i the sum of r_i: max(max(a - b, 0) - c, 0) = max(a - b - c, 0) for b, c >= 0, so that
+// one number stands for all rejections, and a rejection is one pass over the slice. Without draft
+// probabilities a rejection only takes the child's own weight away.
+//
+// Every CTA decides by the same numbers: what a decision needs is spread over the cluster's shared
+// memory (the request's tokens by CTA 0, maxima, sums and the children's logits by their owners),
+// so that the CTAs meet at the same barriers whatever else writes to the inputs meanwhile.
+#include <algorithm>
+
+#include "tree.cuh"
+
+namespace cq {
+namespace {
+
+constexpr int THREADS = 512;
+constexpr int WARPS = THREADS / 32;
+constexpr int MAX_CLUSTER = 8;
+constexpr int MAX = CQ_TREE_MAX;
+constexpr int ONE_BITS = 46;                       // w of the largest logit is 2^46
+constexpr float CUT = -47.0f;                      // below 2^CUT of the largest: 0 (less than half a unit)
+
+// 2^(i / 256) in units of 2^-46: the exponential's series in fp64, worked out by the compiler.
+struct Pow2Table { unsigned long long v[256]; };
+constexpr Pow2Table pow2_table() {
+    Pow2Table t{};
+    for (int i = 0; i < 256; ++i) {
+        const double x = i * (0.69314718055994530942 / 256.0);
+        double sum = 1.0, term = 1.0;
+        for (int k = 1; k < 24; ++k) {
+            term *= x / k;
+            sum += term;
+        }
+        t.v[i] = static_cast<unsigned long long>(sum * 70368744177664.0 + 0.5);
+    }
+    return t;
+}
+__constant__ Pow2Table POW2 = pow2_table();
+
+// What a request is decided by: CTA 0 reads it, the others copy it.
+struct Request {
+    int first, n, greedy;
+    float c_hi, c_lo;                              // log2(e) / temperature in two parts
+    unsigned long long u_sample;
+    unsigned long long u[MAX];                     // in units of 2^-64
+    int token[MAX];
+    int parent[MAX];
+};
+
+__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint64_t v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_cluster32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+// All threads of the cluster; what they wrote before is visible behind it.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// u in [0, 1) in units of 2^-64, exact (a float has 24 bits and is at least 2^-149).
+__device__ __forceinline__ uint64_t unit64(float u) {
+    if (!(u > 0.0f)) return 0;
+    return __float2ull_rz(fminf(u, 0.99999994f) * 18446744073709551616.0f);
+}
+// A probability: 1 is 2^64 - 1.
+__device__ __forceinline__ uint64_t prob64(float q) { return q > 0.0f ? __float2ull_rz(fminf(q, 1.0f) * 18446744073709551616.0f) : 0; }
+
+// The order of floats as unsigned integers; NaN and +infinity on top.
+__device__ __forceinline__ uint32_t order_of(float z) {
+    const uint32_t b = __float_as_uint(__fadd_rn(z, 0.0f));      // -0 is 0
+    if (!(z < INFINITY)) return 0xffffffffu;
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) { return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o); }
+
+// w of logit z beside the row's largest, m (finite); c = log2(e) / temperature. The exponent
+// x = (z - m) c is held to 2^-40: the difference and its rounding error, times c in two parts. Then
+// 2^x = 2^I * table[8 bits] * (1 + y + y^2 / 2 + y^3 / 6), y < 2^-8.5 in units of 2^-40; the next term is
+// 2^-38.
+__device__ __forceinline__ uint64_t weight(float z, float m, float c_hi, float c_lo, const unsigned long long* table) {
+    const float d = __fsub_rn(z, m);
+    const float p = __fmul_rn(d, c_hi);
+    if (!(p > CUT)) return z == m ? uint64_t(1) << ONE_BITS : 0;
+    const float bb = __fsub_rn(d, z);
+    const float err = __fadd_rn(__fsub_rn(z, __fsub_rn(d, bb)), __fsub_rn(-m, bb));      // z - m = d + err
+    float e = __fmaf_rn(d, c_hi, -p);
+    e = __fmaf_rn(d, c_lo, e);
+    e = __fmaf_rn(err, c_hi, e);
+    const float n = rintf(p), f = __fsub_rn(p, n);
+    const float f1 = rintf(f * 1048576.0f);                                             // 2^20
+    const float f2 = __fadd_rn(__fmaf_rn(f1, -9.5367431640625e-07f, f), e);
+    const int64_t x = (static_cast<int64_t>(static_cast<int>(n)) << 40) + (static_cast<int64_t>(static_cast<int>(f1)) << 20) +
+                      __float2int_rn(f2 * 1099511627776.0f);                            // 2^40
+    if (x >= 0) return uint64_t(1) << ONE_BITS;
+    const int down = -static_cast<int>(x >> 40);                                        // 1 .. 48
+    const uint32_t g = static_cast<uint32_t>(x);
+    const uint64_t t = table[static_cast<uint32_t>(x >> 32) & 255u];
+    const uint32_t y = __umulhi(g, 2977044472u);                                        // ln 2 in units of 2^-32
+    const uint32_t y2 = __umulhi(y, y) >> 9;
+    const uint32_t y3 = __umulhi(__umulhi(y2, y), 1431655765u) >> 8;
+    const uint64_t w = t + ((static_cast<uint64_t>(static_cast<uint32_t>(t >> 15)) * (y + y2 + y3)) >> 25);
+    return (w + (uint64_t(1) << (down - 1))) >> down;
+}
+
+// max(w - q A, 0), A = a_hi 2^64 + a_lo.
+__device__ __forceinline__ uint64_t without(uint64_t w, uint64_t q, uint64_t a_lo, uint32_t a_hi) {
+    const uint64_t lo = __umul64hi(q, a_lo);
+    if (a_hi != 0 && (__umul64hi(q, a_hi) != 0 || q * a_hi + lo < lo)) return 0;
+    const uint64_t t = lo + q * a_hi;
+    return w > t ? w - t : 0;
+}
+
+struct Shared {
+    unsigned long long table[256];
+    unsigned long long xchg[2][MAX_CLUSTER];       // maxima, then sums, alternately
+    unsigned long long part[WARPS];                // the warps' sums of r, over their own stretch of the slice
+    unsigned long long child[MAX];                 // logit and draft probability of the node's children
+    Request rq;
+    int gone[MAX];                                 // tokens rejected at this node (no draft probabilities)
+};
+
+template <bool DRAFT>
+__global__ void __launch_bounds__(THREADS) tree_verify_kernel(const VerifyArgs a, const int cluster, const int slice, const int stretch) {
+    pdl_trigger();
+    extern __shared__ __align__(16) float row[];   // [slice] of the node's logits
+    __shared__ Shared sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int r = blockIdx.x / cluster;
+    const uint32_t rank = cluster_rank();
+    if (tid < 256) sh.table[tid] = POW2.v[tid];
+    pdl_wait();
+    const int lo = static_cast<int>(min(static_cast<int64_t>(rank) * slice, static_cast<int64_t>(a.V)));
+    const int len = min(slice, a.V - lo);          // this CTA's values; 0 for none
+    const int w0 = min(warp * stretch, len), w1 = min(w0 + stretch, len);
+    if (rank == 0) {
+        const int first = min(max(a.q_start[r], 0), a.T);
+        const int n = max(min(a.q_start[r + 1], a.T) - first, 0);
+        if (tid == 0) {
+            const float t = a.temperature[r];
+            const bool greedy = !(t >= 5.421010862427522e-20f);                          // 2^-64
+            const double c = 1.4426950408889634 / (greedy ? 1.0 : static_cast<double>(fminf(t, 1.8446744073709552e19f)));
+            sh.rq.first = first;
+            sh.rq.n = n;
+            sh.rq.greedy = greedy;
+            sh.rq.c_hi = static_cast<float>(c);
+            sh.rq.c_lo = static_cast<float>(c - static_cast<double>(sh.rq.c_hi));
+            sh.rq.u_sample = unit64(a.u_sample[r]);
+            if (n > MAX) atomicOr(a.status, CQ_DEV_TREE);
+        }
+        if (tid < min(n, MAX)) {
+            int p = a.parent[first + tid];
+            if (p < -1 || p >= tid) {
+                atomicOr(a.status, CQ_DEV_TREE);
+                p = -1;
+            }
+            sh.rq.parent[tid] = p;
+            sh.rq.token[tid] = a.tokens[first + tid];
+            sh.rq.u[tid] = unit64(a.u_accept[first + tid]);
+        }
+    }
+    cluster_sync();
+    if (rank != 0) {
+        const uint32_t from = mapa(smem_u32(&sh.rq), 0);
+        static_assert(sizeof(Request) % 4 == 0, "copied as words");
+        for (int i = tid; i < static_cast<int>(sizeof(Request) / 4); i += THREADS)
+            reinterpret_cast<uint32_t*>(&sh.rq)[i] = ld_cluster32(from + 4 * i);
+        __syncthreads();
+    }
+    const int n = sh.rq.n, first = sh.rq.first;
+    const bool lead = rank == 0 && tid == 0;
+    int32_t* path = a.path + static_cast<int64_t>(r) * a.max_path;
+    int kept = 0, next = -1;
+
+    // Spreads a CTA's number and gives all of them, each CTA's in its place.
+    int turn = 0;
+    auto spread = [&](uint64_t mine) {
+        if (tid < cluster) st_cluster(mapa(smem_u32(&sh.xchg[turn][rank]), tid), mine);
+        cluster_sync();
+        turn ^= 1;
+        return sh.xchg[turn ^ 1];
+    };
+    // The warps' sums to sh.part and the CTA's to all threads.
+    auto sum_of = [&](uint64_t s) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        __syncthreads();                           // the last readers of part are through
+        if (lane == 0) sh.part[warp] = s;
+        __syncthreads();
+        uint64_t all = 0;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) all += sh.part[w];
+        return all;
+    };
+
+    if (n > 0 && n <= MAX) {
+        int node = 0;
+        kept = 1;
+        if (lead) path[0] = 0;
+        const float c_hi = sh.rq.c_hi, c_lo = sh.rq.c_lo;
+        for (;;) {
+            // ---- the node's row: into shared memory, its largest logit and that one's smallest index
+            const float* z = a.logits + static_cast<int64_t>(first + node) * a.logits_stride + lo;
+            __syncthreads();                       // nobody looks at the last row any more
+            uint64_t key = 0;
+            for (int i0 = w0; i0 < w1; i0 += 32 * 8) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int i = i0 + 32 * k + lane;
+                    v[k] = i < w1 ? z[i] : -INFINITY;
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int i = i0 + 32 * k + lane;
+                    if (i < w1) row[i] = v[k];
+                    const uint64_t o = static_cast<uint64_t>(order_of(v[k])) << 32 | static_cast<uint32_t>(~(lo + i));
+                    if (i < w1) key = max(key, o);
+                }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
+            if (lane == 0) sh.part[warp] = key;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) key = max(key, static_cast<uint64_t>(sh.part[w]));
+            const unsigned long long* got = spread(key);
+            for (int c = 0; c < cluster; ++c) key = max(key, static_cast<uint64_t>(got[c]));
+            const uint32_t top = static_cast<uint32_t>(key >> 32);
+            const float m = value_of(top);
+            if (top == 0xffffffffu || m == -INFINITY) {
+                if (lead) atomicOr(a.status, CQ_DEV_LOGITS);
+                break;
+            }
+            const int best = static_cast<int>(~static_cast<uint32_t>(key));
+            // ---- its children, one bit each
+            uint64_t children = 0;
+            if (kept < a.max_path) {
+                const uint32_t c0 = __ballot_sync(0xffffffffu, lane < n && sh.rq.parent[lane] == node && lane > 0);
+                const uint32_t c1 = __ballot_sync(0xffffffffu, lane + 32 < n && sh.rq.parent[lane + 32] == node);
+                children = static_cast<uint64_t>(c1) << 32 | c0;
+            }
+            int taken = -1;
+            if (sh.rq.greedy) {
+                for (uint64_t left = children; left != 0 && taken < 0; left &= left - 1) {
+                    const int j = __ffsll(static_cast<long long>(left)) - 1;
+                    if (sh.rq.token[j] == best) taken = j;
+                }
+                if (taken < 0) next = best;
+            } else {
+                uint64_t s = 0;
+                for (int i = w0 + lane; i < w1; i += 32) s += weight(row[i], m, c_hi, c_lo, sh.table);
+                s = sum_of(s);
+                // the children's logits and draft probabilities, from the CTA that has them
+                if (tid < MAX && (children >> tid & 1) != 0) {
+                    const int x = sh.rq.token[tid];
+                    if (x >= lo && x < lo + len) {
+                        const float q = DRAFT ? a.draft[static_cast<int64_t>(first + node) * a.draft_stride + x] : 0.0f;
+                        const uint64_t v = static_cast<uint64_t>(__float_as_uint(q)) << 32 | __float_as_uint(row[x - lo]);
+                        for (int c = 0; c < cluster; ++c) st_cluster(mapa(smem_u32(&sh.child[tid]), c), v);
+                    }
+                }
+                got = spread(s);
+                uint64_t tot[MAX_CLUSTER], R = 0, a_lo = 0;
+                uint32_t a_hi = 0;
+                int gone = 0;
+#pragma unroll
+                for (int c = 0; c < MAX_CLUSTER; ++c) {
+                    tot[c] = c < cluster ? got[c] : 0;
+                    R += tot[c];
+                }
+                for (uint64_t left = children; left != 0 && taken < 0; left &= left - 1) {
+                    const int j = __ffsll(static_cast<long long>(left)) - 1, x = sh.rq.token[j];
+                    if (x < 0 || x >= a.V) continue;
+                    const uint64_t v = sh.child[j];
+                    uint64_t w = weight(__uint_as_float(static_cast<uint32_t>(v)), m, c_hi, c_lo, sh.table);
+                    if constexpr (DRAFT) {
+                        const uint64_t q = prob64(__uint_as_float(static_cast<uint32_t>(v >> 32)));
+                        w = without(w, q, a_lo, a_hi);
+                        if (__umul64hi(sh.rq.u[j], __umul64hi(q, R)) < w) {
+                            taken = j;
+                            break;
+                        }
+                        // one pass for the next distribution's sums
+                        const uint64_t n_lo = a_lo + R;
+                        const uint32_t n_hi = a_hi + (n_lo < a_lo);
+                        const float* dr = a.draft + static_cast<int64_t>(first + node) * a.draft_stride + lo;
+                        uint64_t rs = 0;
+                        for (int i = w0 + lane; i < w1; i += 32)
+                            rs += without(weight(row[i], m, c_hi, c_lo, sh.table), prob64(dr[i]), n_lo, n_hi);
+                        const uint64_t before = lane < WARPS ? sh.part[lane] : 0;       // kept where nothing is left
+                        rs = sum_of(rs);
+                        got = spread(rs);
+                        uint64_t sum = 0;
+                        for (int c = 0; c < cluster; ++c) sum += got[c];
+                        if (sum != 0) {
+                            R = sum;
+                            a_lo = n_lo;
+                            a_hi = n_hi;
+#pragma unroll
+                            for (int c = 0; c < MAX_CLUSTER; ++c) tot[c] = c < cluster ? got[c] : 0;
+                        } else {
+                            __syncthreads();
+                            if (tid < WARPS) sh.part[tid] = before;
+                            __syncthreads();
+                        }
+                    } else {
+                        for (int k = 0; k < gone; ++k)
+                            if (sh.gone[k] == x) w = 0;
+                        if (__umul64hi(sh.rq.u[j], R) < w) {
+                            taken = j;
+                            break;
+                        }
+                        if (w != 0 && w != R) {
+                            R -= w;
+                            const int owner = x / slice;
+#pragma unroll
+                            for (int c = 0; c < MAX_CLUSTER; ++c)
+                                if (c == owner) tot[c] -= w;
+                            __syncthreads();
+                            if (tid == 0) {
+                                sh.gone[gone] = x;
+                                if (owner == static_cast<int>(rank)) sh.part[(x - lo) / stretch] -= w;
+                            }
+                            ++gone;
+                            __syncthreads();
+                        }
+                    }
+                }
+                if (taken < 0) {
+                    // ---- the next token: the CTA, the warp's stretch and the place in it where the sums pass u R
+                    uint64_t t = __umul64hi(sh.rq.u_sample, R);
+                    int owner = -1;
+#pragma unroll
+                    for (int c = 0; c < MAX_CLUSTER; ++c)
+                        if (owner < 0) {
+                            if (t < tot[c]) owner = c; else t -= tot[c];
+                        }
+                    if (owner == static_cast<int>(rank)) {
+                        __syncthreads();
+                        int w = 0;
+                        while (w < WARPS - 1 && t >= sh.part[w]) t -= sh.part[w++];
+                        const int s0 = min(w * stretch, len), s1 = min(s0 + stretch, len);
+                        const int per = (stretch + THREADS - 1) / THREADS, i0 = s0 + tid * per, i1 = min(i0 + per, s1);
+                        const float* dr = DRAFT ? a.draft + static_cast<int64_t>(first + node) * a.draft_stride + lo : nullptr;
+                        auto value = [&](int i) {
+                            uint64_t v = weight(row[i], m, c_hi, c_lo, sh.table);
+                            if constexpr (DRAFT) v = without(v, prob64(a_lo | a_hi ? dr[i] : 0.0f), a_lo, a_hi);
+                            else
+                                for (int k = 0; k < gone; ++k)
+                                    if (sh.gone[k] == lo + i) v = 0;
+                            return v;
+                        };
+                        uint64_t mine = 0;
+                        for (int i = i0; i < i1; ++i) mine += value(i);
+                        uint64_t upto = mine;
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const uint64_t up = __shfl_up_sync(0xffffffffu, upto, o);
+                            if (lane >= o) upto += up;
+                        }
+                        __syncthreads();
+                        if (lane == 31) sh.part[warp] = upto;
+                        __syncthreads();
+                        for (int k = 0; k < warp; ++k) upto += sh.part[k];
+                        if (t < upto && t >= upto - mine) {                          // one thread
+                            uint64_t c = upto - mine;
+                            int i = i0;
+                            for (; i < i1 - 1; ++i) {
+                                c += value(i);
+                                if (t < c) break;
+                            }
+                            a.next[r] = lo + i;
+                        }
+                    }
+                    next = -2;                     // written by its owner
+                }
+            }
+            if (taken < 0) break;
+            node = taken;
+            if (lead) path[kept] = node;
+            ++kept;
+        }
+    }
+    if (rank == 0) {
+        for (int i = kept + tid; i < a.max_path; i += THREADS) path[i] = -1;
+        if (tid == 0) {
+            a.count[r] = kept;
+            if (next != -2) a.next[r] = next;
+        }
+    }
+    cluster_sync();                                // nobody leaves while another may look at its shared memory
+}
+
+template <bool DRAFT>
+cudaError_t launch_t(const DeviceInfo& dev, const VerifyArgs& a, cudaStream_t s) {
+    // CTAs of a request: a slice of 4096 values is eight a thread; eight CTAs at most, whose slices of 2^18
+    // values fit in shared memory.
+    int cluster = 1;
+    while (cluster < MAX_CLUSTER && a.V > 4096 * cluster) cluster *= 2;
+    const int slice = (a.V + cluster - 1) / cluster, stretch = (slice + WARPS - 1) / WARPS;
+    const int smem = slice * 4;
+    if (smem > dev.smem_optin - static_cast<int>(sizeof(Shared)) - 1024) return cudaErrorInvalidConfiguration;
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(tree_verify_kernel<DRAFT>), smem);
+    if (e != cudaSuccess) return e;
+    return launch_kernel_cluster(tree_verify_kernel<DRAFT>, dim3(static_cast<unsigned>(a.R * cluster)), dim3(THREADS),
+                                 static_cast<size_t>(smem), s, dim3(cluster), a, cluster, slice, stretch);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_verify(const DeviceInfo& dev, const VerifyArgs& a, cudaStream_t s) {
+    return a.draft != nullptr ? launch_t<true>(dev, a, s) : launch_t<false>(dev, a, s);
+}
+
+}  // namespace cq
