@@ -51,10 +51,10 @@ cudaError_t launch_attn(const DeviceInfo& dev, const KvView& c, int dtype, const
     pl.tile_rows = tiles ? TILE_ROWS : INT_MAX;
     pl.after_tiles = tiles;
     if (tiles) {
-        const cudaError_t e = (a.tree != nullptr ? launch_attn_tree_tiles : launch_attn_tiles)(dev, c, dtype, a, pl, s);
+        const cudaError_t e = launch_attn_tiles(dev, c, dtype, a, pl, s);
         if (e != cudaSuccess) return e;
     }
-    return (a.tree != nullptr ? launch_attn_tree_rows : launch_attn_rows)(dev, c, dtype, a, pl, s);
+    return launch_attn_rows(dev, c, dtype, a, pl, s);
 }
 
 }  // namespace cq

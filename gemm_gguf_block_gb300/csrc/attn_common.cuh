@@ -265,14 +265,9 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int first, int h, i
         a.lse[tok * a.heads + head] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m - off + SUM_LOG + log2f(l));
 }
 
-// (the kernels under a tree's masks are built by themselves: attn_tree_tiles.cu, attn_tree_rows.cu)
 cudaError_t launch_attn_tiles(const DeviceInfo& dev, const KvView& c, int dtype, const AttnArgs& a, const RowsPlan& pl,
                               cudaStream_t s);
 cudaError_t launch_attn_rows(const DeviceInfo& dev, const KvView& c, int dtype, const AttnArgs& a, const RowsPlan& pl,
                              cudaStream_t s);
-cudaError_t launch_attn_tree_tiles(const DeviceInfo& dev, const KvView& c, int dtype, const AttnArgs& a, const RowsPlan& pl,
-                                   cudaStream_t s);
-cudaError_t launch_attn_tree_rows(const DeviceInfo& dev, const KvView& c, int dtype, const AttnArgs& a, const RowsPlan& pl,
-                                  cudaStream_t s);
 
 }  // namespace cq

@@ -1,13 +1,13 @@
 // Norm and rotation of queries and keys (cq_qk_rope in include/cq_tree.h).
 //
-// A head of D values lies with D / 4 lanes, four values each; its sum of squares
-// is a few shuffles, and the partner of a value is in the same lane (adjacent
-// pairs) or rot / 8 lanes away. The angles are the same for all heads of a token:
-// a CTA takes a few tokens, works out their sines and cosines once and goes over
-// the heads. An angle is held as a 64-bit fraction of a turn: the frequency's
-// fraction times the position, modulo 2^64, is exact, where fp32 would lose it
-// (a position of 10^5 at one radian is known to 2^-8 of a radian) and fp64 runs at
-// a sixty-fourth of fp32's rate.
+// D / 8 lanes hold a head, each two groups of four neighbouring values that are turned into one
+// another (halves), or within themselves (adjacent pairs): a rotation moves nothing between
+// lanes, and a head's sum of squares is three or four shuffles for two or four heads. The angles are
+// the same for all heads of a token: a CTA goes through the tokens a few at a time and works out the
+// next ones' sines and cosines while these ones' rows are on their way. An angle is held as a 64-bit
+// fraction of a turn: the frequency's fraction times the position, modulo 2^64, is exact, where fp32
+// would lose it (a position of 10^5 at one radian is known to 2^-8 of a radian) and fp64 runs at
+// a sixty-fourth of fp32's rate; a thread keeps one frequency's fraction for all its tokens.
 #include <algorithm>
 
 #include "tree.cuh"
@@ -17,123 +17,129 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
-constexpr int MOST_TOKENS = 16;             // of a CTA
-constexpr int BATCH = 4;                    // heads of a warp's lanes in flight
+constexpr int MOST_TOKENS = 4;              // of a round
+constexpr int BATCH = 4;                    // heads of a lane in flight
 
 template <typename TI, typename TO, int D>
 __global__ void __launch_bounds__(THREADS) qk_rope_kernel(const RopeArgs a, const int tokens) {
     pdl_trigger();
     pdl_wait();
-    constexpr int LPH = D / 4, HPW = 32 / LPH;          // lanes of a head, heads of a warp
-    __shared__ __align__(16) float cs[MOST_TOKENS][D / 2], sn[MOST_TOKENS][D / 2];
+    constexpr int LPH = D / 8, HPW = 32 / LPH;          // lanes of a head, heads of a warp
+    // angles in the order of the lanes that use them: lane l its 4 l .. 4 l + 3
+    __shared__ __align__(16) float cs[2][MOST_TOKENS][D / 2], sn[2][MOST_TOKENS][D / 2];
+    __shared__ int where[2][MOST_TOKENS];               // the tokens' positions
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int half = a.rot / 2, H = a.heads[0] + a.heads[1];
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
-    const int nt = static_cast<int>(min(static_cast<int64_t>(tokens), a.T - t0));
+    const int l = lane % LPH, turned = a.rot / 8;       // lanes of a head that turn
+    // the lane's two groups of four: (l, l + turned) of the turned ones, then the others two by two
+    const int g0 = l < turned ? l : 2 * turned + 2 * (l - turned), g1 = l < turned ? l + turned : g0 + 1;
 
-    // item: (token, head), heads of a token in order
-    struct Item { int t, h; };
-    const int step = WARPS * HPW;
-    auto forward = [&](Item& it) {
-        it.h += step;
-        while (it.h >= H) { it.h -= H; ++it.t; }
-    };
-    Item it{0, warp * HPW + lane / LPH};
-    while (it.h >= H) { it.h -= H; ++it.t; }
-    const int d0 = (lane % LPH) * 4;
-    Raw4<TI> v[BATCH];
-    Item at[BATCH];
-    int pos[BATCH];
-    auto load = [&]() {
-#pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
-            at[b] = it;
-            pos[b] = -1;
-            v[b].zero();
-            if (it.t < nt) {
-                const int which = it.h >= a.heads[0], h = it.h - (which ? a.heads[0] : 0);
-                const int64_t t = t0 + it.t;
-                pos[b] = a.positions[t];
-                v[b].load(static_cast<const TI*>(a.x[which]) + t * a.x_stride[which] + h * D + d0);
-            }
-            forward(it);
-        }
-    };
-    load();                                              // on its way while the angles are worked out
-
-    // thread: one frequency, every (THREADS / half)-th token
-    if (half > 0 && tid < THREADS / half * half) {
-        const int i = tid % half;
+    // thread: one frequency, every per-th token of a round
+    const int mine = half > 0 && tid < THREADS / half * half ? tid % half : -1, per = half > 0 ? THREADS / half : 1;
+    uint64_t turn = 0;
+    if (mine >= 0) {
+        const int e = mine & 3, ml = mine >> 2;
+        const int i = !a.adjacent ? mine : e < 2 ? 2 * ml + e : 2 * (ml + turned) + e - 2;
         constexpr double INV = 0.15915494309189535, INV_LO = -9.839338337591243e-18;   // 1 / 2 pi in two parts
         const double f = a.freqs[i];
         double hi = f * INV;
         const double lo = fma(f, INV, -hi) + f * INV_LO;
         hi -= floor(hi);                                 // exact
-        const uint64_t turn = static_cast<uint64_t>(hi * 18446744073709551616.0) +
-                              static_cast<uint64_t>(static_cast<int64_t>(lo * 18446744073709551616.0));
-        for (int t = tid / half; t < nt; t += THREADS / half) {
+        turn = static_cast<uint64_t>(hi * 18446744073709551616.0) +
+               static_cast<uint64_t>(static_cast<int64_t>(lo * 18446744073709551616.0));
+    }
+    auto angles = [&](int64_t t0, int buf) {
+        if (tid < tokens && t0 + tid < a.T) where[buf][tid] = a.positions[t0 + tid];
+        if (mine < 0) return;
+        for (int t = tid / half; t < tokens && t0 + t < a.T; t += per) {
             const int64_t phase = static_cast<int64_t>(turn * static_cast<uint64_t>(static_cast<int64_t>(a.positions[t0 + t])));
             float s, c;
             sincospif(static_cast<float>(phase) * 1.0842021724855044e-19f, &s, &c);       // 2^-63: half turns
-            cs[t][i] = c;
-            sn[t][i] = s;
+            cs[buf][t][mine] = c;
+            sn[buf][t][mine] = s;
         }
-    }
-    __syncthreads();
+    };
 
-    // the lane's angles and its partner's lane
-    const bool turned = d0 < a.rot;
-    const int i0 = a.adjacent ? d0 / 2 : d0 < half ? d0 : d0 - half;
-    const int other = a.adjacent || !turned ? lane : d0 < half ? lane + half / 4 : lane - half / 4;
-    const float side = d0 < half ? -1.0f : 1.0f;
-    for (;;) {
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * tokens;
+    int buf = 0;
+    int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
+    if (t0 < a.T) angles(t0, 0);
+    for (; t0 < a.T; t0 += stride, buf ^= 1) {
+        __syncthreads();
+        const int nt = static_cast<int>(min(static_cast<int64_t>(tokens), a.T - t0));
+        // (token, head) of the lane, heads of a token in order
+        int t = 0, h = warp * HPW + lane / LPH;
+        while (h >= H) { h -= H; ++t; }
+        bool first = true;
+        do {
+            Raw4<TI> v[BATCH][2];
+            int at_t[BATCH], at_h[BATCH];
 #pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
-            const Item x = at[b];
-            const int which = x.h >= a.heads[0], h = x.h - (which ? a.heads[0] : 0);
-            const bool on = x.t < nt && pos[b] >= 0;
-            float4 f = v[b].value();
-            float ss = fmaf(f.x, f.x, f.y * f.y) + fmaf(f.z, f.z, f.w * f.w);
-#pragma unroll
-            for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (on && a.w[which] != nullptr) {
-                const float4 w = *reinterpret_cast<const float4*>(a.w[which] + d0);
-                const float r = __frsqrt_rn(fmaf(ss, 1.0f / D, a.eps));
-                f = make_float4(f.x * r * w.x, f.y * r * w.y, f.z * r * w.z, f.w * r * w.w);
-            }
-            float4 g;
-            g.x = __shfl_sync(0xffffffffu, f.x, other);
-            g.y = __shfl_sync(0xffffffffu, f.y, other);
-            g.z = __shfl_sync(0xffffffffu, f.z, other);
-            g.w = __shfl_sync(0xffffffffu, f.w, other);
-            if (!on) continue;
-            if (turned) {
-                if (a.adjacent) {
-                    const float2 c = *reinterpret_cast<const float2*>(&cs[x.t][i0]), s = *reinterpret_cast<const float2*>(&sn[x.t][i0]);
-                    f = make_float4(f.x * c.x - f.y * s.x, f.y * c.x + f.x * s.x, f.z * c.y - f.w * s.y, f.w * c.y + f.z * s.y);
-                } else {
-                    const float4 c = *reinterpret_cast<const float4*>(&cs[x.t][i0]), s = *reinterpret_cast<const float4*>(&sn[x.t][i0]);
-                    f = make_float4(fmaf(side * g.x, s.x, f.x * c.x), fmaf(side * g.y, s.y, f.y * c.y),
-                                    fmaf(side * g.z, s.z, f.z * c.z), fmaf(side * g.w, s.w, f.w * c.w));
+            for (int b = 0; b < BATCH; ++b) {
+                at_t[b] = t < nt && where[buf][t] >= 0 ? t : -1;
+                at_h[b] = h;
+                v[b][0].zero();
+                v[b][1].zero();
+                if (at_t[b] >= 0) {
+                    const int which = h >= a.heads[0];
+                    const TI* p = static_cast<const TI*>(a.x[which]) + (t0 + t) * a.x_stride[which] + (h - (which ? a.heads[0] : 0)) * D;
+                    v[b][0].load(p + 4 * g0);
+                    v[b][1].load(p + 4 * g1);
                 }
+                h += WARPS * HPW;
+                while (h >= H) { h -= H; ++t; }
             }
-            store4(static_cast<TO*>(a.y[which]) + (t0 + x.t) * a.y_stride[which] + h * D + d0, f);
-        }
-        // (the first item of a batch is the earliest of its lanes; a warp leaves as one)
-        if (!__any_sync(0xffffffffu, it.t < nt)) break;
-        load();
+            if (first && t0 + stride < a.T) angles(t0 + stride, buf ^ 1);
+            first = false;
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                const int which = at_h[b] >= a.heads[0];
+                float4 x = v[b][0].value(), y = v[b][1].value();
+                float ss = fmaf(x.x, x.x, x.y * x.y) + fmaf(x.z, x.z, x.w * x.w) + (fmaf(y.x, y.x, y.y * y.y) + fmaf(y.z, y.z, y.w * y.w));
+#pragma unroll
+                for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                if (at_t[b] < 0) continue;
+                if (a.w[which] != nullptr) {
+                    const float4 w = *reinterpret_cast<const float4*>(a.w[which] + 4 * g0), z = *reinterpret_cast<const float4*>(a.w[which] + 4 * g1);
+                    const float r = rsqrtf(fmaf(ss, 1.0f / D, a.eps));
+                    x = make_float4(x.x * r * w.x, x.y * r * w.y, x.z * r * w.z, x.w * r * w.w);
+                    y = make_float4(y.x * r * z.x, y.y * r * z.y, y.z * r * z.z, y.w * r * z.w);
+                }
+                if (l < turned) {
+                    const float4 c = *reinterpret_cast<const float4*>(&cs[buf][at_t[b]][4 * l]), s = *reinterpret_cast<const float4*>(&sn[buf][at_t[b]][4 * l]);
+                    const float4 p = x, q = y;
+                    if (a.adjacent) {
+                        x = make_float4(p.x * c.x - p.y * s.x, p.y * c.x + p.x * s.x, p.z * c.y - p.w * s.y, p.w * c.y + p.z * s.y);
+                        y = make_float4(q.x * c.z - q.y * s.z, q.y * c.z + q.x * s.z, q.z * c.w - q.w * s.w, q.w * c.w + q.z * s.w);
+                    } else {
+                        x = make_float4(p.x * c.x - q.x * s.x, p.y * c.y - q.y * s.y, p.z * c.z - q.z * s.z, p.w * c.w - q.w * s.w);
+                        y = make_float4(q.x * c.x + p.x * s.x, q.y * c.y + p.y * s.y, q.z * c.z + p.z * s.z, q.w * c.w + p.w * s.w);
+                    }
+                }
+                TO* p = static_cast<TO*>(a.y[which]) + (t0 + at_t[b]) * a.y_stride[which] + (at_h[b] - (which ? a.heads[0] : 0)) * D;
+                store4(p + 4 * g0, x);
+                store4(p + 4 * g1, y);
+            }
+        } while (__any_sync(0xffffffffu, t < nt));       // (a warp stays together: it shuffles)
     }
+}
+
+template <typename TI, typename TO, int D>
+cudaError_t launch_d(const DeviceInfo& dev, const RopeArgs& a, cudaStream_t s) {
+    // Tokens of a round: one where there are SMs for all of them, else four, so that a warp has several heads' loads
+    // in flight between barriers. As many CTAs as run at once: each goes on to further tokens.
+    int tokens = 1, ctas = 0;
+    while (tokens < MOST_TOKENS && a.T / (2 * tokens) >= 4 * dev.sm_count) tokens *= 2;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, qk_rope_kernel<TI, TO, D>, THREADS, 0);
+    if (e != cudaSuccess) return e;
+    const int64_t rounds = (a.T + tokens - 1) / tokens;
+    return launch_kernel(qk_rope_kernel<TI, TO, D>, dim3(static_cast<unsigned>(std::min<int64_t>(rounds, static_cast<int64_t>(dev.sm_count) * std::max(ctas, 1)))),
+                         dim3(THREADS), 0, s, a, tokens);
 }
 
 template <typename TI, typename TO>
 cudaError_t launch_t(const DeviceInfo& dev, int64_t D, const RopeArgs& a, cudaStream_t s) {
-    // Tokens of a CTA: enough heads for its warps' loads in flight, as long as there are CTAs for every SM.
-    const int H = a.heads[0] + a.heads[1];
-    int tokens = 1;
-    while (tokens < MOST_TOKENS && (tokens * H < 8 * WARPS || tokens < 4) && a.T / (2 * tokens) >= 2 * dev.sm_count) tokens *= 2;
-    const dim3 grid(static_cast<unsigned>((a.T + tokens - 1) / tokens));
-    return D == 64 ? launch_kernel(qk_rope_kernel<TI, TO, 64>, grid, dim3(THREADS), 0, s, a, tokens)
-                   : launch_kernel(qk_rope_kernel<TI, TO, 128>, grid, dim3(THREADS), 0, s, a, tokens);
+    return D == 64 ? launch_d<TI, TO, 64>(dev, a, s) : launch_d<TI, TO, 128>(dev, a, s);
 }
 
 }  // namespace

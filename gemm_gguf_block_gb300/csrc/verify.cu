@@ -19,6 +19,7 @@
 // memory (the request's tokens by CTA 0, maxima, sums and the children's logits by their owners),
 // so that the CTAs meet at the same barriers whatever else writes to the inputs meanwhile.
 #include <algorithm>
+#include <climits>
 
 #include "tree.cuh"
 
@@ -29,6 +30,7 @@ constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int MAX_CLUSTER = 8;
 constexpr int MAX = CQ_TREE_MAX;
+constexpr int BATCH = 16;                          // loads of a thread in flight
 constexpr int ONE_BITS = 46;                       // w of the largest logit is 2^46
 constexpr float CUT = -47.0f;                      // below 2^CUT of the largest: 0 (less than half a unit)
 
@@ -90,13 +92,16 @@ __device__ __forceinline__ uint64_t unit64(float u) {
 // A probability: 1 is 2^64 - 1.
 __device__ __forceinline__ uint64_t prob64(float q) { return q > 0.0f ? __float2ull_rz(fminf(q, 1.0f) * 18446744073709551616.0f) : 0; }
 
-// The order of floats as unsigned integers; NaN and +infinity on top.
-__device__ __forceinline__ uint32_t order_of(float z) {
-    const uint32_t b = __float_as_uint(__fadd_rn(z, 0.0f));      // -0 is 0
-    if (!(z < INFINITY)) return 0xffffffffu;
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
+__device__ __forceinline__ float max_nan(float a, float b) {      // NaN if either is
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
 }
-__device__ __forceinline__ float value_of(uint32_t o) { return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o); }
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // w of logit z beside the row's largest, m (finite); c = log2(e) / temperature. The exponent
 // x = (z - m) c is held to 2^-40: the difference and its rounding error, times c in two parts. Then
@@ -137,15 +142,18 @@ __device__ __forceinline__ uint64_t without(uint64_t w, uint64_t q, uint64_t a_l
 
 struct Shared {
     unsigned long long table[256];
-    unsigned long long xchg[2][MAX_CLUSTER];       // maxima, then sums, alternately
+    unsigned long long xchg[2][MAX_CLUSTER];       // what the CTAs spread, alternately
+    unsigned long long tot[MAX_CLUSTER];           // the CTAs' sums of r
     unsigned long long part[WARPS];                // the warps' sums of r, over their own stretch of the slice
     unsigned long long child[MAX];                 // logit and draft probability of the node's children
+    unsigned long long weight[MAX];                // their w
+    float top[WARPS];
     Request rq;
-    int gone[MAX];                                 // tokens rejected at this node (no draft probabilities)
+    int gone[MAX], gone_at[MAX];                   // tokens rejected at this node, and whose (no draft probabilities)
 };
 
 template <bool DRAFT>
-__global__ void __launch_bounds__(THREADS) tree_verify_kernel(const VerifyArgs a, const int cluster, const int slice, const int stretch) {
+__global__ void __launch_bounds__(THREADS, 2) tree_verify_kernel(const VerifyArgs a, const int cluster, const int slice, const int stretch) {
     pdl_trigger();
     extern __shared__ __align__(16) float row[];   // [slice] of the node's logits
     __shared__ Shared sh;
@@ -172,7 +180,7 @@ __global__ void __launch_bounds__(THREADS) tree_verify_kernel(const VerifyArgs a
             sh.rq.u_sample = unit64(a.u_sample[r]);
             if (n > MAX) atomicOr(a.status, CQ_DEV_TREE);
         }
-        if (tid < min(n, MAX)) {
+        if (n <= MAX && tid < n) {
             int p = a.parent[first + tid];
             if (p < -1 || p >= tid) {
                 atomicOr(a.status, CQ_DEV_TREE);
@@ -196,7 +204,8 @@ __global__ void __launch_bounds__(THREADS) tree_verify_kernel(const VerifyArgs a
     int32_t* path = a.path + static_cast<int64_t>(r) * a.max_path;
     int kept = 0, next = -1;
 
-    // Spreads a CTA's number and gives all of them, each CTA's in its place.
+    // Spreads a CTA's number and gives all of them, each CTA's in its place. (A buffer is written again two
+    // turns on: by then every CTA has passed the barrier between, and read it.)
     int turn = 0;
     auto spread = [&](uint64_t mine) {
         if (tid < cluster) st_cluster(mapa(smem_u32(&sh.xchg[turn][rank]), tid), mine);
@@ -212,8 +221,18 @@ __global__ void __launch_bounds__(THREADS) tree_verify_kernel(const VerifyArgs a
         if (lane == 0) sh.part[warp] = s;
         __syncthreads();
         uint64_t all = 0;
-#pragma unroll
         for (int w = 0; w < WARPS; ++w) all += sh.part[w];
+        return all;
+    };
+    // The CTAs' sums of r spread and held in sh.tot; the sum of all.
+    auto totals = [&](uint64_t mine) {
+        const unsigned long long* got = spread(mine);
+        uint64_t all = 0;
+        for (int c = 0; c < cluster; ++c) all += got[c];
+        if (all != 0) {
+            if (tid < cluster) sh.tot[tid] = got[tid];
+            __syncthreads();
+        }
         return all;
     };
 
@@ -222,41 +241,33 @@ __global__ void __launch_bounds__(THREADS) tree_verify_kernel(const VerifyArgs a
         kept = 1;
         if (lead) path[0] = 0;
         const float c_hi = sh.rq.c_hi, c_lo = sh.rq.c_lo;
+        const bool greedy = sh.rq.greedy != 0;
         for (;;) {
-            // ---- the node's row: into shared memory, its largest logit and that one's smallest index
+            // ---- the node's row: into shared memory, its largest logit (NaN if any is)
             const float* z = a.logits + static_cast<int64_t>(first + node) * a.logits_stride + lo;
             __syncthreads();                       // nobody looks at the last row any more
-            uint64_t key = 0;
-            for (int i0 = w0; i0 < w1; i0 += 32 * 8) {
-                float v[8];
+            float m = -INFINITY;
+            for (int i0 = w0 + lane; i0 < w1; i0 += 32 * BATCH) {
+                float v[BATCH];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int i = i0 + 32 * k + lane;
-                    v[k] = i < w1 ? z[i] : -INFINITY;
-                }
+                for (int k = 0; k < BATCH; ++k) v[k] = i0 + 32 * k < w1 ? z[i0 + 32 * k] : -INFINITY;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int i = i0 + 32 * k + lane;
-                    if (i < w1) row[i] = v[k];
-                    const uint64_t o = static_cast<uint64_t>(order_of(v[k])) << 32 | static_cast<uint32_t>(~(lo + i));
-                    if (i < w1) key = max(key, o);
+                for (int k = 0; k < BATCH; ++k) {
+                    if (i0 + 32 * k < w1) row[i0 + 32 * k] = v[k];
+                    m = max_nan(m, v[k]);
                 }
             }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
-            if (lane == 0) sh.part[warp] = key;
+            for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (lane == 0) sh.top[warp] = m;
             __syncthreads();
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) key = max(key, static_cast<uint64_t>(sh.part[w]));
-            const unsigned long long* got = spread(key);
-            for (int c = 0; c < cluster; ++c) key = max(key, static_cast<uint64_t>(got[c]));
-            const uint32_t top = static_cast<uint32_t>(key >> 32);
-            const float m = value_of(top);
-            if (top == 0xffffffffu || m == -INFINITY) {
+            for (int w = 0; w < WARPS; ++w) m = max_nan(m, sh.top[w]);
+            const unsigned long long* got = spread(__float_as_uint(m));
+            for (int c = 0; c < cluster; ++c) m = max_nan(m, __uint_as_float(static_cast<uint32_t>(got[c])));
+            if (!(fabsf(m) < INFINITY)) {
                 if (lead) atomicOr(a.status, CQ_DEV_LOGITS);
                 break;
             }
-            const int best = static_cast<int>(~static_cast<uint32_t>(key));
             // ---- its children, one bit each
             uint64_t children = 0;
             if (kept < a.max_path) {
@@ -265,64 +276,89 @@ __global__ void __launch_bounds__(THREADS) tree_verify_kernel(const VerifyArgs a
                 children = static_cast<uint64_t>(c1) << 32 | c0;
             }
             int taken = -1;
-            if (sh.rq.greedy) {
+            if (greedy) {
+                // the largest logit's smallest index
+                int at = INT_MAX;
+                for (int i = w0 + lane; i < w1; i += 32)
+                    if (row[i] == m) { at = lo + i; break; }
+                at = __reduce_min_sync(0xffffffffu, at);
+                if (lane == 0) sh.part[warp] = at;
+                __syncthreads();
+                for (int w = 0; w < WARPS; ++w) at = min(at, static_cast<int>(sh.part[w]));
+                got = spread(at);
+                for (int c = 0; c < cluster; ++c) at = min(at, static_cast<int>(got[c]));
                 for (uint64_t left = children; left != 0 && taken < 0; left &= left - 1) {
                     const int j = __ffsll(static_cast<long long>(left)) - 1;
-                    if (sh.rq.token[j] == best) taken = j;
+                    if (sh.rq.token[j] == at) taken = j;
                 }
-                if (taken < 0) next = best;
+                if (taken < 0) next = at;
             } else {
-                uint64_t s = 0;
-                for (int i = w0 + lane; i < w1; i += 32) s += weight(row[i], m, c_hi, c_lo, sh.table);
-                s = sum_of(s);
-                // the children's logits and draft probabilities, from the CTA that has them
-                if (tid < MAX && (children >> tid & 1) != 0) {
-                    const int x = sh.rq.token[tid];
-                    if (x >= lo && x < lo + len) {
-                        const float q = DRAFT ? a.draft[static_cast<int64_t>(first + node) * a.draft_stride + x] : 0.0f;
-                        const uint64_t v = static_cast<uint64_t>(__float_as_uint(q)) << 32 | __float_as_uint(row[x - lo]);
-                        for (int c = 0; c < cluster; ++c) st_cluster(mapa(smem_u32(&sh.child[tid]), c), v);
+                const float* dr = DRAFT ? a.draft + static_cast<int64_t>(first + node) * a.draft_stride + lo : nullptr;
+                // The sum of w: exactly, with the warps' and the CTAs' parts; the path's rows in front of the last need it only
+                // to tell on which side of it a random number falls.
+                auto exact = [&]() {
+                    uint64_t s = 0;
+                    for (int i = w0 + lane; i < w1; i += 32) s += weight(row[i], m, c_hi, c_lo, sh.table);
+                    return totals(sum_of(s));
+                };
+                uint64_t R = 0, below = 0, above = 0;       // the sum of r (0: not known yet) and bounds on it
+                if (children != 0) {
+                    float s = 0.0f;
+                    for (int i = w0 + lane; i < w1; i += 32) s += exp2_fast((row[i] - m) * c_hi);
+                    s = fminf(s, 1e6f);
+                    const uint64_t mine = sum_of(static_cast<uint64_t>(__float2ull_rn(s * 70368744177664.0f)));
+                    // the children's logits and draft probabilities, from the CTA that has them
+                    if (tid < MAX && (children >> tid & 1) != 0) {
+                        const int x = sh.rq.token[tid];
+                        if (x >= lo && x < lo + len) {
+                            const uint64_t v = static_cast<uint64_t>(__float_as_uint(DRAFT ? dr[x - lo] : 0.0f)) << 32 | __float_as_uint(row[x - lo]);
+                            for (int c = 0; c < cluster; ++c) st_cluster(mapa(smem_u32(&sh.child[tid]), c), v);
+                        }
                     }
+                    got = spread(mine);
+                    for (int c = 0; c < cluster; ++c) above += got[c];
+                    below = above - (above >> 15);
+                    above += above >> 15;
+                    if (tid < MAX && (children >> tid & 1) != 0)
+                        sh.weight[tid] = weight(__uint_as_float(static_cast<uint32_t>(sh.child[tid])), m, c_hi, c_lo, sh.table);
+                    __syncthreads();
                 }
-                got = spread(s);
-                uint64_t tot[MAX_CLUSTER], R = 0, a_lo = 0;
+                uint64_t a_lo = 0;
                 uint32_t a_hi = 0;
                 int gone = 0;
-#pragma unroll
-                for (int c = 0; c < MAX_CLUSTER; ++c) {
-                    tot[c] = c < cluster ? got[c] : 0;
-                    R += tot[c];
-                }
                 for (uint64_t left = children; left != 0 && taken < 0; left &= left - 1) {
                     const int j = __ffsll(static_cast<long long>(left)) - 1, x = sh.rq.token[j];
                     if (x < 0 || x >= a.V) continue;
-                    const uint64_t v = sh.child[j];
-                    uint64_t w = weight(__uint_as_float(static_cast<uint32_t>(v)), m, c_hi, c_lo, sh.table);
+                    const uint64_t u = sh.rq.u[j];
+                    uint64_t w = sh.weight[j];
                     if constexpr (DRAFT) {
-                        const uint64_t q = prob64(__uint_as_float(static_cast<uint32_t>(v >> 32)));
+                        const uint64_t q = prob64(__uint_as_float(static_cast<uint32_t>(sh.child[j] >> 32)));
+                        if (R == 0) {
+                            if (__umul64hi(u, __umul64hi(q, above)) < w) {
+                                taken = j;
+                                break;
+                            }
+                            R = exact();
+                        }
                         w = without(w, q, a_lo, a_hi);
-                        if (__umul64hi(sh.rq.u[j], __umul64hi(q, R)) < w) {
+                        if (__umul64hi(u, __umul64hi(q, R)) < w) {
                             taken = j;
                             break;
                         }
                         // one pass for the next distribution's sums
                         const uint64_t n_lo = a_lo + R;
                         const uint32_t n_hi = a_hi + (n_lo < a_lo);
-                        const float* dr = a.draft + static_cast<int64_t>(first + node) * a.draft_stride + lo;
                         uint64_t rs = 0;
-                        for (int i = w0 + lane; i < w1; i += 32)
-                            rs += without(weight(row[i], m, c_hi, c_lo, sh.table), prob64(dr[i]), n_lo, n_hi);
-                        const uint64_t before = lane < WARPS ? sh.part[lane] : 0;       // kept where nothing is left
-                        rs = sum_of(rs);
-                        got = spread(rs);
-                        uint64_t sum = 0;
-                        for (int c = 0; c < cluster; ++c) sum += got[c];
+                        for (int i = w0 + lane; i < w1; i += 32) {
+                            const float q1 = dr[i];
+                            rs += without(weight(row[i], m, c_hi, c_lo, sh.table), prob64(q1), n_lo, n_hi);
+                        }
+                        const uint64_t before = tid < WARPS ? sh.part[tid] : 0;         // kept where nothing is left
+                        const uint64_t sum = totals(sum_of(rs));
                         if (sum != 0) {
                             R = sum;
                             a_lo = n_lo;
                             a_hi = n_hi;
-#pragma unroll
-                            for (int c = 0; c < MAX_CLUSTER; ++c) tot[c] = c < cluster ? got[c] : 0;
                         } else {
                             __syncthreads();
                             if (tid < WARPS) sh.part[tid] = before;
@@ -331,20 +367,28 @@ __global__ void __launch_bounds__(THREADS) tree_verify_kernel(const VerifyArgs a
                     } else {
                         for (int k = 0; k < gone; ++k)
                             if (sh.gone[k] == x) w = 0;
-                        if (__umul64hi(sh.rq.u[j], R) < w) {
+                        if (__umul64hi(u, above) < w) {
                             taken = j;
                             break;
                         }
-                        if (w != 0 && w != R) {
-                            R -= w;
-                            const int owner = x / slice;
-#pragma unroll
-                            for (int c = 0; c < MAX_CLUSTER; ++c)
-                                if (c == owner) tot[c] -= w;
+                        if (R == 0 && __umul64hi(u, below) < w) {                      // between the bounds: exactly, then
+                            R = exact();
+                            for (int k = 0; k < gone; ++k) R -= sh.weight[sh.gone_at[k]];
+                            above = below = R;
+                            if (__umul64hi(u, R) < w) {
+                                taken = j;
+                                break;
+                            }
+                        }
+                        // (its weight may be all that is left only where the bounds are exact: else something of r is beside it)
+                        if (w != 0 && w != above) {
+                            above -= w;
+                            below = below > w ? below - w : 0;
+                            if (R != 0) R -= w;
                             __syncthreads();
                             if (tid == 0) {
                                 sh.gone[gone] = x;
-                                if (owner == static_cast<int>(rank)) sh.part[(x - lo) / stretch] -= w;
+                                sh.gone_at[gone] = j;
                             }
                             ++gone;
                             __syncthreads();
@@ -353,26 +397,36 @@ __global__ void __launch_bounds__(THREADS) tree_verify_kernel(const VerifyArgs a
                 }
                 if (taken < 0) {
                     // ---- the next token: the CTA, the warp's stretch and the place in it where the sums pass u R
-                    uint64_t t = __umul64hi(sh.rq.u_sample, R);
-                    int owner = -1;
-#pragma unroll
-                    for (int c = 0; c < MAX_CLUSTER; ++c)
-                        if (owner < 0) {
-                            if (t < tot[c]) owner = c; else t -= tot[c];
-                        }
-                    if (owner == static_cast<int>(rank)) {
+                    if (R == 0) {
+                        R = exact();
+                        for (int k = 0; k < gone; ++k) R -= sh.weight[sh.gone_at[k]];
+                    }
+                    if (!DRAFT && gone > 0) {
                         __syncthreads();
+                        if (tid == 0)
+                            for (int k = 0; k < gone; ++k) {
+                                const int x = sh.gone[k], owner = x / slice;
+                                sh.tot[owner] -= sh.weight[sh.gone_at[k]];
+                                if (owner == static_cast<int>(rank)) sh.part[(x - lo) / stretch] -= sh.weight[sh.gone_at[k]];
+                            }
+                        __syncthreads();
+                    }
+                    uint64_t t = __umul64hi(sh.rq.u_sample, R);
+                    int owner = 0;
+                    while (owner < cluster - 1 && t >= sh.tot[owner]) t -= sh.tot[owner++];
+                    if (owner == static_cast<int>(rank)) {
                         int w = 0;
                         while (w < WARPS - 1 && t >= sh.part[w]) t -= sh.part[w++];
                         const int s0 = min(w * stretch, len), s1 = min(s0 + stretch, len);
                         const int per = (stretch + THREADS - 1) / THREADS, i0 = s0 + tid * per, i1 = min(i0 + per, s1);
-                        const float* dr = DRAFT ? a.draft + static_cast<int64_t>(first + node) * a.draft_stride + lo : nullptr;
                         auto value = [&](int i) {
                             uint64_t v = weight(row[i], m, c_hi, c_lo, sh.table);
-                            if constexpr (DRAFT) v = without(v, prob64(a_lo | a_hi ? dr[i] : 0.0f), a_lo, a_hi);
-                            else
+                            if constexpr (DRAFT) {
+                                if ((a_lo | a_hi) != 0) v = without(v, prob64(dr[i]), a_lo, a_hi);
+                            } else {
                                 for (int k = 0; k < gone; ++k)
                                     if (sh.gone[k] == lo + i) v = 0;
+                            }
                             return v;
                         };
                         uint64_t mine = 0;
