@@ -15,6 +15,15 @@ namespace {
 // bf16 at 128: 77 / 128 / 182 against 139.
 constexpr int TILE_ROWS = 40;
 
+// Trees: a call's requests go to one kernel, all of them, by the widest's rows -- a tree costs the tiles the same
+// whatever its width, and tiles beside rows slow both (64 contexts of 200-8190, bf16, 12-36 rows: 276 us with the border
+// at 33 rows, 118 all in the tiles, 162 all in the rows kernel; fp32, 12-56 rows: 429 with the border at 40, 200, 266).
+// Few (request, kv head) pairs leave the rows kernel enough SMs for longer. 32 query and 8 kv heads of 128, 1500 keys,
+// rows kernel and tiles: 64 requests of 16 rows 78 and 105 us, of 24 rows 129 and 104 (fp32 107 and 167, 182 and 167);
+// 16 requests of 16 rows 35 and 30, of 32 rows 49 and 30 (fp32 40 and 46, 63 and 47); one request of 1000 keys, 32
+// rows 19 and 26, 128 rows 21 and 27; 2 requests of 20000 keys at 64, 32 rows 43 and 42, 48 rows 54 and 42.
+constexpr int TREE_ROWS = 16, TREE_ROWS_FEW = 32, TREE_FEW = 32;
+
 // The workspace: the rows kernel's counters (the part that has to be zero) and parts, then the
 // tiles kernel's. All but the counters is written by a call before it is read.
 static_assert(ATTN_MAX_CTAS * sizeof(int) <= CQ_ATTN_WORKSPACE_ZERO, "the counters");
@@ -47,8 +56,10 @@ cudaError_t launch_attn(const DeviceInfo& dev, const KvView& c, int dtype, const
     const int64_t G = a.heads / c.heads;
     // Which kernel a request goes to is decided on the GPU by its own length: the host
     // only says whether there may be any for the tiles.
-    const bool tiles = a.max_new * G >= TILE_ROWS;
-    pl.tile_rows = tiles ? TILE_ROWS : INT_MAX;
+    const bool trees = a.tree != nullptr && a.max_new <= CQ_TREE_MAX;
+    const bool few = static_cast<int64_t>(a.R) * c.heads < TREE_FEW;
+    const bool tiles = trees ? a.max_new * G > (few ? TREE_ROWS_FEW : TREE_ROWS) : a.max_new * G >= TILE_ROWS;
+    pl.tile_rows = !tiles ? INT_MAX : trees ? 1 : TILE_ROWS;
     pl.after_tiles = tiles;
     if (tiles) {
         const cudaError_t e = launch_attn_tiles(dev, c, dtype, a, pl, s);

@@ -39,13 +39,6 @@
 namespace cq {
 namespace {
 
-constexpr int KEYS = 128;                 // keys of a step
-constexpr int SOFT = 256;                 // softmax threads
-constexpr int CONV = 128;                 // converter threads
-constexpr int THREADS = SOFT + CONV + 128;   // the last four warps: one issues the MMAs
-// Registers a thread of each role. 512 threads are launched with 128 each, and the
-// roles' sum is that: 256 * 176 + 128 * 104 + 128 * 56 = 512 * 128.
-constexpr int REGS_SOFT = 176, REGS_CONV = 104, REGS_MMA = 56;
 constexpr float OFF = TILES_OFF, RAISE = 8.0f;
 constexpr int MIN_STEPS = 3;              // a part of an item has at least so many, where it has parts
 constexpr int INFO = 4;                   // steps whose scales are kept
@@ -66,9 +59,21 @@ struct RowMap {
     }
 };
 
-template <typename T, int D> struct Tiles {
+template <typename T, int D, bool NARROW> struct Tiles {
     static constexpr bool F32 = std::is_same<T, float>::value;
-    static constexpr int MT = F32 ? 1 : 2;                 // row tiles
+    static_assert(!(F32 && NARROW), "fp32 has one row tile always");
+    // Two row tiles a CTA and four converter warps; NARROW: one tile, a row's keys halved between two threads as in fp32,
+    // and eight converter warps.
+    static constexpr int KEYS = 128;                       // keys of a step
+    static constexpr int SOFT = 256;                       // softmax threads
+    static constexpr int CONV = NARROW ? 256 : 128;        // converter threads
+    static constexpr int THREADS = SOFT + CONV + 128;      // the last four warps: one issues the MMAs
+    // Registers a thread of each role; the roles' sum is what the launch gives. 512 threads have 128
+    // each: 256 * 176 + 128 * 104 + 128 * 56 = 512 * 128. 640 have 96: 256 * 128 + 256 * 80 + 128 * 64 = 640 * 96.
+    static constexpr int REGS_SOFT = NARROW ? 128 : 176, REGS_CONV = NARROW ? 80 : 104, REGS_MMA = NARROW ? 64 : 56;
+    static constexpr int KW = KEYS / (CONV / 32);          // keys of a converter warp
+    static constexpr int NBK = KW / 16;                    // their blocks of 16
+    static constexpr int MT = F32 || NARROW ? 1 : 2;       // row tiles
     static constexpr int ROWS = 128 * MT;
     static constexpr int SPLIT = SOFT / (128 * MT);        // softmax threads of a row
     static constexpr int KT = KEYS / SPLIT;                // their keys
@@ -88,22 +93,24 @@ template <typename T, int D> struct Tiles {
     // results: of P's first part and of the other two. (The MMAs' sums are cut off, not rounded:
     // the small parts' 16 additions a step would cost a sum of full size as much as the first
     // part's 8.)
-    static constexpr int SBUF = F32 && D == 64 ? 2 : 1;
+    // NARROW: two steps' scores, P in columns of its own. (Two steps' P as well gain nothing.)
+    static constexpr int SBUF = (F32 && D == 64) || NARROW ? 2 : 1;
     static constexpr uint32_t S0 = 0, S1 = 128;
     static constexpr uint32_t SP = 128 * SBUF;             // P, 64 columns a tile; fp32: P's third part
-    static constexpr uint32_t O0 = F32 ? SP + 64 : SP + 128;
-    static constexpr uint32_t O1 = O0 + (F32 ? D : 128);   // fp32: the smaller result; else the second tile's
+    static constexpr uint32_t O0 = SP + 64 * MT;
+    static constexpr uint32_t O1 = O0 + (F32 ? D : NARROW ? 0 : 128);   // fp32: the smaller result; two tiles: the second's
     static_assert(O1 + D <= 512, "tensor memory");
 };
 
-template <typename T, int D, bool TREE>
-__global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, const AttnArgs a, const RowsPlan pl) {
+template <typename T, int D, bool TREE, bool NARROW>
+__global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_kernel(const KvView c, const AttnArgs a, const RowsPlan pl) {
     // The rows kernel that follows begins when every CTA of this one has passed here, and
     // does not wait for the end of it: what both read is complete by then.
     pdl_wait();
     pdl_trigger();
-    using W = Tiles<T, D>;
+    using W = Tiles<T, D, NARROW>;
     constexpr bool F32 = W::F32;
+    constexpr int KEYS = W::KEYS, SOFT = W::SOFT, CONV = W::CONV, THREADS = W::THREADS;
     constexpr int MT = W::MT, ROWS = W::ROWS, SPLIT = W::SPLIT, KT = W::KT, OC = W::OC, SBUF = W::SBUF;
     extern __shared__ uint8_t tiles_smem[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tiles_smem) + 1023) & ~uintptr_t(1023));
@@ -134,12 +141,34 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         key0_ = key0_ / KEYS * KEYS;
         return stop_ > key0_ ? (stop_ - 1 - key0_) / KEYS + 1 : 0;       // (stop may be near 2^31)
     };
+    // Trees: long requests first, where they are few enough to be put in order: the items that begin last are short.
+    // (64 contexts of 200-8190, trees of 3-9 tokens: 123 us, in the requests' order 158)
+    constexpr int SORTED = 128;
+    __shared__ int sort_len[TREE ? SORTED : 1], sort_order[TREE ? SORTED : 1];
+    const bool sorted = TREE && a.R > 1 && a.R <= SORTED;
+    if constexpr (TREE) {
+        if (sorted) {
+            int f_, n_, kv_ = 0;
+            if (tid < a.R) {
+                request_of(c, a, tid, f_, n_, kv_);
+                sort_len[tid] = kv_;
+            }
+            __syncthreads();
+            if (tid < a.R) {
+                int rank = 0;
+                for (int i = 0; i < a.R; ++i) rank += sort_len[i] > kv_ || (sort_len[i] == kv_ && i < tid);
+                sort_order[rank] = tid;
+            }
+            __syncthreads();
+        }
+    }
     // The sum of count(n, kv) over the requests; where the CTA's index falls into a request's
     // count, notes the request and the index in it.
     auto over_requests = [&](auto&& count) {
         int64_t carry = 0;
         for (int r0 = 0; r0 < a.R; r0 += THREADS) {
-            const int r_ = r0 + tid;
+            int r_ = r0 + tid;
+            if (TREE && sorted && r_ < a.R) r_ = sort_order[r_];
             int f_ = 0, n_ = 0, kv_ = 0;
             int64_t x = 0;
             if (r_ < a.R) {
@@ -195,7 +224,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         const int64_t units_all = over_requests(units_of);
         const int64_t share = pl.sms * 6 * steps_all / (6 * steps_all + units_all);
         const int64_t room = max(share - items, int64_t(1));
-        const int per = max(MIN_STEPS, static_cast<int>(min((steps_all + room - 1) / room, static_cast<int64_t>(INT_MAX / 2))));
+        int per = max(MIN_STEPS, static_cast<int>(min((steps_all + room - 1) / room, static_cast<int64_t>(INT_MAX / 2))));
+        if constexpr (TREE) {
+            // That leaves SMs idle where a few parts a little shorter would fit: the shortest of some lengths that does.
+            // (4 contexts of 30k-60k: 32 items, 128 parts of 93 steps by the rule above)
+            for (int k = 0, fine = max(MIN_STEPS, static_cast<int>((steps_all + share - 1) / max(share, int64_t(1)))); k < 8 && fine < per; ++k, fine += fine / 16 + 1)
+                if (over_requests([&](int n_, int kv_) { return steps_of(n_, kv_, fine); }) <= share) per = fine;
+        }
         if (tid == 0) item[0] = -1;
         __syncthreads();
         over_requests([&](int n_, int kv_) { return steps_of(n_, kv_, per); });
@@ -255,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
 
     if (warp < SOFT / 32) {
         // ------------------------------------------------------------ softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(W::REGS_SOFT));
         const int mt = (warp >> 2) / SPLIT, part = (warp >> 2) % SPLIT;      // row tile, part of the keys
         const int lrow = (warp & 3) * 32 + lane;            // row of the tile, lane of tensor memory
         const int row = 128 * mt + lrow;                    // of the item
@@ -328,7 +363,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         if (row < rows) token_range<TREE>(a, n, kv, my_tok, from, stop);
         if (TREE && row < rows) mask = tree_mask(a, first, n, my_tok);
         const uint32_t s_col0 = tmem + lanes + W::S0 + KT * part;
-        const uint32_t p_col = tmem + lanes + W::SP + 64 * mt;                         // 16-bit types
+        const uint32_t p_col = tmem + lanes + W::SP + 64 * mt + KT / 2 * part;         // 16-bit types
         const uint32_t p3_col = tmem + lanes + W::SP + KT / 2 * part;
         const uint32_t o_col = tmem + lanes + (mt == 0 ? W::O0 : W::O1) + OC * part;
         constexpr int CHUNKS = KT / 32;
@@ -594,7 +629,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         }
     } else if (warp < (SOFT + CONV) / 32) {
         // ---------------------------------------------------------- converters
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_CONV));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::REGS_CONV));
         // A load takes 16 dimensions a lane of 8 keys. Eight lanes (a phase of a 16-byte
         // access) hold four pieces of an even key and four of the odd one after it; at D = 128
         // the other half of the row: the bytes then come from different banks of the lines,
@@ -604,26 +639,27 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         const int odd = (lane >> 2) & 1, ck = 2 * (lane >> 3) + odd;
         auto piece = [&](int i) { return (lane & 3) + (D == 128 ? 4 * (odd ^ i) : 0); };
         constexpr int NL = D / 64;                          // loads a lane and 8 keys
-        constexpr int GROUPS = KEYS / 8 / 4;                // groups of 8 keys of a warp: 4, keys 32 cw ..
+        constexpr int KW = W::KW, NBK = W::NBK;
+        constexpr int GROUPS = KW / 8;                      // groups of 8 keys of a warp: keys KW cw ..
         const int32_t* table = a.table + static_cast<int64_t>(r) * a.max_blocks;
         const int64_t head_off = static_cast<int64_t>(h) * c.page_size * D;
-        // The warp's two blocks of 16 keys of a step: lanes 0 and 1 look them up. A step's
+        // The warp's blocks of 16 keys of a step, two (one where there are eight warps): a lane each looks them up. A step's
         // table entries are fetched two steps ahead, its scales and bytes one: no lookup
         // is waited for in the loop, and a step's loads run behind the one before's stores.
-        auto block_at = [&](int j) { return key0 + j * KEYS + 32 * cw + 16 * lane; };
-        auto has_keys = [&](int j) { return lane < 2 && j < steps && block_at(j) < tstop; };
+        auto block_at = [&](int j) { return key0 + j * KEYS + KW * cw + 16 * lane; };
+        auto has_keys = [&](int j) { return lane < NBK && j < steps && block_at(j) < tstop; };
         auto entry = [&](int j) { return has_keys(j) ? table[block_at(j) >> c.page_shift] : -1; };
         auto checked = [&](int e, int j) {
             if (e >= 0 && e < c.num_pages) return e;
             if (has_keys(j)) atomicOr(a.status, CQ_DEV_KV_PAGE);
             return -1;
         };
-        int64_t at[2];
+        int64_t at[NBK];
         auto place = [&](int page, int j) {
             const int k = block_at(j);
             const int64_t mine = page >= 0 ? page * c.page_stride + head_off + static_cast<int64_t>(k & (c.page_size - 1)) * D : -1;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) at[b] = __shfl_sync(0xffffffffu, mine, b);
+            for (int b = 0; b < NBK; ++b) at[b] = __shfl_sync(0xffffffffu, mine, b);
         };
         float p_ks = 0.0f, p_vs = 0.0f;
         auto scales = [&](int page) {
@@ -644,8 +680,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         int put[NL][2];                                     // a piece's places in the operand; 8 keys on are 8 rows
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            put[i][0] = tc::tile_off_sw128(32 * cw + ck, 16 * piece(i), KEYS);
-            put[i][1] = tc::tile_off_sw128(32 * cw + ck, 16 * piece(i) + 8, KEYS);
+            put[i][0] = tc::tile_off_sw128(KW * cw + ck, 16 * piece(i), KEYS);
+            put[i][1] = tc::tile_off_sw128(KW * cw + ck, 16 * piece(i) + 8, KEYS);
         }
         auto store = [&](uint8_t* dst, const uint4 (&x)[GROUPS][NL], bool bf) {      // bf: bfloat16
 #pragma unroll
@@ -685,10 +721,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
                 value_factors<F32>(p_vs, in.y, in.z);
             }
             // the step that used this entry before is past its softmax: the scores of two steps ago were its next
-            if (lane < 2) {
-                info[j % INFO][0][2 * cw + lane] = in.x;
-                info[j % INFO][1][2 * cw + lane] = in.y;
-                info[j % INFO][2][2 * cw + lane] = in.z;
+            if (lane < NBK) {
+                info[j % INFO][0][NBK * cw + lane] = in.x;
+                info[j % INFO][1][NBK * cw + lane] = in.y;
+                info[j % INFO][2][NBK * cw + lane] = in.z;
             }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars[B_INFO + j % INFO]);
@@ -705,7 +741,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         }
     } else {
         // --------------------------------------------------------- MMA issuer
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_MMA));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::REGS_MMA));
         if (warp == (SOFT + CONV) / 32 && steps > 0) {
         const uint32_t lead = tc::elect_one();
         const uint32_t q0 = smem_u32(smem + W::OFF_Q), k0 = smem_u32(smem + W::OFF_K), v0 = smem_u32(smem + W::OFF_V);
@@ -717,28 +753,28 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
         // values are 16 rows of 128 bytes.
         const uint64_t qd = tc::smem_desc_sw128(q0, 1024), kd = tc::smem_desc_sw128(k0, 1024),
                        vd = tc::smem_desc_sw128_mn(v0, KEYS * 128, 1024);
-        auto scores = [&](int m, int st) {                  // fp32: m is the buffer
+        auto scores = [&](int m, int st) {                  // one tile: m is the buffer
             const uint32_t d = tmem + (MT == 2 || m == 0 ? W::S0 : W::S1);
             const uint64_t bd = kd + st * (W::KB >> 4);
 #pragma unroll
             for (int part = 0; part < (F32 ? 2 : 1); ++part) {
-                const uint64_t ad = qd + (F32 ? 1 - part : m) * (W::QB >> 4);      // fp32: the lower parts first, while the sums are small
+                const uint64_t ad = qd + (F32 ? 1 - part : MT == 2 ? m : 0) * (W::QB >> 4);      // fp32: the lower parts first, while the sums are small
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
-                    tc::mma_f16_lead(d, ad + off, bd + off, ID_S, part > 0 || k > 0, lead);
+                    const uint32_t off = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4, off_k = ((k >> 2) * (KEYS * 128) + (k & 3) * 32) >> 4;
+                    tc::mma_f16_lead(d, ad + off, bd + off_k, ID_S, part > 0 || k > 0, lead);
                 }
             }
         };
-        auto product = [&](int m, int st, bool add) {       // m: the tile; fp32: the scores' buffer
+        auto product = [&](int m, int st, bool add) {       // m: the tile; one tile: the scores' buffer
             const uint64_t bd = vd + st * (W::KB >> 4);
-            const uint32_t p0 = tmem + (MT == 2 ? W::SP + 64 * m : m == 0 ? W::S0 : W::S1);
+            const uint32_t p0 = tmem + (MT == 2 ? W::SP + 64 * m : NARROW ? W::SP : m == 0 ? W::S0 : W::S1);
 #pragma unroll
             for (int part = 0; part < (F32 ? 3 : 1); ++part)
 #pragma unroll
                 for (int k = 0; k < KEYS / 16; ++k) {
-                    const uint32_t own = k / (KT / 16) * KT + k % (KT / 16) * 8;      // P in its thread's scores
-                    const uint32_t d = F32 ? (part == 0 ? W::O0 : W::O1) : m == 0 ? W::O0 : W::O1;
+                    const uint32_t own = NARROW ? k * 8 : k / (KT / 16) * KT + k % (KT / 16) * 8;      // P in its thread's scores
+                    const uint32_t d = F32 ? (part == 0 ? W::O0 : W::O1) : MT == 1 || m == 0 ? W::O0 : W::O1;
                     tc::mma_f16_ts_lead(tmem + d, part < 2 ? p0 + KT / 2 * part + own : tmem + W::SP + 8 * k,
                                         bd + k * (2048 >> 4), ID_O, part > 1 || k > 0 ? 1u : add, lead);
                 }
@@ -809,18 +845,28 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const KvView c, 
     if (warp == (SOFT + CONV) / 32) tc::tmem_dealloc(tmem, 512);
 }
 
-template <typename T, int D, bool TREE>
-cudaError_t launch_tiles_t(const DeviceInfo& dev, const KvView& c, const AttnArgs& a, const RowsPlan& pl, cudaStream_t s) {
-    using W = Tiles<T, D>;
+template <typename T, int D, bool TREE, bool NARROW>
+cudaError_t launch_tiles_n(const DeviceInfo& dev, const KvView& c, const AttnArgs& a, const RowsPlan& pl, cudaStream_t s) {
+    using W = Tiles<T, D, NARROW>;
     if (W::SMEM > dev.smem_optin) return cudaErrorInvalidConfiguration;
-    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_tiles_kernel<T, D, TREE>), W::SMEM);
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_tiles_kernel<T, D, TREE, NARROW>), W::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t G = a.heads / c.heads;
     // Each request that this kernel takes has at most one part-filled item more than its rows make
     int64_t items = (a.T * G / W::ROWS + std::min<int64_t>(a.R, a.T * G / pl.tile_rows + 1)) * c.heads;
     if (items > 0x7fffffff) return cudaErrorInvalidConfiguration;
     items = std::max<int64_t>(items, pl.sms);              // parts of items
-    return launch_kernel(attn_tiles_kernel<T, D, TREE>, dim3(static_cast<unsigned>(items)), dim3(THREADS), W::SMEM, s, c, a, pl);
+    return launch_kernel(attn_tiles_kernel<T, D, TREE, NARROW>, dim3(static_cast<unsigned>(items)), dim3(W::THREADS), W::SMEM, s, c, a, pl);
+}
+
+template <typename T, int D, bool TREE>
+cudaError_t launch_tiles_t(const DeviceInfo& dev, const KvView& c, const AttnArgs& a, const RowsPlan& pl, cudaStream_t s) {
+    if constexpr (TREE && !std::is_same<T, float>::value) {
+        // Trees that fit one tile (64 requests of 1500 keys, 48 rows: 101 us, 135 with two tiles; 4 of 30k-60k keys and
+        // 96-192 rows: 222 in two items for 193)
+        if (a.max_new * (a.heads / c.heads) <= 128) return launch_tiles_n<T, D, TREE, true>(dev, c, a, pl, s);
+    }
+    return launch_tiles_n<T, D, TREE, false>(dev, c, a, pl, s);
 }
 
 template <bool TREE>

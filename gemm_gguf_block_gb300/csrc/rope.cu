@@ -82,7 +82,8 @@ __global__ void __launch_bounds__(THREADS) qk_rope_kernel(const RopeArgs a, cons
                 v[b][1].zero();
                 if (at_t[b] >= 0) {
                     const int which = h >= a.heads[0];
-                    const TI* p = static_cast<const TI*>(a.x[which]) + (t0 + t) * a.x_stride[which] + (h - (which ? a.heads[0] : 0)) * D;
+                    const TI* p = static_cast<const TI*>(which ? a.x[1] : a.x[0]) + (t0 + t) * (which ? a.x_stride[1] : a.x_stride[0]) +
+                                  (which ? h - a.heads[0] : h) * D;
                     v[b][0].load(p + 4 * g0);
                     v[b][1].load(p + 4 * g1);
                 }
@@ -99,8 +100,9 @@ __global__ void __launch_bounds__(THREADS) qk_rope_kernel(const RopeArgs a, cons
 #pragma unroll
                 for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
                 if (at_t[b] < 0) continue;
-                if (a.w[which] != nullptr) {
-                    const float4 w = *reinterpret_cast<const float4*>(a.w[which] + 4 * g0), z = *reinterpret_cast<const float4*>(a.w[which] + 4 * g1);
+                const float* norm = which ? a.w[1] : a.w[0];
+                if (norm != nullptr) {
+                    const float4 w = *reinterpret_cast<const float4*>(norm + 4 * g0), z = *reinterpret_cast<const float4*>(norm + 4 * g1);
                     const float r = rsqrtf(fmaf(ss, 1.0f / D, a.eps));
                     x = make_float4(x.x * r * w.x, x.y * r * w.y, x.z * r * w.z, x.w * r * w.w);
                     y = make_float4(y.x * r * z.x, y.y * r * z.y, y.z * r * z.z, y.w * r * z.w);
@@ -116,7 +118,8 @@ __global__ void __launch_bounds__(THREADS) qk_rope_kernel(const RopeArgs a, cons
                         y = make_float4(q.x * c.x + p.x * s.x, q.y * c.y + p.y * s.y, q.z * c.z + p.z * s.z, q.w * c.w + p.w * s.w);
                     }
                 }
-                TO* p = static_cast<TO*>(a.y[which]) + (t0 + at_t[b]) * a.y_stride[which] + (at_h[b] - (which ? a.heads[0] : 0)) * D;
+                TO* p = static_cast<TO*>(which ? a.y[1] : a.y[0]) + (t0 + at_t[b]) * (which ? a.y_stride[1] : a.y_stride[0]) +
+                        (which ? at_h[b] - a.heads[0] : at_h[b]) * D;
                 store4(p + 4 * g0, x);
                 store4(p + 4 * g1, y);
             }

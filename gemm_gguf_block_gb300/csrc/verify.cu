@@ -26,12 +26,12 @@
 namespace cq {
 namespace {
 
-constexpr int THREADS = 512;
+constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int MAX_CLUSTER = 8;
 constexpr int MAX = CQ_TREE_MAX;
 constexpr int BATCH = 16;                          // loads of a thread in flight
-constexpr int ONE_BITS = 46;                       // w of the largest logit is 2^46
+constexpr int ILP = 4;                             // exponentials of a thread side by side
 constexpr float CUT = -47.0f;                      // below 2^CUT of the largest: 0 (less than half a unit)
 
 // 2^(i / 256) in units of 2^-46: the exponential's series in fp64, worked out by the compiler.
@@ -104,39 +104,54 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 // w of logit z beside the row's largest, m (finite); c = log2(e) / temperature. The exponent
-// x = (z - m) c is held to 2^-40: the difference and its rounding error, times c in two parts. Then
-// 2^x = 2^I * table[8 bits] * (1 + y + y^2 / 2 + y^3 / 6), y < 2^-8.5 in units of 2^-40; the next term is
-// 2^-38.
+// x = (z - m) c is held to 2^-40: the difference and its rounding error, times c in two parts; it is cut into whole
+// numbers by adding 1.5 * 2^23 (conversions run at an eighth of that rate). Then 2^x = 2^I * table[8 bits] *
+// (1 + y + y^2 / 2 + y^3 / 6), y < 2^-8.5 in units of 2^-40; the next term is 2^-38.
 __device__ __forceinline__ uint64_t weight(float z, float m, float c_hi, float c_lo, const unsigned long long* table) {
+    constexpr float CUTTER = 12582912.0f;                                               // 0x4b400000
     const float d = __fsub_rn(z, m);
     const float p = __fmul_rn(d, c_hi);
-    if (!(p > CUT)) return z == m ? uint64_t(1) << ONE_BITS : 0;
+    if (!(p > CUT)) return 0;
     const float bb = __fsub_rn(d, z);
     const float err = __fadd_rn(__fsub_rn(z, __fsub_rn(d, bb)), __fsub_rn(-m, bb));      // z - m = d + err
     float e = __fmaf_rn(d, c_hi, -p);
     e = __fmaf_rn(d, c_lo, e);
     e = __fmaf_rn(err, c_hi, e);
-    const float n = rintf(p), f = __fsub_rn(p, n);
-    const float f1 = rintf(f * 1048576.0f);                                             // 2^20
-    const float f2 = __fadd_rn(__fmaf_rn(f1, -9.5367431640625e-07f, f), e);
-    const int64_t x = (static_cast<int64_t>(static_cast<int>(n)) << 40) + (static_cast<int64_t>(static_cast<int>(f1)) << 20) +
-                      __float2int_rn(f2 * 1099511627776.0f);                            // 2^40
-    if (x >= 0) return uint64_t(1) << ONE_BITS;
-    const int down = -static_cast<int>(x >> 40);                                        // 1 .. 48
+    const float t0 = __fadd_rn(p, CUTTER), f = __fsub_rn(p, __fsub_rn(t0, CUTTER));      // whole part, rest in [-1/2, 1/2]
+    const float t1 = __fmaf_rn(f, 1048576.0f, CUTTER);                                   // in units of 2^-20
+    const float t2 = __fmaf_rn(__fadd_rn(__fmaf_rn(__fsub_rn(t1, CUTTER), -9.5367431640625e-07f, f), e), 1099511627776.0f, CUTTER);
+    // x = t0 2^40 + t1 2^20 + t2 in units of 2^-40, each without its 0x4b400000
+    const uint64_t above = static_cast<uint64_t>(__float_as_uint(t0) - 0x4b400000u) << 40 | __float_as_uint(t2);
+    const uint64_t x = above + (static_cast<uint64_t>(__float_as_uint(t1)) << 20) - (0x4b400000ull << 20) - 0x4b400000ull;
+    const int down = -(static_cast<int>(x >> 32) >> 8);                                 // 0 .. 48
     const uint32_t g = static_cast<uint32_t>(x);
     const uint64_t t = table[static_cast<uint32_t>(x >> 32) & 255u];
     const uint32_t y = __umulhi(g, 2977044472u);                                        // ln 2 in units of 2^-32
     const uint32_t y2 = __umulhi(y, y) >> 9;
-    const uint32_t y3 = __umulhi(__umulhi(y2, y), 1431655765u) >> 8;
+    const uint32_t y3 = __umulhi(y2 * 683u, y) >> 19;                                   // 683 / 2048: a third
     const uint64_t w = t + ((static_cast<uint64_t>(static_cast<uint32_t>(t >> 15)) * (y + y2 + y3)) >> 25);
-    return (w + (uint64_t(1) << (down - 1))) >> down;
+    return (w + ((uint64_t(1) << down) >> 1)) >> down;
 }
 
-// max(w - q A, 0), A = a_hi 2^64 + a_lo.
-__device__ __forceinline__ uint64_t without(uint64_t w, uint64_t q, uint64_t a_lo, uint32_t a_hi) {
-    const uint64_t lo = __umul64hi(q, a_lo);
-    if (a_hi != 0 && (__umul64hi(q, a_hi) != 0 || q * a_hi + lo < lo)) return 0;
-    const uint64_t t = lo + q * a_hi;
+// max(w - q A, 0), A = a_hi 2^64 + a_lo; q a probability: 24 bits, q = f 2^-s.
+__device__ __forceinline__ uint64_t without(uint64_t w, float q, uint64_t a_lo, uint32_t a_hi) {
+    const uint32_t b = __float_as_uint(fminf(fmaxf(q, 0.0f), 1.0f));                    // (NaN: 0)
+    const uint32_t f = (b & 0x7fffffu) | 0x800000u;
+    const int s = 150 - static_cast<int>(b >> 23);                                      // 23 (q = 1) .. 150 (0 and subnormal: nothing is left)
+    // f A: 24 bits by 70
+    const uint64_t lo = static_cast<uint64_t>(f) * static_cast<uint32_t>(a_lo);
+    const uint64_t hi = static_cast<uint64_t>(f) * static_cast<uint32_t>(a_lo >> 32) + (lo >> 32);      // < 2^57
+    uint64_t t;
+    if (a_hi == 0) {
+        t = s >= 96 ? 0 : s >= 32 ? hi >> (s - 32) : hi << (32 - s) | static_cast<uint32_t>(lo) >> s;
+    } else {
+        const uint64_t top = static_cast<uint64_t>(f) * a_hi;                           // < 2^31, in units of 2^64
+        if (s < 64 && top >> s != 0) return 0;
+        t = s >= 96 ? 0 : s >= 32 ? hi >> (s - 32) : hi << (32 - s) | static_cast<uint32_t>(lo) >> s;
+        const uint64_t more = s >= 128 ? 0 : s >= 64 ? top >> (s - 64) : top << (64 - s);
+        if (t + more < t) return 0;
+        t += more;
+    }
     return w > t ? w - t : 0;
 }
 
@@ -153,7 +168,7 @@ struct Shared {
 };
 
 template <bool DRAFT>
-__global__ void __launch_bounds__(THREADS, 2) tree_verify_kernel(const VerifyArgs a, const int cluster, const int slice, const int stretch) {
+__global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArgs a, const int cluster, const int slice, const int stretch) {
     pdl_trigger();
     extern __shared__ __align__(16) float row[];   // [slice] of the node's logits
     __shared__ Shared sh;
@@ -298,12 +313,20 @@ __global__ void __launch_bounds__(THREADS, 2) tree_verify_kernel(const VerifyArg
                 // to tell on which side of it a random number falls.
                 auto exact = [&]() {
                     uint64_t s = 0;
-                    for (int i = w0 + lane; i < w1; i += 32) s += weight(row[i], m, c_hi, c_lo, sh.table);
+                    for (int i0 = w0 + lane; i0 < w1; i0 += 32 * ILP) {
+#pragma unroll
+                        for (int k = 0; k < ILP; ++k) {
+                            const int i = i0 + 32 * k;
+                            const uint64_t w = weight(i < w1 ? row[i] : -INFINITY, m, c_hi, c_lo, sh.table);
+                            s += w;
+                        }
+                    }
                     return totals(sum_of(s));
                 };
                 uint64_t R = 0, below = 0, above = 0;       // the sum of r (0: not known yet) and bounds on it
                 if (children != 0) {
                     float s = 0.0f;
+#pragma unroll 8
                     for (int i = w0 + lane; i < w1; i += 32) s += exp2_fast((row[i] - m) * c_hi);
                     s = fminf(s, 1e6f);
                     const uint64_t mine = sum_of(static_cast<uint64_t>(__float2ull_rn(s * 70368744177664.0f)));
@@ -332,7 +355,8 @@ __global__ void __launch_bounds__(THREADS, 2) tree_verify_kernel(const VerifyArg
                     const uint64_t u = sh.rq.u[j];
                     uint64_t w = sh.weight[j];
                     if constexpr (DRAFT) {
-                        const uint64_t q = prob64(__uint_as_float(static_cast<uint32_t>(sh.child[j] >> 32)));
+                        const float q1 = __uint_as_float(static_cast<uint32_t>(sh.child[j] >> 32));
+                        const uint64_t q = prob64(q1);
                         if (R == 0) {
                             if (__umul64hi(u, __umul64hi(q, above)) < w) {
                                 taken = j;
@@ -340,7 +364,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_verify_kernel(const VerifyArg
                             }
                             R = exact();
                         }
-                        w = without(w, q, a_lo, a_hi);
+                        w = without(w, q1, a_lo, a_hi);
                         if (__umul64hi(u, __umul64hi(q, R)) < w) {
                             taken = j;
                             break;
@@ -349,9 +373,15 @@ __global__ void __launch_bounds__(THREADS, 2) tree_verify_kernel(const VerifyArg
                         const uint64_t n_lo = a_lo + R;
                         const uint32_t n_hi = a_hi + (n_lo < a_lo);
                         uint64_t rs = 0;
-                        for (int i = w0 + lane; i < w1; i += 32) {
-                            const float q1 = dr[i];
-                            rs += without(weight(row[i], m, c_hi, c_lo, sh.table), prob64(q1), n_lo, n_hi);
+                        for (int i0 = w0 + lane; i0 < w1; i0 += 32 * BATCH) {
+                            float q[BATCH];
+#pragma unroll
+                            for (int k = 0; k < BATCH; ++k) q[k] = i0 + 32 * k < w1 ? dr[i0 + 32 * k] : 0.0f;
+#pragma unroll
+                            for (int k = 0; k < BATCH; ++k) {
+                                const int i = i0 + 32 * k;
+                                rs += without(weight(i < w1 ? row[i] : -INFINITY, m, c_hi, c_lo, sh.table), q[k], n_lo, n_hi);
+                            }
                         }
                         const uint64_t before = tid < WARPS ? sh.part[tid] : 0;         // kept where nothing is left
                         const uint64_t sum = totals(sum_of(rs));
@@ -422,7 +452,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_verify_kernel(const VerifyArg
                         auto value = [&](int i) {
                             uint64_t v = weight(row[i], m, c_hi, c_lo, sh.table);
                             if constexpr (DRAFT) {
-                                if ((a_lo | a_hi) != 0) v = without(v, prob64(dr[i]), a_lo, a_hi);
+                                if ((a_lo | a_hi) != 0) v = without(v, dr[i], a_lo, a_hi);
                             } else {
                                 for (int k = 0; k < gone; ++k)
                                     if (sh.gone[k] == lo + i) v = 0;

@@ -212,3 +212,21 @@ def test_captured_and_on_another_stream():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) and torch.equal(a, d) for a, b, d in zip(want, got, held))
+
+
+def test_sums_of_rejected_residuals_past_64_bits():
+    """A flat distribution of 200000 tokens (a sum of 2^63.6 units) and drafts that all lie where it does not: the
+    residuals that were taken away add up to more than 2^64."""
+    torch, cq = torch_cuda(), cq_built()
+    V = 200000
+    c = _case(21, V, [9, 12], 1.0, draft=True, spread=0.0)
+    c["logits"][:] = 0.0
+    c["draft"][:] = 0.0
+    rng = np.random.default_rng(3)
+    for f, n in zip(c["q_start"][:-1], (9, 12)):
+        at = rng.permutation(V)[:16]
+        c["draft"][f:f + n, at] = 1.0 / 16
+        c["parent"][f + 1:f + n], c["tokens"][f + 1:f + n] = 0, at[:n - 1]
+    c["u_accept"][:] = 0.9
+    count, _, nxt = _check(torch, cq, c)
+    assert count.tolist() == [1, 1]
