@@ -30,8 +30,7 @@ constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int MAX_CLUSTER = 8;
 constexpr int MAX = CQ_TREE_MAX;
-constexpr int BATCH = 16;                          // loads of a thread in flight
-constexpr int ILP = 4;                             // exponentials of a thread side by side
+constexpr int PIECE = 128;                         // values that a warp takes at a time, four neighbours a lane
 constexpr float CUT = -47.0f;                      // below 2^CUT of the largest: 0 (less than half a unit)
 
 // 2^(i / 256) in units of 2^-46: the exponential's series in fp64, worked out by the compiler.
@@ -74,9 +73,19 @@ __device__ __forceinline__ uint32_t ld_cluster32(uint32_t addr) {
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
-// All threads of the cluster; what they wrote before is visible behind it.
+// All threads of the cluster; what the first two warps wrote to others' shared memory is visible behind it.
+// (A release by every warp is a fence by every warp.)
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    if (threadIdx.x < MAX) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ void cp_async16(void* smem_dst, const void* gsrc) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)), "l"(gsrc) : "memory");
+}
+// Four values from global memory, those from n on 0.
+__device__ __forceinline__ float4 load4(const float* p, int n, bool aligned) {
+    if (aligned && n >= 4) return *reinterpret_cast<const float4*>(p);
+    return make_float4(n > 0 ? p[0] : 0.0f, n > 1 ? p[1] : 0.0f, n > 2 ? p[2] : 0.0f, n > 3 ? p[3] : 0.0f);
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -159,7 +168,7 @@ struct Shared {
     unsigned long long table[256];
     unsigned long long xchg[2][MAX_CLUSTER];       // what the CTAs spread, alternately
     unsigned long long tot[MAX_CLUSTER];           // the CTAs' sums of r
-    unsigned long long part[WARPS];                // the warps' sums of r, over their own stretch of the slice
+    unsigned long long parts[2][WARPS];            // the warps' sums over their own stretch of the slice, alternately
     unsigned long long child[MAX];                 // logit and draft probability of the node's children
     unsigned long long weight[MAX];                // their w
     float top[WARPS];
@@ -168,9 +177,9 @@ struct Shared {
 };
 
 template <bool DRAFT>
-__global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArgs a, const int cluster, const int slice, const int stretch) {
+__global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArgs a, const int cluster, const int slice, const int stretch, const bool few) {
     pdl_trigger();
-    extern __shared__ __align__(16) float row[];   // [slice] of the node's logits
+    extern __shared__ __align__(16) float row[];   // [WARPS * stretch]: the node's logits, -infinity past the slice
     __shared__ Shared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = blockIdx.x / cluster;
@@ -179,7 +188,8 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
     pdl_wait();
     const int lo = static_cast<int>(min(static_cast<int64_t>(rank) * slice, static_cast<int64_t>(a.V)));
     const int len = min(slice, a.V - lo);          // this CTA's values; 0 for none
-    const int w0 = min(warp * stretch, len), w1 = min(w0 + stretch, len);
+    // a warp's values: whole pieces, four neighbours a lane; a thread reads what it has brought itself
+    const int w0 = warp * stretch + 4 * lane, w1 = min((warp + 1) * stretch, (len + 3) & ~3);
     if (rank == 0) {
         const int first = min(max(a.q_start[r], 0), a.T);
         const int n = max(min(a.q_start[r + 1], a.T) - first, 0);
@@ -228,16 +238,25 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
         turn ^= 1;
         return sh.xchg[turn ^ 1];
     };
-    // The warps' sums to sh.part and the CTA's to all threads.
+    // The warps' sums to `part` and the CTA's to all threads. (A buffer is written again two barriers on.)
+    int side = 0;
+    unsigned long long* part = sh.parts[0];
     auto sum_of = [&](uint64_t s) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        __syncthreads();                           // the last readers of part are through
-        if (lane == 0) sh.part[warp] = s;
+        part = sh.parts[side];
+        side ^= 1;
+        if (lane == 0) part[warp] = s;
         __syncthreads();
         uint64_t all = 0;
-        for (int w = 0; w < WARPS; ++w) all += sh.part[w];
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) all += part[w];
         return all;
+    };
+    // A row's slice on its way into L2.
+    auto ahead = [&](const float* p) {
+        const uintptr_t p0 = (reinterpret_cast<uintptr_t>(p) + 15) & ~uintptr_t(15), p1 = reinterpret_cast<uintptr_t>(p + len) & ~uintptr_t(15);
+        if (tid == 0 && p1 > p0) bulk_prefetch_l2(reinterpret_cast<const void*>(p0), static_cast<uint32_t>(p1 - p0));
     };
     // The CTAs' sums of r spread and held in sh.tot; the sum of all.
     auto totals = [&](uint64_t mine) {
@@ -258,19 +277,39 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
         const float c_hi = sh.rq.c_hi, c_lo = sh.rq.c_lo;
         const bool greedy = sh.rq.greedy != 0;
         for (;;) {
-            // ---- the node's row: into shared memory, its largest logit (NaN if any is)
+            // ---- the node's row: into shared memory
             const float* z = a.logits + static_cast<int64_t>(first + node) * a.logits_stride + lo;
+            const float* dr = DRAFT ? a.draft + static_cast<int64_t>(first + node) * a.draft_stride + lo : nullptr;
+            const bool al = (reinterpret_cast<uintptr_t>(z) & 15) == 0, al_d = (reinterpret_cast<uintptr_t>(dr) & 15) == 0;
             __syncthreads();                       // nobody looks at the last row any more
-            float m = -INFINITY;
-            for (int i0 = w0 + lane; i0 < w1; i0 += 32 * BATCH) {
-                float v[BATCH];
+            for (int i = w0; i < (warp + 1) * stretch; i += PIECE) {
+                if (al && i + 4 <= len) {
+                    cp_async16(row + i, z + i);
+                } else {
 #pragma unroll
-                for (int k = 0; k < BATCH; ++k) v[k] = i0 + 32 * k < w1 ? z[i0 + 32 * k] : -INFINITY;
-#pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    if (i0 + 32 * k < w1) row[i0 + 32 * k] = v[k];
-                    m = max_nan(m, v[k]);
+                    for (int k = 0; k < 4; ++k) {
+                        if (i + k < len) cp_async4(row + i + k, z + i + k, 4);
+                        else row[i + k] = -INFINITY;
+                    }
                 }
+            }
+            cp_async_commit();
+            // ---- its children, one bit each
+            uint64_t children = 0;
+            if (kept < a.max_path) {
+                const uint32_t c0 = __ballot_sync(0xffffffffu, lane < n && sh.rq.parent[lane] == node && lane > 0);
+                const uint32_t c1 = __ballot_sync(0xffffffffu, lane + 32 < n && sh.rq.parent[lane + 32] == node);
+                children = static_cast<uint64_t>(c1) << 32 | c0;
+            }
+            if (few && children != 0)               // the row that is likeliest next
+                ahead(a.logits + static_cast<int64_t>(first + __ffsll(static_cast<long long>(children)) - 1) * a.logits_stride + lo);
+            // ---- its largest logit, NaN if any is
+            cp_async_wait_all();
+            float m = -INFINITY;
+#pragma unroll 4
+            for (int i = w0; i < w1; i += PIECE) {
+                const float4 v = *reinterpret_cast<const float4*>(row + i);
+                m = max_nan(max_nan(m, max_nan(v.x, v.y)), max_nan(v.z, v.w));
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -283,23 +322,20 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
                 if (lead) atomicOr(a.status, CQ_DEV_LOGITS);
                 break;
             }
-            // ---- its children, one bit each
-            uint64_t children = 0;
-            if (kept < a.max_path) {
-                const uint32_t c0 = __ballot_sync(0xffffffffu, lane < n && sh.rq.parent[lane] == node && lane > 0);
-                const uint32_t c1 = __ballot_sync(0xffffffffu, lane + 32 < n && sh.rq.parent[lane + 32] == node);
-                children = static_cast<uint64_t>(c1) << 32 | c0;
-            }
             int taken = -1;
             if (greedy) {
                 // the largest logit's smallest index
                 int at = INT_MAX;
-                for (int i = w0 + lane; i < w1; i += 32)
-                    if (row[i] == m) { at = lo + i; break; }
+                for (int i = w0; i < w1 && at == INT_MAX; i += PIECE)
+#pragma unroll
+                    for (int k = 3; k >= 0; --k)
+                        if (row[i + k] == m) at = lo + i + k;
                 at = __reduce_min_sync(0xffffffffu, at);
-                if (lane == 0) sh.part[warp] = at;
+                part = sh.parts[side];
+                side ^= 1;
+                if (lane == 0) part[warp] = at;
                 __syncthreads();
-                for (int w = 0; w < WARPS; ++w) at = min(at, static_cast<int>(sh.part[w]));
+                for (int w = 0; w < WARPS; ++w) at = min(at, static_cast<int>(part[w]));
                 got = spread(at);
                 for (int c = 0; c < cluster; ++c) at = min(at, static_cast<int>(got[c]));
                 for (uint64_t left = children; left != 0 && taken < 0; left &= left - 1) {
@@ -308,26 +344,25 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
                 }
                 if (taken < 0) next = at;
             } else {
-                const float* dr = DRAFT ? a.draft + static_cast<int64_t>(first + node) * a.draft_stride + lo : nullptr;
                 // The sum of w: exactly, with the warps' and the CTAs' parts; the path's rows in front of the last need it only
                 // to tell on which side of it a random number falls.
                 auto exact = [&]() {
                     uint64_t s = 0;
-                    for (int i0 = w0 + lane; i0 < w1; i0 += 32 * ILP) {
-#pragma unroll
-                        for (int k = 0; k < ILP; ++k) {
-                            const int i = i0 + 32 * k;
-                            const uint64_t w = weight(i < w1 ? row[i] : -INFINITY, m, c_hi, c_lo, sh.table);
-                            s += w;
-                        }
+                    for (int i = w0; i < w1; i += PIECE) {
+                        const float4 v = *reinterpret_cast<const float4*>(row + i);
+                        s += weight(v.x, m, c_hi, c_lo, sh.table) + weight(v.y, m, c_hi, c_lo, sh.table) +
+                             weight(v.z, m, c_hi, c_lo, sh.table) + weight(v.w, m, c_hi, c_lo, sh.table);
                     }
                     return totals(sum_of(s));
                 };
                 uint64_t R = 0, below = 0, above = 0;       // the sum of r (0: not known yet) and bounds on it
                 if (children != 0) {
                     float s = 0.0f;
-#pragma unroll 8
-                    for (int i = w0 + lane; i < w1; i += 32) s += exp2_fast((row[i] - m) * c_hi);
+#pragma unroll 4
+                    for (int i = w0; i < w1; i += PIECE) {
+                        const float4 v = *reinterpret_cast<const float4*>(row + i);
+                        s += (exp2_fast((v.x - m) * c_hi) + exp2_fast((v.y - m) * c_hi)) + (exp2_fast((v.z - m) * c_hi) + exp2_fast((v.w - m) * c_hi));
+                    }
                     s = fminf(s, 1e6f);
                     const uint64_t mine = sum_of(static_cast<uint64_t>(__float2ull_rn(s * 70368744177664.0f)));
                     // the children's logits and draft probabilities, from the CTA that has them
@@ -362,6 +397,7 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
                                 taken = j;
                                 break;
                             }
+                            ahead(dr);
                             R = exact();
                         }
                         w = without(w, q1, a_lo, a_hi);
@@ -373,26 +409,26 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
                         const uint64_t n_lo = a_lo + R;
                         const uint32_t n_hi = a_hi + (n_lo < a_lo);
                         uint64_t rs = 0;
-                        for (int i0 = w0 + lane; i0 < w1; i0 += 32 * BATCH) {
-                            float q[BATCH];
-#pragma unroll
-                            for (int k = 0; k < BATCH; ++k) q[k] = i0 + 32 * k < w1 ? dr[i0 + 32 * k] : 0.0f;
-#pragma unroll
-                            for (int k = 0; k < BATCH; ++k) {
-                                const int i = i0 + 32 * k;
-                                rs += without(weight(i < w1 ? row[i] : -INFINITY, m, c_hi, c_lo, sh.table), q[k], n_lo, n_hi);
-                            }
+                        auto next_q = [&](int i) { return load4(dr + i, i < w1 ? len - i : 0, al_d); };
+                        float4 d0 = next_q(w0), d1 = next_q(w0 + PIECE);
+                        for (int i = w0; i < w1; i += PIECE) {
+                            const float4 v = *reinterpret_cast<const float4*>(row + i), d = d0;
+                            d0 = d1;
+                            d1 = next_q(i + 2 * PIECE);
+                            rs += without(weight(v.x, m, c_hi, c_lo, sh.table), d.x, n_lo, n_hi) +
+                                  without(weight(v.y, m, c_hi, c_lo, sh.table), d.y, n_lo, n_hi) +
+                                  without(weight(v.z, m, c_hi, c_lo, sh.table), d.z, n_lo, n_hi) +
+                                  without(weight(v.w, m, c_hi, c_lo, sh.table), d.w, n_lo, n_hi);
                         }
-                        const uint64_t before = tid < WARPS ? sh.part[tid] : 0;         // kept where nothing is left
+                        unsigned long long* before = part;                              // kept where nothing is left
                         const uint64_t sum = totals(sum_of(rs));
                         if (sum != 0) {
                             R = sum;
                             a_lo = n_lo;
                             a_hi = n_hi;
                         } else {
-                            __syncthreads();
-                            if (tid < WARPS) sh.part[tid] = before;
-                            __syncthreads();
+                            part = before;
+                            side ^= 1;                                                  // the next sums do not go there
                         }
                     } else {
                         for (int k = 0; k < gone; ++k)
@@ -437,7 +473,7 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
                             for (int k = 0; k < gone; ++k) {
                                 const int x = sh.gone[k], owner = x / slice;
                                 sh.tot[owner] -= sh.weight[sh.gone_at[k]];
-                                if (owner == static_cast<int>(rank)) sh.part[(x - lo) / stretch] -= sh.weight[sh.gone_at[k]];
+                                if (owner == static_cast<int>(rank)) part[(x - lo) / stretch] -= sh.weight[sh.gone_at[k]];
                             }
                         __syncthreads();
                     }
@@ -446,7 +482,7 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
                     while (owner < cluster - 1 && t >= sh.tot[owner]) t -= sh.tot[owner++];
                     if (owner == static_cast<int>(rank)) {
                         int w = 0;
-                        while (w < WARPS - 1 && t >= sh.part[w]) t -= sh.part[w++];
+                        while (w < WARPS - 1 && t >= part[w]) t -= part[w++];
                         const int s0 = min(w * stretch, len), s1 = min(s0 + stretch, len);
                         const int per = (stretch + THREADS - 1) / THREADS, i0 = s0 + tid * per, i1 = min(i0 + per, s1);
                         auto value = [&](int i) {
@@ -467,10 +503,11 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
                             const uint64_t up = __shfl_up_sync(0xffffffffu, upto, o);
                             if (lane >= o) upto += up;
                         }
+                        part = sh.parts[side];
+                        side ^= 1;
+                        if (lane == 31) part[warp] = upto;
                         __syncthreads();
-                        if (lane == 31) sh.part[warp] = upto;
-                        __syncthreads();
-                        for (int k = 0; k < warp; ++k) upto += sh.part[k];
+                        for (int k = 0; k < warp; ++k) upto += part[k];
                         if (t < upto && t >= upto - mine) {                          // one thread
                             uint64_t c = upto - mine;
                             int i = i0;
@@ -506,13 +543,15 @@ cudaError_t launch_t(const DeviceInfo& dev, const VerifyArgs& a, cudaStream_t s)
     // values fit in shared memory.
     int cluster = 1;
     while (cluster < MAX_CLUSTER && a.V > 4096 * cluster) cluster *= 2;
-    const int slice = (a.V + cluster - 1) / cluster, stretch = (slice + WARPS - 1) / WARPS;
-    const int smem = slice * 4;
+    const int slice = ((a.V + cluster - 1) / cluster + 3) / 4 * 4, stretch = ((slice + WARPS - 1) / WARPS + PIECE - 1) / PIECE * PIECE;
+    const int smem = WARPS * stretch * 4;
+    // Where the CTAs are few, a row that may not be needed costs nobody's bandwidth.
+    const bool few = static_cast<int64_t>(a.R) * cluster <= 2 * dev.sm_count;
     if (smem > dev.smem_optin - static_cast<int>(sizeof(Shared)) - 1024) return cudaErrorInvalidConfiguration;
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(tree_verify_kernel<DRAFT>), smem);
     if (e != cudaSuccess) return e;
     return launch_kernel_cluster(tree_verify_kernel<DRAFT>, dim3(static_cast<unsigned>(a.R * cluster)), dim3(THREADS),
-                                 static_cast<size_t>(smem), s, dim3(cluster), a, cluster, slice, stretch);
+                                 static_cast<size_t>(smem), s, dim3(cluster), a, cluster, slice, stretch, few);
 }
 
 }  // namespace
