@@ -17,6 +17,7 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
+constexpr int CTAS = 4;                     // of an SM
 constexpr int MOST_TOKENS = 4;              // of a round
 constexpr int BATCH = 4;                    // heads of a lane in flight
 
@@ -131,13 +132,10 @@ template <typename TI, typename TO, int D>
 cudaError_t launch_d(const DeviceInfo& dev, const RopeArgs& a, cudaStream_t s) {
     // Tokens of a round: one where there are SMs for all of them, else four, so that a warp has several heads' loads
     // in flight between barriers. As many CTAs as run at once: each goes on to further tokens.
-    int tokens = 1, ctas = 0;
-    while (tokens < MOST_TOKENS && a.T / (2 * tokens) >= 4 * dev.sm_count) tokens *= 2;
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, qk_rope_kernel<TI, TO, D>, THREADS, 0);
-    if (e != cudaSuccess) return e;
-    const int64_t rounds = (a.T + tokens - 1) / tokens;
-    return launch_kernel(qk_rope_kernel<TI, TO, D>, dim3(static_cast<unsigned>(std::min<int64_t>(rounds, static_cast<int64_t>(dev.sm_count) * std::max(ctas, 1)))),
-                         dim3(THREADS), 0, s, a, tokens);
+    int tokens = 1;
+    while (tokens < MOST_TOKENS && a.T / (2 * tokens) >= CTAS * dev.sm_count) tokens *= 2;
+    const int64_t rounds = (a.T + tokens - 1) / tokens, ctas = std::min<int64_t>(rounds, static_cast<int64_t>(dev.sm_count) * CTAS);
+    return launch_kernel(qk_rope_kernel<TI, TO, D>, dim3(static_cast<unsigned>(ctas)), dim3(THREADS), 0, s, a, tokens);
 }
 
 template <typename TI, typename TO>

@@ -28,7 +28,7 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
-constexpr int MAX_CLUSTER = 8;
+constexpr int MAX_CLUSTER = 16;
 constexpr int MAX = CQ_TREE_MAX;
 constexpr int PIECE = 128;                         // values that a warp takes at a time, four neighbours a lane
 constexpr float CUT = -47.0f;                      // below 2^CUT of the largest: 0 (less than half a unit)
@@ -301,6 +301,10 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
                 const uint32_t c1 = __ballot_sync(0xffffffffu, lane + 32 < n && sh.rq.parent[lane + 32] == node);
                 children = static_cast<uint64_t>(c1) << 32 | c0;
             }
+            // the thread's child, where this CTA has its token, and its draft probability
+            const int own = tid < MAX && (children >> tid & 1) != 0 ? sh.rq.token[tid] - lo : -1;
+            const bool owns = own >= 0 && own < len;
+            const float own_q = DRAFT && owns ? dr[own] : 0.0f;
             if (few && children != 0)               // the row that is likeliest next
                 ahead(a.logits + static_cast<int64_t>(first + __ffsll(static_cast<long long>(children)) - 1) * a.logits_stride + lo);
             // ---- its largest logit, NaN if any is
@@ -366,12 +370,9 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
                     s = fminf(s, 1e6f);
                     const uint64_t mine = sum_of(static_cast<uint64_t>(__float2ull_rn(s * 70368744177664.0f)));
                     // the children's logits and draft probabilities, from the CTA that has them
-                    if (tid < MAX && (children >> tid & 1) != 0) {
-                        const int x = sh.rq.token[tid];
-                        if (x >= lo && x < lo + len) {
-                            const uint64_t v = static_cast<uint64_t>(__float_as_uint(DRAFT ? dr[x - lo] : 0.0f)) << 32 | __float_as_uint(row[x - lo]);
-                            for (int c = 0; c < cluster; ++c) st_cluster(mapa(smem_u32(&sh.child[tid]), c), v);
-                        }
+                    if (owns) {
+                        const uint64_t v = static_cast<uint64_t>(__float_as_uint(own_q)) << 32 | __float_as_uint(row[own]);
+                        for (int c = 0; c < cluster; ++c) st_cluster(mapa(smem_u32(&sh.child[tid]), c), v);
                     }
                     got = spread(mine);
                     for (int c = 0; c < cluster; ++c) above += got[c];
@@ -539,10 +540,12 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
 
 template <bool DRAFT>
 cudaError_t launch_t(const DeviceInfo& dev, const VerifyArgs& a, cudaStream_t s) {
-    // CTAs of a request: a slice of 4096 values is eight a thread; eight CTAs at most, whose slices of 2^18
-    // values fit in shared memory.
+    // CTAs of a request: a slice of 4096 values is sixteen a thread. Eight, whose slices of 2^18 values fit in shared
+    // memory, or sixteen where requests are few: 1 / 16 / 64 chains of 5 drafts over 128256 values take 40 / 56 / 117 us
+    // with eight, 29 / 46 / 134 with sixteen.
+    const int most = static_cast<int64_t>(a.R) * MAX_CLUSTER <= 2 * dev.sm_count ? MAX_CLUSTER : MAX_CLUSTER / 2;
     int cluster = 1;
-    while (cluster < MAX_CLUSTER && a.V > 4096 * cluster) cluster *= 2;
+    while (cluster < most && a.V > 4096 * cluster) cluster *= 2;
     const int slice = ((a.V + cluster - 1) / cluster + 3) / 4 * 4, stretch = ((slice + WARPS - 1) / WARPS + PIECE - 1) / PIECE * PIECE;
     const int smem = WARPS * stretch * 4;
     // Where the CTAs are few, a row that may not be needed costs nobody's bandwidth.
@@ -550,6 +553,10 @@ cudaError_t launch_t(const DeviceInfo& dev, const VerifyArgs& a, cudaStream_t s)
     if (smem > dev.smem_optin - static_cast<int>(sizeof(Shared)) - 1024) return cudaErrorInvalidConfiguration;
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(tree_verify_kernel<DRAFT>), smem);
     if (e != cudaSuccess) return e;
+    if (cluster > 8) {                             // more than every GPU takes: asked for
+        e = cudaFuncSetAttribute(tree_verify_kernel<DRAFT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     return launch_kernel_cluster(tree_verify_kernel<DRAFT>, dim3(static_cast<unsigned>(a.R * cluster)), dim3(THREADS),
                                  static_cast<size_t>(smem), s, dim3(cluster), a, cluster, slice, stretch, few);
 }

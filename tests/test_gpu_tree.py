@@ -200,6 +200,53 @@ def test_attn_one_tree(dtype, Hq, H, n, past):
     _tree_check(c, *_tree_attend(torch, cq, c, masks), masks)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("max_new", [0, 1, 12, 64, 65, 10 ** 6])
+def test_attn_bound_of_new_tokens_is_a_hint(dtype, max_new):
+    """max_new chooses kernels and their tiles; whatever it says, the results are right."""
+    torch, cq = torch_cuda(), cq_built()
+    new, kv = [9, 64, 1, 70, 30], [400, 300, 50, 170, 30]
+    c = _case(torch, cq, 8, dtype, 8, 2, 64, 16, kv, new)
+    masks = _masks(np.random.default_rng(4), c)
+    _tree_check(c, *_tree_attend(torch, cq, c, masks, max_new=max_new), masks)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("R", [40, 128, 129, 300])
+def test_attn_many_requests(dtype, R):
+    """More requests than are put in order, ragged lengths among them."""
+    torch, cq = torch_cuda(), cq_built()
+    rng = np.random.default_rng(R)
+    new = rng.integers(0, 8, R)
+    new[R // 2] = 7
+    c = _case(torch, cq, R, dtype, 4, 1, 64, 16, new + rng.integers(0, 200, R), new)
+    masks = _masks(rng, c)
+    _tree_check(c, *_tree_attend(torch, cq, c, masks), masks)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,Hq,H", [(48, 8, 2), (16, 8, 2), (64, 2, 2)])
+def test_attn_long_contexts_in_parts(dtype, n, Hq, H):
+    """Few items over long contexts: split over their keys, joined by the other kernel."""
+    torch, cq = torch_cuda(), cq_built()
+    c = _case(torch, cq, n, dtype, Hq, H, 128, 64, [9000, 20011], [n, n - 5])
+    masks = _masks(np.random.default_rng(n), c)
+    masks[2:n - 8] = masks[1]                            # most rows alike: the check goes row by row
+    keep = [0, 1, n - 8, n - 1, n, n + 2, 2 * n - 6]
+    out, lse = _tree_attend(torch, cq, c, masks)
+    q_start = c["q_start"]
+    for t in keep:
+        r = int(t >= q_start[1])
+        one = dict(c, q=c["q"][t:t + 1], table=c["table"][r:r + 1])
+        first, m, kv = int(q_start[r]), int(c["new"][r]), int(c["kv"][r])
+        seen = list(range(kv - m)) + [kv - m + j for j in range(m) if int(masks[t]) >> j & 1]
+        page, row = c["table"][r][np.array(seen) // 64], np.array(seen) % 64
+        want, wl, eo, el = kv_ref.attend(one["q"].float().cpu().numpy(), c["k"][page, :, row][:, :, None], c["v"][page, :, row][:, :, None],
+                                         c["ks"][page], c["vs"][page], np.arange(len(seen))[None], [len(seen)], [0, 1],
+                                         float(np.float32(128 ** -0.5)), False, 0, dtype)
+        assert (np.abs(out[t].float().cpu().numpy() - want[0]) <= eo[0]).all() and (np.abs(lse[t].cpu().numpy() - wl[0]) <= el[0]).all()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_attn_chain_is_causal(dtype):
     """A chain's masks see what the causal call sees: the same results within both calls' rounding."""
