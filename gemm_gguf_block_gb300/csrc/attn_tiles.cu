@@ -81,9 +81,12 @@ template <typename T, int D, bool NARROW> struct Tiles {
     static constexpr int QB = 128 * D * 2;                 // one query operand
     static constexpr int KB = KEYS * D * 2;
     static constexpr int OFF_Q = 1024;
-    static constexpr int OFF_K = OFF_Q + 2 * QB;
+    static constexpr int OFF_K = OFF_Q + (NARROW ? 1 : 2) * QB;
     static constexpr int OFF_V = OFF_K + 2 * KB;
-    static constexpr int SMEM = OFF_V + 2 * KB + 1024;     // + alignment slack of the dynamic base
+    // NARROW: the cache's bytes on their way, a step's keys or values a slot
+    static constexpr int SLOTS = NARROW ? 3 : 0, SLOT = KEYS * D;
+    static constexpr int OFF_RAW = OFF_V + 2 * KB;
+    static constexpr int SMEM = OFF_RAW + SLOTS * SLOT + 1024;     // + alignment slack of the dynamic base
     // Tensor memory columns. 16-bit types: the scores of one tile at a time, both tiles' P, both
     // results. (A tile's scores are there only until its softmax has them in registers, so the
     // other's next ones follow while the first is at work: no softmax waits for its own P's
@@ -667,6 +670,7 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
             p_ks = c.k_scale[page * c.scale_stride + h];
             p_vs = c.v_scale[page * c.scale_stride + h];
         };
+        // (NARROW: bytes by asynchronous copies instead, see below)
         uint4 kr[GROUPS][NL] = {}, vr[GROUPS][NL] = {};
         auto load = [&](const int8_t* src, uint4 (&x)[GROUPS][NL]) {
 #pragma unroll
@@ -699,45 +703,134 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
                     *reinterpret_cast<uint4*>(dst + put[i][1] + 8 * g * 128) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
         };
-        int page = checked(entry(0), 0), ahead = entry(1);
-        scales(page);
-        place(page, 0);
-        load(c.k, kr);
-        load(c.v, vr);
-        for (int j = 0; j < steps; ++j) {
-            const int st = j & 1;
-            if (j % 8 == 0 && __any_sync(0xffffffffu, abort_flag.get())) break;
-            // (the whole warp leaves or none of it: it shuffles)
-            if (!__all_sync(0xffffffffu, tc::wait_or_abort_sleep(&bars[B_K_EMPTY + st], ((j >> 1) & 1) ^ 1, abort_flag, a.status))) break;
-            store(smem + W::OFF_K + st * W::KB, kr, false);
-            fence_proxy_async_smem();
-            tc::mbar_arrive(&bars[B_K_FULL + st]);
-            // What was looked up for this step and the next is taken before any load is issued: right
-            // behind the values' loads, this waits for them, half a step.
-            float3 in = make_float3(0.0f, -INFINITY, 1.0f);
-            if (page >= 0) {
-                in.x = p_ks;
-                // (exact here for the 16-bit types too: 443 us for 437 at the 8192-token prompt)
-                value_factors<F32>(p_vs, in.y, in.z);
+        if constexpr (NARROW) {
+            // A step is shorter than a load takes, and loads into registers are waited for together: whoever takes the keys
+            // waits for the values' loads behind them as well. The bytes come by asynchronous copies instead, three halves
+            // of a step in front; a thread takes what it has copied itself. The lookups of sixteen steps are made at once,
+            // a lane a step: one step's alone are 900 cycles of one instruction behind another.
+            static_assert(!NARROW || NBK == 1, "one block a warp and step");
+            constexpr int BATCH = 16;
+            uint8_t* const raw = smem + W::OFF_RAW + cw * (GROUPS * NL * 512) + lane * 16;
+            auto copy = [&](const int8_t* src, int64_t from, int slot) {
+                if (from >= 0) {                            // else what lies there: integers that meet a P of zero
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+                        for (int i = 0; i < NL; ++i)
+                            cp_async16(raw + slot * W::SLOT + (g * NL + i) * 512, src + from + (8 * g + ck) * D + 16 * piece(i));
+                }
+                cp_async_commit();
+            };
+            auto take = [&](uint4 (&x)[GROUPS][NL], int slot) {
+                cp_async_wait<2>();
+#pragma unroll
+                for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+                    for (int i = 0; i < NL; ++i) x[g][i] = *reinterpret_cast<const uint4*>(raw + slot * W::SLOT + (g * NL + i) * 512);
+            };
+            // the lane's step of a batch that begins at step j0
+            auto key_of = [&](int j0) { return key0 + (j0 + lane) * KEYS + KW * cw; };
+            auto has = [&](int j0) { return lane < BATCH && j0 + lane < steps && key_of(j0) < tstop; };
+            auto entry_of = [&](int j0) { return has(j0) ? table[key_of(j0) >> c.page_shift] : -1; };
+            int n_entry = -1, n_page = -1;
+            int64_t b_at = -1, n_at = -1;                   // the blocks' bytes, this batch's and the next one's
+            float n_ks = 0.0f, n_vs = 0.0f;
+            float3 b_in = make_float3(0.0f, -INFINITY, 1.0f);
+            auto look = [&](int j0) {                       // entries to places; the scales on their way
+                n_page = n_entry >= 0 && n_entry < c.num_pages ? n_entry : -1;
+                if (n_page < 0 && has(j0)) atomicOr(a.status, CQ_DEV_KV_PAGE);
+                n_at = -1;
+                if (n_page >= 0) {
+                    n_at = n_page * c.page_stride + head_off + static_cast<int64_t>(key_of(j0) & (c.page_size - 1)) * D;
+                    n_ks = c.k_scale[n_page * c.scale_stride + h];
+                    n_vs = c.v_scale[n_page * c.scale_stride + h];
+                }
+            };
+            auto open = [&]() {                             // the next batch is this one
+                b_at = n_at;
+                b_in = make_float3(0.0f, -INFINITY, 1.0f);
+                if (n_page >= 0) {
+                    b_in.x = n_ks;
+                    value_factors<F32>(n_vs, b_in.y, b_in.z);
+                }
+            };
+            n_entry = entry_of(0);
+            look(0);
+            copy(c.k, __shfl_sync(0xffffffffu, n_at, 0), 0);
+            copy(c.v, __shfl_sync(0xffffffffu, n_at, 0), 1);
+            copy(c.k, __shfl_sync(0xffffffffu, n_at, 1), 2);
+            int slot = 0;
+            for (int j = 0; j < steps; ++j) {
+                const int st = j & 1, p = j % BATCH;
+                if (j % 8 == 0 && __any_sync(0xffffffffu, abort_flag.get())) break;
+                if (p == 0) open();
+                if (p == 2) n_entry = entry_of(j - p + BATCH);
+                if (p == 7) look(j - p + BATCH);
+                // the step that used this entry before is past its softmax: the scores of two steps ago were its next
+                take(kr, slot);
+                // (the whole warp leaves or none of it: it shuffles)
+                if (!__all_sync(0xffffffffu, tc::wait_or_abort_sleep(&bars[B_K_EMPTY + st], ((j >> 1) & 1) ^ 1, abort_flag, a.status))) break;
+                if (lane == p) {
+                    info[j % INFO][0][cw] = b_in.x;
+                    info[j % INFO][1][cw] = b_in.y;
+                    info[j % INFO][2][cw] = b_in.z;
+                    tc::mbar_arrive(&bars[B_INFO + j % INFO]);
+                }
+                store(smem + W::OFF_K + st * W::KB, kr, false);
+                fence_proxy_async_smem();
+                tc::mbar_arrive(&bars[B_K_FULL + st]);
+                copy(c.v, __shfl_sync(0xffffffffu, p + 1 < BATCH ? b_at : n_at, (j + 1) % BATCH), slot);
+                slot = slot == 2 ? 0 : slot + 1;
+                take(vr, slot);
+                if (!__all_sync(0xffffffffu, tc::wait_or_abort_sleep(&bars[B_V_EMPTY + st], ((j >> 1) & 1) ^ 1, abort_flag, a.status))) break;
+                store(smem + W::OFF_V + st * W::KB, vr, F32);
+                fence_proxy_async_smem();
+                tc::mbar_arrive(&bars[B_V_FULL + st]);
+                copy(c.k, __shfl_sync(0xffffffffu, p + 2 < BATCH ? b_at : n_at, (j + 2) % BATCH), slot);
+                slot = slot == 2 ? 0 : slot + 1;
             }
-            // the step that used this entry before is past its softmax: the scores of two steps ago were its next
-            if (lane < NBK) {
-                info[j % INFO][0][NBK * cw + lane] = in.x;
-                info[j % INFO][1][NBK * cw + lane] = in.y;
-                info[j % INFO][2][NBK * cw + lane] = in.z;
-            }
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bars[B_INFO + j % INFO]);
-            page = checked(ahead, j + 1);
-            ahead = entry(j + 2);
+            cp_async_wait_all();                            // none is in flight when the CTA leaves
+        } else {
+            int page = checked(entry(0), 0), ahead = entry(1);
             scales(page);
-            place(page, j + 1);
+            place(page, 0);
             load(c.k, kr);
-            if (!__all_sync(0xffffffffu, tc::wait_or_abort_sleep(&bars[B_V_EMPTY + st], ((j >> 1) & 1) ^ 1, abort_flag, a.status))) break;
-            store(smem + W::OFF_V + st * W::KB, vr, F32);
-            fence_proxy_async_smem();
-            tc::mbar_arrive(&bars[B_V_FULL + st]);
             load(c.v, vr);
+            for (int j = 0; j < steps; ++j) {
+                const int st = j & 1;
+                if (j % 8 == 0 && __any_sync(0xffffffffu, abort_flag.get())) break;
+                // (the whole warp leaves or none of it: it shuffles)
+                if (!__all_sync(0xffffffffu, tc::wait_or_abort_sleep(&bars[B_K_EMPTY + st], ((j >> 1) & 1) ^ 1, abort_flag, a.status))) break;
+                store(smem + W::OFF_K + st * W::KB, kr, false);
+                fence_proxy_async_smem();
+                tc::mbar_arrive(&bars[B_K_FULL + st]);
+                // What was looked up for this step and the next is taken before any load is issued: right
+                // behind the values' loads, this waits for them, half a step.
+                float3 in = make_float3(0.0f, -INFINITY, 1.0f);
+                if (page >= 0) {
+                    in.x = p_ks;
+                    // (exact here for the 16-bit types too: 443 us for 437 at the 8192-token prompt)
+                    value_factors<F32>(p_vs, in.y, in.z);
+                }
+                // the step that used this entry before is past its softmax: the scores of two steps ago were its next
+                if (lane < NBK) {
+                    info[j % INFO][0][NBK * cw + lane] = in.x;
+                    info[j % INFO][1][NBK * cw + lane] = in.y;
+                    info[j % INFO][2][NBK * cw + lane] = in.z;
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars[B_INFO + j % INFO]);
+                page = checked(ahead, j + 1);
+                ahead = entry(j + 2);
+                scales(page);
+                place(page, j + 1);
+                load(c.k, kr);
+                if (!__all_sync(0xffffffffu, tc::wait_or_abort_sleep(&bars[B_V_EMPTY + st], ((j >> 1) & 1) ^ 1, abort_flag, a.status))) break;
+                store(smem + W::OFF_V + st * W::KB, vr, F32);
+                fence_proxy_async_smem();
+                tc::mbar_arrive(&bars[B_V_FULL + st]);
+                load(c.v, vr);
+            }
         }
     } else {
         // --------------------------------------------------------- MMA issuer

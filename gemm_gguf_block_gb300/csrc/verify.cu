@@ -79,9 +79,6 @@ __device__ __forceinline__ void cluster_sync() {
     if (threadIdx.x < MAX) asm volatile("fence.acq_rel.cluster;" ::: "memory");
     asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ void cp_async16(void* smem_dst, const void* gsrc) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)), "l"(gsrc) : "memory");
-}
 // Four values from global memory, those from n on 0.
 __device__ __forceinline__ float4 load4(const float* p, int n, bool aligned) {
     if (aligned && n >= 4) return *reinterpret_cast<const float4*>(p);
