@@ -17,11 +17,11 @@ constexpr int TILE_ROWS = 40;
 
 // Trees: a call's requests go to one kernel, all of them, by the widest's rows -- a tree costs the tiles the same
 // whatever its width, and tiles beside rows slow both (64 contexts of 200-8190, bf16, 12-36 rows: 276 us with the border
-// at 33 rows, 118 all in the tiles, 162 all in the rows kernel; fp32, 12-56 rows: 429 with the border at 40, 200, 266).
+// at 33 rows, 111 all in the tiles, 162 all in the rows kernel; fp32, 12-56 rows: 429 with the border at 40, 200, 266).
 // Few (request, kv head) pairs leave the rows kernel enough SMs for longer. 32 query and 8 kv heads of 128, 1500 keys,
 // rows kernel and tiles: 64 requests of 16 rows 78 and 105 us, of 24 rows 129 and 104 (fp32 107 and 167, 182 and 167);
-// 16 requests of 16 rows 35 and 30, of 32 rows 49 and 30 (fp32 40 and 46, 63 and 47); one request of 1000 keys, 32
-// rows 19 and 26, 128 rows 21 and 27; 2 requests of 20000 keys at 64, 32 rows 43 and 42, 48 rows 54 and 42.
+// 16 requests of 16 rows 35 and 30, of 32 rows 49 and 29 (fp32 40 and 46, 63 and 47); one request of 1000 keys, 32
+// rows 19 and 26, 128 rows 21 and 27; 2 requests of 20000 keys at 64, 32 rows 43 and 45, 48 rows 54 and 45.
 constexpr int TREE_ROWS = 16, TREE_ROWS_FEW = 32, TREE_FEW = 32;
 
 // The workspace: the rows kernel's counters (the part that has to be zero) and parts, then the

@@ -1,5 +1,6 @@
 // Attention over the 8-bit paged cache for many query rows a (request, kv head):
-// prompts and chunks of them (cq_attn_paged in include/cq_kv.h).
+// prompts and chunks of them (cq_attn_paged in include/cq_kv.h), trees of drafts
+// (cq_attn_tree in include/cq_tree.h).
 //
 // The mathematics is attn_rows.cu's: x_j = log2(e) scale s_k (q . k_j) + log2(s_v),
 // P_j = 2^(x_j - M + OFF), out = sum P_j v_j / sum (P_j / s_v). Here the products
@@ -23,6 +24,12 @@
 // converters' loads and stores it takes 12% less, without the exponentials no less.
 // Few items are split over their keys; the rows kernel, which always follows, joins
 // the parts.
+// Trees: TREE builds have the rows' masks in the steps that are not whole. NARROW ones take a tile of 128 rows alone, two
+// threads a row, with eight converter warps that copy the bytes asynchronously: 64 contexts of 200-8190 keys, 32
+// heads on 8 of 128, bf16, 12 to 36 rows take 111 us (two tiles: 162 together with the rows kernel). A step takes
+// 2400 cycles whatever the rows: 900 of them a thread's exponentials, the rest one wait behind another (scores, meeting,
+// product, converters); an item's beginning and end 9 us. Tried for NARROW without gain: 64 keys a step and two CTAs
+// an SM (the same time), the queries in tensor memory, two steps' P.
 // A block of 16 keys carries (s_k, log2 s_v, 1 / s_v) in shared memory; a block outside
 // the cache or the request's keys has s_k = 0 and log2 s_v = -inf, so P = 0 whatever
 // integers its place holds.

@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) tree_plan_kernel(int R, int T, c
         }
         __syncthreads();
         if (n > MAX) {
-            for (int t = i; t < n; t += MAX) write(static_cast<int64_t>(first) + t, 0, base + t);
+            for (int64_t t = i; t < n; t += MAX) write(first + t, 0, base + t);      // (n may be near 2^31, where a step more passes 32 bits)
         } else if (i < n) {
             uint64_t m = 0;
             int depth = -1;
