@@ -616,36 +616,49 @@ def qk_rope_t(q, k, positions, freqs, *, q_norm=None, k_norm=None, eps: float = 
     None -> (q, k) normed and turned, new or in q_out, k_out (q and k themselves: in place). dtype: of the outputs, that of
     q by default; fp32 inputs take any. Rows of negative positions (padding) are not written: undefined in new tensors."""
     torch, i32, _, dtypes, raw = _torch_tables()
-    fn, shape, kshape, dt = "cq_qk_rope", q.shape, k.shape, q.dtype
+    fn, shape, kshape, dt, i = "cq_qk_rope", q.shape, k.shape, q.dtype, q.get_device()
     if len(shape) != 3 or len(kshape) != 3 or kshape[0] != shape[0] or kshape[2] != shape[2] or k.dtype != dt:
         raise CqError(fn, ERR_SHAPE)
     T, hq, D = shape
-    hk, i = kshape[1], q.get_device()
+    hk = kshape[1]
     qp, qs, _ = _rows(fn, q, hq * D)
     kp, ks, _ = _rows(fn, k, hk * D)
-    pos = _vec(fn, positions, i32, T)
-    half = 0 if freqs is None else freqs.shape[0] if freqs.dim() == 1 else -1
-    fp = None if freqs is None else _vec(fn, freqs, torch.float64, half)
-    ts = [k, positions] + [t for t in (freqs, q_norm, k_norm, q_out, k_out) if t is not None]
-    stream = _stream_of(fn, raw, i, *ts)
-    norms = [None if t is None else _vec(fn, t, torch.float32, D) for t in (q_norm, k_norm)]
+    pos, half, fp, qn, kn = _vec(fn, positions, i32, T), 0, None, None, None
+    stream = _stream_of(fn, raw, i, k, positions)
+    # (straight code: a call on a small batch is the host's time)
+    if freqs is not None:
+        half = freqs.shape[0] if freqs.dim() == 1 else -1
+        fp = _vec(fn, freqs, torch.float64, half)
+        if freqs.get_device() != i:
+            raise CqError(fn, ERR_INVALID_ARG)
+    if q_norm is not None:
+        qn = _vec(fn, q_norm, torch.float32, D)
+        if q_norm.get_device() != i:
+            raise CqError(fn, ERR_INVALID_ARG)
+    if k_norm is not None:
+        kn = _vec(fn, k_norm, torch.float32, D)
+        if k_norm.get_device() != i:
+            raise CqError(fn, ERR_INVALID_ARG)
     ot = dtype or (q_out.dtype if q_out is not None else k_out.dtype if k_out is not None else dt)
-    outs = []
-    for x, y, h in ((q, q_out, hq), (k, k_out, hk)):
-        if y is None:
-            y = torch.empty(x.shape, dtype=ot, device=x.device)
-            outs += [y, y.data_ptr(), h * D]
-        else:
-            yp, ys, Ty = _rows(fn, y, h * D)
-            if Ty != T or y.dtype != ot:
-                raise CqError(fn, ERR_SHAPE)
-            outs += [y, yp, ys]
-    qo, qop, qos, ko, kop, kos = outs
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=ot, device=q.device)
+        qop, qos = q_out.data_ptr(), hq * D
+    else:
+        qop, qos, To = _rows(fn, q_out, hq * D)
+        if To != T or q_out.dtype != ot or q_out.get_device() != i:
+            raise CqError(fn, ERR_SHAPE)
+    if k_out is None:
+        k_out = torch.empty(kshape, dtype=ot, device=k.device)
+        kop, kos = k_out.data_ptr(), hk * D
+    else:
+        kop, kos, To = _rows(fn, k_out, hk * D)
+        if To != T or k_out.dtype != ot or k_out.get_device() != i:
+            raise CqError(fn, ERR_SHAPE)
     st = (_lib or lib()).cq_qk_rope(dtypes.get(dt, -1), dtypes.get(ot, -1), T, hq, hk, D, 2 * half, 1 if adjacent else 0, qp,
-                                    qs, kp, ks, pos, fp, norms[0], norms[1], eps, qop, qos, kop, kos, stream)
+                                    qs, kp, ks, pos, fp, qn, kn, eps, qop, qos, kop, kos, stream)
     if st:
         raise CqError(fn, st)
-    return qo, ko
+    return q_out, k_out
 
 
 def tree_plan_t(kv_len, q_start, parent):

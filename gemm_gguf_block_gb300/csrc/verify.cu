@@ -3,9 +3,9 @@
 // A cluster of CTAs walks one request's tree from its first token: only the rows on the path of
 // kept tokens are read, each CTA its slice of the vocabulary, which stays in shared memory for as
 // long as the row is looked at. Probabilities are whole numbers,
-//   w_v = 2^46 * 2^((z_v - max z) log2(e) / temperature), rounded,
-// so that sums are exact whatever their order, W = sum w < 2^64 for 2^18 values, and the
-// rounding moves a value of the distribution function by 2^-46 sqrt(V) of the largest, not by
+//   w_v = 2^45 * 2^((z_v - max z) log2(e) / temperature), rounded,
+// so that sums are exact whatever their order, W = sum w <= 2^63 for 2^18 values, and the
+// rounding moves a value of the distribution function by 2^-45 sqrt(V) of the largest, not by
 // fp32's 2^-24: a random number that falls near a border of a 10^5-value distribution still gives
 // the token that 64 bits give. The exponential of fp32 units would not do, and fp64 runs at a
 // sixty-fourth of fp32's rate; whole-number arithmetic costs about 45 instructions a value.
@@ -31,9 +31,9 @@ constexpr int WARPS = THREADS / 32;
 constexpr int MAX_CLUSTER = 16;
 constexpr int MAX = CQ_TREE_MAX;
 constexpr int PIECE = 128;                         // values that a warp takes at a time, four neighbours a lane
-constexpr float CUT = -47.0f;                      // below 2^CUT of the largest: 0 (less than half a unit)
+constexpr float CUT = -46.0f;                      // below 2^CUT of the largest: 0 (less than half a unit)
 
-// 2^(i / 256) in units of 2^-46: the exponential's series in fp64, worked out by the compiler.
+// 2^(i / 256) in units of 2^-45: the exponential's series in fp64, worked out by the compiler.
 struct Pow2Table { unsigned long long v[256]; };
 constexpr Pow2Table pow2_table() {
     Pow2Table t{};
@@ -44,7 +44,7 @@ constexpr Pow2Table pow2_table() {
             term *= x / k;
             sum += term;
         }
-        t.v[i] = static_cast<unsigned long long>(sum * 70368744177664.0 + 0.5);
+        t.v[i] = static_cast<unsigned long long>(sum * 35184372088832.0 + 0.5);
     }
     return t;
 }
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
                         s += (exp2_fast((v.x - m) * c_hi) + exp2_fast((v.y - m) * c_hi)) + (exp2_fast((v.z - m) * c_hi) + exp2_fast((v.w - m) * c_hi));
                     }
                     s = fminf(s, 1e6f);
-                    const uint64_t mine = sum_of(static_cast<uint64_t>(__float2ull_rn(s * 70368744177664.0f)));
+                    const uint64_t mine = sum_of(static_cast<uint64_t>(__float2ull_rn(s * 35184372088832.0f)));
                     // the children's logits and draft probabilities, from the CTA that has them
                     if (owns) {
                         const uint64_t v = static_cast<uint64_t>(__float_as_uint(own_q)) << 32 | __float_as_uint(row[own]);

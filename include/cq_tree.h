@@ -115,7 +115,7 @@ cq_status cq_attn_tree(const cq_kv_cache* cache, cq_dtype dtype, int64_t R, int6
  * reached ends the request there, with next = -1, and is flagged (CQ_DEV_LOGITS). Parents as in cq_tree_plan; drafts whose
  * parent is -1 are never kept. A request without tokens, or of more than CQ_TREE_MAX (flagged,
  * CQ_DEV_TREE), gets count 0 and next -1.
- * Probabilities are held as whole numbers to 2^-46 of the row's largest, each within 2^-36 of its own
+ * Probabilities are held as whole numbers to 2^-45 of the row's largest, each within 2^-36 of its own
  * size, and summed exactly: results do not depend on timing or on how the work is split.
  * The rows of tokens that are not kept are not read.
  * R <= 16384; 1 <= V <= 262144; T < 2^31; 1 <= max_path <= CQ_TREE_MAX. All 4-byte aligned,

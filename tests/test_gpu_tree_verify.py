@@ -215,7 +215,7 @@ def test_captured_and_on_another_stream():
 
 
 def test_sums_of_rejected_residuals_past_64_bits():
-    """A flat distribution of 200000 tokens (a sum of 2^63.6 units) and drafts that all lie where it does not: the
+    """A flat distribution of 200000 tokens (a sum of 2^62.6 units) and drafts that all lie where it does not: the
     residuals that were taken away add up to more than 2^64."""
     torch, cq = torch_cuda(), cq_built()
     V = 200000
@@ -230,3 +230,26 @@ def test_sums_of_rejected_residuals_past_64_bits():
     c["u_accept"][:] = 0.9
     count, _, nxt = _check(torch, cq, c)
     assert count.tolist() == [1, 1]
+
+
+@pytest.mark.parametrize("V", [262144, 262143])
+@pytest.mark.parametrize("draft", [False, True])
+def test_flat_rows_of_the_largest_vocabulary(V, draft):
+    """Every value at its largest: the largest sums there are. u = (k + 1/2) / V falls into the middle of token k."""
+    torch, cq = torch_cuda(), cq_built()
+    c = _case(22, V, [1, 3, 2], 1.0, draft=draft, spread=0.0, chain=True)
+    c["logits"][:] = -7.5
+    if draft:
+        c["draft"][:] = 1.0 / V
+    c["u_accept"][:] = 0.5
+    c["u_sample"][:] = [0.5 / V, (V // 2 + 0.5) / V, (V - 0.5) / V]
+    got = [x.cpu().numpy() for x in _run(torch, cq, c)]
+    if not draft:                                        # (with it the drafts are kept: u q < p for u = 1/2)
+        assert got[0].tolist() == [1, 1, 1]
+        want = [0, V // 2, V - 1]
+        # a rejected draft takes its own step away in front of the token, at most one of two
+        assert all(abs(int(g) - w) <= 2 for g, w in zip(got[2], want)) and got[2][0] == 0
+    else:
+        assert got[0].tolist() == [1, 3, 2] and got[2].tolist() == [0, V // 2, V - 1]
+    if V == 262144:                                      # (whose borders 64 bits hold exactly)
+        _check(torch, cq, c)

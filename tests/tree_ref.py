@@ -97,7 +97,7 @@ def verify(logits, tokens, parent, q_start, temperature, u_accept, u_sample, max
                 p[int(z.argmax())] = 1.0
             else:
                 p = np.exp((z - top) / t)
-                p[p < 2.0 ** -47] = 0.0                  # less than half a unit of 2^-46
+                p[p < 2.0 ** -46] = 0.0                  # less than half a unit of 2^-45
                 p /= p.sum()
             taken = None
             for j in range(1, n):
