@@ -21,6 +21,7 @@
 #include <algorithm>
 #include <climits>
 
+#include "tc.cuh"
 #include "tree.cuh"
 
 namespace cq {
@@ -109,27 +110,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// w of logit z beside the row's largest, m (finite); c = log2(e) / temperature. The exponent
-// x = (z - m) c is held to 2^-40: the difference and its rounding error, times c in two parts; it is cut into whole
-// numbers by adding 1.5 * 2^23 (conversions run at an eighth of that rate). Then 2^x = 2^I * table[8 bits] *
-// (1 + y + y^2 / 2 + y^3 / 6), y < 2^-8.5 in units of 2^-40; the next term is 2^-38.
-__device__ __forceinline__ uint64_t weight(float z, float m, float c_hi, float c_lo, const unsigned long long* table) {
-    constexpr float CUTTER = 12582912.0f;                                               // 0x4b400000
-    const float d = __fsub_rn(z, m);
-    const float p = __fmul_rn(d, c_hi);
-    if (!(p > CUT)) return 0;
-    const float bb = __fsub_rn(d, z);
-    const float err = __fadd_rn(__fsub_rn(z, __fsub_rn(d, bb)), __fsub_rn(-m, bb));      // z - m = d + err
-    float e = __fmaf_rn(d, c_hi, -p);
-    e = __fmaf_rn(d, c_lo, e);
-    e = __fmaf_rn(err, c_hi, e);
-    const float t0 = __fadd_rn(p, CUTTER), f = __fsub_rn(p, __fsub_rn(t0, CUTTER));      // whole part, rest in [-1/2, 1/2]
-    const float t1 = __fmaf_rn(f, 1048576.0f, CUTTER);                                   // in units of 2^-20
-    const float t2 = __fmaf_rn(__fadd_rn(__fmaf_rn(__fsub_rn(t1, CUTTER), -9.5367431640625e-07f, f), e), 1099511627776.0f, CUTTER);
-    // x = t0 2^40 + t1 2^20 + t2 in units of 2^-40, each without its 0x4b400000
+// The whole-number part of an exponential: t0, t1, t2 are x's parts in units of 1, 2^-20 and 2^-40, each with 1.5 * 2^23 added.
+// 2^x = 2^I * table[8 bits] * (1 + y + y^2 / 2 + y^3 / 6), y < 2^-8.5 in units of 2^-40; the next term is 2^-38.
+__device__ __forceinline__ uint64_t weight_of(float t0, float t1, float t2, const unsigned long long* table) {
     const uint64_t above = static_cast<uint64_t>(__float_as_uint(t0) - 0x4b400000u) << 40 | __float_as_uint(t2);
     const uint64_t x = above + (static_cast<uint64_t>(__float_as_uint(t1)) << 20) - (0x4b400000ull << 20) - 0x4b400000ull;
-    const int down = -(static_cast<int>(x >> 32) >> 8);                                 // 0 .. 48
+    const int down = -(static_cast<int>(x >> 32) >> 8);                                 // 0 .. 47
     const uint32_t g = static_cast<uint32_t>(x);
     const uint64_t t = table[static_cast<uint32_t>(x >> 32) & 255u];
     const uint32_t y = __umulhi(g, 2977044472u);                                        // ln 2 in units of 2^-32
@@ -137,6 +123,42 @@ __device__ __forceinline__ uint64_t weight(float z, float m, float c_hi, float c
     const uint32_t y3 = __umulhi(y2 * 683u, y) >> 19;                                   // 683 / 2048: a third
     const uint64_t w = t + ((static_cast<uint64_t>(static_cast<uint32_t>(t >> 15)) * (y + y2 + y3)) >> 25);
     return (w + ((uint64_t(1) << down) >> 1)) >> down;
+}
+
+constexpr float CUTTER = 12582912.0f;              // 0x4b400000: adding it leaves a whole number
+
+// w of two logits beside the row's largest, m (finite); c = log2(e) / temperature. The exponent
+// x = (z - m) c is held to 2^-40: the difference and its rounding error, times c in two parts; it is cut into whole
+// numbers by additions (conversions run at an eighth of their rate). The fp32 steps go two logits at a time (115 us one
+// at a time, 111 so, at 64 chains of 5 drafts over 128256 values).
+struct Two { uint64_t a, b; };
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t y;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
+__device__ __forceinline__ Two weights(float z0, float z1, float m, float c_hi, float c_lo, const unsigned long long* table) {
+    auto both = [](float x) { return tc::pk(x, x); };
+    const uint64_t z = tc::pk(z0, z1), less = both(-1.0f), nm = both(-m), ch = both(c_hi), cut = both(CUTTER);
+    const uint64_t d = tc::add2(z, nm), np = mul2(d, both(-c_hi));                      // -p
+    const uint64_t bb = tc::fma2(z, less, d);
+    const uint64_t err = tc::add2(tc::fma2(tc::fma2(bb, less, d), less, z), tc::fma2(bb, less, nm));
+    const uint64_t e = tc::fma2(err, ch, tc::fma2(d, both(c_lo), tc::fma2(d, ch, np)));
+    const uint64_t t0 = tc::fma2(np, less, cut), nf = tc::add2(np, tc::add2(t0, both(-CUTTER)));      // -f
+    const uint64_t t1 = tc::fma2(nf, both(-1048576.0f), cut);
+    const uint64_t nf2 = tc::fma2(tc::add2(t1, both(-CUTTER)), both(9.5367431640625e-07f), nf);
+    const uint64_t t2 = tc::fma2(tc::fma2(nf2, less, e), both(1099511627776.0f), cut);
+    float p0, p1, a0, a1, b0, b1, c0, c1;
+    tc::upk(np, p0, p1);
+    tc::upk(t0, a0, a1);
+    tc::upk(t1, b0, b1);
+    tc::upk(t2, c0, c1);
+    return Two{p0 < -CUT ? weight_of(a0, b0, c0, table) : 0, p1 < -CUT ? weight_of(a1, b1, c1, table) : 0};
+}
+
+// One logit's, by the same steps: what is taken from a sum is what went into it.
+__device__ __forceinline__ uint64_t weight(float z, float m, float c_hi, float c_lo, const unsigned long long* table) {
+    return weights(z, z, m, c_hi, c_lo, table).a;
 }
 
 // max(w - q A, 0), A = a_hi 2^64 + a_lo; q a probability: 24 bits, q = f 2^-s.
@@ -351,8 +373,8 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
                     uint64_t s = 0;
                     for (int i = w0; i < w1; i += PIECE) {
                         const float4 v = *reinterpret_cast<const float4*>(row + i);
-                        s += weight(v.x, m, c_hi, c_lo, sh.table) + weight(v.y, m, c_hi, c_lo, sh.table) +
-                             weight(v.z, m, c_hi, c_lo, sh.table) + weight(v.w, m, c_hi, c_lo, sh.table);
+                        const Two x = weights(v.x, v.y, m, c_hi, c_lo, sh.table), y = weights(v.z, v.w, m, c_hi, c_lo, sh.table);
+                        s += (x.a + x.b) + (y.a + y.b);
                     }
                     return totals(sum_of(s));
                 };
@@ -413,10 +435,9 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
                             const float4 v = *reinterpret_cast<const float4*>(row + i), d = d0;
                             d0 = d1;
                             d1 = next_q(i + 2 * PIECE);
-                            rs += without(weight(v.x, m, c_hi, c_lo, sh.table), d.x, n_lo, n_hi) +
-                                  without(weight(v.y, m, c_hi, c_lo, sh.table), d.y, n_lo, n_hi) +
-                                  without(weight(v.z, m, c_hi, c_lo, sh.table), d.z, n_lo, n_hi) +
-                                  without(weight(v.w, m, c_hi, c_lo, sh.table), d.w, n_lo, n_hi);
+                            const Two x = weights(v.x, v.y, m, c_hi, c_lo, sh.table), y = weights(v.z, v.w, m, c_hi, c_lo, sh.table);
+                            rs += (without(x.a, d.x, n_lo, n_hi) + without(x.b, d.y, n_lo, n_hi)) +
+                                  (without(y.a, d.z, n_lo, n_hi) + without(y.b, d.w, n_lo, n_hi));
                         }
                         unsigned long long* before = part;                              // kept where nothing is left
                         const uint64_t sum = totals(sum_of(rs));
