@@ -154,11 +154,12 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
     // Trees: long requests first, where they are few enough to be put in order: the items that begin last are short.
     // (64 contexts of 200-8190, trees of 3-9 tokens: 123 us, in the requests' order 158)
     constexpr int SORTED = 128;
-    __shared__ int sort_len[TREE ? SORTED : 1], sort_order[TREE ? SORTED : 1];
-    const bool sorted = TREE && a.R > 1 && a.R <= SORTED;
+    __shared__ int sort_len[TREE ? SORTED : 1];
+    __shared__ int4 in_order[TREE ? SORTED : 1];            // request, first token, new tokens, length
+    const bool sorted = TREE && a.R <= SORTED;
     if constexpr (TREE) {
         if (sorted) {
-            int f_, n_, kv_ = 0;
+            int f_ = 0, n_ = 0, kv_ = 0;
             if (tid < a.R) {
                 request_of(c, a, tid, f_, n_, kv_);
                 sort_len[tid] = kv_;
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
             if (tid < a.R) {
                 int rank = 0;
                 for (int i = 0; i < a.R; ++i) rank += sort_len[i] > kv_ || (sort_len[i] == kv_ && i < tid);
-                sort_order[rank] = tid;
+                in_order[rank] = make_int4(tid, f_, n_, kv_);
             }
             __syncthreads();
         }
@@ -178,11 +179,15 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
         int64_t carry = 0;
         for (int r0 = 0; r0 < a.R; r0 += THREADS) {
             int r_ = r0 + tid;
-            if (TREE && sorted && r_ < a.R) r_ = sort_order[r_];
             int f_ = 0, n_ = 0, kv_ = 0;
             int64_t x = 0;
             if (r_ < a.R) {
-                request_of(c, a, r_, f_, n_, kv_);
+                if (TREE && sorted) {
+                    const int4 q_ = in_order[r_];
+                    r_ = q_.x; f_ = q_.y; n_ = q_.z; kv_ = q_.w;
+                } else {
+                    request_of(c, a, r_, f_, n_, kv_);
+                }
                 x = count(n_, kv_);
             }
             int64_t s = x;
@@ -195,6 +200,7 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
             __syncthreads();
             int64_t before = carry, all = 0;
             for (int w = 0; w < THREADS / 32; ++w) {
+                if (TREE && r0 + 32 * w >= a.R) break;       // (a tree call's few requests are a few warps')
                 if (w < warp) before += scan[w];
                 all += scan[w];
             }
