@@ -85,7 +85,9 @@ cq_status cq_tree_plan(int64_t R, int64_t T, const int32_t* kv_len, const int32_
  * (mask: uint64 [T]; bits from n on are not looked at, any pattern is allowed).
  * A request of more than CQ_TREE_MAX new tokens is causal, its masks are not
  * read: prompts and chunks may stand beside trees. Everything else as there,
- * with no window (max_new, the workspace, precision, rows that see nothing, pages outside the cache).
+ * with no window (max_new, the workspace, precision, rows that see nothing, pages outside the cache), but that
+ * max_new <= CQ_TREE_MAX sends a call's requests to one kernel, all of them: with max_new * q_heads / kv_heads <= 16
+ * (32 where R * kv_heads < 32) binary16 calls' probabilities have 22 bits, above that 11.
  */
 cq_status cq_attn_tree(const cq_kv_cache* cache, cq_dtype dtype, int64_t R, int64_t T, int64_t q_heads,
                        int64_t max_new, const void* q, int64_t q_stride, const int32_t* block_table,
