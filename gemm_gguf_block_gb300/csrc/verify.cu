@@ -130,7 +130,7 @@ constexpr float CUTTER = 12582912.0f;              // 0x4b400000: adding it leav
 // w of two logits beside the row's largest, m (finite); c = log2(e) / temperature. The exponent
 // x = (z - m) c is held to 2^-40: the difference and its rounding error, times c in two parts; it is cut into whole
 // numbers by additions (conversions run at an eighth of their rate). The fp32 steps go two logits at a time (115 us one
-// at a time, 111 so, at 64 chains of 5 drafts over 128256 values).
+// at a time, 112 so, at 64 chains of 5 drafts over 128256 values; 109 since the CTAs meet once a row).
 struct Two { uint64_t a, b; };
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t y;
@@ -188,9 +188,9 @@ struct Shared {
     unsigned long long xchg[2][MAX_CLUSTER];       // what the CTAs spread, alternately
     unsigned long long tot[MAX_CLUSTER];           // the CTAs' sums of r
     unsigned long long parts[2][WARPS];            // the warps' sums over their own stretch of the slice, alternately
-    unsigned long long child[MAX];                 // logit and draft probability of the node's children
+    unsigned long long children[2][MAX];           // logit and draft probability of a node's children, alternately
     unsigned long long weight[MAX];                // their w
-    float top[WARPS];
+    float2 top[WARPS];                             // largest logits and sums of exponentials
     Request rq;
     int gone[MAX], gone_at[MAX];                   // tokens rejected at this node, and whose (no draft probabilities)
 };
@@ -326,9 +326,10 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
             const float own_q = DRAFT && owns ? dr[own] : 0.0f;
             if (few && children != 0)               // the row that is likeliest next
                 ahead(a.logits + static_cast<int64_t>(first + __ffsll(static_cast<long long>(children)) - 1) * a.logits_stride + lo);
-            // ---- its largest logit, NaN if any is
+            // ---- its largest logit, NaN if any is, and where a child is to be tested the sum of its exponentials in fp32: each
+            // warp's beside its own largest, so that the CTAs meet once for both
             cp_async_wait_all();
-            float m = -INFINITY;
+            float m = -INFINITY, sum = 0.0f;
 #pragma unroll 4
             for (int i = w0; i < w1; i += PIECE) {
                 const float4 v = *reinterpret_cast<const float4*>(row + i);
@@ -336,11 +337,36 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (lane == 0) sh.top[warp] = m;
+            if (children != 0 && !greedy && m > -INFINITY) {
+#pragma unroll 4
+                for (int i = w0; i < w1; i += PIECE) {
+                    const float4 v = *reinterpret_cast<const float4*>(row + i);
+                    sum += (exp2_fast((v.x - m) * c_hi) + exp2_fast((v.y - m) * c_hi)) + (exp2_fast((v.z - m) * c_hi) + exp2_fast((v.w - m) * c_hi));
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            }
+            // (largest, sum) of some stretches as those of all of them; a stretch without a finite value has a sum of 0
+            auto joined = [&](const float2* part_of, int count) {
+                float top = -INFINITY, all = 0.0f;
+                for (int k = 0; k < count; ++k) top = max_nan(top, part_of[k].x);
+                for (int k = 0; k < count; ++k)
+                    if (part_of[k].y > 0.0f) all = fmaf(part_of[k].y, exp2_fast((part_of[k].x - top) * c_hi), all);
+                return make_float2(top, all);
+            };
+            if (lane == 0) sh.top[warp] = make_float2(m, sum);
             __syncthreads();
-            for (int w = 0; w < WARPS; ++w) m = max_nan(m, sh.top[w]);
-            const unsigned long long* got = spread(__float_as_uint(m));
-            for (int c = 0; c < cluster; ++c) m = max_nan(m, __uint_as_float(static_cast<uint32_t>(got[c])));
+            const float2 here = joined(sh.top, WARPS);
+            // the children's logits and draft probabilities, from the CTA that has them (to a place of its own: another CTA may
+            // still be at the node before)
+            unsigned long long* const child = sh.children[kept & 1];
+            if (owns) {
+                const uint64_t v = static_cast<uint64_t>(__float_as_uint(own_q)) << 32 | __float_as_uint(row[own]);
+                for (int c = 0; c < cluster; ++c) st_cluster(mapa(smem_u32(&child[tid]), c), v);
+            }
+            const unsigned long long* got = spread(static_cast<uint64_t>(__float_as_uint(here.y)) << 32 | __float_as_uint(here.x));
+            const float2 row_of = joined(reinterpret_cast<const float2*>(got), cluster);
+            m = row_of.x;
             if (!(fabsf(m) < INFINITY)) {
                 if (lead) atomicOr(a.status, CQ_DEV_LOGITS);
                 break;
@@ -380,25 +406,13 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
                 };
                 uint64_t R = 0, below = 0, above = 0;       // the sum of r (0: not known yet) and bounds on it
                 if (children != 0) {
-                    float s = 0.0f;
-#pragma unroll 4
-                    for (int i = w0; i < w1; i += PIECE) {
-                        const float4 v = *reinterpret_cast<const float4*>(row + i);
-                        s += (exp2_fast((v.x - m) * c_hi) + exp2_fast((v.y - m) * c_hi)) + (exp2_fast((v.z - m) * c_hi) + exp2_fast((v.w - m) * c_hi));
-                    }
-                    s = fminf(s, 1e6f);
-                    const uint64_t mine = sum_of(static_cast<uint64_t>(__float2ull_rn(s * 35184372088832.0f)));
-                    // the children's logits and draft probabilities, from the CTA that has them
-                    if (owns) {
-                        const uint64_t v = static_cast<uint64_t>(__float_as_uint(own_q)) << 32 | __float_as_uint(row[own]);
-                        for (int c = 0; c < cluster; ++c) st_cluster(mapa(smem_u32(&sh.child[tid]), c), v);
-                    }
-                    got = spread(mine);
-                    for (int c = 0; c < cluster; ++c) above += got[c];
+                    // Terms good to 2^-17 (arguments up to 46, three roundings), brought to the row's largest in two steps
+                    // more, in sums of some tens: within 2^-15.
+                    above = __float2ull_rn(row_of.y * 35184372088832.0f);
                     below = above - (above >> 15);
                     above += above >> 15;
                     if (tid < MAX && (children >> tid & 1) != 0)
-                        sh.weight[tid] = weight(__uint_as_float(static_cast<uint32_t>(sh.child[tid])), m, c_hi, c_lo, sh.table);
+                        sh.weight[tid] = weight(__uint_as_float(static_cast<uint32_t>(child[tid])), m, c_hi, c_lo, sh.table);
                     __syncthreads();
                 }
                 uint64_t a_lo = 0;
@@ -410,7 +424,7 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
                     const uint64_t u = sh.rq.u[j];
                     uint64_t w = sh.weight[j];
                     if constexpr (DRAFT) {
-                        const float q1 = __uint_as_float(static_cast<uint32_t>(sh.child[j] >> 32));
+                        const float q1 = __uint_as_float(static_cast<uint32_t>(child[j] >> 32));
                         const uint64_t q = prob64(q1);
                         if (R == 0) {
                             if (__umul64hi(u, __umul64hi(q, above)) < w) {
@@ -560,7 +574,7 @@ template <bool DRAFT>
 cudaError_t launch_t(const DeviceInfo& dev, const VerifyArgs& a, cudaStream_t s) {
     // CTAs of a request: a slice of 4096 values is sixteen a thread. Eight, whose slices of 2^18 values fit in shared
     // memory, or sixteen where requests are few: 1 / 16 / 64 chains of 5 drafts over 128256 values take 40 / 56 / 117 us
-    // with eight, 29 / 46 / 134 with sixteen.
+    // with eight, 29 / 46 / 134 with sixteen (27 / 43 / 109 now, by this rule).
     const int most = static_cast<int64_t>(a.R) * MAX_CLUSTER <= 2 * dev.sm_count ? MAX_CLUSTER : MAX_CLUSTER / 2;
     int cluster = 1;
     while (cluster < most && a.V > 4096 * cluster) cluster *= 2;
