@@ -38,9 +38,9 @@ def tree_plan(kv_len, q_start, parent, T):
 def rope(x, w, eps, positions, freqs, adjacent, half_step):
     """Norm and rotation of x [T, heads, D] (what the call gets) in long doubles, and a bound on the error of results
     whose type rounds by half_step (relative). With u = 2^-24, per output a cos phi - b sin phi:
-      the norm: squares and sums of positive numbers 9 u, halved by the root; mean and eps, the root and two
-        products 3.5 u: 8 u of the value;
-      sine and cosine: the angle in half turns rounds by u of at most pi, each function by 2 ulp = 4 u: 8 u;
+      the norm: squares and sums of positive numbers 8 u, halved by the root; mean and eps 0.5 u, the root 2 ulp = 4 u,
+        two products 2 u: 10.5 u of the value;
+      sine and cosine: the angle in half turns rounds by u of at most pi, each function by 1 ulp = 2 u: 5.2 u;
       the products and their sum: 2 u;
     18 u (|a| + |b|) in all, and the rounding to the result's type (with its smallest subnormal step).
     """
