@@ -88,8 +88,8 @@ class AttentionBlock:
 
     def keep(self, count, path):
         """After a step: the tokens path[r][0 .. count[r]) of each request's new ones stay (int32 [R], [R, most] on the
-        device, as cq.tree_verify_t gives them; all of count for a request that had none new is 0), the others go, with
-        the pages that nothing is left in."""
+        device, as cq.tree_verify_t gives them; count 0 for a request that had none new), the others go, with the pages
+        that nothing is left in. A request of more than cq.TREE_MAX new tokens keeps them all, whatever its count."""
         new_len = cq.kv_move_t(self.cache, self.table, self.kv_len, self.q_start, count, path)
         self._give_back(new_len, new_len.tolist())       # the one read of the step: the host's lengths
 

@@ -90,13 +90,17 @@ __global__ void __launch_bounds__(MOVE_THREADS) kv_move_kernel(const KvView c, c
     const int P = c.page_size, shift = c.page_shift;
     const int n0 = a.q_start[r], n1 = a.q_start[r + 1], kv = a.kv_len[r], asked = a.count[r];
     const int n = n1 > n0 ? static_cast<int>(min(static_cast<int64_t>(n1) - n0, static_cast<int64_t>(INT32_MAX))) : 0;
+    if (n > MAX) {                                 // no tree: a prompt beside them keeps its tokens
+        if (lead && a.new_len != nullptr) a.new_len[r] = max(kv, 0);
+        return;
+    }
     const int count = min(min(max(asked, 0), n), a.max_path);
     const int64_t base = static_cast<int64_t>(kv) - n;
     if (lead) {
         if (count != asked) atomicOr(a.status, CQ_DEV_TREE);
         if (a.new_len != nullptr) a.new_len[r] = static_cast<int32_t>(max(base + count, int64_t(0)));
     }
-    if (count == 0 || n > MAX) return;
+    if (count == 0) return;
     float* scales = which ? c.v_scale : c.k_scale;
     int8_t* values = which ? c.v : c.k;
     // (a length shorter than its new tokens: the first of them have no position)

@@ -143,8 +143,8 @@ cq_status cq_tree_verify(int64_t R, int64_t T, int64_t V, const float* logits, i
  * changes nothing.
  *   new_len[r] = b + count[r], at least 0                   (int32 [R]; may be NULL)
  * count[r] is cut to [0, n] and to max_path, a path entry outside [0, n) leaves its row
- * as it is; both are flagged (CQ_DEV_TREE). Of a request of more than CQ_TREE_MAX tokens no row is
- * moved (count and new_len as said). Pages outside the cache, and positions outside the table, are
+ * as it is; both are flagged (CQ_DEV_TREE). A request of more than CQ_TREE_MAX tokens is no tree (a prompt beside
+ * them): it keeps all of them, count and path are not looked at, new_len[r] = kv_len[r]. Pages outside the cache, and positions outside the table, are
  * skipped and flagged (CQ_DEV_KV_PAGE). The pages that rows come from and go to are the request's own:
  * one page in two requests of a call is a race. block_table as in cq_attn_paged.
  * R <= 16384; 1 <= max_path <= CQ_TREE_MAX. Asynchronous, one launch, no allocation.

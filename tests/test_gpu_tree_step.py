@@ -114,3 +114,27 @@ def test_helpers_refuse_tensors_on_the_host_and_of_other_types():
                     with pytest.raises(cq.CqError):
                         call(**{**args, name: x.to(torch.int16)})
     assert cq.cq_read_global_status()[0] in (cq.OK, cq.ERR_DEVICE_STATUS)
+
+
+def test_a_prompt_beside_trees_keeps_its_tokens():
+    """A step with a prompt of more than TREE_MAX tokens, a tree and a request that takes no part: verification gives
+    the prompt count 0 (it has no drafts), and keep() leaves it whole."""
+    torch, cq = torch_cuda(), cq_built()
+    from gemm_gguf_block_gb300 import attn_block
+    block, _, _ = attn_block.tree_demo(hidden=256, q_heads=4, kv_heads=2, head_dim=64, vocab=500, prompts=(30, 9, 20), steps=1)
+    block.end(0)
+    past, taken = list(block.past), block.taken
+    new = [70, 6, 0]
+    parent = torch.tensor([-1] * 70 + [-1, 0, 0, 1, 1, 2], dtype=torch.int32, device="cuda")
+    block.step(torch.randn(76, 256, device="cuda"), new, parent)
+    for r, first, n in ((0, 0, 70), (1, 70, 6)):
+        want = block.dense(r, first, n)
+        assert ((block.attended[first:first + n].double() - want).norm() <= 1e-5 * want.norm()).item()
+    before = cq.kv_read_t(block.cache, block.slots)
+    path = torch.tensor([[-1, -1, -1], [0, 2, 5], [-1, -1, -1]], dtype=torch.int32, device="cuda")
+    block.keep(torch.tensor([0, 3, 0], dtype=torch.int32, device="cuda"), path)
+    assert block.past == [70, past[1] + 3, past[2]]
+    assert block.taken == sum(-(-n // 16) for n in block.past)
+    after = cq.kv_read_t(block.cache, block.slots)
+    assert all(torch.equal(a[:70], b[:70]) for a, b in zip(before, after))
+    assert cq.cq_read_global_status() == (cq.OK, 0)

@@ -136,11 +136,12 @@ def move(q, scale, table, kv_len, q_start, count, path):
     for r in range(len(kv_len)):
         n = max(int(q_start[r + 1]) - int(q_start[r]), 0)
         base = int(kv_len[r]) - n
+        if n > 64:                                       # no tree: it keeps its tokens
+            new_len.append(max(int(kv_len[r]), 0))
+            continue
         c = min(max(int(count[r]), 0), n, path.shape[1])
         bits |= DEV_TREE if c != int(count[r]) else 0
         new_len.append(max(base + c, 0))
-        if n > 64:
-            continue
 
         def place(i):
             at = base + i
