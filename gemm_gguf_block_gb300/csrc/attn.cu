@@ -1,6 +1,7 @@
 // Dispatch of the attention over the 8-bit paged cache (cq_attn_paged in
 // include/cq_kv.h, cq_attn_tree in
 // include/cq_tree.h) and its workspace.
+#include <algorithm>
 #include <climits>
 
 #include "attn_common.cuh"
@@ -23,6 +24,13 @@ constexpr int TILE_ROWS = 40;
 // 16 requests of 16 rows 35 and 30, of 32 rows 49 and 29 (fp32 40 and 46, 63 and 47); one request of 1000 keys, 32
 // rows 19 and 26, 128 rows 21 and 27; 2 requests of 20000 keys at 64, 32 rows 43 and 45, 48 rows 54 and 45.
 constexpr int TREE_ROWS = 16, TREE_ROWS_FEW = 32, TREE_FEW = 32;
+
+// 16-bit calls under masks take one row tile a CTA where the widest request fits it (bf16, 64 requests of 1500 keys, 48
+// rows: 101 us, 135 with two tiles; 4 of 30k-60k keys and 96-192 rows: 222 in two items for 193). binary16 ones also up to this
+// many new tokens: the probabilities' second part has columns there alone, and trees have it whatever stands beside them. For
+// longer prompts two tiles are worth the trees' time in the rows kernel: a prompt of 2000 / 4000 tokens beside 31 trees of 16
+// (1500 keys) takes 123 / 263 us in one tile and 196 / 288 the other way, beside 31 of 6 156 / 302 and 134 / 227.
+constexpr int PAIRS_NEW = 2048;
 
 // The workspace: the rows kernel's counters (the part that has to be zero) and parts, then the
 // tiles kernel's. All but the counters is written by a call before it is read.
@@ -60,6 +68,10 @@ cudaError_t launch_attn(const DeviceInfo& dev, const KvView& c, int dtype, const
     const bool few = static_cast<int64_t>(a.R) * c.heads < TREE_FEW;
     const bool tiles = trees ? a.max_new * G > (few ? TREE_ROWS_FEW : TREE_ROWS) : a.max_new * G >= TILE_ROWS;
     pl.tile_rows = !tiles ? INT_MAX : trees ? 1 : TILE_ROWS;
+    const bool pairs = a.tree != nullptr && dtype == CQ_F16;
+    pl.one_tile = a.max_new * G <= 128 || (pairs && a.max_new <= PAIRS_NEW);
+    // beyond that the two tiles' P, of 11 bits, is for prompts alone: the trees are the rows kernel's
+    if (tiles && pairs && !pl.one_tile) pl.tile_rows = static_cast<int>(std::max<int64_t>(TILE_ROWS, CQ_TREE_MAX * G + 1));
     pl.after_tiles = tiles;
     if (tiles) {
         const cudaError_t e = launch_attn_tiles(dev, c, dtype, a, pl, s);

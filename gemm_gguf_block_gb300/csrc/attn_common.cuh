@@ -35,6 +35,7 @@ struct RowsPlan {
     float* tile_part;    // [ATTN_TILE_CTAS][256][head_dim + 4]
     int sms;             // CTAs that the tiles kernel may split its items into
     int after_tiles;     // the rows kernel follows the tiles kernel and runs beside it
+    int one_tile;        // 16-bit calls under masks: the tiles kernel's build with one row tile a CTA
     int tile_rows;       // a request with at least so many rows of a kv head is attn_tiles.cu's; INT_MAX: none is
 };
 

@@ -69,6 +69,11 @@ struct RowMap {
 template <typename T, int D, bool NARROW> struct Tiles {
     static constexpr bool F32 = std::is_same<T, float>::value;
     static_assert(!(F32 && NARROW), "fp32 has one row tile always");
+    // binary16 trees: P in two parts (21 bits), so that a tree's precision, 22 bits in the rows kernel, does not hang on
+    // what stands beside it in the call. (64 contexts of 200-8190, 12-36 rows: 124 us, 111 with one part.) bfloat16's
+    // results have 8 bits: one part.
+    static constexpr bool PAIR = NARROW && std::is_same<T, __half>::value;
+    static constexpr int PARTS = F32 ? 3 : PAIR ? 2 : 1;   // of P
     // Two row tiles a CTA and four converter warps; NARROW: one tile, a row's keys halved between two threads as in fp32,
     // and eight converter warps.
     static constexpr int KEYS = 128;                       // keys of a step
@@ -109,7 +114,8 @@ template <typename T, int D, bool NARROW> struct Tiles {
     static constexpr uint32_t SP = 128 * SBUF;             // P, 64 columns a tile; fp32: P's third part
     static constexpr uint32_t O0 = SP + 64 * MT;
     static constexpr uint32_t O1 = O0 + (F32 ? D : NARROW ? 0 : 128);   // fp32: the smaller result; two tiles: the second's
-    static_assert(O1 + D <= 512, "tensor memory");
+    static constexpr uint32_t P2 = 448;                    // P's second part
+    static_assert(O1 + D <= (PAIR ? P2 : 512), "tensor memory");
 };
 
 template <typename T, int D, bool TREE, bool NARROW>
@@ -515,7 +521,7 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
                     for (int i = 0; i < 16; i += 2) {
                         const float p0 = __uint_as_float(v[ch][16 * b + i]), p1 = __uint_as_float(v[ch][16 * b + i + 1]);
                         sums[(i >> 1) & 1] = tc::add2(sums[(i >> 1) & 1], tc::pk(p0, p1));
-                        if constexpr (!F32) {                // 11 bits: the columns that a second part would take are in use
+                        if constexpr (W::PARTS == 1) {       // 11 bits (two tiles: the columns of a second part are in use)
                             const __half2 x = __floats2half2_rn(p0, p1);
                             pr[ch][8 * b + i / 2] = *reinterpret_cast<const uint32_t*>(&x);
                         }
@@ -524,7 +530,27 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
                     tc::upk(tc::add2(sums[0], sums[1]), s0, s1);
                     l = fmaf(s0 + s1, weight[2 * ch + b], l);        // (a weight is finite, or the sum is not)
                 }
-                if constexpr (F32) {
+                if constexpr (W::PAIR) {
+                    // The first part is cut off to 11 bits, which takes no conversion back; what is left is exact.
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        uint32_t &v0 = v[ch][2 * i], &v1 = v[ch][2 * i + 1];
+                        const float h0 = __uint_as_float(v0 & 0xffffe000u), h1 = __uint_as_float(v1 & 0xffffe000u);
+                        const __half2 x = __floats2half2_rn(h0, h1);
+                        pr[ch][i] = *reinterpret_cast<const uint32_t*>(&x);
+                        float l0, l1;
+                        tc::upk(tc::fma2(tc::pk(h0, h1), tc::pk(-1.0f, -1.0f), tc::pk(__uint_as_float(v0), __uint_as_float(v1))), l0, l1);
+                        v0 = __float_as_uint(l0);
+                        v1 = __float_as_uint(l1);
+                    }
+                    tc::st16(p_col + 16 * ch, pr[ch]);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const __half2 x = __floats2half2_rn(__uint_as_float(v[ch][2 * i]), __uint_as_float(v[ch][2 * i + 1]));
+                        pr[ch][i] = *reinterpret_cast<const uint32_t*>(&x);
+                    }
+                    tc::st16(p_col + (W::P2 - W::SP) + 16 * ch, pr[ch]);
+                } else if constexpr (F32) {
 #pragma unroll
                     for (int p3 = 0; p3 < 3; ++p3) {
 #pragma unroll
@@ -876,13 +902,13 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
             const uint64_t bd = vd + st * (W::KB >> 4);
             const uint32_t p0 = tmem + (MT == 2 ? W::SP + 64 * m : NARROW ? W::SP : m == 0 ? W::S0 : W::S1);
 #pragma unroll
-            for (int part = 0; part < (F32 ? 3 : 1); ++part)
+            for (int part = 0; part < W::PARTS; ++part)
 #pragma unroll
                 for (int k = 0; k < KEYS / 16; ++k) {
                     const uint32_t own = NARROW ? k * 8 : k / (KT / 16) * KT + k % (KT / 16) * 8;      // P in its thread's scores
                     const uint32_t d = F32 ? (part == 0 ? W::O0 : W::O1) : MT == 1 || m == 0 ? W::O0 : W::O1;
-                    tc::mma_f16_ts_lead(tmem + d, part < 2 ? p0 + KT / 2 * part + own : tmem + W::SP + 8 * k,
-                                        bd + k * (2048 >> 4), ID_O, part > 1 || k > 0 ? 1u : add, lead);
+                    tc::mma_f16_ts_lead(tmem + d, part < 2 ? p0 + (NARROW ? W::P2 - W::SP : KT / 2) * part + own : tmem + W::SP + 8 * k,
+                                        bd + k * (2048 >> 4), ID_O, part > (F32 ? 1 : 0) || k > 0 ? 1u : add, lead);
                 }
         };
         auto wait = [&](int bar, int parity) {
@@ -968,9 +994,7 @@ cudaError_t launch_tiles_n(const DeviceInfo& dev, const KvView& c, const AttnArg
 template <typename T, int D, bool TREE>
 cudaError_t launch_tiles_t(const DeviceInfo& dev, const KvView& c, const AttnArgs& a, const RowsPlan& pl, cudaStream_t s) {
     if constexpr (TREE && !std::is_same<T, float>::value) {
-        // Trees that fit one tile (64 requests of 1500 keys, 48 rows: 101 us, 135 with two tiles; 4 of 30k-60k keys and
-        // 96-192 rows: 222 in two items for 193)
-        if (a.max_new * (a.heads / c.heads) <= 128) return launch_tiles_n<T, D, TREE, true>(dev, c, a, pl, s);
+        if (pl.one_tile) return launch_tiles_n<T, D, TREE, true>(dev, c, a, pl, s);
     }
     return launch_tiles_n<T, D, TREE, false>(dev, c, a, pl, s);
 }

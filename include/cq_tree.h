@@ -86,8 +86,8 @@ cq_status cq_tree_plan(int64_t R, int64_t T, const int32_t* kv_len, const int32_
  * A request of more than CQ_TREE_MAX new tokens is causal, its masks are not
  * read: prompts and chunks may stand beside trees. Everything else as there,
  * with no window (max_new, the workspace, precision, rows that see nothing, pages outside the cache), but that
- * max_new <= CQ_TREE_MAX sends a call's requests to one kernel, all of them: with max_new * q_heads / kv_heads <= 16
- * (32 where R * kv_heads < 32) binary16 calls' probabilities have 22 bits, above that 11.
+ * max_new <= CQ_TREE_MAX sends a call's requests to one kernel, all of them, and that the probabilities of binary16
+ * calls' trees have 21 bits, whatever stands beside them (of longer requests 11 at least).
  */
 cq_status cq_attn_tree(const cq_kv_cache* cache, cq_dtype dtype, int64_t R, int64_t T, int64_t q_heads,
                        int64_t max_new, const void* q, int64_t q_stride, const int32_t* block_table,
