@@ -66,7 +66,7 @@ struct RowMap {
     }
 };
 
-template <typename T, int D, bool NARROW> struct Tiles {
+template <typename T, int D, bool TREE, bool NARROW> struct Tiles {
     static constexpr bool F32 = std::is_same<T, float>::value;
     static_assert(!(F32 && NARROW), "fp32 has one row tile always");
     // binary16 trees: P in two parts (21 bits), so that a tree's precision, 22 bits in the rows kernel, does not hang on
@@ -74,6 +74,11 @@ template <typename T, int D, bool NARROW> struct Tiles {
     // results have 8 bits: one part.
     static constexpr bool PAIR = NARROW && std::is_same<T, __half>::value;
     static constexpr int PARTS = F32 ? 3 : PAIR ? 2 : 1;   // of P
+    // fp32 trees: the MMAs' sums are cut off at each addition, 2e-9 of a result a key (1e-5 at 8000 keys, 7e-5 at 60000, where
+    // fp32 sums that round are 1e-6 off). A result begins anew every FLUSH steps, and the softmax threads add the last one to
+    // totals of their own. (64 contexts of 200-8190 keys, 12-36 rows of 128: 212 us, 201 with one result throughout; every
+    // eighth step leaves 1.7e-6, every fourth 1.1e-6.)
+    static constexpr int FLUSH = F32 && TREE ? 4 : 0;
     // Two row tiles a CTA and four converter warps; NARROW: one tile, a row's keys halved between two threads as in fp32,
     // and eight converter warps.
     static constexpr int KEYS = 128;                       // keys of a step
@@ -115,16 +120,18 @@ template <typename T, int D, bool NARROW> struct Tiles {
     static constexpr uint32_t O0 = SP + 64 * MT;
     static constexpr uint32_t O1 = O0 + (F32 ? D : NARROW ? 0 : 128);   // fp32: the smaller result; two tiles: the second's
     static constexpr uint32_t P2 = 448;                    // P's second part
+    static constexpr uint32_t T0 = 448;                    // FLUSH: totals, from a thread's 32nd column on
+    static_assert(FLUSH == 0 || OC == 32 || (OC == 64 && O1 + D <= T0), "totals");
     static_assert(O1 + D <= (PAIR ? P2 : 512), "tensor memory");
 };
 
 template <typename T, int D, bool TREE, bool NARROW>
-__global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_kernel(const KvView c, const AttnArgs a, const RowsPlan pl) {
+__global__ void __launch_bounds__(Tiles<T, D, TREE, NARROW>::THREADS, 1) attn_tiles_kernel(const KvView c, const AttnArgs a, const RowsPlan pl) {
     // The rows kernel that follows begins when every CTA of this one has passed here, and
     // does not wait for the end of it: what both read is complete by then.
     pdl_wait();
     pdl_trigger();
-    using W = Tiles<T, D, NARROW>;
+    using W = Tiles<T, D, TREE, NARROW>;
     constexpr bool F32 = W::F32;
     constexpr int KEYS = W::KEYS, SOFT = W::SOFT, CONV = W::CONV, THREADS = W::THREADS;
     constexpr int MT = W::MT, ROWS = W::ROWS, SPLIT = W::SPLIT, KT = W::KT, OC = W::OC, SBUF = W::SBUF;
@@ -390,6 +397,9 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
         const uint32_t o_col = tmem + lanes + (mt == 0 ? W::O0 : W::O1) + OC * part;
         constexpr int CHUNKS = KT / 32;
         float M = -INFINITY, l = 0.0f;
+        // The results before the last FLUSH steps, and their reference: a thread's first 32 columns, the others in tensor memory.
+        float total[W::FLUSH ? 32 : 1], total_M = -INFINITY;
+        const uint32_t t_col = tmem + lanes + W::T0 + 32 * part;
         bool ok = true;
         // After a wait that ran out (ok false) the loop goes on without waiting: the meetings stay paired.
         auto wait = [&](int bar, int parity) {
@@ -399,6 +409,38 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
                 if (!ok) abort_flag.set(1);
             }
             tc::fence_after();
+        };
+        // The last steps' results to the totals, before step j: its products begin them anew.
+        bool flushed = false;
+        auto flush = [&](const int j) {
+            if constexpr (W::FLUSH > 0) {
+                wait(B_O + mt, (j - 1) & 1);
+                const float f = total_M == M ? 1.0f : exp2_approx(total_M - M);              // 0 from -inf
+                auto added = [&](float was, uint32_t big, uint32_t small) {
+                    return (j > W::FLUSH ? was * f : 0.0f) + (__uint_as_float(big) + __uint_as_float(small));
+                };
+#pragma unroll
+                for (int ch = 0; ch < 2; ++ch) {
+                    uint32_t big[16], small[16];
+                    tc::ld16(o_col + 16 * ch, big);
+                    tc::ld16(o_col + 16 * ch + (W::O1 - W::O0), small);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) total[16 * ch + i] = added(total[16 * ch + i], big[i], small[i]);
+                }
+#pragma unroll 1
+                for (int ch = 2; ch < OC / 16; ++ch) {
+                    uint32_t big[16], small[16], rest[16];
+                    tc::ld16(o_col + 16 * ch, big);
+                    tc::ld16(o_col + 16 * ch + (W::O1 - W::O0), small);
+                    tc::ld16(t_col + 16 * (ch - 2), rest);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) rest[i] = __float_as_uint(added(__uint_as_float(rest[i]), big[i], small[i]));
+                    tc::st16(t_col + 16 * (ch - 2), rest);
+                }
+                total_M = M;
+            }
         };
         // A step; whole: every row sees all its keys.
         auto step = [&](const int j, auto whole_) {
@@ -469,13 +511,13 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
                 for (int i = 0; i < SPLIT; ++i) top = fmaxf(top, exch[j & 1][i][row]);
             }
             const bool raise = top > M + RAISE;
-            bool o_known = j == 0;
+            bool o_known = j == 0 || flushed;
             if (__any_sync(0xffffffffu, raise)) {
                 const float old = M;
                 if (raise) M = top;
                 const float f = raise ? exp2_approx(old - M) : 1.0f;             // 0 from -inf
                 l *= f;
-                if (j > 0) {
+                if (j > 0 && !flushed) {
                     wait(B_O + mt, (j - 1) & 1);
                     o_known = true;
 #pragma unroll 1
@@ -574,6 +616,10 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
         };
         for (int j = 0; j < steps; ++j) {
             const int k0 = key0 + j * KEYS + KT * part;
+            if constexpr (W::FLUSH > 0) {
+                flushed = j > 0 && j % W::FLUSH == 0;
+                if (flushed) flush(j);
+            }
             if (k0 >= all_from && k0 <= all_stop - KT) step(j, std::true_type{});
             else step(j, std::false_type{});
         }
@@ -586,7 +632,9 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
 #pragma unroll
             for (int i = 0; i < SPLIT; ++i) l += exch[steps & 1][i][row];
         }
-        auto load_o = [&](uint32_t at, uint32_t (&orr)[32]) {
+        const float total_f = total_M == M ? 1.0f : exp2_approx(total_M - M);
+        auto load_o = [&](int col, uint32_t (&orr)[32]) {       // of the thread's columns
+            const uint32_t at = o_col + col;
             if (steps == 0) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) orr[i] = 0;
@@ -601,6 +649,18 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
 #pragma unroll
                 for (int i = 0; i < 32; ++i) orr[i] = __float_as_uint(__uint_as_float(orr[i]) + __uint_as_float(os[i]));
             }
+            if constexpr (W::FLUSH > 0) {
+                if (steps > W::FLUSH) {
+                    uint32_t rest[32];
+                    if (col > 0) {
+                        tc::ld32(t_col, rest);
+                        tc::wait_ld();
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        orr[i] = __float_as_uint(fmaf(col > 0 ? __uint_as_float(rest[i]) : total[i], total_f, __uint_as_float(orr[i])));
+                }
+            }
         };
         if (ok && parts > 1) {
             // Sums as they are, fp32, to the workspace: half the columns at a time through the query operand's place.
@@ -612,7 +672,7 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
 #pragma unroll
                 for (int ch = 0; ch < PC / 32; ++ch) {
                     uint32_t orr[32];
-                    load_o(o_col + ps * PC + 32 * ch, orr);
+                    load_o(ps * PC + 32 * ch, orr);
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
                         *reinterpret_cast<uint4*>(mine_ + lane * PC + (((32 * ch + i) / 4) ^ (lane & SW)) * 4) =
@@ -641,7 +701,7 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
 #pragma unroll
             for (int ch = 0; ch < OC / 32; ++ch) {
                 uint32_t orr[32];
-                load_o(o_col + 32 * ch, orr);
+                load_o(32 * ch, orr);
 #pragma unroll
                 for (int i = 0; i < 32; i += CH) {
                     T* dst = reinterpret_cast<T*>(mine + lane * (OC * sizeof(T)) + (((32 * ch + i) / CH) ^ (lane & SW)) * 16);
@@ -951,7 +1011,7 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
                 if (!ok) break;
                 if (m == 0) ok = wait(B_V_FULL + st, (j >> 1) & 1);
                 if (!ok) break;
-                product(SBUF == 2 ? st : m, st, j > 0);
+                product(SBUF == 2 ? st : m, st, W::FLUSH > 0 ? j % (W::FLUSH > 0 ? W::FLUSH : 1) != 0 : j > 0);
                 tc::commit_lead(&bars[B_O + m], lead);
                 if (m == MT - 1) tc::commit_lead(&bars[B_V_EMPTY + st], lead);
                 if (MT == 1 && SBUF == 1 && next) {
@@ -979,7 +1039,7 @@ __global__ void __launch_bounds__(Tiles<T, D, NARROW>::THREADS, 1) attn_tiles_ke
 
 template <typename T, int D, bool TREE, bool NARROW>
 cudaError_t launch_tiles_n(const DeviceInfo& dev, const KvView& c, const AttnArgs& a, const RowsPlan& pl, cudaStream_t s) {
-    using W = Tiles<T, D, NARROW>;
+    using W = Tiles<T, D, TREE, NARROW>;
     if (W::SMEM > dev.smem_optin) return cudaErrorInvalidConfiguration;
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_tiles_kernel<T, D, TREE, NARROW>), W::SMEM);
     if (e != cudaSuccess) return e;

@@ -59,3 +59,44 @@ def test_binary16_probabilities_of_trees_have_21_bits(D, new, bound):
                     2.0 ** -11 * np.abs(want[0]) + 2.0 ** -24
             off = np.abs(got[first + t] - want[0])
             assert (off <= most).all(), f"request {r} token {t}: worst {(off / most).max():.2f} of its bound"
+
+
+@pytest.mark.parametrize("D,n,R", [(64, 1, 57), (128, 2, 57), (64, 20, 12), (128, 20, 12), (128, 60, 6)])
+def test_fp32_sums_of_long_contexts_round(D, n, R):
+    """40000 keys, enough requests that none is split over the keys, and values of one sign between 100 and 127 steps: sums
+    that are cut off at each addition lose some 2^-25 of themselves 2500 times over, 1e-5 (rows kernel) to 5e-5 of every result.
+
+    Bound, relative to the result: every probability may be off by 2 e_s (as in kv_ref.attend, e_s = 2^-18 A + 64 * 2^-23, A =
+    the largest scale |q| |k|), which moves a weighted mean of values in [100, 127] by 2 e_s * 27 / 100 at most; sums that
+    are cut off between two that round: 32 additions of 2^-23 at full size = 2^-18 (the smaller parts of P have sums of their
+    own); up to 2500 additions that round, each within 2^-24 either way, of numbers that grow: taken as independent, five
+    deviations of sqrt(2500 / 3) * 2^-24 / sqrt(3) = 5 * 1e-6; the division and the result's rounding 2^-22.
+    """
+    torch, cq = torch_cuda(), cq_built()
+    kv, P, H, Hq = 40000, 64, 8, 32
+    rng = np.random.default_rng([D, n])
+    pages = kv // P
+    k = rng.integers(-127, 128, (pages, H, P, D)).astype(np.int8)
+    v = rng.integers(100, 128, (pages, H, P, D)).astype(np.int8)
+    ks, vs = np.full((pages, H), 0.01, np.float32), np.full((pages, H), 0.5, np.float32)
+    cache = cq.KVCache(*(dev(torch, x) for x in (k, v, ks, vs)))
+    q = dev(torch, (rng.standard_normal((n, Hq, D)) * 0.3).astype(np.float32)).repeat(R, 1, 1)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(R, 1)             # all read the same pages
+    mask = tree_ref.tree_plan([n], [0, n], tree_ref.random_parents(rng, n), n)[0]
+    out, _ = cq.attn_tree_t(q, cache, table, torch.full((R,), kv, dtype=torch.int32, device="cuda"),
+                            torch.arange(R + 1, dtype=torch.int32, device="cuda") * n, dev(torch, mask.view(np.int64)).repeat(R), n)
+    out = out.double().view(R, n, Hq, D)
+    assert torch.equal(out, out[:1].expand_as(out))
+    for h in (0, H - 1):
+        kk = dev(torch, k[:, h]).double().view(kv, D) * float(ks[0, 0])
+        vv = dev(torch, v[:, h]).double().view(kv, D) * 0.5
+        qq = q[:n, h * 4:h * 4 + 4].double()
+        z = torch.einsum("ngd,kd->ngk", qq, kk) * D ** -0.5
+        hide = torch.zeros((n, kv), dtype=torch.bool, device="cuda")
+        hide[:, kv - n:] = (dev(torch, mask.view(np.int64))[:, None] >> torch.arange(n, device="cuda")) & 1 == 0
+        want = torch.softmax(z.masked_fill_(hide[:, None], -float("inf")), -1) @ vv
+        A = (torch.einsum("ngd,kd->ngk", qq.abs(), kk.abs()) * D ** -0.5).max().item()
+        es = 2.0 ** -18 * A + 64 * 2.0 ** -23
+        most = 2 * es * 0.27 + 2.0 ** -18 + 5e-6 + 2.0 ** -22
+        off = ((out[0, :, h * 4:h * 4 + 4] - want).abs() / want).max().item()
+        assert off <= most, f"{off:.2e} of {most:.2e}"
