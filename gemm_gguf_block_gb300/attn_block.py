@@ -38,6 +38,7 @@ class AttentionBlock:
         self.free = torch.arange(num_pages, dtype=torch.int32, device=dev)     # pages are taken from the front
         self.taken = 0
         self.past = [0] * requests                                             # the host's copy of the lengths
+        self.open = False                                                      # whether the last step may still be kept
         self.ws = cq.attn_workspace_t(q_heads, kv_heads, head_dim, dev)
         self.mask = None
         self.rope = None if freqs is None and q_norm is None and k_norm is None else \
@@ -83,14 +84,18 @@ class AttentionBlock:
         y = self._product(self.wo, self.attended.view(x.shape[0], width), width)
         self.taken += need
         self.past, self.q, self.slots = after, q, slots
-        self.kv_len, self.q_start = kv_len, q_start
+        self.kv_len, self.q_start, self.open = kv_len, q_start, True
         return y
 
     def keep(self, count, path):
         """After a step: the tokens path[r][0 .. count[r]) of each request's new ones stay (int32 [R], [R, most] on the
         device, as cq.tree_verify_t gives them; count 0 for a request that had none new), the others go, with the pages
-        that nothing is left in. A request of more than cq.TREE_MAX new tokens keeps them all, whatever its count."""
+        that nothing is left in. A request of more than cq.TREE_MAX new tokens keeps them all, whatever its count.
+        Once a step: what it has moved is not where the path says any more."""
+        if not self.open:
+            raise cq.CqError("AttentionBlock.keep", cq.ERR_INVALID_ARG)
         new_len = cq.kv_move_t(self.cache, self.table, self.kv_len, self.q_start, count, path)
+        self.open = False
         self._give_back(new_len, new_len.tolist())       # the one read of the step: the host's lengths
 
     def end(self, r: int):

@@ -1,0 +1,113 @@
+"""The attention layer's own bookkeeping -- lengths, pages, what may be kept -- with its calls replaced by their
+definitions on the host."""
+import types
+
+import numpy as np
+import pytest
+
+import kv_ref
+import tree_ref
+from gemm_gguf_block_gb300 import attn_block, cq
+
+torch = pytest.importorskip("torch")
+HIDDEN, HEADS, D, P = 64, 2, 64, 16
+
+
+def _definitions():
+    def plan(past, new, table, free, page, pages, tokens):
+        got = kv_ref.plan(past.numpy(), new.numpy(), table.numpy(), free.numpy(), page, pages, tokens)
+        table.copy_(torch.from_numpy(got[0]))
+        return tuple(torch.from_numpy(x) for x in got[1:])
+
+    def append(cache, k, v, slots):
+        for q, s, x in ((cache.k, cache.k_scale, k), (cache.v, cache.v_scale, v)):
+            kv_ref.append(q.numpy(), s.numpy(), x.reshape(-1, cache.kv_heads, D).numpy(), slots.numpy())
+
+    def tree_plan(kv_len, q_start, parent):
+        mask, pos, _ = tree_ref.tree_plan(kv_len.numpy(), q_start.numpy(), parent.numpy(), parent.shape[0])
+        return torch.from_numpy(mask.view(np.int64)), torch.from_numpy(pos)
+
+    def move(cache, table, kv_len, q_start, count, path):
+        if count.dtype != torch.int32 or count.shape != kv_len.shape or path.dtype != torch.int32 or path.shape[1] > 64:
+            raise cq.CqError("cq_kv_move", cq.ERR_SHAPE)
+        for q, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+            new_len, _ = tree_ref.move(q.numpy(), s.numpy(), table.numpy(), kv_len.numpy(), q_start.numpy(), count.numpy(), path.numpy())
+        return torch.from_numpy(new_len)
+
+    def release(table, old, new, page, pages, capacity):
+        return tuple(torch.from_numpy(np.array(x, np.int32)) for x in
+                     tree_ref.release(table.numpy(), old.numpy(), new.numpy(), page, pages, capacity))
+
+    return types.SimpleNamespace(**{
+        **vars(cq), "attn_workspace_t": lambda *a: None, "quantize_act_t": lambda x, f: x,
+        "gemv_t": lambda w, x, f, k: x @ w, "gemm_t": lambda w, x, f, k: x @ w, "kv_plan_t": plan, "kv_append_t": append,
+        "tree_plan_t": tree_plan, "attn_paged_t": lambda q, *a, **k: (torch.zeros(q.shape), None),
+        "attn_tree_t": lambda q, *a, **k: (torch.zeros(q.shape), None), "kv_move_t": move, "kv_release_t": release})
+
+
+@pytest.fixture
+def block(monkeypatch):
+    """Two requests of 40 tokens after their prompts, on pages of 16."""
+    monkeypatch.setattr(attn_block, "cq", _definitions())
+    g = torch.Generator().manual_seed(0)
+    b = attn_block.AttentionBlock(torch.randn(HIDDEN, 3 * HEADS * D, generator=g), torch.randn(HEADS * D, HIDDEN, generator=g),
+                                  cq.FMT["q8_0"], HIDDEN, HEADS, HEADS, D, requests=2, num_pages=12)
+    b.gen = g
+    b.step(_tokens(b, 80), [40, 40])
+    return b
+
+
+def _tokens(b, n):
+    return torch.randn(n, HIDDEN, generator=b.gen)
+
+
+def _tree_step(b, new):
+    parents = np.concatenate([tree_ref.random_parents(np.random.default_rng(n), n) if n else [] for n in new])
+    b.step(_tokens(b, sum(new)), new, torch.from_numpy(parents.astype(np.int32)))
+
+
+def _i32(*x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+def _pages(b):
+    """The requests' pages; every page is a request's or free, none twice."""
+    mine = [b.table[r, :-(-n // P)].tolist() for r, n in enumerate(b.past)]
+    assert sorted(sum(mine, []) + b.free[b.taken:].tolist()) == list(range(b.cache.num_pages))
+    return mine
+
+
+def _state(b):
+    return (list(b.past), b.taken, b.free.clone(), b.table.clone(), b.cache.k.clone(), b.cache.v.clone(),
+            b.cache.k_scale.clone(), b.cache.v_scale.clone())
+
+
+def _same(a, b):
+    return all(torch.equal(x, y) if isinstance(x, torch.Tensor) else x == y for x, y in zip(a, b))
+
+
+def test_a_step_is_kept_once(block):
+    """The rows have moved: a second call with the path 0, 2, 4 would put token 4's where token 2's is."""
+    _tree_step(block, [20, 20])
+    path = torch.tensor([[0, 2, 4], [0, 3, 17]], dtype=torch.int32)
+    with pytest.raises(cq.CqError):
+        block.keep(_i32(3), path)                        # a refusal leaves the step to be kept
+    block.keep(_i32(3, 3), path)
+    assert block.past == [43, 43]
+    _pages(block)
+    was = _state(block)
+    with pytest.raises(cq.CqError):
+        block.keep(_i32(3, 3), path)
+    assert _same(was, _state(block))
+    _tree_step(block, [5, 1])
+    block.keep(_i32(2, 1), torch.tensor([[0, 3], [0, -1]], dtype=torch.int32))
+    assert block.past == [45, 44]
+    _pages(block)
+
+
+def test_nothing_to_keep_before_a_step(monkeypatch):
+    monkeypatch.setattr(attn_block, "cq", _definitions())
+    b = attn_block.AttentionBlock(torch.zeros(HIDDEN, 3 * HEADS * D), torch.zeros(HEADS * D, HIDDEN), cq.FMT["q8_0"], HIDDEN,
+                                  HEADS, HEADS, D, requests=1, num_pages=2)
+    with pytest.raises(cq.CqError):
+        b.keep(_i32(0), torch.zeros((1, 1), dtype=torch.int32))
