@@ -39,6 +39,7 @@ class AttentionBlock:
         self.taken = 0
         self.past = [0] * requests                                             # the host's copy of the lengths
         self.open = False                                                      # whether the last step may still be kept
+        self.ended = set()                                                     # requests that ended since
         self.ws = cq.attn_workspace_t(q_heads, kv_heads, head_dim, dev)
         self.mask = None
         self.rope = None if freqs is None and q_norm is None and k_norm is None else \
@@ -84,24 +85,37 @@ class AttentionBlock:
         y = self._product(self.wo, self.attended.view(x.shape[0], width), width)
         self.taken += need
         self.past, self.q, self.slots = after, q, slots
-        self.kv_len, self.q_start, self.open = kv_len, q_start, True
+        self.kv_len, self.q_start, self.open, self.ended = kv_len, q_start, True, set()
         return y
 
     def keep(self, count, path):
         """After a step: the tokens path[r][0 .. count[r]) of each request's new ones stay (int32 [R], [R, most] on the
         device, as cq.tree_verify_t gives them; count 0 for a request that had none new), the others go, with the pages
         that nothing is left in. A request of more than cq.TREE_MAX new tokens keeps them all, whatever its count.
-        Once a step: what it has moved is not where the path says any more."""
+        Once a step: what it has moved is not where the path says any more. A request that ended since the step keeps
+        nothing, whatever its count: its pages may be another's by now."""
+        import torch
         if not self.open:
             raise cq.CqError("AttentionBlock.keep", cq.ERR_INVALID_ARG)
+        here = None
+        if self.ended:
+            if count.dtype != torch.int32 or count.shape != (len(self.past),) or count.device != self.table.device:
+                raise cq.CqError("AttentionBlock.keep", cq.ERR_SHAPE)
+            here = torch.tensor([int(r not in self.ended) for r in range(len(self.past))], dtype=torch.int32,
+                                device=self.table.device)
+            count = count * here                         # 0: none of its rows is read or written
         new_len = cq.kv_move_t(self.cache, self.table, self.kv_len, self.q_start, count, path)
         self.open = False
+        if here is not None:
+            new_len = new_len * here
         self._give_back(new_len, new_len.tolist())       # the one read of the step: the host's lengths
 
     def end(self, r: int):
-        """Request r ends: its pages are given back, its place is free for another one."""
+        """Request r ends: its pages are given back, its place is free for another one. Between a step and its keep() too
+        (its accepted tokens hold the text's end, say): the others' tokens are kept as if it were not there."""
         import torch
         left = [0 if i == r else n for i, n in enumerate(self.past)]
+        self.ended.add(r)
         self._give_back(torch.tensor(left, dtype=torch.int32, device=self.table.device), left)
 
     def _give_back(self, new_len, left):

@@ -111,3 +111,63 @@ def test_nothing_to_keep_before_a_step(monkeypatch):
                                   HEADS, HEADS, D, requests=1, num_pages=2)
     with pytest.raises(cq.CqError):
         b.keep(_i32(0), torch.zeros((1, 1), dtype=torch.int32))
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_a_request_ends_between_a_step_and_its_keep(block, wide):
+    """Its accepted tokens held the text's end: the others are kept, its pages stay given back and untouched, its place
+    serves a new prompt."""
+    new = [20, 70] if wide else [20, 20]                 # (a prompt keeps all its tokens, unless it has ended)
+    _tree_step(block, new)
+    rows = block.cache.k.numpy().astype(np.float32)
+    ended = block.table[1, :-(-(40 + new[1]) // P)].tolist()
+    first = block.table[0].tolist()
+    block.end(1)
+    was = block.cache.k[ended].clone()
+    block.keep(_i32(3, 3), torch.tensor([[0, 2, 4], [0, 5, 6]], dtype=torch.int32))
+    assert block.past == [43, 0]
+    assert torch.equal(block.cache.k[ended], was)        # nothing moved in pages that were given back
+    mine = _pages(block)
+    assert mine[0] == first[:3]
+    at = lambda i: (first[i // P], i % P)                # request 0: tokens 0, 2 and 4 of the step at 40, 41, 42
+    scale = block.cache.k_scale.numpy()
+    for i, token in ((40, 40), (41, 42), (42, 44)):
+        (p, row), (src, srow) = at(i), at(token)
+        assert np.abs(block.cache.k[p, :, row].numpy() * scale[p][:, None] - rows[src, :, srow] * scale[src][:, None]).max() <= scale[p].max()
+    block.step(_tokens(block, 31), [1, 30])
+    assert block.past == [44, 30]
+    _pages(block)
+
+
+def test_all_requests_end_before_keep(block):
+    _tree_step(block, [9, 9])
+    block.end(0)
+    block.end(1)
+    block.end(1)
+    block.keep(_i32(1, 1), torch.zeros((2, 1), dtype=torch.int32))
+    assert block.past == [0, 0] and block.taken == 0
+    _pages(block)
+
+
+def test_an_end_does_not_outlive_its_step(block):
+    """A request that ended before a step takes part in it as any other."""
+    block.end(1)
+    _tree_step(block, [4, 12])
+    block.keep(_i32(2, 2), torch.tensor([[0, 3], [0, 7]], dtype=torch.int32))
+    assert block.past == [42, 2]
+    _pages(block)
+    with pytest.raises(cq.CqError):
+        block.end(1)
+        block.keep(_i32(2, 2), torch.zeros((2, 2), dtype=torch.int32))
+
+
+@pytest.mark.parametrize("count", [torch.ones(1, dtype=torch.int32), torch.ones(2, dtype=torch.int64), torch.ones((2, 1), dtype=torch.int32)])
+def test_keep_after_an_end_refuses_what_it_refuses_else(block, count):
+    _tree_step(block, [9, 9])
+    block.end(0)
+    was = _state(block)
+    with pytest.raises(cq.CqError):
+        block.keep(count, torch.zeros((2, 1), dtype=torch.int32))
+    assert _same(was, _state(block))
+    block.keep(_i32(1, 1), torch.zeros((2, 1), dtype=torch.int32))
+    assert block.past == [0, 41]

@@ -1,0 +1,58 @@
+"""Orders of an attention layer's calls that a decoder comes to: requests that end between a step and its keep()."""
+import pytest
+
+from helpers import cq_built, torch_cuda
+
+pytestmark = pytest.mark.gpu
+
+
+def _block(prompts):
+    from gemm_gguf_block_gb300 import attn_block
+    return attn_block.tree_demo(hidden=256, q_heads=4, kv_heads=2, head_dim=64, vocab=500, prompts=prompts, steps=1)[0]
+
+
+def _attends(block, new):
+    first = 0
+    for r, n in enumerate(new):
+        if n:
+            want = block.dense(r, first, n)
+            assert ((block.attended[first:first + n].double() - want).norm() <= 1e-5 * want.norm()).item(), r
+        first += n
+
+
+def _pages(block):
+    mine = [block.table[r, :-(-n // 16)].tolist() for r, n in enumerate(block.past)]
+    assert sorted(sum(mine, []) + block.free[block.taken:].tolist()) == list(range(block.cache.num_pages))
+
+
+@pytest.mark.parametrize("gone", [0, 1, 2])
+def test_a_request_ends_between_a_step_and_its_keep(gone):
+    """The others are kept, every page is a request's or free, and a new prompt takes its place beside them."""
+    torch, cq = torch_cuda(), cq_built()
+    block = _block((30, 41, 20))
+    parent = torch.tensor([-1, 0, 0, 1, 1, 2, 2, 3, 3, 4, 4, 5, 5, 6, 6] * 3, dtype=torch.int32, device="cuda")
+    past = list(block.past)
+    block.step(torch.randn(45, 256, device="cuda"), [15] * 3, parent)
+    _attends(block, [15] * 3)
+    before, slots = cq.kv_read_t(block.cache, block.slots), block.slots.clone()
+    block.end(gone)
+    path = torch.tensor([[0, 2, 6, 13]] * 3, dtype=torch.int32, device="cuda")
+    block.keep(torch.tensor([4] * 3, dtype=torch.int32, device="cuda"), path)
+    assert block.past == [0 if r == gone else n + 4 for r, n in enumerate(past)]
+    _pages(block)
+    after = cq.kv_read_t(block.cache, slots)
+    assert all(torch.equal(a[15 * gone:15 * gone + 15], b[15 * gone:15 * gone + 15]) for a, b in zip(before, after))
+    for r in range(3):
+        if r != gone:                                    # within the steps of the pages' scales
+            pos = torch.arange(past[r], past[r] + 4, device="cuda")
+            page = block.table[r, pos // 16].long()
+            rows = cq.kv_read_t(block.cache, page * 16 + pos % 16)
+            at = 15 * r + path[r].long()
+            for was, now, s in zip(before, rows, (block.cache.k_scale, block.cache.v_scale)):
+                assert ((now - was[at]).abs() <= 0.51 * s[page][:, :, None]).all()
+    new = [1, 1, 1]
+    new[gone] = 37
+    block.step(torch.randn(39, 256, device="cuda"), new)
+    _attends(block, new)
+    _pages(block)
+    assert cq.cq_read_global_status() == (cq.OK, 0)
