@@ -114,6 +114,8 @@ class AttentionBlock:
         """Request r ends: its pages are given back, its place is free for another one. Between a step and its keep() too
         (its accepted tokens hold the text's end, say): the others' tokens are kept as if it were not there."""
         import torch
+        if not 0 <= r < len(self.past):
+            raise cq.CqError("AttentionBlock.end", cq.ERR_SHAPE)
         left = [0 if i == r else n for i, n in enumerate(self.past)]
         self.ended.add(r)
         self._give_back(torch.tensor(left, dtype=torch.int32, device=self.table.device), left)

@@ -171,3 +171,14 @@ def test_keep_after_an_end_refuses_what_it_refuses_else(block, count):
     assert _same(was, _state(block))
     block.keep(_i32(1, 1), torch.zeros((2, 1), dtype=torch.int32))
     assert block.past == [0, 41]
+
+
+@pytest.mark.parametrize("r", [-1, -2, 2, 100])
+def test_end_refuses_requests_that_are_not_there(block, r):
+    _tree_step(block, [9, 9])
+    was = _state(block)
+    with pytest.raises(cq.CqError):
+        block.end(r)
+    assert _same(was, _state(block))
+    block.keep(_i32(2, 2), torch.tensor([[0, 3], [0, 7]], dtype=torch.int32))
+    assert block.past == [42, 42]
