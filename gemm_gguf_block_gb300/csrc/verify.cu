@@ -222,7 +222,6 @@ __global__ void __launch_bounds__(THREADS, 3) tree_verify_kernel(const VerifyArg
             sh.rq.c_hi = static_cast<float>(c);
             sh.rq.c_lo = static_cast<float>(c - static_cast<double>(sh.rq.c_hi));
             sh.rq.u_sample = unit64(a.u_sample[r]);
-            if (n > MAX) atomicOr(a.status, CQ_DEV_TREE);
         }
         if (n <= MAX && tid < n) {
             int p = a.parent[first + tid];

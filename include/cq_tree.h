@@ -35,8 +35,8 @@ extern "C" {
 #define CQ_TREE_MAX 64
 
 /* Device status word bits of these calls, in the library's word (cq_read_global_status). */
-#define CQ_DEV_TREE   0x100 /* a parent that does not come before its child, a request of more than CQ_TREE_MAX tokens
-                               (cq_tree_verify), a path or count outside the request (cq_kv_move) */
+#define CQ_DEV_TREE   0x100 /* a parent that does not come before its child, a path or count outside the request
+                               (cq_kv_move) */
 #define CQ_DEV_LOGITS 0x200 /* cq_tree_verify: a row with NaN or +infinity, or without a finite value, was reached */
 
 /*
@@ -117,8 +117,8 @@ cq_status cq_attn_tree(const cq_kv_cache* cache, cq_dtype dtype, int64_t R, int6
  * 0, 1 and more as 1 - 2^-24. Tokens outside [0, V) are never kept. -infinity is
  * a logit of probability 0. A row with NaN or +infinity or nothing finite that is
  * reached ends the request there, with next = -1, and is flagged (CQ_DEV_LOGITS). Parents as in cq_tree_plan; drafts whose
- * parent is -1 are never kept. A request without tokens, or of more than CQ_TREE_MAX (flagged,
- * CQ_DEV_TREE), gets count 0 and next -1.
+ * parent is -1 are never kept. A request without tokens, or of more than CQ_TREE_MAX (no
+ * tree: a prompt beside them; nothing of it is read), gets count 0 and next -1.
  * Probabilities are held as whole numbers to 2^-45 of the row's largest, each within 2^-36 of its own
  * size, and summed exactly: results do not depend on timing or on how the work is split.
  * The rows of tokens that are not kept are not read.

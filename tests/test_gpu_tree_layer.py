@@ -56,3 +56,36 @@ def test_a_request_ends_between_a_step_and_its_keep(gone):
     _attends(block, new)
     _pages(block)
     assert cq.cq_read_global_status() == (cq.OK, 0)
+
+
+def test_a_prompt_beside_trees_goes_through_the_verification_unflagged():
+    """Plan, attention, verification and move of one batch: a prompt of more than TREE_MAX tokens, a tree, a request
+    that takes no part. The prompt has no drafts to verify: count 0, no token, no flag; it keeps its tokens."""
+    torch, cq = torch_cuda(), cq_built()
+    import numpy as np
+    import tree_ref
+    block = _block((30, 9, 20))
+    block.end(0)
+    past = list(block.past)
+    parent = torch.tensor([7] * 70 + [-1, 0, 0, 1, 1, 2], dtype=torch.int32, device="cuda")      # (a prompt's are not read)
+    y = block.step(torch.randn(76, 256, device="cuda"), [70, 6, 0], parent)
+    _attends(block, [70, 6, 0])
+    logits = (y @ torch.randn(256, 300, device="cuda"))
+    logits *= 3.0 / logits.std()
+    tokens = torch.randint(0, 300, (76,), dtype=torch.int32, device="cuda")
+    tokens[71:73] = logits[70].topk(2).indices
+    tokens[73:75] = logits[71].topk(2).indices
+    tokens[75] = logits[72].argmax()
+    for temp in (0.0, 0.8):
+        args = (logits, tokens, parent, block.q_start, torch.full((3,), temp, device="cuda"), torch.rand(76, device="cuda"),
+                torch.rand(3, device="cuda"))
+        count, path, token = cq.tree_verify_t(*args, 6)
+        a = [x.cpu().numpy() for x in args]              # the tree by itself
+        want = tree_ref.verify(a[0][70:], a[1][70:], a[2][70:], np.array([0, 6]), a[4][1:2], a[5][70:], a[6][1:2], 6)
+        assert count.tolist() == [0, want[0][0], 0] and token.tolist() == [-1, want[2][0], -1]
+        assert path.tolist() == [[-1] * 6, want[1][0].tolist(), [-1] * 6]
+        assert cq.cq_read_global_status() == (cq.OK, 0)
+    block.keep(count, path)
+    assert block.past == [70, past[1] + int(want[0][0]), past[2]]
+    _pages(block)
+    assert cq.cq_read_global_status() == (cq.OK, 0)
