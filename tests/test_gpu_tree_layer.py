@@ -89,3 +89,30 @@ def test_a_prompt_beside_trees_goes_through_the_verification_unflagged():
     assert block.past == [70, past[1] + int(want[0][0]), past[2]]
     _pages(block)
     assert cq.cq_read_global_status() == (cq.OK, 0)
+
+
+def test_well_formed_calls_flag_nothing():
+    """Each call by itself with what it documents as well-formed, the status read after each; one malformed parent, one
+    malformed path and a row without a distribution are flagged, with their bits and no others."""
+    torch, cq = torch_cuda(), cq_built()
+    i32, f32 = dict(dtype=torch.int32, device="cuda"), dict(dtype=torch.float32, device="cuda")
+    cache = cq.KVCache.empty(4, 2, 16, 64)
+    kv, start, table = torch.tensor([5], **i32), torch.tensor([0, 3], **i32), torch.tensor([[1, 2]], **i32)
+    parent, pos = torch.tensor([-1, 0, 0], **i32), torch.tensor([2, 3, 3], **i32)
+    logits, u = torch.zeros(3, 10, **f32), torch.zeros(3, **f32)
+    mask, _ = cq.tree_plan_t(kv, start, parent)
+    verify = lambda z, p: cq.tree_verify_t(z, torch.tensor([1, 2, 3], **i32), p, start, torch.ones(1, **f32), u, u[:1], 3)
+    move = lambda path: cq.kv_move_t(cache, table, kv, start, torch.tensor([2], **i32), path)
+    good = [lambda: cq.tree_plan_t(kv, start, parent), lambda: cq.qk_rope_t(torch.zeros(3, 4, 64, **f32), torch.zeros(3, 2, 64, **f32), pos, None),
+            lambda: cq.attn_tree_t(torch.zeros(3, 4, 64, **f32), cache, table, kv, start, mask, 3), lambda: verify(logits, parent),
+            lambda: move(torch.tensor([[0, 2, -1]], **i32)), lambda: cq.kv_release_t(table, kv, kv, 16, 4, 3)]
+    for call in good:
+        call()
+        assert cq.cq_read_global_status() == (cq.OK, 0)
+    bad = [(lambda: cq.tree_plan_t(kv, start, parent + 1), cq.DEV_TREE), (lambda: verify(logits, parent + 1), cq.DEV_TREE),
+           (lambda: move(torch.tensor([[0, 3, -1]], **i32)), cq.DEV_TREE),
+           (lambda: verify(logits / 0.0, parent), cq.DEV_LOGITS),
+           (lambda: cq.attn_tree_t(torch.zeros(3, 4, 64, **f32), cache, table + 3, kv, start, mask, 3), cq.DEV_KV_PAGE)]
+    for call, bits in bad:
+        call()
+        assert cq.cq_read_global_status() == (cq.ERR_DEVICE_STATUS, bits)
