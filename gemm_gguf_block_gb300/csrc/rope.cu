@@ -42,12 +42,14 @@ __global__ void __launch_bounds__(THREADS) qk_rope_kernel(const RopeArgs a, cons
         const int e = mine & 3, ml = mine >> 2;
         const int i = !a.adjacent ? mine : e < 2 ? 2 * ml + e : 2 * (ml + turned) + e - 2;
         constexpr double INV = 0.15915494309189535, INV_LO = -9.839338337591243e-18;   // 1 / 2 pi in two parts
-        const double f = a.freqs[i];
-        double hi = f * INV;
-        const double lo = fma(f, INV, -hi) + f * INV_LO;
+        // a negative frequency's is the positive one's, negated: exact, where the fraction of a small negative number is not
+        const double f = a.freqs[i], size = fabs(f);
+        double hi = size * INV;
+        const double lo = fma(size, INV, -hi) + size * INV_LO;
         hi -= floor(hi);                                 // exact
         turn = static_cast<uint64_t>(hi * 18446744073709551616.0) +
                static_cast<uint64_t>(static_cast<int64_t>(lo * 18446744073709551616.0));
+        if (f < 0.0) turn = 0 - turn;
     }
     auto angles = [&](int64_t t0, int buf) {
         if (tid < tokens && t0 + tid < a.T) where[buf][tid] = a.positions[t0 + tid];
