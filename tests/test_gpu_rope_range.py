@@ -1,4 +1,4 @@
-"""Norm and rotation at the ends of what the call takes: frequencies of either sign at far positions."""
+"""Norm and rotation at the ends of what the call takes: frequencies of either sign at far positions, rows of tiny values."""
 import numpy as np
 import pytest
 
@@ -34,3 +34,24 @@ def test_negative_frequencies_are_the_positive_ones_turned_back(D, adjacent):
     size[..., ia] = size[..., b] = size[..., ia] + size[..., b]
     size[..., ia[far]] = size[..., b[far]] = np.inf
     assert (np.abs(got - ref) <= 8.25 * 2.0 ** -24 * size).all()
+
+
+@pytest.mark.parametrize("scale", [1e-13, 1e-15, 1e-19, 1e-25, 1e-36, 1e-40])
+@pytest.mark.parametrize("eps", [0.0, 1e-45, 1e-30, 1e-26])
+@pytest.mark.parametrize("D", [64, 128])
+def test_norms_of_tiny_rows(scale, eps, D):
+    """Rows whose squares are below fp32's smallest numbers, beside ordinary ones, with an eps that does not hide it."""
+    torch, cq = torch_cuda(), cq_built()
+    rng = np.random.default_rng([D, int(-np.log10(scale))])
+    x = rng.standard_normal((19, 4, D))
+    x[:, 1:] *= scale
+    x[:, 2] *= 10.0 ** -rng.uniform(0, 2, (19, 1))
+    x = x.astype(np.float32)
+    w = (1 + 0.3 * rng.standard_normal(D)).astype(np.float32)
+    pos = rng.integers(0, 100000, 19).astype(np.int32)
+    freqs = 10000.0 ** (-2.0 * np.arange(D // 2) / D)
+    q, k = cq.qk_rope_t(dev(torch, x), dev(torch, x[:, 1:2]), dev(torch, pos), dev(torch, freqs), q_norm=dev(torch, w), k_norm=dev(torch, w), eps=eps)
+    want, bound = tree_ref.rope(x, w, eps, pos, freqs, False, 2.0 ** -24)
+    off = np.abs(q.cpu().numpy().astype(np.longdouble) - want)
+    assert (off <= bound).all(), f"worst {(off / bound).max():.2f} of its bound"
+    assert torch.equal(k[:, 0], q[:, 1])
