@@ -148,13 +148,16 @@ __global__ void __launch_bounds__(THREADS) qk_rope_kernel(const RopeArgs a, cons
     }
 }
 
+constexpr int64_t rounds_of(int64_t T, int tokens) { return (T + tokens - 1) / tokens; }
+static_assert(rounds_of(INT32_MAX, MOST_TOKENS) == INT32_MAX / MOST_TOKENS + 1, "the largest T is in range");
+
 template <typename TI, typename TO, int D>
 cudaError_t launch_d(const DeviceInfo& dev, const RopeArgs& a, cudaStream_t s) {
     // Tokens of a round: one where there are SMs for all of them, else four, so that a warp has several heads' loads
     // in flight between barriers. As many CTAs as run at once: each goes on to further tokens.
     int tokens = 1;
     while (tokens < MOST_TOKENS && a.T / (2 * tokens) >= CTAS * dev.sm_count) tokens *= 2;
-    const int64_t rounds = (a.T + tokens - 1) / tokens, ctas = std::min<int64_t>(rounds, static_cast<int64_t>(dev.sm_count) * CTAS);
+    const int64_t ctas = std::min<int64_t>(rounds_of(a.T, tokens), static_cast<int64_t>(dev.sm_count) * CTAS);
     return launch_kernel(qk_rope_kernel<TI, TO, D>, dim3(static_cast<unsigned>(ctas)), dim3(THREADS), 0, s, a, tokens);
 }
 
