@@ -18,11 +18,16 @@ constexpr int TILE_ROWS = 40;
 
 // Trees: a call's requests go to one kernel, all of them, by the widest's rows -- a tree costs the tiles the same
 // whatever its width, and tiles beside rows slow both (64 contexts of 200-8190, bf16, 12-36 rows: 276 us with the border
-// at 33 rows, 111 all in the tiles, 162 all in the rows kernel; fp32, 12-56 rows: 429 with the border at 40, 200, 266).
-// Few (request, kv head) pairs leave the rows kernel enough SMs for longer. 32 query and 8 kv heads of 128, 1500 keys,
-// rows kernel and tiles: 64 requests of 16 rows 78 and 105 us, of 24 rows 129 and 104 (fp32 107 and 167, 182 and 167);
-// 16 requests of 16 rows 35 and 30, of 32 rows 49 and 29 (fp32 40 and 46, 63 and 47); one request of 1000 keys, 32
-// rows 19 and 26, 128 rows 21 and 27; 2 requests of 20000 keys at 64, 32 rows 43 and 45, 48 rows 54 and 45.
+// at 33 rows, 111 all in the tiles, 162 all in the rows kernel). Few (request, kv head) pairs leave the rows kernel enough
+// SMs for longer. Rows kernel / tiles, us, 32 query and 8 kv heads of 128, bf16 (binary16's tiles take 12% more, fp32 takes
+// 1.2 to 1.75 times as long in both):
+//   64 requests of 1500 keys    12 rows 75 / 101     16 rows 78 / 102    24 rows 129 / 103    64 rows 239 / 104
+//   16 requests of 1500 keys    12 rows 31 / 28      16 rows 35 / 28     24 rows 45 / 29      64 rows 76 / 29
+//   2 requests of 20000 keys    12 rows 46 / 52      24 rows 61 / 56     32 rows 67 / 57      64 rows 98 / 57
+//   1 request of 1000 keys      16 rows 19 / 25      32 rows 19 / 25     64 rows 20 / 25      128 rows 22 / 26
+// What decides is rows times keys for each SM, and the host is not told the keys: the borders suit many requests, and
+// few with long contexts. One short context of 64 rows and more takes a quarter longer than it would in the rows kernel, 16
+// requests of 16 rows a quarter longer than in the tiles.
 constexpr int TREE_ROWS = 16, TREE_ROWS_FEW = 32, TREE_FEW = 32;
 
 // 16-bit calls under masks take one row tile a CTA where the widest request fits it (bf16, 64 requests of 1500 keys, 48
