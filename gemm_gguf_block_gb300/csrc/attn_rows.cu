@@ -176,9 +176,12 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
     // as one: in bfloat16 the second part moved no error against 64 bits (1.7e-3 is the result's
     // rounding) and cost 62 -> 66 us at 64 ragged contexts; in binary16 it takes 2.5e-4 to 2.1e-4.
     constexpr bool SPLIT_P = !std::is_same<T, __nv_bfloat16>::value;
-    // fp32 trees: a product is summed by itself and added with rounding: the MMAs cut their sums off at each addition, 5e-6
-    // of a result at 20000 keys a request for 7e-7. (64 requests of 1500 keys, 12 rows: 110 us, 103 without.)
-    constexpr bool FRESH = F32 && TREE;
+    // Trees: the MMAs cut their sums off at each addition, up to 1e-8 of a result a key of the warp (7e-5 at 40000 keys of
+    // one sign, 10000 a warp), so that a warp's sums begin anew every FLUSH tiles, and the last ones go to totals that round, in
+    // the warp's part of the merge region: every 128 keys for fp32 results, every 2048 for binary16 (2e-5 at most, a twentieth
+    // of half a step), every 32768 for bfloat16. (64 requests of 1500 keys, 12 rows of 128: fp32
+    // 106 us, 103 with one sum throughout, bfloat16 75.5 and 74.6.)
+    constexpr int FLUSH = TREE ? (F32 ? 128 : SPLIT_P ? 2048 : 32768) / (16 * 128 / D) : 0;
     constexpr int RT = W::RT, ROWF = W::ROWF;
     constexpr float OFF = W::OFF, RAISE = W::RAISE;
     constexpr int NSUB = 128 / D, KST = D / 16, MT = D / 16;      // a tile: NSUB blocks of 16 keys, 2 KB of keys
@@ -454,6 +457,34 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.0f;
 
+        // The sums so far to the totals (beside their references); last: the totals to the sums. A lane keeps its own values.
+        auto flush = [&](bool old, bool last) {
+            float* const mine_ = merge + warp * RT * ROWF + lane;
+            float* const ref = ml + warp * RT * 2;
+            float f[NB][2];
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float was = old ? ref[8 * b + 2 * tq + e] : 0.0f;
+                    f[b][e] = !old ? 0.0f : was == M[b][e] ? 1.0f : exp2_approx(was - M[b][e]);      // 0 from -inf
+                }
+            __syncwarp();
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                if (g == 0) { ref[8 * b + 2 * tq] = M[b][0]; ref[8 * b + 2 * tq + 1] = M[b][1]; }
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float& x = o[b][i][e];
+                        float* const at = mine_ + ((b * MT + i) * 4 + e) * 32;
+                        if (old) x = fmaf(*at, f[b][e & 1], x);
+                        if (!last) { *at = x; x = 0.0f; }
+                    }
+            }
+            __syncwarp();                                         // (last: the region takes the rows next)
+        };
         for (int t = 0; t < mine; ++t) {
             // what belongs to this tile, before the batch moves on
             bool on[NSUB];
@@ -613,15 +644,8 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
                     for (int x = 0; x < 2; ++x) {
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
-                            float fresh[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            float (&sum)[4] = FRESH ? fresh : o[b][2 * w + x];
-                            if constexpr (FRESH) mma16816(sum, va[x], plo[b].x, plo[b].y);
-                            mma16816(sum, va[x], ph[b].x, ph[b].y);
-                            if constexpr (SPLIT_P && !FRESH) mma16816(sum, va[x], plo[b].x, plo[b].y);
-                            if constexpr (FRESH) {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) o[b][2 * w + x][i] += fresh[i];
-                            }
+                            mma16816(o[b][2 * w + x], va[x], ph[b].x, ph[b].y);
+                            if constexpr (SPLIT_P) mma16816(o[b][2 * w + x], va[x], plo[b].x, plo[b].y);
                         }
                         if constexpr (F32) {
                             if (small) {
@@ -630,14 +654,8 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
                                 for (int i = 0; i < 4; ++i) vb[i] = half_to_bf16(va[x][i]);
 #pragma unroll
                                 for (int b = 0; b < NB; ++b) {
-                                    float fresh[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                                    float (&sum)[4] = FRESH ? fresh : o[b][2 * w + x];
-                                    mma16816_bf16(sum, vb, ps[b].x, ps[b].y);
-                                    mma16816_bf16(sum, vb, pt[b].x, pt[b].y);
-                                    if constexpr (FRESH) {
-#pragma unroll
-                                        for (int i = 0; i < 4; ++i) o[b][2 * w + x][i] += fresh[i];
-                                    }
+                                    mma16816_bf16(o[b][2 * w + x], vb, ps[b].x, ps[b].y);
+                                    mma16816_bf16(o[b][2 * w + x], vb, pt[b].x, pt[b].y);
                                 }
                             }
                         }
@@ -645,6 +663,12 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
                 }
             }
             if (more) load_v(t + 1);
+            if constexpr (FLUSH > 0) {
+                if (more && (t + 1) % FLUSH == 0) flush(t + 1 > FLUSH, false);
+            }
+        }
+        if constexpr (FLUSH > 0) {
+            if (mine > FLUSH) flush(true, true);
         }
 
         // ---- the warps' parts of the piece

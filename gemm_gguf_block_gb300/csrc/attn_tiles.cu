@@ -70,15 +70,17 @@ template <typename T, int D, bool TREE, bool NARROW> struct Tiles {
     static constexpr bool F32 = std::is_same<T, float>::value;
     static_assert(!(F32 && NARROW), "fp32 has one row tile always");
     // binary16 trees: P in two parts (21 bits), so that a tree's precision, 22 bits in the rows kernel, does not hang on
-    // what stands beside it in the call. (64 contexts of 200-8190, 12-36 rows: 124 us, 111 with one part.) bfloat16's
+    // what stands beside it in the call. (64 contexts of 200-8190, 12-36 rows: 128 us, 114 with one part.) bfloat16's
     // results have 8 bits: one part.
     static constexpr bool PAIR = NARROW && std::is_same<T, __half>::value;
     static constexpr int PARTS = F32 ? 3 : PAIR ? 2 : 1;   // of P
-    // fp32 trees: the MMAs' sums are cut off at each addition, 2e-9 of a result a key (1e-5 at 8000 keys, 7e-5 at 60000, where
-    // fp32 sums that round are 1e-6 off). A result begins anew every FLUSH steps, and the softmax threads add the last one to
-    // totals of their own. (64 contexts of 200-8190 keys, 12-36 rows of 128: 212 us, 201 with one result throughout; every
-    // eighth step leaves 1.7e-6, every fourth 1.1e-6.)
-    static constexpr int FLUSH = F32 && TREE ? 4 : 0;
+    // Trees: the MMAs' sums are cut off at each addition, up to 5e-9 of a result a key, 1e-8 with P in two parts (fp32: 7e-5 at
+    // 60000 random keys, 2e-4 at 40000 of one sign, where sums that round are 1e-6 off; binary16 7e-4 at 65536 of one sign, its
+    // own rounding 2e-4). So a result begins anew every FLUSH steps, and the softmax threads add the last one to totals of their
+    // own: every 512 keys for fp32 (1.1e-6 at any length; every eighth step leaves 1.7e-6), every 4096 for binary16 (4e-5 at most),
+    // every 32768 for bfloat16 (2e-4, a twentieth of half a step). 64 contexts of 200-8190 keys, 12-36 rows of 128: fp32 212 us,
+    // 201 with one result throughout, binary16 128 and 124, bfloat16 113 and 111 (whose contexts are too short to come here).
+    static constexpr int FLUSH = !TREE ? 0 : F32 ? 4 : PAIR ? 32 : 256;
     // Two row tiles a CTA and four converter warps; NARROW: one tile, a row's keys halved between two threads as in fp32,
     // and eight converter warps.
     static constexpr int KEYS = 128;                       // keys of a step
@@ -121,7 +123,7 @@ template <typename T, int D, bool TREE, bool NARROW> struct Tiles {
     static constexpr uint32_t O1 = O0 + (F32 ? D : NARROW ? 0 : 128);   // fp32: the smaller result; two tiles: the second's
     static constexpr uint32_t P2 = 448;                    // P's second part
     static constexpr uint32_t T0 = 448;                    // FLUSH: totals, from a thread's 32nd column on
-    static_assert(FLUSH == 0 || OC == 32 || (OC == 64 && O1 + D <= T0), "totals");
+    static_assert(!F32 || FLUSH == 0 || OC == 32 || (OC == 64 && O1 + D <= T0), "totals");
     static_assert(O1 + D <= (PAIR ? P2 : 512), "tensor memory");
 };
 
@@ -397,8 +399,9 @@ __global__ void __launch_bounds__(Tiles<T, D, TREE, NARROW>::THREADS, 1) attn_ti
         const uint32_t o_col = tmem + lanes + (mt == 0 ? W::O0 : W::O1) + OC * part;
         constexpr int CHUNKS = KT / 32;
         float M = -INFINITY, l = 0.0f;
-        // The results before the last FLUSH steps, and their reference: a thread's first 32 columns, the others in tensor memory.
-        float total[W::FLUSH ? 32 : 1], total_M = -INFINITY;
+        // The results before the last FLUSH steps, and their reference. fp32: a thread's first 32 columns, the others in tensor
+        // memory; 16-bit types, which come here rarely and have no column left: in local memory.
+        float total[!W::FLUSH ? 1 : F32 ? 32 : OC], total_M = -INFINITY;
         const uint32_t t_col = tmem + lanes + W::T0 + 32 * part;
         bool ok = true;
         // After a wait that ran out (ok false) the loop goes on without waiting: the meetings stay paired.
@@ -410,15 +413,13 @@ __global__ void __launch_bounds__(Tiles<T, D, TREE, NARROW>::THREADS, 1) attn_ti
             }
             tc::fence_after();
         };
-        // The last steps' results to the totals, before step j: its products begin them anew.
-        bool flushed = false;
+        // The last steps' results to the totals, before step j, whose products begin them anew.
+        auto factor = [&]() { return total_M == M ? 1.0f : exp2_approx(total_M - M); };      // 0 from -inf
         auto flush = [&](const int j) {
-            if constexpr (W::FLUSH > 0) {
-                wait(B_O + mt, (j - 1) & 1);
-                const float f = total_M == M ? 1.0f : exp2_approx(total_M - M);              // 0 from -inf
-                auto added = [&](float was, uint32_t big, uint32_t small) {
-                    return (j > W::FLUSH ? was * f : 0.0f) + (__uint_as_float(big) + __uint_as_float(small));
-                };
+            wait(B_O + mt, (j - 1) & 1);
+            const float f = factor();
+            auto add = [&](float was, float now) { return (j > W::FLUSH ? was * f : 0.0f) + now; };
+            if constexpr (F32) {
 #pragma unroll
                 for (int ch = 0; ch < 2; ++ch) {
                     uint32_t big[16], small[16];
@@ -426,7 +427,8 @@ __global__ void __launch_bounds__(Tiles<T, D, TREE, NARROW>::THREADS, 1) attn_ti
                     tc::ld16(o_col + 16 * ch + (W::O1 - W::O0), small);
                     tc::wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) total[16 * ch + i] = added(total[16 * ch + i], big[i], small[i]);
+                    for (int i = 0; i < 16; ++i)
+                        total[16 * ch + i] = add(total[16 * ch + i], __uint_as_float(big[i]) + __uint_as_float(small[i]));
                 }
 #pragma unroll 1
                 for (int ch = 2; ch < OC / 16; ++ch) {
@@ -436,11 +438,21 @@ __global__ void __launch_bounds__(Tiles<T, D, TREE, NARROW>::THREADS, 1) attn_ti
                     tc::ld16(t_col + 16 * (ch - 2), rest);
                     tc::wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) rest[i] = __float_as_uint(added(__uint_as_float(rest[i]), big[i], small[i]));
+                    for (int i = 0; i < 16; ++i)
+                        rest[i] = __float_as_uint(add(__uint_as_float(rest[i]), __uint_as_float(big[i]) + __uint_as_float(small[i])));
                     tc::st16(t_col + 16 * (ch - 2), rest);
                 }
-                total_M = M;
+            } else {
+#pragma unroll 1
+                for (int col = 0; col < OC; col += 16) {
+                    uint32_t x[16];
+                    tc::ld16(o_col + col, x);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) total[col + i] = add(total[col + i], __uint_as_float(x[i]));
+                }
             }
+            total_M = M;
         };
         // A step; whole: every row sees all its keys.
         auto step = [&](const int j, auto whole_) {
@@ -511,13 +523,13 @@ __global__ void __launch_bounds__(Tiles<T, D, TREE, NARROW>::THREADS, 1) attn_ti
                 for (int i = 0; i < SPLIT; ++i) top = fmaxf(top, exch[j & 1][i][row]);
             }
             const bool raise = top > M + RAISE;
-            bool o_known = j == 0 || flushed;
+            bool o_known = j == 0;
             if (__any_sync(0xffffffffu, raise)) {
                 const float old = M;
                 if (raise) M = top;
                 const float f = raise ? exp2_approx(old - M) : 1.0f;             // 0 from -inf
                 l *= f;
-                if (j > 0 && !flushed) {
+                if (j > 0) {
                     wait(B_O + mt, (j - 1) & 1);
                     o_known = true;
 #pragma unroll 1
@@ -614,17 +626,44 @@ __global__ void __launch_bounds__(Tiles<T, D, TREE, NARROW>::THREADS, 1) attn_ti
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars[B_P + mt]);
         };
-        for (int j = 0; j < steps; ++j) {
-            const int k0 = key0 + j * KEYS + KT * part;
-            if constexpr (W::FLUSH > 0) {
-                flushed = j > 0 && j % W::FLUSH == 0;
-                if (flushed) flush(j);
+        // (One tile: a loop in a loop, 128 us for 130 at binary16's 64 contexts. Elsewhere that spills: 197 us for 193, bfloat16,
+        // 4 contexts of 30k-60k.)
+        if constexpr (NARROW) {
+            for (int j = 0; j < steps;) {
+                if (j > 0) flush(j);
+                for (const int until = min(j + W::FLUSH, steps); j < until; ++j) {
+                    const int k0 = key0 + j * KEYS + KT * part;
+                    if (k0 >= all_from && k0 <= all_stop - KT) step(j, std::true_type{});
+                    else step(j, std::false_type{});
+                }
             }
-            if (k0 >= all_from && k0 <= all_stop - KT) step(j, std::true_type{});
-            else step(j, std::false_type{});
+        } else {
+            for (int j = 0; j < steps; ++j) {
+                const int k0 = key0 + j * KEYS + KT * part;
+                if constexpr (W::FLUSH > 0) {
+                    if (j > 0 && j % W::FLUSH == 0) flush(j);
+                }
+                if (k0 >= all_from && k0 <= all_stop - KT) step(j, std::true_type{});
+                else step(j, std::false_type{});
+            }
         }
         // ---- the rows
         if (steps > 0) wait(B_O + mt, (steps - 1) & 1);
+        if constexpr (W::FLUSH > 0 && !F32) {               // the totals to the results (fp32: as the rows are written)
+            if (steps > W::FLUSH) {
+                const float f = factor();
+#pragma unroll 1
+                for (int col = 0; col < OC; col += 16) {
+                    uint32_t x[16];
+                    tc::ld16(o_col + col, x);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(fmaf(total[col + i], f, __uint_as_float(x[i])));
+                    tc::st16(o_col + col, x);
+                }
+                tc::wait_st();
+            }
+        }
         if constexpr (SPLIT > 1) {
             exch[steps & 1][part][row] = l;
             meet();
@@ -632,7 +671,7 @@ __global__ void __launch_bounds__(Tiles<T, D, TREE, NARROW>::THREADS, 1) attn_ti
 #pragma unroll
             for (int i = 0; i < SPLIT; ++i) l += exch[steps & 1][i][row];
         }
-        const float total_f = total_M == M ? 1.0f : exp2_approx(total_M - M);
+        const float total_f = factor();
         auto load_o = [&](int col, uint32_t (&orr)[32]) {       // of the thread's columns
             const uint32_t at = o_col + col;
             if (steps == 0) {
@@ -648,17 +687,16 @@ __global__ void __launch_bounds__(Tiles<T, D, TREE, NARROW>::THREADS, 1) attn_ti
                 tc::wait_ld();
 #pragma unroll
                 for (int i = 0; i < 32; ++i) orr[i] = __float_as_uint(__uint_as_float(orr[i]) + __uint_as_float(os[i]));
-            }
-            if constexpr (W::FLUSH > 0) {
-                if (steps > W::FLUSH) {
-                    uint32_t rest[32];
-                    if (col > 0) {
-                        tc::ld32(t_col, rest);
-                        tc::wait_ld();
-                    }
+                if constexpr (W::FLUSH > 0) {
+                    if (steps > W::FLUSH) {
+                        if (col > 0) {
+                            tc::ld32(t_col, os);
+                            tc::wait_ld();
+                        }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        orr[i] = __float_as_uint(fmaf(col > 0 ? __uint_as_float(rest[i]) : total[i], total_f, __uint_as_float(orr[i])));
+                        for (int i = 0; i < 32; ++i)
+                            orr[i] = __float_as_uint(fmaf(col > 0 ? __uint_as_float(os[i]) : total[i], total_f, __uint_as_float(orr[i])));
+                    }
                 }
             }
         };

@@ -142,8 +142,9 @@ cq_status cq_kv_read(const cq_kv_cache* cache, cq_dtype dtype, int64_t T, const 
  * reaches a row, whatever it or its block's scale holds. Rows of no request
  * (t >= q_start[R]) are not written. Softmax statistics and sums are fp32,
  * exponentials and the factors of 16-bit calls' value scales good to 2^-22. The tensor cores' sums
- * are cut off at each addition of 16 keys: a fp32 prompt or chunk over a long context (where requests
- * are many: few are split over their keys) loses 1e-9 to 5e-9 of its results a key, values of one sign most.
+ * are cut off at each addition of 16 keys: a prompt or chunk over a long context (where requests are
+ * many: few are split over their keys) loses 1e-9 to 5e-9 of its results a key, values of one sign most,
+ * a decoded token a quarter to half of that: fp32 calls feel it from some thousand keys on, binary16 ones from 50000.
  * What the products take:
  *   fp32 q 22 bits, the probabilities 22 (those below 2^-15 of the row's largest 16 at least)
  *   16-bit q as it is (values below 2^-22 of the row's largest to 2^-33 of it)

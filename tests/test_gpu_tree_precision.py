@@ -100,3 +100,44 @@ def test_fp32_sums_of_long_contexts_round(D, n, R):
         most = 2 * es * 0.27 + 2.0 ** -18 + 5e-6 + 2.0 ** -22
         off = ((out[0, :, h * 4:h * 4 + 4] - want).abs() / want).max().item()
         assert off <= most, f"{off:.2e} of {most:.2e}"
+
+
+@pytest.mark.parametrize("dtype,D,n,R,kv", [("f16", 64, 1, 57, 262144), ("f16", 128, 3, 57, 262144), ("f16", 64, 20, 12, 262144),
+                                            ("f16", 128, 60, 12, 262144), ("bf16", 64, 20, 12, 524288), ("bf16", 128, 60, 12, 524288)])
+def test_16_bit_sums_of_very_long_contexts_round(dtype, D, n, R, kv):
+    """As above, where what is cut off passes the result's own rounding: contexts of a quarter and half a million keys.
+
+    Bound: half a step of the result; the probabilities' errors as above, and of bfloat16's 11 bits 2^-12 (their roundings
+    do not fall into step: a mean of them is far less); sums that are cut off go over 512 additions (binary16: 4096 keys,
+    two parts) or 2048 (bfloat16: 32768 keys) and grow evenly, so that they are half their size on average, each off by at
+    most 2^-23 for the sum and as much for the products that are cut off beside it: 2^-14 and 2^-12; and 5e-6 for those
+    that round."""
+    torch, cq = torch_cuda(), cq_built()
+    P, H, Hq = 64, 8, 32
+    g = torch.Generator(device="cuda")
+    g.manual_seed(kv + D + n)
+    shape = (kv // P, H, P, D)
+    k = torch.randint(-127, 128, shape, generator=g, dtype=torch.int8, device="cuda")
+    v = torch.randint(100, 128, shape, generator=g, dtype=torch.int8, device="cuda")
+    s = torch.tensor([0.01, 0.5018], device="cuda")
+    cache = cq.KVCache(k, v, s[:1].expand(shape[0], H).contiguous(), s[1:].expand(shape[0], H).contiguous())
+    dt = torch.float16 if dtype == "f16" else torch.bfloat16
+    q = (torch.randn(n, Hq, D, generator=g, device="cuda") * 0.3).to(dt)
+    table = torch.arange(shape[0], dtype=torch.int32, device="cuda").repeat(R, 1)
+    mask = torch.tensor([1 << i | 1 for i in range(n)], dtype=torch.int64, device="cuda")
+    out, _ = cq.attn_tree_t(q.repeat(R, 1, 1), cache, table, torch.full((R,), kv, dtype=torch.int32, device="cuda"),
+                            torch.arange(R + 1, dtype=torch.int32, device="cuda") * n, mask.repeat(R), n)
+    out = out.view(R, n, Hq, D)
+    h = H - 1
+    kk, vv = (x[:, h].reshape(kv, D).double() * y.double() for x, y in ((k, s[0]), (v, s[1])))
+    t = slice(0, n, max(n // 6, 1))
+    qq = q[t, h * 4:].double()
+    z = torch.einsum("ngd,kd->ngk", qq, kk) * D ** -0.5
+    z[:, :, kv - n:].masked_fill_(((mask[t, None] >> torch.arange(n, device="cuda")) & 1 == 0)[:, None], -float("inf"))
+    want = torch.softmax(z, -1) @ vv
+    A = (qq.abs().sum(-1).max() * kk.abs().max() * D ** -0.5).item()
+    es = 2.0 ** -18 * A + 64 * 2.0 ** -23
+    most = 2 * es * 0.27 + (2.0 ** -14 if dtype == "f16" else 2 * 2.0 ** -12) + 5e-6
+    half = torch.finfo(dt).eps / 2 * torch.exp2(torch.floor(torch.log2(want)))
+    off = (out[:, t, h * 4:].double() - want).abs()       # all requests read the same
+    assert (off <= half + most * want).all(), f"{(off / (half + most * want)).max().item():.2f} of its bound"
