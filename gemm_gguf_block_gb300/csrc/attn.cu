@@ -18,7 +18,7 @@ constexpr int TILE_ROWS = 40;
 
 // Trees: a call's requests go to one kernel, all of them, by the widest's rows -- a tree costs the tiles the same
 // whatever its width, and tiles beside rows slow both (64 contexts of 200-8190, bf16, 12-36 rows: 276 us with the border
-// at 33 rows, 111 all in the tiles, 162 all in the rows kernel). Few (request, kv head) pairs leave the rows kernel enough
+// at 33 rows, 113 all in the tiles, 162 all in the rows kernel). Few (request, kv head) pairs leave the rows kernel enough
 // SMs for longer. Rows kernel / tiles, us, 32 query and 8 kv heads of 128, bf16 (binary16's tiles take 12% more, fp32 takes
 // 1.2 to 1.75 times as long in both):
 //   64 requests of 1500 keys    12 rows 75 / 101     16 rows 78 / 102    24 rows 129 / 103    64 rows 239 / 104

@@ -26,7 +26,7 @@
 // the parts.
 // Trees: TREE builds have the rows' masks in the steps that are not whole. NARROW ones take a tile of 128 rows alone, two
 // threads a row, with eight converter warps that copy the bytes asynchronously: 64 contexts of 200-8190 keys, 32
-// heads on 8 of 128, bf16, 12 to 36 rows take 111 us (two tiles: 162 together with the rows kernel). A step takes
+// heads on 8 of 128, bf16, 12 to 36 rows take 113 us (two tiles: 162 together with the rows kernel). A step takes
 // 2400 cycles whatever the rows: 900 of them a thread's exponentials, the rest one wait behind another (scores, meeting,
 // product, converters); an item's beginning and end 9 us. Tried for NARROW without gain: 64 keys a step and two CTAs
 // an SM (the same time), the queries in tensor memory, two steps' P.

@@ -52,7 +52,7 @@ extern "C" {
  * taken to 2^-62 of a turn, so that phi is as good as that times the position (2^-31 of a turn
  * at 2^31) and its sine and cosine as fp32's. Frequencies are finite, below 2^31 in size.
  * Rows with a negative position (padding) are not written. Sums of squares are fp32: |x|
- * up to 1e18. in = out, or in = CQ_F32; q_out may be q and k_out may be k, with the same type and stride
+ * up to 1e18, and any size below. in = out, or in = CQ_F32; q_out may be q and k_out may be k, with the same type and stride
  * (in place); any other overlap of inputs and outputs is a race. Either of q_heads and
  * kv_heads may be 0 (its pointers are not read).
  * head_dim 64 or 128; rot_dim a multiple of 8, 0 to head_dim (0: freqs may be NULL);
