@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(THREADS, Rows<T, D, NB>::CTAS) attn_rows_kerne
     // the warp's part of the merge region: every 128 keys for fp32 results, every 2048 for binary16 (2e-5 at most, a twentieth
     // of half a step), every 32768 for bfloat16. (64 requests of 1500 keys, 12 rows of 128: fp32
     // 106 us, 103 with one sum throughout, bfloat16 75.5 and 74.6.)
+    static_assert(NB * (D / 16) * 4 * 32 <= 8 * NB * (D + 4), "a lane's results in the warp's part");
     constexpr int FLUSH = TREE ? (F32 ? 128 : SPLIT_P ? 2048 : 32768) / (16 * 128 / D) : 0;
     constexpr int RT = W::RT, ROWF = W::ROWF;
     constexpr float OFF = W::OFF, RAISE = W::RAISE;

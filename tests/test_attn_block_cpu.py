@@ -182,3 +182,56 @@ def test_end_refuses_requests_that_are_not_there(block, r):
     assert _same(was, _state(block))
     block.keep(_i32(2, 2), torch.tensor([[0, 3], [0, 7]], dtype=torch.int32))
     assert block.past == [42, 42]
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_any_order_of_steps_keeps_and_ends(monkeypatch, seed):
+    """Random orders of the three calls, refused ones among them, against lists of the requests' keys: lengths, pages (each a
+    request's or free, none twice), and every stored row within six steps of its page's scale (half a step a raise)."""
+    monkeypatch.setattr(attn_block, "cq", _definitions())
+    rng, R = np.random.default_rng(seed), 3
+    g = torch.Generator().manual_seed(seed)
+    b = attn_block.AttentionBlock(torch.randn(HIDDEN, 3 * HEADS * D, generator=g), torch.randn(HEADS * D, HIDDEN, generator=g),
+                                  cq.FMT["q8_0"], HIDDEN, HEADS, HEADS, D, requests=R, num_pages=40)
+    b.gen = g
+    want, open_step = [[] for _ in range(R)], None       # keys of each request; (new tokens, lengths before, ended since)
+    for _ in range(40):
+        op = rng.choice(["step", "tree", "keep", "keep", "end"])
+        if op in ("step", "tree"):
+            new = [int(rng.choice([0, 1, 3, 12, 30, 70])) for _ in range(R)]
+            parents = [tree_ref.random_parents(rng, n) if n else [] for n in new]
+            x = _tokens(b, sum(new))
+            if sum(new) == 0 or sum(-(-(len(w) + n) // P) for w, n in zip(want, new)) > 40:
+                with pytest.raises(cq.CqError):
+                    b.step(x, new)
+                continue
+            b.step(x, new, torch.from_numpy(np.concatenate(parents).astype(np.int32)) if op == "tree" else None)
+            open_step = (new, [len(w) for w in want], set())
+            k = (x @ b.wqkv)[:, HEADS * D:2 * HEADS * D].reshape(-1, HEADS, D).split(new)
+            want = [w + list(rows) for w, rows in zip(want, k)]
+        elif op == "keep":
+            most = int(rng.integers(1, 20))
+            new = open_step[0] if open_step else [0] * R
+            paths = [np.sort(rng.permutation(n)[:int(rng.integers(0, min(n, most) + 1))]).tolist() if n <= 64 else [] for n in new]
+            args = (_i32(*map(len, paths)), torch.tensor([(p + [-1] * most)[:most] for p in paths], dtype=torch.int32))
+            if open_step is None:
+                with pytest.raises(cq.CqError):
+                    b.keep(*args)
+                continue
+            b.keep(*args)
+            for r, (n, base) in enumerate(zip(*open_step[:2])):
+                if r not in open_step[2] and n <= 64:
+                    want[r] = want[r][:base] + [want[r][base + i] for i in paths[r]]
+            open_step = None
+        else:
+            r = int(rng.integers(R))
+            b.end(r)
+            want[r] = []
+            if open_step:
+                open_step[2].add(r)
+        assert b.past == [len(w) for w in want]
+        _pages(b)
+        for r, w in enumerate(want):
+            for i, row in enumerate(w):
+                scale = b.cache.k_scale[int(b.table[r, i // P])][:, None]
+                assert ((b.cache.k[int(b.table[r, i // P]), :, i % P] * scale - row).abs() <= 6 * scale).all()
