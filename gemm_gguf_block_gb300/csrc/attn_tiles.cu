@@ -77,10 +77,10 @@ template <typename T, int D, bool TREE, bool NARROW> struct Tiles {
     // Trees: the MMAs' sums are cut off at each addition, up to 5e-9 of a result a key, 1e-8 with P in two parts (fp32: 7e-5 at
     // 60000 random keys, 2e-4 at 40000 of one sign, where sums that round are 1e-6 off; binary16 7e-4 at 65536 of one sign, its
     // own rounding 2e-4). So a result begins anew every FLUSH steps, and the softmax threads add the last one to totals of their
-    // own: every 512 keys for fp32 (1.1e-6 at any length; every eighth step leaves 1.7e-6), every 4096 for binary16 (4e-5 at most),
-    // every 32768 for bfloat16 (2e-4, a twentieth of half a step). 64 contexts of 200-8190 keys, 12-36 rows of 128: fp32 212 us,
+    // own: every 512 keys for fp32 (1.1e-6 at any length; every eighth step leaves 1.7e-6), every 4096 for binary16 in two parts and 8192 in
+    // one (4e-5 at most), every 32768 for bfloat16 (2e-4, a twentieth of half a step). 64 contexts of 200-8190 keys, 12-36 rows of 128: fp32 212 us,
     // 201 with one result throughout, binary16 128 and 124, bfloat16 113 and 111 (whose contexts are too short to come here).
-    static constexpr int FLUSH = !TREE ? 0 : F32 ? 4 : PAIR ? 32 : 256;
+    static constexpr int FLUSH = !TREE ? 0 : F32 ? 4 : PAIR ? 32 : std::is_same<T, __half>::value ? 64 : 256;
     // Two row tiles a CTA and four converter warps; NARROW: one tile, a row's keys halved between two threads as in fp32,
     // and eight converter warps.
     static constexpr int KEYS = 128;                       // keys of a step

@@ -88,7 +88,7 @@ cq_status cq_tree_plan(int64_t R, int64_t T, const int32_t* kv_len, const int32_
  * with no window (max_new, the workspace, precision, rows that see nothing, pages outside the cache), but that
  * max_new <= CQ_TREE_MAX sends a call's requests to one kernel, all of them, and that the probabilities of binary16
  * calls' trees have 21 bits, whatever stands beside them (of longer requests 11 at least). The tensor cores'
- * sums, cut off rather than rounded at each addition of 16 keys, go over 512 keys at most in fp32 calls, 4096 in
+ * sums, cut off rather than rounded at each addition of 16 keys, go over 512 keys at most in fp32 calls, 8192 in
  * binary16 and 32768 in bfloat16 ones; what they add up to rounds.
  */
 cq_status cq_attn_tree(const cq_kv_cache* cache, cq_dtype dtype, int64_t R, int64_t T, int64_t q_heads,

@@ -141,3 +141,38 @@ def test_16_bit_sums_of_very_long_contexts_round(dtype, D, n, R, kv):
     half = torch.finfo(dt).eps / 2 * torch.exp2(torch.floor(torch.log2(want)))
     off = (out[:, t, h * 4:].double() - want).abs()       # all requests read the same
     assert (off <= half + most * want).all(), f"{(off / (half + most * want)).max().item():.2f} of its bound"
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_binary16_prompts_over_very_long_contexts_round(D):
+    """The same for a prompt in a call that has two row tiles a CTA (by the bound of new tokens): 100 tokens over a quarter of a
+    million keys each, requests enough that none is split over its keys.
+
+    Bound: half a step of the result; probabilities of 11 bits 2^-12, as of bfloat16 above; sums that are cut off over 512
+    additions (8192 keys): 2^-14; scores and exponentials as above, and 5e-6."""
+    torch, cq = torch_cuda(), cq_built()
+    P, H, Hq, n, R, kv = 64, 8, 16, 100, 12, 262144
+    g = torch.Generator(device="cuda")
+    g.manual_seed(D)
+    shape = (kv // P, H, P, D)
+    k = torch.randint(-127, 128, shape, generator=g, dtype=torch.int8, device="cuda")
+    v = torch.randint(100, 128, shape, generator=g, dtype=torch.int8, device="cuda")
+    s = torch.tensor([0.01, 0.5018], device="cuda")
+    cache = cq.KVCache(k, v, s[:1].expand(shape[0], H).contiguous(), s[1:].expand(shape[0], H).contiguous())
+    q = (torch.randn(n, Hq, D, generator=g, device="cuda") * 0.3).half()
+    table = torch.arange(shape[0], dtype=torch.int32, device="cuda").repeat(R, 1)
+    out, _ = cq.attn_tree_t(q.repeat(R, 1, 1), cache, table, torch.full((R,), kv, dtype=torch.int32, device="cuda"),
+                            torch.arange(R + 1, dtype=torch.int32, device="cuda") * n,
+                            torch.zeros(R * n, dtype=torch.int64, device="cuda"), 3000)
+    t, h = torch.tensor([0, 41, 99], device="cuda"), H - 1
+    kk, vv = (x[:, h].reshape(kv, D).double() * y.double() for x, y in ((k, s[0]), (v, s[1])))
+    qq = q[t, h * 2:].double()
+    z = torch.einsum("ngd,kd->ngk", qq, kk) * D ** -0.5
+    for i, at in enumerate(t.tolist()):
+        z[i, :, kv - n + at + 1:] = -float("inf")
+    want = torch.softmax(z, -1) @ vv
+    A = (qq.abs().sum(-1).max() * kk.abs().max() * D ** -0.5).item()
+    most = 2 * (2.0 ** -18 * A + 64 * 2.0 ** -23) * 0.27 + 2.0 ** -12 + 2.0 ** -14 + 5e-6
+    half = 2.0 ** -11 * torch.exp2(torch.floor(torch.log2(want)))
+    off = (out.view(R, n, Hq, D)[:, t, h * 2:].double() - want).abs()
+    assert (off <= half + most * want).all(), f"{(off / (half + most * want)).max().item():.2f} of its bound"
